@@ -410,6 +410,85 @@ kdt_status kdt_kv_compact(void *c_kv, void *k_pe, kdt_dtype dtype, int D_c, int 
                           int64_t kv_row_stride, int32_t *prefix_len, const int32_t *acc_nodes,
                           const int32_t *n_acc, int update_prefix, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * The 8-bit latent cache: the same step on a cache of a little over half the bytes.
+ *
+ * Row j of sequence b (656 bytes instead of bf16's 1152) is
+ *   c_q8     uint8 [B,L,512]  e4m3 codes (1 sign, 4 exponent, 3 mantissa bits) of the latent
+ *   c_scale  uint8 [B,L,16]   one power of two for each 32 consecutive codes (E8M0: byte s
+ *                             stands for 2^(s-127))
+ *   k_pe     bf16  [B,L,64]   rotated rope key, kept in 16 bits
+ * and stands for c[d] = e4m3(c_q8[d]) * 2^(c_scale[d/32] - 127). Scale bytes lie in
+ * [27, 227] (2^-100 .. 2^100), or are 255: a group that held an infinity or NaN, which
+ * reads as NaN. Within that range every value is a bf16 number exactly, so the attention
+ * below loses nothing against one over the bf16 cache of the same values. The codes 0x7f
+ * and 0xff (e4m3's NaN) are never written and are not valid in a cache.
+ * Rows are contiguous; all three bases are 16-byte aligned.
+ * ------------------------------------------------------------------------------ */
+#define KDT_Q8_GROUP 32
+
+/* Arguments of kdt_latent_write_q8. */
+typedef struct {
+    int B, T;               /* sequences, new rows per sequence (tree nodes, or a prompt chunk): T >= 1 */
+    int D_c, D_r;           /* must be 512 and 64 */
+    kdt_dtype dtype;        /* element type of c, k and gamma */
+    const void *c;          /* latent of row (b,i): the 512 elements at c + (b*T + i) * c_row_stride */
+    int64_t c_row_stride;   /* elements, 0 = 512; else >= 512 and a multiple of 16 bytes */
+    const void *k;          /* its rope key, not yet rotated: 64 elements at k + (b*T + i) * k_row_stride */
+    int64_t k_row_stride;   /* elements, 0 = 64; else >= 64 */
+    const void *gamma;      /* [512] weight of the latent's RMS norm, or NULL: no norm */
+    float eps;              /* the norm's epsilon, >= 0 (used with gamma) */
+    const int32_t *pos;     /* device [B,T] rotary positions, or NULL: k is written as it is */
+    double base;            /* angle base (theta), > 0 (used with pos) */
+    const int32_t *prefix_len; /* device [B]: row (b,i) goes to cache row prefix_len[b] + i */
+    const int32_t *n_rows;  /* device [B]: sequence b has rows i < n_rows[b] only (a padded batch), or NULL: T */
+    uint8_t *c_q8;          /* the cache */
+    uint8_t *c_scale;
+    void *k_pe;
+    int64_t kv_row_stride;  /* L: cache rows per sequence, >= 1 */
+} kdt_latent_write_args;
+
+/*
+ * kdt_latent_write_q8 -- norm, rotate, quantise and store new rows in one pass.
+ * For every row x = c[b,i,:]:  y_d = x_d * r * gamma_d with r = 1 / sqrt(mean x^2 + eps)
+ * (y = x without gamma), in float32. For each group of 32: a = max |y_d|, e = the least
+ * integer with a <= 448 * 2^e, clamped to [-100, 100] (a = 0 gives -100); the scale byte
+ * is e + 127 and the codes are e4m3 (round to nearest even, at most 448) of y_d * 2^-e.
+ * If a is infinite or NaN the byte is 255 and the codes are 0.
+ * k_pe[row] is k rotated as by kdt_rope_neox (position pos[b,i], width 64), the angle
+ * taken exactly modulo a full turn and its cosine and sine in float32, rounded once to bf16.
+ * Cache rows outside [0, L), and rows of sequences beyond n_rows, are left as they were.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE (sizes, strides, alignment, B*T > 2^31 - 1),
+ * KDT_ERR_UNSUPPORTED (D_c, D_r, dtype), KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_latent_write_q8(const kdt_latent_write_args *a, cudaStream_t stream);
+
+/*
+ * kdt_latent_read_q8 -- cache rows back in 16 or 32 bits, e.g. to move a sequence to the
+ * bf16 cache kdt_verify_attn reads, or to expand a stretch of keys and values.
+ *   c_q8, c_scale, k_pe, L (kv_row_stride)  the cache, B sequences
+ *   start    device int32 [B]: first cache row of sequence b, or NULL: 0
+ *   n_rows   device int32 [B]: rows of sequence b to read (of the R), or NULL: R
+ *   c        device [B,R,512], k device [B,R,64], both of `dtype` (KDT_F32 or KDT_BF16);
+ *            either may be NULL. Row (b,i) gets cache row start[b] + i exactly (every
+ *            stored value is a bf16 number); a cache row outside [0, L) reads as zeros;
+ *            rows i >= n_rows[b] of c and k are left as they were.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE (also alignment, B*R > 2^31 - 1),
+ * KDT_ERR_UNSUPPORTED, KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_latent_read_q8(const uint8_t *c_q8, const uint8_t *c_scale, const void *k_pe, int64_t kv_row_stride,
+                              int B, int R, const int32_t *start, const int32_t *n_rows, kdt_dtype dtype, void *c,
+                              void *k, cudaStream_t stream);
+
+/*
+ * kdt_kv_compact_q8 -- kdt_kv_compact for the 8-bit cache: the codes, scales and rope keys
+ * of the accepted path's rows move to rows prefix_len[b] + k, in place; the same rules.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE, KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_kv_compact_q8(uint8_t *c_q8, uint8_t *c_scale, void *k_pe, int B, int T, int64_t kv_row_stride,
+                             int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int update_prefix,
+                             cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,8 +4,8 @@ The compute path is libkdt.so (C ABI in include/kdt.h, CUDA kernels in csrc/);
 this package holds the build script and a thin ctypes binding with the same names.
 """
 from .kdt import (  # noqa: F401
-    DEFAULT_SCALE, EXPORTS, IMPLS, KdtError, RopeArgs, VerifyArgs, build_visibility, host_buffer_size, kv_compact,
-    lib, make_args, merge_attn_states, plan, rope_neox, status_str, tree_accept, tree_build, verify_attn,
+    DEFAULT_SCALE, EXPORTS, IMPLS, KdtError, LatentWriteArgs, RopeArgs, VerifyArgs, build_visibility,
+    host_buffer_size, kv_compact, kv_compact_q8, latent_read_q8, latent_write_q8, lib, make_args, merge_attn_states, plan, rope_neox, status_str, tree_accept, tree_build, verify_attn,
     vc_up_proj, verify_attn_host, verify_attn_noalloc, workspace_size,
 )
 

@@ -22,21 +22,6 @@ int sm_count() {
     return v;
 }
 
-namespace {
-
-constexpr size_t kAlign = 256;
-
-// Problems with at most this many (query row x cache row) pairs go to the SIMT kernel on
-// 16-row tiles when the caller leaves the choice to the library: the crossovers measured
-// on GB300 (device time, L2 flushed) against the tensor-core kernel for bf16 inputs (about
-// 0.6 GFLOP; below it the 16-row SIMT kernel took 0.45-0.8 of the tensor kernel's time) and
-// against the 64-row SIMT kernel for fp32 inputs (about 1.1 GFLOP; 0.1-0.8 of its time).
-constexpr int64_t kSmallShapeWorkBf16 = (int64_t)1 << 18;
-constexpr int64_t kSmallShapeWorkF32 = (int64_t)1 << 19;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Every tensor a verify call touches must be device memory of the current device. The
 // tensor-core kernel encodes TMA tensor maps over c_kv, k_pe and q_pe and loads key tiles
 // with cluster multicast; those are issued here over this GPU's own memory only, never
@@ -59,6 +44,21 @@ kdt_status check_on_current_device(std::initializer_list<const void *> ptrs) {
     }
     return KDT_OK;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+// Problems with at most this many (query row x cache row) pairs go to the SIMT kernel on
+// 16-row tiles when the caller leaves the choice to the library: the crossovers measured
+// on GB300 (device time, L2 flushed) against the tensor-core kernel for bf16 inputs (about
+// 0.6 GFLOP; below it the 16-row SIMT kernel took 0.45-0.8 of the tensor kernel's time) and
+// against the 64-row SIMT kernel for fp32 inputs (about 1.1 GFLOP; 0.1-0.8 of its time).
+constexpr int64_t kSmallShapeWorkBf16 = (int64_t)1 << 18;
+constexpr int64_t kSmallShapeWorkF32 = (int64_t)1 << 19;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Plan;
 int unit_rows_of(const Plan &p);

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <initializer_list>
 #include <stdint.h>
 
 #include "kdt.h"
@@ -114,6 +115,10 @@ cudaError_t launch_vc_proj(const float *o, const void *w_vc, int R, int H, int D
 
 // Per-device SM count (cached).
 int sm_count();
+
+// KDT_OK when every non-NULL pointer is device memory of the current device, else
+// KDT_ERR_NOT_DEVICE (KDT_ERR_CUDA if the query itself fails).
+kdt_status check_on_current_device(std::initializer_list<const void *> ptrs);
 
 // kdt_verify_attn with the device-memory checks selectable: the caller's tensors
 // (check_tensors) and the workspace (check_workspace) must be device memory of the current

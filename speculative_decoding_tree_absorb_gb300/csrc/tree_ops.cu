@@ -125,18 +125,20 @@ __global__ void tree_accept_kernel(const int32_t *__restrict__ parent, const int
 // (row prefix + path[k] >= prefix + k) is never a row an earlier step wrote. The path is
 // moved in chunks of rows staged through shared memory: every source row of a chunk is
 // read before any of its destinations is written, and later chunks read no row an
-// earlier chunk wrote. Entries outside the tree or the cache are not copied.
+// earlier chunk wrote. Entries outside the tree or the cache are not copied. An 8-bit cache
+// has a third array, c_scale (s_vec = 1 vector a row; else NULL and 0).
 constexpr int kCompactSmem = 40 * 1024;
 
-__global__ void __launch_bounds__(256) kv_compact_kernel(uint4 *c_kv, uint4 *k_pe, int c_vec, int r_vec, int64_t L,
-                                                         int32_t *prefix_len, const int32_t *acc_nodes,
-                                                         const int32_t *n_acc, int T, int update_prefix) {
+__global__ void __launch_bounds__(256) kv_compact_kernel(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec,
+                                                         int r_vec, int s_vec, int64_t L, int32_t *prefix_len,
+                                                         const int32_t *acc_nodes, const int32_t *n_acc, int T,
+                                                         int update_prefix) {
     __shared__ uint4 stage[kCompactSmem / 16];
     __shared__ int src_row[kCompactSmem / 32];
     const int b = blockIdx.x;
     const int64_t p0 = prefix_len[b];
     const int n = min(max(n_acc[b], 0), T);
-    const int row_vec = c_vec + r_vec;
+    const int row_vec = c_vec + r_vec + s_vec;
     const int chunk = kCompactSmem / 16 / row_vec;      // rows staged at a time
     for (int k0 = 1; k0 < n; k0 += chunk) {
         const int kn = min(chunk, n - k0);
@@ -149,7 +151,8 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(uint4 *c_kv, uint4 *k_p
             const int t = v / row_vec, e = v - t * row_vec, src = src_row[t];
             if (src < 0) continue;
             const int64_t r = (int64_t)b * L + p0 + src;
-            stage[v] = e < c_vec ? c_kv[r * c_vec + e] : k_pe[r * r_vec + (e - c_vec)];
+            stage[v] = e < c_vec ? c_kv[r * c_vec + e]
+                                 : (e < c_vec + r_vec ? k_pe[r * r_vec + (e - c_vec)] : c_scale[r]);
         }
         __syncthreads();
         for (int v = threadIdx.x; v < kn * row_vec; v += blockDim.x) {
@@ -157,7 +160,8 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(uint4 *c_kv, uint4 *k_p
             if (src_row[t] < 0) continue;
             const int64_t r = (int64_t)b * L + p0 + k0 + t;
             if (e < c_vec) c_kv[r * c_vec + e] = stage[v];
-            else k_pe[r * r_vec + (e - c_vec)] = stage[v];
+            else if (e < c_vec + r_vec) k_pe[r * r_vec + (e - c_vec)] = stage[v];
+            else c_scale[r] = stage[v];
         }
         __syncthreads();
     }
@@ -474,9 +478,24 @@ kdt_status kdt_kv_compact(void *c_kv, void *k_pe, kdt_dtype dtype, int D_c, int 
     if (!c_kv || !k_pe || !prefix_len || !acc_nodes || !n_acc) return KDT_ERR_NULL_ARG;
     if (!aligned16(c_kv) || !aligned16(k_pe)) return KDT_ERR_BAD_SHAPE;
     if (((int64_t)D_c * esz + (int64_t)D_r * esz) > kCompactSmem) return KDT_ERR_BAD_SHAPE;
-    kv_compact_kernel<<<B, 256, 0, stream>>>(static_cast<uint4 *>(c_kv), static_cast<uint4 *>(k_pe),
-                                             D_c * esz / 16, D_r * esz / 16, kv_row_stride, prefix_len, acc_nodes,
+    kv_compact_kernel<<<B, 256, 0, stream>>>(static_cast<uint4 *>(c_kv), static_cast<uint4 *>(k_pe), nullptr,
+                                             D_c * esz / 16, D_r * esz / 16, 0, kv_row_stride, prefix_len, acc_nodes,
                                              n_acc, T, update_prefix ? 1 : 0);
+    return cudaGetLastError() == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+}
+
+kdt_status kdt_kv_compact_q8(uint8_t *c_q8, uint8_t *c_scale, void *k_pe, int B, int T, int64_t kv_row_stride,
+                             int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int update_prefix,
+                             cudaStream_t stream) {
+    if (B < 0 || T < 1 || T > kMaxT || kv_row_stride < T) return KDT_ERR_BAD_SHAPE;
+    if (B == 0) return KDT_OK;
+    if (!c_q8 || !c_scale || !k_pe || !prefix_len || !acc_nodes || !n_acc) return KDT_ERR_NULL_ARG;
+    if (!aligned16(c_q8) || !aligned16(c_scale) || !aligned16(k_pe)) return KDT_ERR_BAD_SHAPE;
+    const kdt_status st = check_on_current_device({c_q8, c_scale, k_pe, prefix_len, acc_nodes, n_acc});
+    if (st != KDT_OK) return st;
+    kv_compact_kernel<<<B, 256, 0, stream>>>(reinterpret_cast<uint4 *>(c_q8), static_cast<uint4 *>(k_pe),
+                                             reinterpret_cast<uint4 *>(c_scale), kDc / 16, kDr * 2 / 16, 1,
+                                             kv_row_stride, prefix_len, acc_nodes, n_acc, T, update_prefix ? 1 : 0);
     return cudaGetLastError() == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
 

@@ -27,7 +27,7 @@ EXPORTS = ("kdt_status_str", "kdt_version", "kdt_build_visibility", "kdt_verify_
            "kdt_verify_attn_workspace_size", "kdt_verify_attn_plan", "kdt_merge_attn_states",
            "kdt_verify_attn_noalloc", "kdt_rope_neox", "kdt_tree_accept", "kdt_kv_compact", "kdt_tree_build",
            "kdt_verify_attn_host", "kdt_verify_attn_host_buffer_size", "kdt_vc_up_proj",
-           "kdt_test_verify_attn_wait_expiry")
+           "kdt_test_verify_attn_wait_expiry", "kdt_latent_write_q8", "kdt_latent_read_q8", "kdt_kv_compact_q8")
 
 
 class KdtError(RuntimeError):
@@ -61,6 +61,20 @@ class RopeArgs(ctypes.Structure):
         ("k_pe", ctypes.c_void_p), ("kv_row_stride", ctypes.c_int64),
         ("prefix_len", ctypes.c_void_p), ("pos", ctypes.c_void_p),
         ("base", ctypes.c_double),
+    ]
+
+
+class LatentWriteArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D_c", ctypes.c_int), ("D_r", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("c", ctypes.c_void_p), ("c_row_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("k_row_stride", ctypes.c_int64),
+        ("gamma", ctypes.c_void_p), ("eps", ctypes.c_float),
+        ("pos", ctypes.c_void_p), ("base", ctypes.c_double),
+        ("prefix_len", ctypes.c_void_p), ("n_rows", ctypes.c_void_p),
+        ("c_q8", ctypes.c_void_p), ("c_scale", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("kv_row_stride", ctypes.c_int64),
     ]
 
 
@@ -118,6 +132,14 @@ def lib():
         L.kdt_tree_build.argtypes = [vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp,
                                      vp, vp]
         L.kdt_tree_build.restype = ctypes.c_int
+        L.kdt_latent_write_q8.argtypes = [ctypes.POINTER(LatentWriteArgs), vp]
+        L.kdt_latent_write_q8.restype = ctypes.c_int
+        L.kdt_latent_read_q8.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int,
+                                         vp, vp, vp]
+        L.kdt_latent_read_q8.restype = ctypes.c_int
+        L.kdt_kv_compact_q8.argtypes = [vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, vp, vp, vp,
+                                        ctypes.c_int, vp]
+        L.kdt_kv_compact_q8.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -375,3 +397,88 @@ def tree_build(cand_tok, cand_lp, N, root_tok=None, stream=None):
     _check(lib().kdt_tree_build(_ptr(cand_tok), _ptr(cand_lp), B, D, K, int(N), _ptr(root_tok), _ptr(parent),
                                 _ptr(tok), _ptr(depth), _ptr(score), _stream_ptr(stream)), "kdt_tree_build")
     return parent, tok, depth, score
+
+
+def _row_stride3(t, name):
+    """Element stride between the (b,i) rows of a [B,T,d] view with a contiguous last dim and
+    equally spaced rows (e.g. a slice of a combined [B,T,576] buffer)."""
+    if t.stride(2) != 1 or (t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.stride(1) * t.shape[1]):
+        raise ValueError(f"{name} must be a [B,T,d] view with a contiguous last dim and equally spaced (b,i) rows")
+    return t.stride(1) if t.shape[1] > 1 else (t.stride(0) if t.shape[0] > 1 else t.shape[2])
+
+
+def _check_q8_cache(c_q8, c_scale, k_pe):
+    """The three arrays of an 8-bit cache: [B,L,512] and [B,L,16] bytes (uint8 or the float8
+    types of the same width), [B,L,64] bf16, contiguous. Returns (B, L)."""
+    import torch
+    B, L = c_q8.shape[0], c_q8.shape[1]
+    if (c_q8.shape[2] != 512 or tuple(c_scale.shape) != (B, L, 16) or tuple(k_pe.shape) != (B, L, 64)
+            or c_q8.element_size() != 1 or c_scale.element_size() != 1 or k_pe.dtype != torch.bfloat16):
+        raise ValueError("an 8-bit cache is c_q8 [B,L,512] and c_scale [B,L,16] of one byte an element and "
+                         "k_pe [B,L,64] bf16")
+    if not (c_q8.is_contiguous() and c_scale.is_contiguous() and k_pe.is_contiguous()):
+        raise ValueError("the arrays of an 8-bit cache must be contiguous")
+    return B, L
+
+
+def _int32_of(t, n, name):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements")
+    return t
+
+
+def latent_write_q8(c, k, c_q8, c_scale, k_pe, prefix_len, *, gamma=None, eps=1e-6, pos=None, base=10000.0,
+                    n_rows=None, stream=None):
+    """Norm, rotate, quantise and store new rows of an 8-bit cache (kdt_latent_write_q8).
+
+    ``c`` [B,T,512] and ``k`` [B,T,64] (float32 or bf16) may be slices of one combined
+    [B,T,576] buffer; row (b,i) goes to cache row prefix_len[b] + i. ``gamma`` [512] is the
+    RMS norm's weight (None: no norm), ``pos`` int32 [B,T] the rotary positions (None: k as
+    it is), ``n_rows`` int32 [B] the rows of each sequence of a padded batch. The cache
+    (``c_q8`` [B,L,512], ``c_scale`` [B,L,16] bytes, ``k_pe`` [B,L,64] bf16) is updated in place.
+    """
+    B, L = _check_q8_cache(c_q8, c_scale, k_pe)
+    T = c.shape[1]
+    if tuple(c.shape) != (B, T, 512) or tuple(k.shape) != (B, T, 64) or k.dtype != c.dtype:
+        raise ValueError("c must be [B,T,512] and k [B,T,64] of the same type, B as in the cache")
+    if gamma is not None and (gamma.numel() != 512 or gamma.dtype != c.dtype or not gamma.is_contiguous()):
+        raise ValueError("gamma must be a contiguous [512] tensor of c's type")
+    _int32_of(prefix_len, B, "prefix_len"), _int32_of(n_rows, B, "n_rows"), _int32_of(pos, B * T, "pos")
+    a = LatentWriteArgs(B, T, 512, 64, _dtype_code(c), c.data_ptr(), _row_stride3(c, "c"), k.data_ptr(),
+                        _row_stride3(k, "k"), None if gamma is None else gamma.data_ptr(), float(eps),
+                        None if pos is None else pos.data_ptr(), float(base), prefix_len.data_ptr(),
+                        None if n_rows is None else n_rows.data_ptr(), c_q8.data_ptr(), c_scale.data_ptr(),
+                        k_pe.data_ptr(), L)
+    _check(lib().kdt_latent_write_q8(ctypes.byref(a), _stream_ptr(stream)), "kdt_latent_write_q8")
+
+
+def latent_read_q8(c_q8, c_scale, k_pe, start, R, *, n_rows=None, dtype=None, out_c=None, out_k=None, stream=None):
+    """Rows start[b] .. start[b] + R of an 8-bit cache as (c [B,R,512], k [B,R,64]) in bf16 (the
+    default) or float32 (kdt_latent_read_q8); ``start`` int32 [B] or None for 0. With ``n_rows``
+    int32 [B] the rows of c and k behind it are not written."""
+    import torch
+    B, L = _check_q8_cache(c_q8, c_scale, k_pe)
+    R = int(R)
+    dtype = dtype or (out_c.dtype if out_c is not None else torch.bfloat16)
+    _int32_of(start, B, "start"), _int32_of(n_rows, B, "n_rows")
+    if out_c is None:
+        out_c = torch.empty((B, R, 512), dtype=dtype, device=c_q8.device)
+    if out_k is None:
+        out_k = torch.empty((B, R, 64), dtype=dtype, device=c_q8.device)
+    for t, d in ((out_c, 512), (out_k, 64)):
+        if tuple(t.shape) != (B, R, d) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("out_c and out_k must be contiguous [B,R,512] and [B,R,64] tensors of dtype")
+    _check(lib().kdt_latent_read_q8(_ptr(c_q8), _ptr(c_scale), _ptr(k_pe), L, B, R, _ptr(start), _ptr(n_rows),
+                                    _dtype_code(out_c), _ptr(out_c), _ptr(out_k), _stream_ptr(stream)),
+           "kdt_latent_read_q8")
+    return out_c, out_k
+
+
+def kv_compact_q8(c_q8, c_scale, k_pe, prefix_len, acc_nodes, n_acc, update_prefix=True, stream=None):
+    """Move the accepted path's rows of an 8-bit cache to prefix_len + k, in place (kdt_kv_compact_q8)."""
+    B, L = _check_q8_cache(c_q8, c_scale, k_pe)
+    T = acc_nodes.shape[1]
+    _int32_of(prefix_len, B, "prefix_len"), _int32_of(acc_nodes, B * T, "acc_nodes"), _int32_of(n_acc, B, "n_acc")
+    _check(lib().kdt_kv_compact_q8(_ptr(c_q8), _ptr(c_scale), _ptr(k_pe), B, T, L, _ptr(prefix_len), _ptr(acc_nodes),
+                                   _ptr(n_acc), 1 if update_prefix else 0, _stream_ptr(stream)), "kdt_kv_compact_q8")

@@ -1,0 +1,109 @@
+"""CPU checks of the 8-bit cache's entry points: struct layout, and refusals made on the host
+before any launch (no call here touches a GPU: addresses are fakes)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def kdt():
+    from speculative_decoding_tree_absorb_gb300 import build_lib
+    build_lib.build()
+    import speculative_decoding_tree_absorb_gb300 as k
+    return k
+
+
+def _layout(struct, ctype, tmp_path):
+    fields = [f[0] for f in struct._fields_]
+    body = "\n".join(f'printf("{f} %zu\\n", offsetof({ctype}, {f}));' for f in fields)
+    prog = tmp_path / "layout.c"
+    prog.write_text(f'#include <stdio.h>\n#include <stddef.h>\n#include "kdt.h"\n'
+                    f'int main(void) {{ printf("size %zu\\n", sizeof({ctype}));\n{body}\nreturn 0; }}\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), "-I", "/usr/local/cuda/include", str(prog), "-o",
+                    str(exe)], check=True)
+    out = dict(line.split() for line in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                       check=True).stdout.splitlines())
+    assert int(out["size"]) == ctypes.sizeof(struct)
+    for f in fields:
+        assert int(out[f]) == getattr(struct, f).offset, f
+
+
+def test_struct_layouts(kdt, tmp_path):
+    _layout(kdt.LatentWriteArgs, "kdt_latent_write_args", tmp_path)
+
+
+def _write(kdt, **kw):
+    a = kdt.LatentWriteArgs(2, 9, 512, 64, 1, 0x10000, 576, 0x10400, 576, None, 1e-6, 0x20000, 10000.0, 0x30000, None,
+                            0x40000, 0x50000, 0x60000, 100)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return kdt.lib().kdt_latent_write_q8(ctypes.byref(a), None)
+
+
+def test_write_refusals(kdt):
+    K = kdt.kdt
+    assert kdt.lib().kdt_latent_write_q8(None, None) == K.KDT_ERR_NULL_ARG
+    for kw in (dict(D_c=256), dict(D_r=32), dict(dtype=2), dict(dtype=-1)):
+        assert _write(kdt, **kw) == K.KDT_ERR_UNSUPPORTED, kw
+    for kw in (dict(B=-1), dict(T=0), dict(B=1 << 20, T=1 << 12), dict(c_row_stride=511), dict(c_row_stride=516),
+               dict(k_row_stride=63), dict(kv_row_stride=0), dict(c=0x10008), dict(k=0x10401), dict(c_q8=0x40008),
+               dict(c_scale=0x50001), dict(k_pe=0x60002), dict(pos=0x20002), dict(prefix_len=0x30001),
+               dict(n_rows=0x30002), dict(gamma=0x70008), dict(gamma=0x70000, eps=float("nan")),
+               dict(gamma=0x70000, eps=-1.0), dict(base=0.0), dict(base=float("nan"))):
+        assert _write(kdt, **kw) == K.KDT_ERR_BAD_SHAPE, kw
+    for kw in ("c", "k", "prefix_len", "c_q8", "c_scale", "k_pe"):
+        assert _write(kdt, **{kw: None}) == K.KDT_ERR_NULL_ARG, kw
+    assert _write(kdt, B=0) == K.KDT_OK
+
+
+def test_read_and_compact_refusals(kdt):
+    K, lib = kdt.kdt, kdt.lib()
+
+    def read(c8=0x10000, sc=0x20000, kp=0x30000, L=100, B=2, R=9, start=0x40000, n=None, dt=1, c=0x50000, k=0x60000):
+        return lib.kdt_latent_read_q8(c8, sc, kp, L, B, R, start, n, dt, c, k, None)
+
+    for kw in (dict(L=0), dict(B=-1), dict(R=-1), dict(B=1 << 20, R=1 << 12), dict(c8=0x10008), dict(sc=0x20004),
+               dict(kp=0x30002), dict(c=0x50004), dict(k=0x60004), dict(start=0x40002), dict(n=0x40001)):
+        assert read(**kw) == K.KDT_ERR_BAD_SHAPE, kw
+    assert read(dt=3) == K.KDT_ERR_UNSUPPORTED
+    for kw in (dict(c8=None), dict(sc=None), dict(kp=None), dict(c=None, k=None)):
+        assert read(**kw) == K.KDT_ERR_NULL_ARG, kw
+    assert read(B=0) == K.KDT_OK and read(R=0) == K.KDT_OK
+
+    def compact(c8=0x10000, sc=0x20000, kp=0x30000, B=2, T=9, L=100, pre=0x40000, acc=0x50000, n=0x60000):
+        return lib.kdt_kv_compact_q8(c8, sc, kp, B, T, L, pre, acc, n, 1, None)
+
+    for kw in (dict(B=-1), dict(T=0), dict(T=4097, L=9999), dict(L=8), dict(c8=0x10008), dict(sc=0x20008),
+               dict(kp=0x30008)):
+        assert compact(**kw) == K.KDT_ERR_BAD_SHAPE, kw
+    for kw in (dict(c8=None), dict(sc=None), dict(kp=None), dict(pre=None), dict(acc=None), dict(n=None)):
+        assert compact(**kw) == K.KDT_ERR_NULL_ARG, kw
+    assert compact(B=0) == K.KDT_OK
+
+
+def test_binding_refuses_wrong_tensors(kdt):
+    import torch
+    c8, sc = torch.zeros(2, 8, 512, dtype=torch.uint8), torch.zeros(2, 8, 16, dtype=torch.uint8)
+    kp = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    pre = torch.zeros(2, dtype=torch.int32)
+    kv = torch.zeros(2, 3, 576)
+    bad = [dict(c=kv[..., :511]), dict(k=kv[..., 512:].to(torch.bfloat16)), dict(c_q8=c8[:, ::2]), dict(c_scale=sc[..., :8]),
+           dict(k_pe=kp.float()), dict(prefix_len=pre.long()), dict(pos=torch.zeros(2, 3)), dict(gamma=torch.zeros(511)),
+           dict(gamma=torch.zeros(512, dtype=torch.bfloat16)), dict(n_rows=torch.zeros(3, dtype=torch.int32)),
+           dict(c=kv.transpose(0, 1)[..., :512])]
+    for kw in bad:
+        args = dict(c=kv[..., :512], k=kv[..., 512:], c_q8=c8, c_scale=sc, k_pe=kp, prefix_len=pre)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            kdt.latent_write_q8(**args)
+    with pytest.raises(TypeError):
+        kdt.latent_write_q8(kv[..., :512].half(), kv[..., 512:].half(), c8, sc, kp, pre)
+    with pytest.raises(ValueError):
+        kdt.latent_read_q8(c8, sc, kp, pre, 4, out_c=torch.zeros(2, 5, 512))
+    with pytest.raises(ValueError):
+        kdt.kv_compact_q8(c8, sc, kp, pre.long(), torch.zeros(2, 3, dtype=torch.int32), pre)
