@@ -82,7 +82,13 @@ typedef enum { KDT_F32 = 0, KDT_BF16 = 1 } kdt_dtype;
  * tcgen05 tensor-core kernel and fp32 inputs the SIMT kernel on 64-row tiles (which
  * computes in fp32; the tensor path would round inputs). kdt_verify_attn_plan reports the
  * choice. Both SIMT forms are valid for both dtypes. */
-typedef enum { KDT_IMPL_AUTO = 0, KDT_IMPL_SIMT = 1, KDT_IMPL_TCGEN05 = 2, KDT_IMPL_SIMT_SMALL = 3 } kdt_impl;
+typedef enum {
+    KDT_IMPL_AUTO = 0,
+    KDT_IMPL_SIMT = 1,
+    KDT_IMPL_TCGEN05 = 2,
+    KDT_IMPL_SIMT_SMALL = 3,
+    KDT_IMPL_Q8_ROWS = 4    /* kdt_verify_attn_q8 only: tensor cores with the keys on the M side */
+} kdt_impl;
 
 /*
  * kdt_build_visibility -- draft-tree parent array -> packed ancestor bits.
@@ -488,6 +494,56 @@ kdt_status kdt_latent_read_q8(const uint8_t *c_q8, const uint8_t *c_scale, const
 kdt_status kdt_kv_compact_q8(uint8_t *c_q8, uint8_t *c_scale, void *k_pe, int B, int T, int64_t kv_row_stride,
                              int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int update_prefix,
                              cudaStream_t stream);
+
+/* Arguments of kdt_verify_attn_q8. Sizes as for kdt_verify_attn. */
+typedef struct {
+    int B, T, H;
+    int D_c, D_r;           /* must be 512 and 64 */
+    const void *q_nope;     /* bf16 [B,T,H,512] absorbed query */
+    int64_t q_nope_row_stride; /* elements between (b,i,h) rows; 0 = 512, else >= 512 and a multiple of 8 */
+    const void *q_pe;       /* bf16 [B,T,H,64] rotated rope query */
+    int64_t q_pe_row_stride;   /* 0 = 64, else >= 64 and a multiple of 8 */
+    const uint8_t *c_q8;    /* the cache */
+    const uint8_t *c_scale;
+    const void *k_pe;
+    int64_t kv_row_stride;  /* L: rows per sequence, >= max_kv_len */
+    const int32_t *prefix_len; /* device [B]; tree node t at row prefix_len[b] + t */
+    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T */
+    const int32_t *parent;  /* device [B,T] parent array, or NULL */
+    const uint32_t *vis;    /* device [B,T,ceil(T/32)] packed visibility bits, or NULL */
+    float scale;
+    void *out;              /* [B,T,H,512] of out_dtype */
+    kdt_dtype out_dtype;    /* KDT_F32 or KDT_BF16 */
+    float *lse;             /* device fp32 [B,T,H], or NULL */
+    int32_t *err;           /* device int32 error word, or NULL (as for kdt_verify_attn) */
+    int impl;               /* KDT_IMPL_AUTO, or KDT_IMPL_Q8_ROWS */
+    int num_splits;         /* 0 = automatic; else the CTAs the (64-row tile, 128-key block) pairs are cut
+                               into equal shares for (at most one per pair) */
+} kdt_verify_q8_args;
+
+/*
+ * kdt_verify_attn_q8 -- kdt_verify_attn over the 8-bit latent cache: the same scores, mask,
+ * softmax, latent output and log-sum-exp, over the values the cache stands for. T = 1 is
+ * plain decoding. Products run on the tensor cores in bf16 (exact for the cache's values)
+ * with float32 sums; scores, softmax statistics and the output's sums are float32, the
+ * weights are rounded to bf16 for the second product, and the output once to out_dtype.
+ * Exactly one of `parent` and `vis` is given; a row that sees no key gets out = 0 and
+ * lse = -inf. A row that sees a NaN group or a non-finite k_pe gets NaN; a row from which
+ * such a key is hidden is not affected by it, and rows of the cache at or beyond
+ * prefix_len[b] + T are never read.
+ * `workspace` must hold kdt_verify_attn_q8_workspace_size(a) bytes (256-byte aligned);
+ * its contents need no initialisation. Calls that may run at the same time, captured ones
+ * included, need workspaces of their own.
+ * Errors: those of kdt_verify_attn, for the same reasons.
+ */
+kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of workspace kdt_verify_attn_q8 needs for these arguments (host-side fields only);
+ * 0 for arguments it would reject. */
+size_t kdt_verify_attn_q8_workspace_size(const kdt_verify_q8_args *a);
+
+/* What kdt_verify_attn_q8 will launch for these arguments. */
+kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
 
 #ifdef __cplusplus
 }

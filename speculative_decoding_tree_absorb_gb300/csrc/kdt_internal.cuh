@@ -113,6 +113,32 @@ cudaError_t launch_merge_two(const float *o_a, const float *lse_a, const float *
 cudaError_t launch_vc_proj(const float *o, const void *w_vc, int R, int H, int Dv, float *v, int32_t *err,
                            cudaStream_t s);
 
+// K5: tree-verify attention over the 8-bit latent cache (kdt_verify_attn_q8), everything
+// validated on the host.
+struct Q8Params {
+    int B, T, H, W;            // W = ceil(T/32) visibility words per query
+    int rows_seq;              // T * H
+    int tiles_seq;             // row tiles a sequence
+    int64_t L;                 // cache rows per sequence
+    const __nv_bfloat16 *q_nope, *q_pe;
+    int64_t q_nope_stride, q_pe_stride;
+    const uint8_t *c_q8, *c_scale;
+    const __nv_bfloat16 *k_pe;
+    const int32_t *prefix_len;
+    const uint32_t *vis;       // [B,T,W]
+    float scale_log2;          // scale * log2(e)
+    void *out;                 // bf16 or float32
+    bool out_bf16;
+    float *lse;
+    float *part_o, *part_lse;  // [2 * ctas][kQ8Rows] piece states (unused with one CTA)
+    int32_t *err;
+    int ctas;
+    bool overlap_vis;          // launched right behind this call's visibility kernel
+};
+constexpr int kQ8Rows = 64;    // query rows of a tile
+constexpr int kQ8Keys = 128;   // keys of a block
+cudaError_t launch_verify_q8_rows(const Q8Params &p, cudaStream_t s);
+
 // Per-device SM count (cached).
 int sm_count();
 

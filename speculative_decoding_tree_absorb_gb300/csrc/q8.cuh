@@ -53,5 +53,41 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
     }
 }
 
+// 16 codes of one group to 16 bf16 values times 2^(byte - 127), exactly, as two 16-byte
+// vectors in order; a NaN group gives zeros. The code's exponent and mantissa bits, moved to
+// where a bf16 number's sit, are the value times 2^-120 (subnormal codes included: they
+// become subnormal bf16 numbers), so one product by 2^(byte - 7) restores it. Scales above
+// 2^7 need a second product, as 2^(byte - 7) is then no bf16 number.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ void widen16(const uint4 &codes, uint32_t byte, uint4 &lo, uint4 &hi) {
+    const uint32_t top = byte > 134u ? 134u : byte;
+    uint32_t f = byte == (uint32_t)kNaN ? 0u : (top + 120u) << 7;
+    f |= f << 16;
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // bytes 2h and 2h + 1 to the upper bytes of the two halves: s eeee mmm 0...
+            const uint32_t x = __byte_perm(c[k], 0u, h == 0 ? 0x1404 : 0x3424);
+            o[2 * k + h] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
+        }
+    }
+    if (byte > 134u && byte != (uint32_t)kNaN) {
+        uint32_t f2 = (byte - 134u + 127u) << 7;
+        f2 |= f2 << 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 }  // namespace q8
 }  // namespace kdt

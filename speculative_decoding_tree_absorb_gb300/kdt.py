@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(PKG, "libkdt.so")
 (KDT_OK, KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE, KDT_ERR_UNSUPPORTED, KDT_ERR_WORKSPACE, KDT_ERR_CUDA,
  KDT_ERR_NOT_DEVICE) = range(7)
 KDT_F32, KDT_BF16 = 0, 1
-IMPLS = {"auto": 0, "simt": 1, "tcgen05": 2, "simt_small": 3}
+IMPLS = {"auto": 0, "simt": 1, "tcgen05": 2, "simt_small": 3, "q8_rows": 4}
 IMPL_NAMES = {v: k for k, v in IMPLS.items()}
 DEFAULT_SCALE = 1.0 / math.sqrt(192.0)
 
@@ -27,7 +27,8 @@ EXPORTS = ("kdt_status_str", "kdt_version", "kdt_build_visibility", "kdt_verify_
            "kdt_verify_attn_workspace_size", "kdt_verify_attn_plan", "kdt_merge_attn_states",
            "kdt_verify_attn_noalloc", "kdt_rope_neox", "kdt_tree_accept", "kdt_kv_compact", "kdt_tree_build",
            "kdt_verify_attn_host", "kdt_verify_attn_host_buffer_size", "kdt_vc_up_proj",
-           "kdt_test_verify_attn_wait_expiry", "kdt_latent_write_q8", "kdt_latent_read_q8", "kdt_kv_compact_q8")
+           "kdt_test_verify_attn_wait_expiry", "kdt_latent_write_q8", "kdt_latent_read_q8", "kdt_kv_compact_q8",
+           "kdt_verify_attn_q8", "kdt_verify_attn_q8_workspace_size", "kdt_verify_attn_q8_plan")
 
 
 class KdtError(RuntimeError):
@@ -75,6 +76,21 @@ class LatentWriteArgs(ctypes.Structure):
         ("prefix_len", ctypes.c_void_p), ("n_rows", ctypes.c_void_p),
         ("c_q8", ctypes.c_void_p), ("c_scale", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
         ("kv_row_stride", ctypes.c_int64),
+    ]
+
+
+class VerifyQ8Args(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("D_c", ctypes.c_int), ("D_r", ctypes.c_int),
+        ("q_nope", ctypes.c_void_p), ("q_nope_row_stride", ctypes.c_int64),
+        ("q_pe", ctypes.c_void_p), ("q_pe_row_stride", ctypes.c_int64),
+        ("c_q8", ctypes.c_void_p), ("c_scale", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("kv_row_stride", ctypes.c_int64),
+        ("prefix_len", ctypes.c_void_p), ("max_kv_len", ctypes.c_int),
+        ("parent", ctypes.c_void_p), ("vis", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("err", ctypes.c_void_p),
+        ("impl", ctypes.c_int), ("num_splits", ctypes.c_int),
     ]
 
 
@@ -140,6 +156,12 @@ def lib():
         L.kdt_kv_compact_q8.argtypes = [vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, vp, vp, vp,
                                         ctypes.c_int, vp]
         L.kdt_kv_compact_q8.restype = ctypes.c_int
+        L.kdt_verify_attn_q8.argtypes = [ctypes.POINTER(VerifyQ8Args), vp, ctypes.c_size_t, vp]
+        L.kdt_verify_attn_q8.restype = ctypes.c_int
+        L.kdt_verify_attn_q8_workspace_size.argtypes = [ctypes.POINTER(VerifyQ8Args)]
+        L.kdt_verify_attn_q8_workspace_size.restype = ctypes.c_size_t
+        L.kdt_verify_attn_q8_plan.argtypes = [ctypes.POINTER(VerifyQ8Args), ctypes.POINTER(Plan)]
+        L.kdt_verify_attn_q8_plan.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -482,3 +504,71 @@ def kv_compact_q8(c_q8, c_scale, k_pe, prefix_len, acc_nodes, n_acc, update_pref
     _int32_of(prefix_len, B, "prefix_len"), _int32_of(acc_nodes, B * T, "acc_nodes"), _int32_of(n_acc, B, "n_acc")
     _check(lib().kdt_kv_compact_q8(_ptr(c_q8), _ptr(c_scale), _ptr(k_pe), B, T, L, _ptr(prefix_len), _ptr(acc_nodes),
                                    _ptr(n_acc), 1 if update_prefix else 0, _stream_ptr(stream)), "kdt_kv_compact_q8")
+
+
+def _q8_size_args(B, T, H, max_kv_len, out_dtype, bits, impl, num_splits) -> VerifyQ8Args:
+    """Arguments with the sizes filled in and placeholder pointers: enough for a plan."""
+    import torch
+    fake = 1 << 12
+    a = VerifyQ8Args(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, fake, int(max_kv_len), fake, int(max_kv_len),
+                     None if bits else fake, fake if bits else None, 1.0, fake,
+                     KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, IMPLS[impl], int(num_splits))
+    return a
+
+
+def verify_attn_q8_plan(B, T, H, max_kv_len, *, out_dtype=None, bits=False, impl="auto", num_splits=0) -> dict:
+    """What verify_attn_q8 launches for these sizes (``bits``: visibility given as bits, not parents)."""
+    p = Plan()
+    a = _q8_size_args(B, T, H, max_kv_len, out_dtype, bits, impl, num_splits)
+    _check(lib().kdt_verify_attn_q8_plan(ctypes.byref(a), ctypes.byref(p)), "kdt_verify_attn_q8_plan")
+    return dict(impl=IMPL_NAMES.get(p.impl, p.impl), num_splits=p.num_splits, num_launches=p.num_launches,
+                ctas=p.ctas, workspace_bytes=int(p.workspace_bytes))
+
+
+def verify_attn_q8_workspace_size(B, T, H, max_kv_len, *, out_dtype=None, bits=False, impl="auto", num_splits=0) -> int:
+    """Bytes of workspace verify_attn_q8 needs for these sizes."""
+    return verify_attn_q8_plan(B, T, H, max_kv_len, out_dtype=out_dtype, bits=bits, impl=impl,
+                               num_splits=num_splits)["workspace_bytes"]
+
+
+def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None, vis=None, max_kv_len=None,
+                   scale=DEFAULT_SCALE, out=None, out_dtype=None, lse=None, err=None, impl="auto", num_splits=0,
+                   workspace=None, stream=None, want_lse=True):
+    """Tree-verify attention over an 8-bit latent cache (kdt_verify_attn_q8).
+
+    ``q_nope`` [B,T,H,512] and ``q_pe`` [B,T,H,64] are bf16 (slices of a combined [B,T,H,576]
+    buffer are taken where they lie); the cache is c_q8 [B,L,512], c_scale [B,L,16], k_pe
+    [B,L,64]. Returns (out [B,T,H,512], lse [B,T,H] fp32 or None); ``out_dtype`` is float32 (the
+    default) or bfloat16. ``max_kv_len`` defaults to L.
+    """
+    import torch
+    B, L = _check_q8_cache(c_q8, c_scale, k_pe)
+    T, H = q_nope.shape[1], q_nope.shape[2]
+    if tuple(q_nope.shape) != (B, T, H, 512) or tuple(q_pe.shape) != (B, T, H, 64):
+        raise ValueError("q_nope must be [B,T,H,512] and q_pe [B,T,H,64], B as in the cache")
+    if q_nope.dtype != torch.bfloat16 or q_pe.dtype != torch.bfloat16:
+        raise TypeError("queries must be bfloat16")
+    _int32_of(prefix_len, B, "prefix_len"), _int32_of(parent, B * T, "parent")
+    if vis is not None and (vis.numel() != B * T * ((T + 31) // 32) or vis.element_size() != 4 or not vis.is_contiguous()):
+        raise ValueError("vis must be a contiguous 32-bit [B,T,ceil(T/32)] tensor")
+    if out is None:
+        out = torch.empty((B, T, H, 512), dtype=out_dtype or torch.float32, device=q_nope.device)
+    elif tuple(out.shape) != (B, T, H, 512) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError("out must be a contiguous [B,T,H,512] tensor of out_dtype")
+    if lse is None and want_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=q_nope.device)
+    elif lse is not None and (lse.numel() != B * T * H or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [B,T,H] tensor")
+    a = VerifyQ8Args(B, T, H, 512, 64, q_nope.data_ptr(), _row_stride(q_nope), q_pe.data_ptr(), _row_stride(q_pe),
+                     c_q8.data_ptr(), c_scale.data_ptr(), k_pe.data_ptr(), L, prefix_len.data_ptr(),
+                     L if max_kv_len is None else int(max_kv_len), None if parent is None else parent.data_ptr(),
+                     None if vis is None else vis.data_ptr(), float(scale), out.data_ptr(), _dtype_code(out),
+                     None if lse is None else lse.data_ptr(), None if err is None else err.data_ptr(),
+                     IMPLS[impl] if isinstance(impl, str) else int(impl), int(num_splits))
+    if workspace is None:
+        need = int(lib().kdt_verify_attn_q8_workspace_size(ctypes.byref(a)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device) if need else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kdt_verify_attn_q8(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream_ptr(stream)),
+           "kdt_verify_attn_q8")
+    return out, lse

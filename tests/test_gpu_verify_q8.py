@@ -1,0 +1,237 @@
+"""GPU parity of kdt_verify_attn_q8 against the float64 oracle (oracle/q8.py) on the cache's own
+values, at the sizes and masks where it can go wrong.
+
+Tolerances. Scores: n = 576 products summed in float32, off by at most ds = n 2^-24 scale
+sum|q||c| (with the largest such sum of the case) -- times ln 2 log2 e = 1 through the
+exponent. Weights: 2^(+-ds) from the scores, 2^-21 from the exponential and the two float32
+products around it, 2^-8 from the rounding to bf16, so an output is off by at most
+(2^-8 + 2 ds + 2^-20) sum_j p_j |c_j|, then rounded to its type (2^-8 or 2^-24 of its value);
+splits add one rounding of 2^-22. lse: ds, the sum's roundings (at most N / 128 + 12 adds
+in a row) and 2^-20 for the logarithm's and the reference's products, relative to 1 + |lse|.
+"""
+import numpy as np
+import pytest
+
+from oracle import q8 as oq
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / np.sqrt(192.0)
+
+
+@pytest.fixture(scope="module")
+def kdt():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_tree_absorb_gb300 import build_lib
+    build_lib.build()
+    import speculative_decoding_tree_absorb_gb300 as k
+    return k
+
+
+def _inputs(seed, T, H, prefix, pad=5, amp=1.0):
+    """Queries, a cache written by quantising random rows, and random trees; rows behind the
+    last tree row hold NaN scales and NaN rope keys."""
+    import torch
+    import speculative_decoding_tree_absorb_gb300 as kdt
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B, L = len(prefix), max(prefix) + T + pad
+    c8 = torch.full((B, L, 512), 0x33, dtype=torch.uint8, device="cuda")
+    sc = torch.full((B, L, 16), 255, dtype=torch.uint8, device="cuda")
+    kp = torch.full((B, L, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    n = torch.tensor([p + T for p in prefix], dtype=torch.int32, device="cuda")
+    kv = torch.randn(B, max(prefix) + T, 576, device="cuda", generator=g)
+    kdt.latent_write_q8(kv[..., :512], kv[..., 512:], c8, sc, kp, torch.zeros(B, dtype=torch.int32, device="cuda"), n_rows=n)
+    q = (torch.randn(B, T, H, 576, device="cuda", generator=g) * amp).to(torch.bfloat16)
+    rng = np.random.RandomState(seed)
+    parent = np.full((B, T), -1, dtype=np.int32)
+    for b in range(B):
+        for i in range(1, T):
+            parent[b, i] = rng.randint(max(0, i - 8), i)
+    return dict(q=q, c8=c8, sc=sc, kp=kp, parent=parent, prefix=list(prefix), T=T, H=H, B=B, L=L)
+
+
+def _call(kdt, d, see=None, **kw):
+    import torch
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    err = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    if see is None:
+        kw["parent"] = torch.from_numpy(d["parent"]).cuda()
+    else:
+        W = (d["T"] + 31) // 32
+        bits = np.zeros(see.shape[:2] + (W,), dtype=np.uint32)
+        for t in range(d["T"]):
+            bits[..., t // 32] |= see[..., t].astype(np.uint32) << np.uint32(t % 32)
+        kw["vis"] = torch.from_numpy(bits.view(np.int32)).cuda()
+    out, lse = kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre, scale=SCALE,
+                                  err=err, max_kv_len=max(d["prefix"]) + d["T"], **kw)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def _check(d, got, out_eps, see=None):
+    out, lse = got
+    for b, P in enumerate(d["prefix"]):
+        N = P + d["T"]
+        c = oq.dequantise(d["c8"][b, :N].cpu().numpy(), d["sc"][b, :N].cpu().numpy())
+        k = d["kp"][b, :N].double().cpu().numpy()
+        q = d["q"][b].double().cpu().numpy()
+        sb = oq.ancestors(d["parent"][b]) if see is None else see[b]
+        ref_o, ref_l = oq.attention(q, c, k, P, sb, SCALE)
+        # sum_j p_j |c_j|, with the same weights
+        for i in range(d["T"]):
+            keys = np.concatenate([np.arange(P), P + np.flatnonzero(sb[i])])
+            if not len(keys):
+                assert (out[b, i] == 0).all() and (lse[b, i] == -np.inf).all()
+                continue
+            kc = np.concatenate([c[keys], k[keys]], -1)
+            s = SCALE * (q[i] @ kc.T)
+            p = np.exp(s - ref_l[i][:, None])
+            mag = p @ np.abs(c[keys])
+            ds = 576 * 2.0 ** -24 * SCALE * (np.abs(q[i]) @ np.abs(kc).T).max()
+            tol = (2.0 ** -8 + 2 * ds + 2.0 ** -20) * mag + (out_eps + 2.0 ** -22) * np.abs(ref_o[i])
+            assert (np.abs(out[b, i] - ref_o[i]) <= tol).all(), (b, i, np.abs(out[b, i] - ref_o[i]).max())
+            tol = ds + (2.0 ** -20 + (len(keys) / 128 + 12) * 2.0 ** -24) * (1 + np.abs(ref_l[i]))
+            assert (np.abs(lse[b, i] - ref_l[i]) <= tol).all(), (b, i, np.abs(lse[b, i] - ref_l[i]).max())
+
+
+CASES = [(1, 1, [0]), (1, 64, [0, 1, 126, 127, 128, 129, 1000]), (9, 8, [37, 37]), (5, 20, [300, 11, 2000]),
+         (33, 3, [65, 600]), (64, 64, [200]), (70, 1, [130, 0]), (1, 128, [9000]), (2, 1024, [70])]
+
+
+@pytest.mark.parametrize("impl,splits", [("auto", 0), ("q8_rows", 0), ("q8_rows", 1), ("q8_rows", 5)])
+@pytest.mark.parametrize("T,H,prefix", CASES)
+def test_parity(kdt, T, H, prefix, impl, splits):
+    import torch
+    d = _inputs(T * 100 + H, T, H, prefix)
+    bf16 = (T + H + splits) % 2 == 0
+    got = _call(kdt, d, impl=impl, num_splits=splits, out_dtype=torch.bfloat16 if bf16 else torch.float32)
+    _check(d, got, 2.0 ** -8 if bf16 else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+def test_caller_bits_and_rows_that_see_nothing(kdt, impl):
+    d = _inputs(11, 40, 6, [0, 0, 130])
+    rng = np.random.RandomState(3)
+    see = rng.rand(3, 40, 40) < 0.3
+    see[0, 5] = see[1] = see[0, 39] = False
+    _check(d, _call(kdt, d, see=see, impl=impl), 2.0 ** -24, see=see)
+    _check(d, _call(kdt, d, see=see, impl=impl, num_splits=3), 2.0 ** -24, see=see)
+
+
+@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+@pytest.mark.parametrize("T,H", [(12, 4), (64, 64)])
+def test_nan_reaches_exactly_the_rows_that_see_it(kdt, impl, T, H):
+    """NaN in a tree node's codes (its group flagged) and an infinity in another's rope key:
+    rows that see neither are bit for bit as without them; rows that see them are NaN."""
+    import torch
+    d = _inputs(21, T, H, [300, 64])
+    clean = _call(kdt, d, impl=impl)
+    d["sc"][0, 300 + 5, 2] = 255
+    d["kp"][1, 64 + 3, 7] = float("inf")
+    out, lse = _call(kdt, d, impl=impl)
+    for b, t in ((0, 5), (1, 3)):
+        sees = oq.ancestors(d["parent"][b])[:, t]
+        assert sees.any() and not sees.all()
+        assert np.array_equal(out[b, ~sees], clean[0][b, ~sees]) and np.array_equal(lse[b, ~sees], clean[1][b, ~sees])
+        if b == 0:
+            assert np.isnan(out[b, sees]).all() and np.isnan(lse[b, sees]).all()
+        else:                                       # scores of +-inf (or NaN): no finite answer but -inf scores
+            s = d["q"][b, :, :, 512 + 7].double().cpu().numpy()[sees]
+            up = s > 0
+            assert np.isnan(out[b, sees][up]).all()
+    d["sc"][0, 7, 0] = 255                            # in the prefix: every row sees it
+    out, lse = _call(kdt, d, impl=impl)
+    assert np.isnan(out[0]).all() and np.isnan(lse[0]).all()
+
+
+@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+def test_outlier_keys_raise_the_reference(kdt, impl):
+    """Keys far larger than the rest, late in the sequence, in several blocks: the running
+    reference rises block after block and old sums are rescaled."""
+    d = _inputs(31, 3, 64, [1500, 700], amp=3.0)
+    for b, P in enumerate(d["prefix"]):
+        for k, row in enumerate(range(100, P, 190)):
+            d["sc"][b, row] += k % 4
+    _check(d, _call(kdt, d, impl=impl, num_splits=1), 2.0 ** -24)
+    _check(d, _call(kdt, d, impl=impl), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+def test_scales_over_the_whole_range(kdt, impl):
+    """Scale bytes from the smallest to above 2^7 (where widening takes a second product)."""
+    import torch
+    d = _inputs(41, 2, 16, [260], amp=2.0 ** -12)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    d["sc"][:, :262] = torch.randint(27, 139, (1, 262, 16), device="cuda", generator=g).to(torch.uint8)
+    _check(d, _call(kdt, d, impl=impl), 2.0 ** -24)
+
+
+def test_same_as_the_bf16_cache(kdt):
+    """On the rows read back to a bf16 cache kdt_verify_attn gives the same within both bounds."""
+    import torch
+    d = _inputs(51, 16, 64, [500, 900])
+    out, lse = _call(kdt, d)
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    c, k = kdt.latent_read_q8(d["c8"], d["sc"], d["kp"], None, d["L"])
+    q = d["q"]
+    o2, l2 = kdt.verify_attn(q[..., :512], q[..., 512:], c, k, pre, parent=torch.from_numpy(d["parent"]).cuda(),
+                             max_kv_len=916, scale=SCALE)
+    assert np.abs(out - o2.double().cpu().numpy()).max() <= 2 * 2e-2
+    assert np.abs(lse - l2.double().cpu().numpy()).max() <= 1e-3
+
+
+@pytest.mark.parametrize("T,H,prefix", [(1, 64, [3000, 5]), (64, 64, [700, 1300])])
+def test_captured_graph_two_streams_and_fresh_inputs(kdt, T, H, prefix):
+    """Two calls captured on two streams with workspaces of their own, replayed on rewritten
+    inputs; results as from plain calls, bit for bit."""
+    import torch
+    d = [_inputs(61 + k, T, H, prefix) for k in (0, 1)]
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    par = [torch.from_numpy(x["parent"]).cuda() for x in d]
+    N = max(prefix) + T
+    ws = [torch.empty(kdt.verify_attn_q8_workspace_size(2, T, H, N), dtype=torch.uint8, device="cuda") for _ in d]
+    outs = [torch.empty(2, T, H, 512, device="cuda") for _ in d]
+    lses = [torch.empty(2, T, H, device="cuda") for _ in d]
+
+    def call(k, out, lse, w):
+        x = d[k]
+        kdt.verify_attn_q8(x["q"][..., :512], x["q"][..., 512:], x["c8"], x["sc"], x["kp"], pre, parent=par[k],
+                           max_kv_len=N, scale=SCALE, out=out, lse=lse, workspace=w)
+
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=a):
+        b.wait_stream(a)
+        call(0, outs[0], lses[0], ws[0])
+        with torch.cuda.stream(b):
+            call(1, outs[1], lses[1], ws[1])
+        a.wait_stream(b)
+    for seed in (1, 2, 3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for x in d:
+            x["q"].copy_(torch.randn(x["q"].shape, device="cuda", generator=g).to(torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            o, l = torch.empty_like(outs[k]), torch.empty_like(lses[k])
+            call(k, o, l, torch.empty_like(ws[k]))
+            torch.cuda.synchronize()
+            assert torch.equal(o, outs[k]) and torch.equal(l, lses[k])
+
+
+def test_not_device_memory_is_refused(kdt):
+    import torch
+    d = _inputs(71, 1, 8, [10])
+    pre = torch.tensor([10], dtype=torch.int32)
+    with pytest.raises(kdt.KdtError) as e:
+        kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre.pin_memory(),
+                           parent=torch.from_numpy(d["parent"]).cuda())
+    assert e.value.status == 6
+    with pytest.raises(kdt.KdtError) as e:
+        kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre.cuda(),
+                           parent=torch.from_numpy(d["parent"]).cuda(),
+                           workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[128:])
+    assert e.value.status == 4

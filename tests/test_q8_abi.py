@@ -35,6 +35,7 @@ def _layout(struct, ctype, tmp_path):
 
 def test_struct_layouts(kdt, tmp_path):
     _layout(kdt.LatentWriteArgs, "kdt_latent_write_args", tmp_path)
+    _layout(kdt.VerifyQ8Args, "kdt_verify_q8_args", tmp_path)
 
 
 def _write(kdt, **kw):
@@ -86,6 +87,48 @@ def test_read_and_compact_refusals(kdt):
     assert compact(B=0) == K.KDT_OK
 
 
+def _verify(kdt, **kw):
+    a = kdt.VerifyQ8Args(2, 9, 8, 512, 64, 0x10000, 576, 0x10400, 576, 0x20000, 0x30000, 0x40000, 100, 0x50000, 46, 0x60000,
+                         None, 0.07, 0x70000, 1, 0x80000, None, 0, 0)
+    ws = kw.pop("ws", (None, 0))
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return kdt.lib().kdt_verify_attn_q8(ctypes.byref(a), ws[0], ws[1], None)
+
+
+def test_verify_q8_refusals(kdt):
+    K = kdt.kdt
+    assert kdt.lib().kdt_verify_attn_q8(None, None, 0, None) == K.KDT_ERR_NULL_ARG
+    for kw in (dict(D_c=256), dict(D_r=32), dict(out_dtype=2), dict(impl=1), dict(impl=3), dict(impl=9), dict(impl=-1)):
+        assert _verify(kdt, **kw) == K.KDT_ERR_UNSUPPORTED, kw
+    for kw in (dict(B=-1), dict(B=65536), dict(T=0), dict(T=4097), dict(H=0), dict(H=1025), dict(max_kv_len=8),
+               dict(max_kv_len=101), dict(num_splits=-1), dict(q_nope=0x10008), dict(q_pe=0x10402), dict(c_q8=0x20008),
+               dict(c_scale=0x30004), dict(k_pe=0x40002), dict(out=0x70008), dict(lse=0x80002), dict(prefix_len=0x50002),
+               dict(parent=0x60001), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_nope_row_stride=504),
+               dict(q_nope_row_stride=516), dict(q_pe_row_stride=56), dict(q_pe_row_stride=68)):
+        assert _verify(kdt, **kw) == K.KDT_ERR_BAD_SHAPE, kw
+    for kw in ("q_nope", "q_pe", "c_q8", "c_scale", "k_pe", "prefix_len", "out", "parent"):
+        assert _verify(kdt, **{kw: None}) == K.KDT_ERR_NULL_ARG, kw
+    assert _verify(kdt, vis=0x90000) == K.KDT_ERR_NULL_ARG                      # both mask inputs
+    assert _verify(kdt) == K.KDT_ERR_WORKSPACE
+    need = kdt.verify_attn_q8_workspace_size(2, 9, 8, 46)
+    assert need > 0
+    assert _verify(kdt, ws=(0x100000, need - 1)) == K.KDT_ERR_WORKSPACE
+    assert _verify(kdt, ws=(0x100010, need)) == K.KDT_ERR_WORKSPACE
+    assert _verify(kdt, B=0) == K.KDT_OK
+
+
+def test_verify_q8_plan(kdt):
+    p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows")
+    # 72 rows a sequence are two 64-row tiles of one 128-key block each
+    assert p["impl"] == "q8_rows" and p["ctas"] == 4 and p["num_launches"] == 3
+    assert p["workspace_bytes"] >= 2 * 9 * 4 + 2 * 4 * 64 * 513 * 4
+    p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows", num_splits=1, bits=True)
+    assert p["ctas"] == 1 and p["num_launches"] == 1 and p["workspace_bytes"] == 0
+    with pytest.raises(kdt.KdtError):
+        kdt.verify_attn_q8_plan(2, 0, 8, 46)
+
+
 def test_binding_refuses_wrong_tensors(kdt):
     import torch
     c8, sc = torch.zeros(2, 8, 512, dtype=torch.uint8), torch.zeros(2, 8, 16, dtype=torch.uint8)
@@ -107,3 +150,21 @@ def test_binding_refuses_wrong_tensors(kdt):
         kdt.latent_read_q8(c8, sc, kp, pre, 4, out_c=torch.zeros(2, 5, 512))
     with pytest.raises(ValueError):
         kdt.kv_compact_q8(c8, sc, kp, pre.long(), torch.zeros(2, 3, dtype=torch.int32), pre)
+
+
+def test_verify_q8_binding_refuses_wrong_tensors(kdt):
+    import torch
+    c8, sc = torch.zeros(2, 8, 512, dtype=torch.uint8), torch.zeros(2, 8, 16, dtype=torch.uint8)
+    kp = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    pre, par = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    q = torch.zeros(2, 3, 4, 576, dtype=torch.bfloat16)
+    for kw in (dict(q_nope=q[..., :511]), dict(q_pe=q[:1, ..., 512:]), dict(parent=par.long()), dict(prefix_len=pre[:1]),
+               dict(out=torch.zeros(2, 3, 4, 512), out_dtype=torch.bfloat16), dict(out=torch.zeros(2, 3, 4, 511)),
+               dict(lse=torch.zeros(2, 3, 4, dtype=torch.float64)), dict(vis=torch.zeros(2, 3, 2, dtype=torch.int32)),
+               dict(k_pe=kp[:, :, :32]), dict(q_nope=q.transpose(1, 2)[..., :512].transpose(1, 2)[:, ::2])):
+        args = dict(q_nope=q[..., :512], q_pe=q[..., 512:], c_q8=c8, c_scale=sc, k_pe=kp, prefix_len=pre, parent=par)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            kdt.verify_attn_q8(**args)
+    with pytest.raises(TypeError):
+        kdt.verify_attn_q8(q[..., :512].float(), q[..., 512:].float(), c8, sc, kp, pre, parent=par)
