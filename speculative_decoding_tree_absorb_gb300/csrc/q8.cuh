@@ -53,40 +53,54 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
     }
 }
 
-// 16 codes of one group to 16 bf16 values times 2^(byte - 127), exactly, as two 16-byte
-// vectors in order; a NaN group gives zeros. The code's exponent and mantissa bits, moved to
-// where a bf16 number's sit, are the value times 2^-120 (subnormal codes included: they
-// become subnormal bf16 numbers), so one product by 2^(byte - 7) restores it. Scales above
-// 2^7 need a second product, as 2^(byte - 7) is then no bf16 number.
+// Widening to bf16 for the matrix instructions, exactly. A code's exponent and mantissa bits,
+// moved to where a bf16 number's sit, are the value times 2^-120 (subnormal codes included: they
+// become subnormal bf16 numbers), so one product by 2^(byte - 127 + 120) restores it. For bytes
+// above kHighByte that is no bf16 number: factor() then stops there and factor_high() is the
+// rest, for a second product. A NaN group's factor is 0 (its key is flagged instead).
+constexpr uint32_t kHighByte = 134;
+
+__device__ __forceinline__ uint32_t factor(uint32_t byte) {              // bf16 bits
+    return byte == (uint32_t)kNaN ? 0u : (min(byte, kHighByte) + 120u) << 7;
+}
+
+__device__ __forceinline__ uint32_t factor_high(uint32_t byte) {
+    return (max(byte, kHighByte) - kHighByte + 127u) << 7;
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-__device__ __forceinline__ void widen16(const uint4 &codes, uint32_t byte, uint4 &lo, uint4 &hi) {
-    const uint32_t top = byte > 134u ? 134u : byte;
-    uint32_t f = byte == (uint32_t)kNaN ? 0u : (top + 120u) << 7;
-    f |= f << 16;
-    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // bytes 2h and 2h + 1 to the upper bytes of the two halves: s eeee mmm 0...
-            const uint32_t x = __byte_perm(c[k], 0u, h == 0 ? 0x1404 : 0x3424);
-            o[2 * k + h] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
-        }
-    }
-    if (byte > 134u && byte != (uint32_t)kNaN) {
-        uint32_t f2 = (byte - 134u + 127u) << 7;
-        f2 |= f2 << 16;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
-    }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
+// Codes (0, 2) and (1, 3) of a word as pairs of bf16 bit patterns times 2^-120. A pair has the
+// codes in the low bytes of its halves: 16 x moves exponent and mantissa to bits 4..10 and the
+// sign to bit 11, and 0xf0 times the sign bit moves it on to bit 15 (2048 + 0xf0 * 128 = 2^15).
+// That is two logic operations and two multiply-adds, on different pipes, against a byte
+// permute, a shift and two logic operations for a pair in order.
+__device__ __forceinline__ void spread(uint32_t w, uint32_t &even, uint32_t &odd) {
+    const uint32_t e = w & 0x00ff00ffu, o = __byte_perm(w, 0u, 0x4341);
+    even = e * 16u + (e & 0x00800080u) * 0xf0u;
+    odd = o * 16u + (o & 0x00800080u) * 0xf0u;
+}
+
+// Eight codes to eight bf16 values, each four in the order (0, 2, 1, 3); f holds the factor twice.
+__device__ __forceinline__ uint4 widen8(const uint2 &codes, uint32_t f) {
+    uint4 o;
+    spread(codes.x, o.x, o.y);
+    spread(codes.y, o.z, o.w);
+    o.x = mul_bf16x2(o.x, f);
+    o.y = mul_bf16x2(o.y, f);
+    o.z = mul_bf16x2(o.z, f);
+    o.w = mul_bf16x2(o.w, f);
+    return o;
+}
+
+// Eight bf16 values in order to the order widen8 gives.
+__device__ __forceinline__ uint4 reorder8(const uint4 &v) {
+    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                      __byte_perm(v.z, v.w, 0x7632));
 }
 
 }  // namespace q8

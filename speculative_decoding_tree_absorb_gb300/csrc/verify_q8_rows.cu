@@ -23,7 +23,7 @@
 //    reference by more than 2^20; the exact maxima (shuffles) and the rescale of O^T are
 //    taken when one does, which the first block of an item always makes it do. p <= 2^20
 //    keeps l and O (float32) far from overflow, and the result does not depend on the
-//    reference. l is summed per key and reduced once an item.
+//    reference.
 //  * The (row tile, key block) pairs of the batch are cut into equal contiguous shares, one
 //    CTA an SM; tiles cut by a share boundary leave normalised pieces that a second kernel
 //    joins by log-sum-exp.
@@ -45,12 +45,12 @@ using namespace tc;
 
 constexpr int kRowsT = kQ8Rows;                     // query rows of a tile (N)
 constexpr int kKeysB = kQ8Keys;                     // keys of a block (M)
-// Warps: 0 issues the MMAs (1-3 idle), 4-11 softmax, 12-19 converters. The launch gives each
-// of the five warpgroups 96 registers a thread; they trade: 40 + 2 * 136 + 2 * 80 <= 5 * 96.
-constexpr int kSoftWarps = 8, kConvWarps = 8, kSoft0 = 4, kConv0 = 12;
+// Warps: 0 issues the MMAs, 1-3 copy the rope keys, 4-11 softmax, 12-27 converters (four for each
+// pair of tiles). The launch gives each of the seven warpgroups 72 registers a thread; they trade.
+constexpr int kSoftWarps = 8, kConvWarps = 16, kRopeWarps = 3, kSoft0 = 4, kConv0 = 12;
 constexpr int kThreads = 32 * (kConv0 + kConvWarps);
-constexpr int kRegsMma = 40, kRegsSoft = 136, kRegsConv = 80;
-static_assert(kRegsMma + 2 * kRegsSoft + 2 * kRegsConv <= 5 * 96, "the warpgroups' shares exceed the launch's registers");
+constexpr int kRegsLaunch = 72, kRegsMma = 40, kRegsSoft = 120, kRegsConv = 56;
+static_assert(kRegsMma + 2 * kRegsSoft + 4 * kRegsConv <= 7 * kRegsLaunch, "the warpgroups' shares exceed the launch's registers");
 constexpr int kPairs = 4;                           // pairs of 64-dim tiles (128 latent dims each)
 constexpr int kKTile = kKeysB * 128;                // [128 keys x 64 dims] bf16: 16 KB
 constexpr int kQTile = kRowsT * 128;                // [64 rows x 64 dims] bf16: 8 KB
@@ -60,18 +60,17 @@ constexpr int kSmem = kOffQ + 9 * kQTile + 1024;    // + alignment slack
 constexpr uint32_t kColS = 256;                     // S^T columns; O^T tile q at 64 q
 constexpr float kRaise = 20.f;                      // log2 units
 constexpr uint64_t kWait = 200000000ull;            // ns
-constexpr int kAhead = 2;                           // blocks the L2 prefetch runs ahead
+constexpr int kAhead = 3;                           // blocks the L2 prefetch runs ahead
 
 struct Bars {
-    uint64_t kfull[kPairs];     // a pair of latent tiles converted (8 warps)
+    uint64_t kfull[kPairs];     // a pair of latent tiles converted 
     uint64_t kempty[kPairs];    // O^T's MMAs read it
-    uint64_t rfull;             // rope tile stored (8 warps)
+    uint64_t rfull;             // rope tile stored (rope warps)
     uint64_t sfull;             // scores of the block in tensor memory
-    uint64_t pfull;             // P^T stored, O^T rescaled if needed (8 warps)
+    uint64_t pfull;             // P^T stored, O^T rescaled if needed 
     uint64_t pdone;             // the block's O^T complete, P^T's space free
-    uint64_t qfull;             // Q tiles of the item stored (8 warps)
-    uint64_t qempty;            // the item's last score MMAs ran
-    uint64_t ofree;             // O^T of the item read out (8 warps)
+    uint64_t qfull;             // Q tiles of the item stored 
+    uint64_t ofree;             // O^T of the item read out 
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
@@ -80,7 +79,9 @@ struct Bars {
 
 struct Shared {
     Bars bar;
-    alignas(16) float m[kRowsT];   // read as float4
+    alignas(16) float nm[kRowsT];   // minus the reference (read as float4)
+    alignas(16) float zero[kRowsT];
+    alignas(16) float m[kRowsT];    // the reference, log2 units
     alignas(16) float alpha[kRowsT];
     alignas(16) float inv[kRowsT];
     float red[4][kRowsT];       // per key quadrant
@@ -99,6 +100,12 @@ __device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parit
     return __all_sync(0xffffffffu, wait_for(bar, b, parity, err, code));
 }
 
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <int kId, int kCount>
 __device__ __forceinline__ bool barrier_or(bool flag) {
     uint32_t r;
@@ -113,11 +120,25 @@ __device__ __forceinline__ bool barrier_or(bool flag) {
     return r != 0;
 }
 
-template <int kN> __device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+template <int kN> __device__ __forceinline__ void set_regs() {
+    if constexpr (kN > kRegsLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+    if constexpr (kN < kRegsLaunch) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
 }
-template <int kN> __device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+
+// 16 bytes to a shared-memory address (32-bit addressing: the tiles' offsets stay immediates).
+__device__ __forceinline__ void sts(uint32_t addr, const uint4 &v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 16 bytes (the first `bytes` of them copied, the others zero) from global to shared memory.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -192,6 +213,24 @@ __device__ __forceinline__ void find_share(const Q8Params &p, int64_t C, int64_t
     __syncwarp();
 }
 
+// Which of the 32 rows from row0 on see tree key t (t < 0: a prefix key, all of them; t >= T:
+// behind the tree, none): bit r for row row0 + r, whose query is node (row0 + r) / H. Rows at or
+// beyond rows_seq get any value.
+__device__ __forceinline__ uint32_t seen_by(const Q8Params &p, const Item &it, int t, int row0) {
+    if (t < 0) return ~0u;
+    if (t >= p.T) return 0u;
+    uint32_t see = 0u;
+    int i = row0 / p.H, left = p.H - (row0 - i * p.H);
+    for (int r = 0; r < 32 && i < p.T; ++i) {                // one node at a time: `left` rows of it
+        const uint32_t bits = __ldg(p.vis + ((int64_t)it.b * p.T + i) * p.W + (t >> 5));
+        const int n = min(left, 32 - r);
+        if ((bits >> (t & 31)) & 1u) see |= (0xffffffffu >> (32 - n)) << r;
+        r += n;
+        left = p.H;
+    }
+    return see;
+}
+
 // x[r] of 32 lanes reduced over the lanes for all 32 r at once: lane r gets row r's result.
 // Step `off` exchanges the half of the array that the other lane keeps.
 template <typename Op>
@@ -224,23 +263,21 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared sh;
     Bars &bar = sh.bar;
-    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                            ~static_cast<uintptr_t>(1023));
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0) tmem_alloc(&bar.tmem, 512);
     if (warp == 4) find_share(p, gridDim.x, blockIdx.x, lane, bar.work);
     if (threadIdx.x == 32) {
         for (int i = 0; i < kPairs; ++i) {
-            mbar_init(&bar.kfull[i], kConvWarps);
+            mbar_init(&bar.kfull[i], kConvWarps / kPairs);
             mbar_init(&bar.kempty[i], 1);
         }
-        mbar_init(&bar.rfull, kConvWarps);
+        mbar_init(&bar.rfull, kRopeWarps);
         mbar_init(&bar.sfull, 1);
         mbar_init(&bar.pfull, kSoftWarps);
         mbar_init(&bar.pdone, 1);
-        mbar_init(&bar.qfull, kConvWarps);
-        mbar_init(&bar.qempty, 1);
+        mbar_init(&bar.qfull, kSoftWarps);
         mbar_init(&bar.ofree, kSoftWarps);
         mbar_init(&bar.drain, 1);
         bar.abort_flag = 0;
@@ -252,149 +289,169 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    Item it = {bar.work[0], bar.work[1], bar.work[2], bar.work[3], 0, 0};
-    bool have = fill(p, it);
-    uint32_t g = 0, ii = 0;                                  // blocks and items so far
 
     if (warp >= kSoft0 && warp < kSoft0 + kSoftWarps) {
         // ------------------------- softmax, correction and epilogue -------------------------
         // key = lane of S^T; half = which 32 rows of the tile; srow: one row a thread of the first 64
-        regs_inc<kRegsSoft>();
+        set_regs<kRegsSoft>();
+        Item it = {bar.work[0], bar.work[1], bar.work[2], bar.work[3], 0, 0};
+        bool have = fill(p, it);
+        uint32_t g = 0, ii = 0;                              // blocks and items so far
         const int half = (warp - kSoft0) >> 2, key = 32 * (warp & 3) + lane;
         const int srow = (int)threadIdx.x - 32 * kSoft0;
-        unsigned char *prow = smem + kOffR + key * 128;
+        const uint32_t prow = smem + kOffR + key * 128;
         bool ok = true, vis_ready = false;
-        for (; have; have = advance(p, it), ++ii) {
-            const int row0 = it.rt * kRowsT + 32 * half;     // first of this warp's 32 rows
-            float l[32];
+        // this thread's 32 scores of the block at key0, scaled, plus off[row]; -inf where hidden
+        auto scores = [&](int key0, const float *off, float (&x)[32]) {
+            uint32_t raw[32];
+            tmem_ld32(lane_addr(tmem + kColS, warp, 32 * half), raw);
+            tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 32; ++r) l[r] = 0.f;
-            if (srow < kRowsT) sh.m[srow] = -INFINITY;
+            for (int q = 0; q < 8; ++q) {
+                const float4 o = reinterpret_cast<const float4 *>(off + 32 * half)[q];
+                x[4 * q] = fmaf(__uint_as_float(raw[4 * q]), p.scale_log2, o.x);
+                x[4 * q + 1] = fmaf(__uint_as_float(raw[4 * q + 1]), p.scale_log2, o.y);
+                x[4 * q + 2] = fmaf(__uint_as_float(raw[4 * q + 2]), p.scale_log2, o.z);
+                x[4 * q + 3] = fmaf(__uint_as_float(raw[4 * q + 3]), p.scale_log2, o.w);
+            }
+            if (sh.bad[g & 1][key]) {                        // NaN wherever it is seen
+#pragma unroll
+                for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(0x7fffffffu);
+            }
+            if (key0 + kKeysB > it.P) {                      // the block holds tree keys, or rows behind them
+                if (!vis_ready) {
+                    griddep_wait();
+                    vis_ready = true;
+                }
+                const uint32_t see = seen_by(p, it, key0 + key - it.P, it.rt * kRowsT + 32 * half);
+#pragma unroll
+                for (int r = 0; r < 32; ++r) x[r] = (see >> r) & 1u ? x[r] : -INFINITY;
+            }
+        };
+        // an item's rows of Q, in the order widening gives the dims: a warp takes 8 rows
+        auto load_q = [&](const Item &q) {
+            const int r0 = 8 * (warp - kSoft0), R0 = q.rt * kRowsT + r0, sub = lane & 7, kq = lane >> 3;
+            const int64_t base = (int64_t)q.b * p.rows_seq + R0;
+#pragma unroll 4
+            for (int r = 0; r < 8; ++r) {
+                const bool live = R0 + r < p.rows_seq;
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_nope + (base + r) * p.q_nope_stride);
+                const uint32_t dst = smem + kOffQ + (r0 + r) * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = 32 * h + lane;             // 16-byte chunk of the row's 64
+                    const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    sts(dst + (c >> 3) * kQTile + (((c & 7) ^ ((r0 + r) & 7)) << 4), q8::reorder8(v));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 4 * h + kq;
+                const uint4 v = R0 + r < p.rows_seq
+                                    ? __ldg(reinterpret_cast<const uint4 *>(p.q_pe + (base + r) * p.q_pe_stride) + sub)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+                sts(smem + kOffQ + 8 * kQTile + (r0 + r) * 128 + ((sub ^ ((r0 + r) & 7)) << 4), v);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.qfull);
+        };
+        if (have) load_q(it);
+        if (srow < kRowsT) sh.zero[srow] = 0.f;
+        for (; have; have = advance(p, it), ++ii) {
+            float l = 0.f;                                   // of row `lane` of the 32, over this warp's keys
+            if (srow < kRowsT) {
+                sh.m[srow] = -INFINITY;
+                sh.nm[srow] = INFINITY;
+            }
             barrier_or<1, 256>(false);
             bool fail = false;
             for (int j = 0; j < it.nb; ++j, ++g) {
+                const int key0 = (it.kb + j) * kKeysB;
                 ok = ok && warp_wait(bar, &bar.sfull, g & 1, p.err, -41);
-                float x[32];
-                bool raise = false;
-                if (ok) {
-                    tc_fence_after();
-                    uint32_t raw[32];
-                    tmem_ld32(lane_addr(tmem + kColS, warp, 32 * half), raw);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    const int key0 = (it.kb + j) * kKeysB, kk = key0 + key;
+                float x[32];                                 // score - reference
+                const float *off = sh.nm;                    // (+inf for a row without a reference yet)
+                bool raised = false;
+                if (ok) tc_fence_after();
+#pragma unroll 1
+                for (;;) {
+                    if (ok) scores(key0, off, x);
+                    if (off == sh.nm) {
+                        if (raised) break;
+                        float top = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(raw[r]) * p.scale_log2;
-                    if (sh.bad[g & 1][key]) {                // NaN wherever it is seen
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(0x7fffffffu);
+                        for (int r = 0; r < 32; r += 2) top = fmax3(top, x[r], x[r + 1]);
+                        if (!barrier_or<1, 256>(!ok || top > kRaise)) break;
+                        if ((fail = barrier_or<1, 256>(!ok))) break;
+                        off = sh.zero;                       // some row's reference has to rise: once more for
+                        continue;                            // the scores themselves
                     }
-                    if (key0 + kKeysB > it.P) {              // the block holds tree keys, or rows behind them
-                        if (!vis_ready) {
-                            griddep_wait();
-                            vis_ready = true;
-                        }
-                        const int t = kk - it.P;             // this key's tree index
-                        if (t >= p.T) {
-#pragma unroll
-                            for (int r = 0; r < 32; ++r) x[r] = -INFINITY;
-                        } else if (t >= 0) {
-                            int i = min(row0, p.rows_seq - 1) / p.H, left = p.H - (row0 - i * p.H);
-                            const uint32_t *word = p.vis + ((int64_t)it.b * p.T + i) * p.W + (t >> 5);
-                            uint32_t bits = __ldg(word);
-#pragma unroll
-                            for (int r = 0; r < 32; ++r) {
-                                if (left == 0 && i + 1 < p.T) {
-                                    ++i;
-                                    left = p.H;
-                                    word += p.W;
-                                    bits = __ldg(word);
-                                }
-                                --left;
-                                if (!((bits >> (t & 31)) & 1u)) x[r] = -INFINITY;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 m4 = reinterpret_cast<const float4 *>(sh.m + 32 * half)[q];
-                        raise |= x[4 * q] > m4.x + kRaise || x[4 * q + 1] > m4.y + kRaise || x[4 * q + 2] > m4.z + kRaise ||
-                                 x[4 * q + 3] > m4.w + kRaise;
-                    }
-                }
-                if (barrier_or<1, 256>(raise || !ok)) {
-                    fail = barrier_or<1, 256>(!ok);
-                    if (fail) break;
-                    // some row's reference has to rise: the block's maxima, quadrant by quadrant
-                    const float mx = transpose_reduce(x, lane, [](float a, float b) { return fmaxf(a, b); });
-                    sh.red[warp & 3][32 * half + lane] = mx;
+                    // the block's maxima, quadrant by quadrant
+                    sh.red[warp & 3][32 * half + lane] =
+                        transpose_reduce(x, lane, [](float a, float b) { return fmaxf(a, b); });
                     barrier_or<1, 256>(false);
                     if (srow < kRowsT) {
                         const int r = srow;
-                        const float top = fmaxf(fmaxf(sh.red[0][r], sh.red[1][r]), fmaxf(sh.red[2][r], sh.red[3][r]));
+                        const float to = fmaxf(fmaxf(sh.red[0][r], sh.red[1][r]), fmaxf(sh.red[2][r], sh.red[3][r]));
                         const float m = sh.m[r];
                         float a = 1.f;
-                        if (top > m + kRaise) {
-                            a = m == -INFINITY ? 1.f : ex2(m - top);
-                            sh.m[r] = top;
+                        if (to > m + kRaise) {
+                            a = m == -INFINITY ? 1.f : ex2(m - to);
+                            sh.m[r] = to;
+                            sh.nm[r] = -to;
                         }
                         sh.alpha[r] = a;
                     }
                     barrier_or<1, 256>(false);
-                    if (j > 0) {                             // O^T and l of the blocks before
-                        ok = warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -42);
-                        if (ok) {
-                            tc_fence_after();
+                    if (j > 0) {                             // O^T (complete: the block before waited) and l
 #pragma unroll 1
-                            for (int q = 0; q < kPairs; ++q) {
-                                uint32_t o[32];
-                                const uint32_t addr = lane_addr(tmem, warp, kRowsT * q + 32 * half);
-                                tmem_ld32(addr, o);
-                                tmem_wait_ld();
+                        for (int q = 0; q < kPairs; ++q) {
+                            uint32_t o[32];
+                            const uint32_t addr = lane_addr(tmem, warp, kRowsT * q + 32 * half);
+                            tmem_ld32(addr, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int r = 0; r < 32; ++r)
-                                    o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[32 * half + r]);
-                                tmem_st32(addr, o);
-                            }
-                            tmem_wait_st();
-                            tc_fence_before();
+                            for (int r = 0; r < 32; ++r)
+                                o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[32 * half + r]);
+                            tmem_st32(addr, o);
                         }
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) l[r] *= sh.alpha[32 * half + r];
+                        tmem_wait_st();
+                        l *= sh.alpha[32 * half + lane];
                     }
+                    raised = true;
+                    off = sh.nm;
                 }
-                if (ok) {
-                    sh.bad[g & 1][key] = 0u;                 // (both halves write the same)
-                    // p = 2^(x - m) to this key's row of P^T; a row with no visible key yet has m = -inf
+                if (fail) break;
+                // p = 2^(score - m) to this key's row of P^T
+                tc_fence_before();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t o[4];
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float2 m2 = reinterpret_cast<const float2 *>(sh.m + 32 * half)[4 * u + v];
-                            const int r = 8 * u + 2 * v;
-                            const float p0 = m2.x == -INFINITY ? x[r] + INFINITY : ex2(x[r] - m2.x);
-                            const float p1 = m2.y == -INFINITY ? x[r + 1] + INFINITY : ex2(x[r + 1] - m2.y);
-                            // (x = -inf there, or NaN: a hidden key's NaN never gets here)
-                            const float q0 = m2.x == -INFINITY && x[r] == -INFINITY ? 0.f : p0;
-                            const float q1 = m2.y == -INFINITY && x[r + 1] == -INFINITY ? 0.f : p1;
-                            l[r] += q0;
-                            l[r + 1] += q1;
-                            o[v] = q8::pack_bf16(q0, q1);
-                        }
-                        *reinterpret_cast<uint4 *>(prow + (((4 * half + u) ^ (key & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int v = 0; v < 4; ++v) {
+                        const int r = 8 * u + 2 * v;
+                        x[r] = ex2(x[r]);
+                        x[r + 1] = ex2(x[r + 1]);
+                        o[v] = q8::pack_bf16(x[r], x[r + 1]);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.pfull);
+                    sts(prow + (((4 * half + u) ^ (key & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pfull);
+                // the sums while the tensor cores work on P^T (a running sum a thread and row would take 32
+                // registers)
+                l += transpose_reduce(x, lane, [](float a, float b) { return a + b; });
+                if (j + 1 == it.nb) {                        // the next item's Q: this one's scores are done
+                    Item nx = it;
+                    if (advance(p, nx)) load_q(nx);
+                }
+                ok = warp_wait(bar, &bar.pdone, g & 1, p.err, -42);
+                sh.bad[g & 1][key] = 0u;                     // every warp has read it: pdone follows all of pfull
             }
             if (fail) break;
             // l over the keys, then out = O / l and lse = ln2 (m + log2 l)
-            const float ls = transpose_reduce(l, lane, [](float a, float b) { return a + b; });
-            sh.red[warp & 3][32 * half + lane] = ls;
-            ok = ok && warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -43);
+            sh.red[warp & 3][32 * half + lane] = l;
             if (barrier_or<1, 256>(!ok)) break;
             // all blocks of the tile: final rows; else a piece, in slot 2c for the share's first item
             const bool whole = it.kb == 0 && it.nb == (it.P + p.T + kKeysB - 1) / kKeysB;
@@ -410,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             }
             barrier_or<1, 256>(false);
             tc_fence_after();
-            const int rows = min(32, p.rows_seq - row0);     // of this warp's 32 (may be <= 0)
+            const int dim = (key & ~3) | ((key & 1) << 1) | ((key >> 1) & 1);    // widening's order of the dims
+            const int rows = min(32, p.rows_seq - it.rt * kRowsT - 32 * half);   // of this warp's 32 (may be <= 0)
 #pragma unroll 1
             for (int q = 0; q < kPairs; ++q) {
                 uint32_t o[32];
                 tmem_ld32(lane_addr(tmem, warp, kRowsT * q + 32 * half), o);
                 tmem_wait_ld();
-                const int64_t at = (first + 32 * half) * kDc + 128 * q + key;
+                const int64_t at = (first + 32 * half) * kDc + 128 * q + dim;
                 if (whole && kBf16Out) {
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at;
 #pragma unroll
@@ -435,118 +493,122 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         }
     } else if (warp >= kConv0) {
         // --------------------------------- converters ---------------------------------
-        // A step is 128 keys x 128 bytes: one pair of latent tiles (codes), or the rope tile. Warp
-        // cw takes keys 16 cw .. + 16, four at a time: 8 lanes a key, 16 bytes a lane.
-        regs_dec<kRegsConv>();
-        const int cw = warp - kConv0, sub = lane & 7, kq = lane >> 3;
-        struct Regs {
-            uint4 v[4];
-            uint32_t s[4];
-        };
-        bool ok = true;
-        Regs cur;
-        auto load = [&](int j, int step, Regs &x) {
-            const int kv = it.P + p.T, key0 = (it.kb + j) * kKeysB + 16 * cw + kq;
+        // Four warps a pair of latent tiles, 32 keys each, so that a pair is converted as soon as
+        // O^T's MMAs have released it, whatever the others do, in one pass: wait, widen, store, fence,
+        // arrive, then all loads for the next block. (With every warp taking a share of every pair the
+        // pairs followed one another, each as long as that whole chain: 9.0 k clocks a block.) Four
+        // keys at a time: 8 lanes a key, 8 codes of each tile a lane (one 16-byte chunk of bf16, so
+        // eight lanes' stores cover all banks).
+        set_regs<kRegsConv>();
+        Item it = {bar.work[0], bar.work[1], bar.work[2], bar.work[3], 0, 0};
+        const int pair = (warp - kConv0) >> 2, k0 = 32 * ((warp - kConv0) & 3), sub = lane & 7, kq = lane >> 3;
+        // shared-memory place of key k0 + kq (key k0 + kq + 4 t follows at + 512 t), and this lane's
+        // swizzled chunk for even and odd t (which flip bit 2 of the key)
+        const uint32_t krow0 = smem + 2 * pair * kKTile + (k0 + kq) * 128 + ((sub ^ kq) << 4), krow1 = krow0 ^ 64;
+        const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;  // the lane's group of a tile's two
+        uint2 a[8], b[8];      // codes of key k0 + kq + 4 t in the pair's first and second tile
+        uint32_t sc;           // the four scale bytes of key k0 + lane
+        int j = 0;
+        auto load = [&]() {    // block j of item it, which then moves on
+            const int key0 = (it.kb + j) * kKeysB + k0, left = it.P + p.T - key0;
+            const int64_t row = (int64_t)it.b * p.L + key0;
+            const uint8_t *cp = p.c_q8 + (row + kq) * kDc + 128 * pair + 8 * sub;
+            sc = lane < left ? __ldg(reinterpret_cast<const uint32_t *>(p.c_scale + (row + lane) * (kDc / KDT_Q8_GROUP)) + pair)
+                             : 0x7f7f7f7fu;
+            if (left >= 32) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int kk = key0 + 4 * t;
-                x.v[t] = make_uint4(0u, 0u, 0u, 0u);
-                x.s[t] = 127u;
-                if (kk < kv) {
-                    const int64_t row = (int64_t)it.b * p.L + kk;
-                    if (step < kPairs) {
-                        x.v[t] = __ldg(reinterpret_cast<const uint4 *>(p.c_q8 + row * kDc) + 8 * step + sub);
-                        x.s[t] = __ldg(p.c_scale + row * (kDc / KDT_Q8_GROUP) + 4 * step + (sub >> 1));
-                    } else {
-                        x.v[t] = __ldg(reinterpret_cast<const uint4 *>(p.k_pe + row * kDr) + sub);
+                for (int t = 0; t < 8; ++t) {
+                    a[t] = __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc));
+                    b[t] = __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc + 64));
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    a[t] = b[t] = make_uint2(0u, 0u);
+                    if (kq + 4 * t < left) {
+                        a[t] = __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc));
+                        b[t] = __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc + 64));
                     }
                 }
+            }
+            if (++j == it.nb) {
+                j = 0;
+                advance(p, it);
             }
         };
-        if (have) load(0, 0, cur);
-        while (have && ok) {
-            // the item's rows of Q: warp cw takes rows 8 cw .. + 8
-            ok = ii == 0 || warp_wait(bar, &bar.qempty, (ii - 1) & 1, p.err, -44);
-            if (!ok) break;
-            {
-                const int r0 = 8 * cw, R0 = it.rt * kRowsT + r0;
-                const int64_t base = (int64_t)it.b * p.rows_seq + R0;
-#pragma unroll 2
-                for (int r = 0; r < 8; ++r) {
-                    const bool live = R0 + r < p.rows_seq;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_nope + (base + r) * p.q_nope_stride);
-                    unsigned char *dst = smem + kOffQ + (r0 + r) * 128;
+        const uint32_t G = (uint32_t)bar.work[0];            // blocks of the share
+        if (fill(p, it)) load();
+        for (uint32_t g = 0; g < G; ++g) {
+            // the pair's space: read by O^T's MMAs of the block before
+            if (g > 0 && !warp_wait(bar, &bar.kempty[pair], (g - 1) & 1, p.err, -45)) break;
+            // a lane turns the scale bytes of its key into factors, a pair for each tile
+            const uint32_t b0 = sc & 255u, b1 = (sc >> 8) & 255u, b2 = (sc >> 16) & 255u, b3 = sc >> 24;
+            const uint32_t fa = q8::factor(b0) | (q8::factor(b1) << 16), fb = q8::factor(b2) | (q8::factor(b3) << 16);
+            const bool nan = b0 == (uint32_t)q8::kNaN || b1 == (uint32_t)q8::kNaN || b2 == (uint32_t)q8::kNaN ||
+                             b3 == (uint32_t)q8::kNaN;
+            if (nan) sh.bad[g & 1][k0 + lane] = 1u;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = 32 * h + lane;         // 16-byte chunk of the row's 64
-                        const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * kQTile + (((c & 7) ^ ((r0 + r) & 7)) << 4)) = v;
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = 4 * h + kq;
-                    const bool live = R0 + r < p.rows_seq;
-                    const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(p.q_pe + (base + r) * p.q_pe_stride) + sub)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(smem + kOffQ + 8 * kQTile + (r0 + r) * 128 + ((sub ^ ((r0 + r) & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.qfull);
+            for (int t = 0; t < 8; ++t) {
+                const uint32_t dst = ((t & 1) ? krow1 : krow0) + 512 * t;
+                sts(dst, q8::widen8(a[t], __byte_perm(__shfl_sync(0xffffffffu, fa, 4 * t + kq), 0u, pick)));
+                sts(dst + kKTile, q8::widen8(b[t], __byte_perm(__shfl_sync(0xffffffffu, fb, 4 * t + kq), 0u, pick)));
             }
-            const int nb = it.nb;
-            for (int j = 0; j < nb && ok; ++j, ++g) {
-#pragma unroll
-                for (int step = 0; step <= kPairs; ++step) {
-                    Regs nxt;
-                    if (step < kPairs) {
-                        load(j, step + 1, nxt);
-                    } else if (j + 1 < nb) {
-                        load(j + 1, 0, nxt);
-                    } else if ((have = advance(p, it))) {
-                        load(0, 0, nxt);
-                    }
-                    // the tile's space: read by O^T's MMAs of the block before
-                    if (g > 0) {
-                        uint64_t *b = step < kPairs ? &bar.kempty[step] : &bar.pdone;
-                        if (!(ok = warp_wait(bar, b, (g - 1) & 1, p.err, step < kPairs ? -45 : -46))) break;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int kr = 16 * cw + 4 * t + kq;     // key of the block
-                        if (step < kPairs) {
-                            if (cur.s[t] == (uint32_t)q8::kNaN) sh.bad[g & 1][kr] = 1u;
-                            uint4 lo, hi;
-                            q8::widen16(cur.v[t], cur.s[t], lo, hi);
-                            // chunks 2 (sub % 4) and + 1 of tile sub / 4; the lanes of the second tile
-                            // store theirs in the other order, so that eight lanes cover all banks
-                            unsigned char *dst = smem + (2 * step + (sub >> 2)) * kKTile + kr * 128;
-                            const int c0 = 2 * (sub & 3), sw = kr & 7, second = sub >> 2;
-                            *reinterpret_cast<uint4 *>(dst + (((c0 + second) ^ sw) << 4)) = second ? hi : lo;
-                            *reinterpret_cast<uint4 *>(dst + (((c0 + 1 - second) ^ sw) << 4)) = second ? lo : hi;
-                        } else {
-                            *reinterpret_cast<uint4 *>(smem + kOffR + kr * 128 + ((sub ^ (kr & 7)) << 4)) = cur.v[t];
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(step < kPairs ? &bar.kfull[step] : &bar.rfull);
-                    cur = nxt;
+            // some scale above 2^7: a second product
+            if (__any_sync(0xffffffffu, max(max(b0, b1), max(b2, b3)) > q8::kHighByte)) {
+                const uint32_t ha = q8::factor_high(b0) | (q8::factor_high(b1) << 16);
+                const uint32_t hb = q8::factor_high(b2) | (q8::factor_high(b3) << 16);
+#pragma unroll 1
+                for (int t = 0; t < 16; ++t) {
+                    const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, t < 8 ? ha : hb, 4 * (t & 7) + kq), 0u, pick);
+                    const uint32_t dst = ((t & 1) ? krow1 : krow0) + 512 * (t & 7) + (t >> 3) * kKTile;
+                    uint4 v = lds(dst);
+                    v.x = q8::mul_bf16x2(v.x, f);
+                    v.y = q8::mul_bf16x2(v.y, f);
+                    v.z = q8::mul_bf16x2(v.z, f);
+                    v.w = q8::mul_bf16x2(v.w, f);
+                    sts(dst, v);
                 }
             }
-            ++ii;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.kfull[pair]);
+            if (g + 1 < G) load();
         }
     } else {
-        regs_dec<kRegsMma>();
-        if (warp == 0 && elect_one()) {
+        set_regs<kRegsMma>();
+        if (warp > 0) {
+        // ---------------- rope keys: 16-byte asynchronous copies, zeros behind the last row ----------------
+        Item it = {bar.work[0], bar.work[1], bar.work[2], bar.work[3], 0, 0};
+        bool ok = true;
+        uint32_t g = 0;
+        for (bool have = fill(p, it); have && ok; have = advance(p, it)) {
+            for (int j = 0; j < it.nb; ++j, ++g) {
+                // its space held P^T of the block before
+                if (g > 0 && !(ok = warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -46))) break;
+                const int key0 = (it.kb + j) * kKeysB, left = it.P + p.T - key0;
+                const __nv_bfloat16 *src = p.k_pe + ((int64_t)it.b * p.L + key0) * kDr;
+                for (int c = 32 * (warp - 1) + lane; c < kKeysB * 8; c += 32 * kRopeWarps) {
+                    const int key = c >> 3;                  // a row behind the last is not read (0 bytes)
+                    cp_async16(smem + kOffR + key * 128 + (((c & 7) ^ (key & 7)) << 4), key < left ? src + 8 * c : src,
+                               key < left ? 16u : 0u);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.rfull);
+            }
+        }
+        } else if (elect_one()) {
         // -------------------------------- MMA issuer --------------------------------
+        Item it = {bar.work[0], bar.work[1], bar.work[2], bar.work[3], 0, 0};
+        bool have = fill(p, it);
+        uint32_t g = 0, ii = 0;                              // blocks and items so far
         const uint32_t id_s = idesc_bf16_f32(kKeysB, kRowsT, 0, 0), id_o = idesc_bf16_f32(kKeysB, kRowsT, 1, 1);
         // Descriptors differ only in their low words (address and leading stride); each use adds a
         // constant to a base the compiler cannot see through, or it would keep all of them live.
         const uint64_t d0 = sdesc_sw128(0, 0, 1024);
         const uint32_t dhi = (uint32_t)(d0 >> 32);
-        const uint32_t base = smem_u32(smem) >> 4, lbo_k = (16u >> 4) << 16, lbo_mn = ((uint32_t)kKTile >> 4) << 16;
+        const uint32_t base = smem >> 4, lbo_k = (16u >> 4) << 16, lbo_mn = ((uint32_t)kKTile >> 4) << 16;
         auto desc = [&](uint32_t lo) { return ((uint64_t)dhi << 32) | lo; };
         auto opaque = [](uint32_t v) {
             asm volatile("" : "+r"(v));
@@ -592,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 for (int t = 0; t < 4; ++t) mma_ss(tmem + kColS, desc(rd + 2 * t), desc(qr + 2 * t), id_s, 1u);
                 mma_commit(&bar.sfull);
                 prefetch();
-                if (j == it.nb - 1) mma_commit(&bar.qempty);
                 if (!(ok = wait_for(bar, &bar.pfull, g & 1, p.err, -50))) break;
                 // the item before: its O^T has been read out
                 if (j == 0 && ii > 0 && !(ok = wait_for(bar, &bar.ofree, (ii - 1) & 1, p.err, -51))) break;
