@@ -545,6 +545,42 @@ size_t kdt_verify_attn_q8_workspace_size(const kdt_verify_q8_args *a);
 /* What kdt_verify_attn_q8 will launch for these arguments. */
 kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
 
+/* ------------------------------------------------------------------------------
+ * Sampled acceptance, beside the greedy kdt_tree_accept.
+ * ------------------------------------------------------------------------------ */
+
+/*
+ * kdt_tree_sample -- verify a drafted tree against the target's probabilities from given
+ * random numbers. The emitted tokens (the accepted drafts and the bonus token) are
+ * distributed as samples of the target, whatever was drafted.
+ * At node i of sequence b, with l the V logits of (b,i): w_j = e^{(l_j - max l) / temperature},
+ * held to 2^-44 of the largest, Z = sum_j w_j. From the root, the children c of the current
+ * node are tried in index order: c is accepted, and becomes the current node, when
+ *     u_node[b,c] * (Z - sum of the weights of the siblings tried before) < w_{tok[c]}
+ * (a token that an earlier sibling drafted too counts once: the later one is never accepted).
+ * When no child is accepted the bonus token is the least j with sum_{k <= j} w'_k >
+ * u_bonus[b] * sum_k w'_k, where w' is w with the children's tokens set to 0.
+ * Sums and comparisons are made in fixed point or 64 bits: the result does not depend on how
+ * the work is split.
+ *   parent   device int32 [B,T], -1 <= parent[b,i] < i;  tok device int32 [B,T] (tok[b,0] unused)
+ *   logits   device, row (b,i) at logits + (b*T + i) * row_stride elements, V of them used, of
+ *            dtype; row_stride 0 = V. -inf is a token that cannot be drawn.
+ *   u_node   device float32 [B,T], u_bonus device float32 [B]: numbers in [0, 1)
+ *   acc_nodes, n_acc, bonus  out, as kdt_tree_accept's: they feed kdt_kv_compact(_q8)
+ *   logp     device float32 [B,T] out, or NULL: entry k < n_acc is the log-probability (natural,
+ *            under the target at this temperature) of the token emitted after path node k; 0 behind
+ *   err      device int32, or NULL: zeroed, then 1 + (b*T + i) of the first parent entry outside
+ *            [-1, i) (skipped), child on the way whose token is outside [0, V) (never accepted), or
+ *            node on the way whose logits have a NaN, a +inf or nothing but -inf (the walk ends
+ *            there with bonus -1; also when a u of 1 or more leaves nothing to draw from).
+ * Sizes: T <= 4096, V <= 524288, temperature in [1e-3, 1e3] (kdt_tree_accept is the greedy limit).
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE, KDT_ERR_UNSUPPORTED, KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_tree_sample(const int32_t *parent, const int32_t *tok, const void *logits, kdt_dtype dtype, int B, int T,
+                           int V, int64_t row_stride, double temperature, const float *u_node, const float *u_bonus,
+                           int32_t *acc_nodes, int32_t *n_acc, int32_t *bonus, float *logp, int32_t *err,
+                           cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -85,3 +85,36 @@ def attention(q, c, k_pe, prefix, see, scale):
         out[i] = (p @ c[keys]) / z
         lse[i] = (m + np.log(z))[:, 0]
     return out, lse
+
+
+def sample_weights(logits, temperature):
+    """Weights of one row, in units of 2^-44 of the largest (float64 integers)."""
+    y = (logits.astype(np.float64) - np.max(logits)) / temperature
+    return np.floor(np.exp(y) * 2.0 ** 44 + 0.5)
+
+
+def tree_sample(parent, tok, logits, u_node, u_bonus, temperature):
+    """One sequence: logits callable (node -> float64 row [V]). Returns (path, bonus, logp)."""
+    T = len(parent)
+    node, path, logp = 0, [0], []
+    while True:
+        row = logits(node)
+        if not np.isfinite(np.max(row)) or np.isnan(row).any():
+            return path, -1, logp + [0.0]
+        w = sample_weights(row, temperature)
+        lw = (row - np.max(row)) / temperature - math.log(w.sum() / 2.0 ** 44)
+        left, step = w.copy(), None
+        for c in range(node + 1, T):
+            if parent[c] != node or not 0 <= tok[c] < len(w):
+                continue
+            if u_node[c] * left.sum() < left[tok[c]]:
+                step = c
+                break
+            left[tok[c]] = 0.0
+        if step is None:
+            run = np.cumsum(left)
+            bonus = int(np.searchsorted(run, float(u_bonus) * run[-1], side="right"))
+            return path, bonus, logp + [lw[bonus]]
+        logp.append(lw[tok[step]])
+        path.append(step)
+        node = step

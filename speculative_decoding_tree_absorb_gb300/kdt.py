@@ -28,7 +28,8 @@ EXPORTS = ("kdt_status_str", "kdt_version", "kdt_build_visibility", "kdt_verify_
            "kdt_verify_attn_noalloc", "kdt_rope_neox", "kdt_tree_accept", "kdt_kv_compact", "kdt_tree_build",
            "kdt_verify_attn_host", "kdt_verify_attn_host_buffer_size", "kdt_vc_up_proj",
            "kdt_test_verify_attn_wait_expiry", "kdt_latent_write_q8", "kdt_latent_read_q8", "kdt_kv_compact_q8",
-           "kdt_verify_attn_q8", "kdt_verify_attn_q8_workspace_size", "kdt_verify_attn_q8_plan")
+           "kdt_verify_attn_q8", "kdt_verify_attn_q8_workspace_size", "kdt_verify_attn_q8_plan",
+           "kdt_tree_sample")
 
 
 class KdtError(RuntimeError):
@@ -162,6 +163,9 @@ def lib():
         L.kdt_verify_attn_q8_workspace_size.restype = ctypes.c_size_t
         L.kdt_verify_attn_q8_plan.argtypes = [ctypes.POINTER(VerifyQ8Args), ctypes.POINTER(Plan)]
         L.kdt_verify_attn_q8_plan.restype = ctypes.c_int
+        L.kdt_tree_sample.argtypes = [vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                      ctypes.c_double, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.kdt_tree_sample.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -572,3 +576,28 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
     _check(lib().kdt_verify_attn_q8(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream_ptr(stream)),
            "kdt_verify_attn_q8")
     return out, lse
+
+
+def tree_sample(parent, tok, logits, u_node, u_bonus, *, temperature=1.0, err=None, want_logp=True, stream=None):
+    """Sampled verification of a drafted tree (kdt_tree_sample). ``logits`` [B,T,V] float32 or bf16 (equally
+    spaced rows, a contiguous last dim), ``u_node`` [B,T] and ``u_bonus`` [B] float32 random numbers in
+    [0, 1). Returns (acc_nodes [B,T], n_acc [B], bonus [B]) int32 and logp [B,T] float32 (or None)."""
+    import torch
+    B, T = parent.shape
+    V = logits.shape[2]
+    if tuple(logits.shape) != (B, T, V):
+        raise ValueError("logits must be [B,T,V], B and T as in parent")
+    row_stride = _row_stride3(logits, "logits")
+    _int32_of(parent, B * T, "parent"), _int32_of(tok, B * T, "tok")
+    for t, n, name in ((u_node, B * T, "u_node"), (u_bonus, B, "u_bonus")):
+        if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+    dev = logits.device
+    acc = torch.empty((B, T), dtype=torch.int32, device=dev)
+    n = torch.empty(B, dtype=torch.int32, device=dev)
+    bonus = torch.empty(B, dtype=torch.int32, device=dev)
+    logp = torch.empty((B, T), dtype=torch.float32, device=dev) if want_logp else None
+    _check(lib().kdt_tree_sample(_ptr(parent), _ptr(tok), _ptr(logits), _dtype_code(logits), B, T, V, row_stride,
+                                 float(temperature), _ptr(u_node), _ptr(u_bonus), _ptr(acc), _ptr(n), _ptr(bonus),
+                                 _ptr(logp), _ptr(err), _stream_ptr(stream)), "kdt_tree_sample")
+    return acc, n, bonus, logp

@@ -168,3 +168,30 @@ def test_verify_q8_binding_refuses_wrong_tensors(kdt):
             kdt.verify_attn_q8(**args)
     with pytest.raises(TypeError):
         kdt.verify_attn_q8(q[..., :512].float(), q[..., 512:].float(), c8, sc, kp, pre, parent=par)
+
+
+def test_tree_sample_refusals(kdt):
+    K = kdt.kdt
+
+    def call(parent=0x10000, tok=0x20000, logits=0x30000, dt=1, B=2, T=9, V=1000, stride=0, temp=1.0, un=0x40000,
+             ub=0x50000, acc=0x60000, n=0x70000, bonus=0x80000, logp=None, err=None):
+        return kdt.lib().kdt_tree_sample(parent, tok, logits, dt, B, T, V, stride, temp, un, ub, acc, n, bonus, logp, err,
+                                         None)
+
+    for kw in (dict(B=-1), dict(B=65536), dict(T=0), dict(T=4097), dict(V=0), dict(V=524289), dict(stride=999),
+               dict(temp=0.0), dict(temp=-1.0), dict(temp=float("nan")), dict(temp=1e-4), dict(temp=1e4),
+               dict(logits=0x30001), dict(dt=0, logits=0x30002), dict(un=0x40002), dict(acc=0x60001), dict(logp=0x90002),
+               dict(err=0x90001)):
+        assert call(**kw) == K.KDT_ERR_BAD_SHAPE, kw
+    assert call(dt=2) == K.KDT_ERR_UNSUPPORTED
+    for kw in ("parent", "tok", "logits", "un", "ub", "acc", "n", "bonus"):
+        assert call(**{kw: None}) == K.KDT_ERR_NULL_ARG, kw
+    assert call(B=0) == K.KDT_OK
+    import torch
+    par, u = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    lg = torch.zeros(2, 3, 10)
+    for kw in (dict(logits=lg[:1]), dict(tok=par.long()), dict(u_node=u.double()), dict(u_bonus=u), dict(logits=lg[..., ::2])):
+        args = dict(parent=par, tok=par, logits=lg, u_node=u, u_bonus=u[:, 0].contiguous())
+        args.update(kw)
+        with pytest.raises(ValueError):
+            kdt.tree_sample(**args)
