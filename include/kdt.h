@@ -516,9 +516,11 @@ typedef struct {
     kdt_dtype out_dtype;    /* KDT_F32 or KDT_BF16 */
     float *lse;             /* device fp32 [B,T,H], or NULL */
     int32_t *err;           /* device int32 error word, or NULL (as for kdt_verify_attn) */
-    int impl;               /* KDT_IMPL_AUTO, or KDT_IMPL_Q8_ROWS */
+    int impl;               /* KDT_IMPL_AUTO (by the rows T * H of a sequence), KDT_IMPL_TCGEN05 (256 rows
+                               at a time on 4-CTA clusters) or KDT_IMPL_Q8_ROWS (64 rows on one SM) */
     int num_splits;         /* 0 = automatic; else the CTAs the (64-row tile, 128-key block) pairs are cut
-                               into equal shares for (at most one per pair) */
+                               into equal shares for (at most one per pair), or the clusters (at most
+                               those resident at once) */
 } kdt_verify_q8_args;
 
 /*

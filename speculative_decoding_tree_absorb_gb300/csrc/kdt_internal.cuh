@@ -62,6 +62,9 @@ struct VerifyParams {
     // arrival to withhold (0 = none, 1 = the first item's Q-ready arrivals).
     uint64_t wait_ns = 0;
     int fault = 0;
+    // 8-bit cache (launch_verify_tc_q8): c_kv holds codes, c_scale their scale bytes; out may be bf16
+    const uint8_t *c_scale = nullptr;
+    bool out_bf16 = false;
 };
 
 // K0: parent -> packed ancestor bits.
@@ -98,6 +101,9 @@ int tc_max_clusters();    // 4-CTA clusters resident at once on the current devi
 int tc_keys_per_block();
 constexpr int kTcSchedWords = 2 + 48 + 1;   // R, boundary cost, cut points of up to 48 clusters
 cudaError_t launch_verify_tc(const VerifyParams &p, cudaStream_t s);
+// The same over the 8-bit latent cache.
+int tc_q8_max_clusters();
+cudaError_t launch_verify_tc_q8(const VerifyParams &p, cudaStream_t s);
 
 // K2: merge the split partials into out/lse.
 cudaError_t launch_merge_splits(const float *part_o, const float *part_lse, int num_splits, int64_t rows,
@@ -133,6 +139,7 @@ struct Q8Params {
     float *part_o, *part_lse;  // [2 * ctas][kQ8Rows] piece states (unused with one CTA)
     int32_t *err;
     int ctas;
+    bool pieces;               // tiles may be cut between CTAs: a second kernel joins their pieces
     bool overlap_vis;          // launched right behind this call's visibility kernel
 };
 constexpr int kQ8Rows = 64;    // query rows of a tile

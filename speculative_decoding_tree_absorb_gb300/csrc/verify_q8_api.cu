@@ -15,15 +15,22 @@ struct Q8Plan {
     int impl = KDT_IMPL_Q8_ROWS;
     int ctas = 0, launches = 0;
     int tiles_seq = 0;
-    size_t vis_off = 0, po_off = 0, pl_off = 0, ws_bytes = 0;
+    bool pieces = false;                   // a second kernel joins the pieces of what the split cut
+    int splits = 0;                        // CTAs, or 4-CTA clusters, the work is shared among
+    size_t vis_off = 0, po_off = 0, pl_off = 0, sched_off = 0, ws_bytes = 0;
 };
+
+// Kernel by rows a sequence: the 4-CTA cluster kernel takes 256 rows of a sequence at a time, the
+// rows kernel 64 on one SM.
+bool many_rows(int tiles, int units) { return tiles > 2 * units; }
 
 kdt_status check_args(const kdt_verify_q8_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;
     if (a->B < 0 || a->B > 65535 || a->T < 1 || a->T > kMaxT || a->H < 1 || a->H > 1024) return KDT_ERR_BAD_SHAPE;
     if (a->D_c != kDc || a->D_r != kDr) return KDT_ERR_UNSUPPORTED;
     if (a->out_dtype != KDT_F32 && a->out_dtype != KDT_BF16) return KDT_ERR_UNSUPPORTED;
-    if (a->impl != KDT_IMPL_AUTO && a->impl != KDT_IMPL_Q8_ROWS) return KDT_ERR_UNSUPPORTED;
+    if (a->impl != KDT_IMPL_AUTO && a->impl != KDT_IMPL_TCGEN05 && a->impl != KDT_IMPL_Q8_ROWS)
+        return KDT_ERR_UNSUPPORTED;
     if (a->num_splits < 0) return KDT_ERR_BAD_SHAPE;
     if (a->B == 0) return KDT_OK;
     if (!a->q_nope || !a->q_pe || !a->c_q8 || !a->c_scale || !a->k_pe || !a->prefix_len || !a->out)
@@ -54,24 +61,43 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
     }
     const int rows_seq = a->T * a->H;
     p.tiles_seq = (rows_seq + kQ8Rows - 1) / kQ8Rows;
-    const int64_t tiles = (int64_t)p.tiles_seq * a->B;
-    const int64_t pairs = tiles * ((a->max_kv_len + kQ8Keys - 1) / kQ8Keys);
-    if (tiles > INT32_MAX || pairs / sm_count() > INT32_MAX / 2) return KDT_ERR_BAD_SHAPE;
-    int64_t C = a->num_splits > 0 ? a->num_splits : sm_count();
-    if (C > pairs) C = pairs;
-    if (pairs / C > INT32_MAX / 2) return KDT_ERR_BAD_SHAPE;
-    p.ctas = (int)C;
+    const int units_seq = (rows_seq + tc_rows_per_unit() - 1) / tc_rows_per_unit();
+    p.impl = a->impl != KDT_IMPL_AUTO ? a->impl : (many_rows(p.tiles_seq, units_seq) ? KDT_IMPL_TCGEN05 : KDT_IMPL_Q8_ROWS);
+    const bool tc = p.impl == KDT_IMPL_TCGEN05;
+    const int nblk = (a->max_kv_len + kQ8Keys - 1) / kQ8Keys;
+    int piece_rows;
+    if (tc) {
+        if ((int64_t)a->B * rows_seq > INT32_MAX || a->kv_row_stride > INT32_MAX) return KDT_ERR_BAD_SHAPE;
+        const int resident = tc_q8_max_clusters();
+        p.splits = a->num_splits > 0 && a->num_splits < resident ? a->num_splits : resident;
+        p.ctas = 4 * p.splits;
+        piece_rows = tc_rows_per_unit();
+    } else {
+        const int64_t tiles = (int64_t)p.tiles_seq * a->B, pairs = tiles * nblk;
+        if (tiles > INT32_MAX) return KDT_ERR_BAD_SHAPE;
+        int64_t C = a->num_splits > 0 ? a->num_splits : sm_count();
+        if (C > pairs) C = pairs;
+        if (pairs / C > INT32_MAX / 2) return KDT_ERR_BAD_SHAPE;
+        p.ctas = p.splits = (int)C;
+        piece_rows = kQ8Rows;
+    }
+    // a tile of one block is never cut
+    p.pieces = p.splits > 1 && (tc || nblk > 1);
     size_t off = 0;
     if (a->parent) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
-    if (p.ctas > 1) {
-        const size_t prow = (size_t)2 * p.ctas * kQ8Rows;
+    if (p.pieces) {
+        const size_t prow = (size_t)2 * p.splits * piece_rows;
         p.po_off = off;
         off = align_up(off + prow * kDc * sizeof(float));
         p.pl_off = off;
         off = align_up(off + prow * sizeof(float));
+        if (tc) {
+            p.sched_off = off;
+            off = align_up(off + kTcSchedWords * sizeof(int64_t));
+        }
     }
     p.ws_bytes = off;
-    p.launches = (a->parent ? 1 : 0) + 1 + (p.ctas > 1 ? 1 : 0);
+    p.launches = (a->parent ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
     *out = p;
     return KDT_OK;
 }
@@ -94,7 +120,7 @@ kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *out) {
     const kdt_status st = make_plan(a, &p);
     if (st != KDT_OK) return st;
     out->impl = p.impl;
-    out->num_splits = p.ctas;
+    out->num_splits = p.splits;
     out->num_launches = p.launches;
     out->ctas = p.ctas;
     out->workspace_bytes = p.ws_bytes;
@@ -111,6 +137,46 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
                                        a->vis, a->out, a->lse, a->err, p.ws_bytes ? workspace : nullptr})) != KDT_OK)
         return st;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
+    const uint32_t *vis = a->vis;
+    if (a->parent) {
+        uint32_t *bits = reinterpret_cast<uint32_t *>(ws + p.vis_off);
+        if (launch_build_visibility(a->parent, a->B, a->T, bits, a->err, stream) != cudaSuccess) return KDT_ERR_CUDA;
+        vis = bits;
+    } else if (a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t), stream) != cudaSuccess) {
+        return KDT_ERR_CUDA;
+    }
+    if (p.impl == KDT_IMPL_TCGEN05) {
+        VerifyParams v;
+        v.B = a->B;
+        v.T = a->T;
+        v.H = a->H;
+        v.W = (a->T + 31) / 32;
+        v.L = a->kv_row_stride;
+        v.max_kv = a->max_kv_len;
+        v.q_nope = a->q_nope;
+        v.q_pe = a->q_pe;
+        v.q_nope_stride = a->q_nope_row_stride ? a->q_nope_row_stride : kDc;
+        v.q_pe_stride = a->q_pe_row_stride ? a->q_pe_row_stride : kDr;
+        v.c_kv = a->c_q8;
+        v.c_scale = a->c_scale;
+        v.k_pe = a->k_pe;
+        v.prefix_len = a->prefix_len;
+        v.vis = vis;
+        v.scale_log2 = a->scale * 1.4426950408889634f;
+        v.out = static_cast<float *>(a->out);
+        v.out_bf16 = a->out_dtype == KDT_BF16;
+        v.lse = a->lse;
+        v.part_o = reinterpret_cast<float *>(ws + p.po_off);
+        v.part_lse = reinterpret_cast<float *>(ws + p.pl_off);
+        v.tc_sched = p.pieces ? reinterpret_cast<int64_t *>(ws + p.sched_off) : nullptr;
+        v.rows_total = (int64_t)a->B * a->T * a->H;
+        v.tc_clusters = p.splits;
+        v.num_splits = p.splits;
+        v.blocks_per_split = 0;
+        v.err = a->err;
+        v.overlap_vis = a->parent != nullptr;
+        return launch_verify_tc_q8(v, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+    }
     Q8Params q = {};
     q.B = a->B;
     q.T = a->T;
@@ -127,6 +193,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     q.c_scale = a->c_scale;
     q.k_pe = static_cast<const __nv_bfloat16 *>(a->k_pe);
     q.prefix_len = a->prefix_len;
+    q.vis = vis;
     q.scale_log2 = a->scale * 1.4426950408889634f;
     q.out = a->out;
     q.out_bf16 = a->out_dtype == KDT_BF16;
@@ -135,15 +202,8 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     q.part_lse = reinterpret_cast<float *>(ws + p.pl_off);
     q.err = a->err;
     q.ctas = p.ctas;
-    if (a->parent) {
-        uint32_t *vis = reinterpret_cast<uint32_t *>(ws + p.vis_off);
-        if (launch_build_visibility(a->parent, a->B, a->T, vis, a->err, stream) != cudaSuccess) return KDT_ERR_CUDA;
-        q.vis = vis;
-        q.overlap_vis = true;
-    } else {
-        q.vis = a->vis;
-        if (a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t), stream) != cudaSuccess) return KDT_ERR_CUDA;
-    }
+    q.pieces = p.pieces;
+    q.overlap_vis = a->parent != nullptr;
     return launch_verify_q8_rows(q, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
 

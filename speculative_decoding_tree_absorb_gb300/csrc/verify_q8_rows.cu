@@ -787,7 +787,7 @@ template <bool kBf16Out> cudaError_t launch(const Q8Params &p, cudaStream_t s) {
     cfg.attrs = pdl;
     cfg.numAttrs = p.overlap_vis ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, verify_q8_rows_kernel<kBf16Out>, p)) != cudaSuccess) return e;
-    if (p.ctas > 1) {
+    if (p.pieces) {
         cudaLaunchConfig_t mc = {};
         mc.gridDim = dim3((unsigned)((int64_t)p.B * p.tiles_seq), kRowsT / 8);
         mc.blockDim = dim3(256);

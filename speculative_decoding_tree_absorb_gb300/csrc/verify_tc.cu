@@ -43,10 +43,20 @@
 //    O (fp32) far from overflow; a smaller one rescales often on caches with
 //    outlier keys (a few times larger than the rest), and every rescale drains the
 //    P.V pipe.
+//  * The same kernel runs over the 8-bit latent cache (kQ8): there is no TMA for latents
+//    then. Four more warps a CTA load codes to registers, widen them to bf16 (exact: e4m3
+//    times a power of two) and store the same swizzled tiles into the same rings: in an
+//    S-CTA its 64 keys of each key chunk, in an O-CTA its 128 columns of each value chunk.
+//    Widening leaves each four dims in the order (0, 2, 1, 3): Q is loaded in that order and
+//    O written back from it. A CTA widens 32 k codes a block (about 800 instructions a warp
+//    in the 3700 clocks a block takes), so the widening hides behind the MMAs. A NaN group
+//    gives NaN keys, so that rows which see it become NaN, and zero values, so that it does
+//    not reach rows from which it is hidden.
 //  * Every wait is bounded; on a lost arrival the kernel records a status in the
 //    caller's error word, drains its own in-flight copies and MMAs, frees TMEM and
 //    returns (no trap, no hang).
 #include "kdt_internal.cuh"
+#include "q8.cuh"
 #include "tc_ptx.cuh"
 
 #include <atomic>
@@ -101,6 +111,12 @@ constexpr int kRows = 128;             // query rows per CTA (the pair's MMA has
 constexpr int kKeys = 128;             // keys per block (S MMA N, P.V K)
 constexpr int kHalfKeys = kKeys / 2;   // keys of a block held by one S-CTA
 constexpr int kThreads = 384;          // 12 warps
+// 8-bit cache: warps 12-15 widen. The launch gives each of the four warpgroups 128 registers a
+// thread; they trade (issuers and loaders, two of softmax, widening).
+constexpr int kThreadsQ8 = 512;
+constexpr int kRegsQ8[4] = {72, 168, 168, 104};
+static_assert(kRegsQ8[0] + kRegsQ8[1] + kRegsQ8[2] + kRegsQ8[3] <= 4 * 128, "the warpgroups' shares exceed the launch's registers");
+constexpr int kWidenWarps = 4;
 constexpr int kQPrefetchBlocks = 6;               // blocks before an item's end that warm L2 with the next Q
 constexpr uint32_t kQPrefetchChunk = 32768;       // bytes per L2 prefetch request
 constexpr int kKvPrefetchBlocks = 4;              // key blocks the L2 prefetch runs ahead of the loads
@@ -218,6 +234,10 @@ struct TcParams {
     uint64_t wait_ns;              // wait limit (kWaitLimit unless a test shortens it)
     int fault;                     // test hook: 1 = withhold the first item's Q-ready arrivals
     int64_t *sched;                // [R, kov, cut points B[0..C]] for the merge pass, or NULL
+    // 8-bit cache
+    const uint8_t *c_q8, *c_scale;
+    int64_t L;                     // cache rows per sequence
+    bool out_bf16;                 // out is bf16
 };
 
 // ---- work decomposition ----------------------------------------------------------------
@@ -578,7 +598,7 @@ __device__ __forceinline__ float scaled_max64(const float (&x)[64], float scale)
 // p = 2^(scale * x - m) for 64 keys of one row, packed to bf16 into a 128-byte
 // swizzled row of a P tile; returns the fp32 sum of the p. kScaled: x already holds
 // scale * score (hidden keys -inf) and m may be -inf (all hidden so far: p = 0).
-template <bool kScaled>
+template <bool kScaled, bool kQ8>
 __device__ __forceinline__ float stage_p_row(const float (&x)[64], float scale, float m, unsigned char *dst_row,
                                              int row) {
     float lsum = 0.f;
@@ -593,6 +613,10 @@ __device__ __forceinline__ float stage_p_row(const float (&x)[64], float scale, 
             if (kScaled) {
                 e0 = live ? fast_exp2(x[u * 8 + 2 * q] + nm) : 0.f;
                 e1 = live ? fast_exp2(x[u * 8 + 2 * q + 1] + nm) : 0.f;
+                if (kQ8 && !live) {                        // -inf, or the NaN of a key the row sees
+                    if (x[u * 8 + 2 * q] != x[u * 8 + 2 * q]) e0 = x[u * 8 + 2 * q];
+                    if (x[u * 8 + 2 * q + 1] != x[u * 8 + 2 * q + 1]) e1 = x[u * 8 + 2 * q + 1];
+                }
             } else {
                 e0 = fast_exp2(fmaf(x[u * 8 + 2 * q], scale, nm));
                 e1 = fast_exp2(fmaf(x[u * 8 + 2 * q + 1], scale, nm));
@@ -610,7 +634,84 @@ __device__ __forceinline__ uint32_t tmem_lane_addr(uint32_t base, int warp, uint
     return base + ((uint32_t)(32 * (warp & 3)) << 16) + col;
 }
 
-__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+// ---- widening (8-bit cache) ------------------------------------------------------------------
+// Registers a warpgroup takes for its role.
+template <int kN> __device__ __forceinline__ void set_regs() {
+    if constexpr (kN > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+    if constexpr (kN < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+}
+
+// One warp's share of a chunk, 16 sets of 8 codes a lane: kTiles tiles of 64 dims, 16 / kTiles
+// groups of four keys (8 lanes a key, 8 codes a lane: one 16-byte chunk of a tile's row).
+template <int kTiles> struct Codes {
+    static constexpr int kSets = 16 / kTiles;        // groups of four keys
+    uint2 c[kSets][kTiles];
+    uint32_t s;    // scale bytes of two tiles: of key `lane`, or (four tiles) of key lane % 16, tiles 2 (lane / 16) and + 1
+};
+
+// Load keys row0 .. of sequence b, dims dim0 .. (row0: the warp's first key, may be negative:
+// rows before 0 give zeros).
+template <int kTiles>
+__device__ __forceinline__ void load_codes(const TcParams &p, int b, int row0, int dim0, int lane, Codes<kTiles> &x) {
+    constexpr int kKeysW = 4 * Codes<kTiles>::kSets;     // keys of the warp: 16 or 32
+    const int sub = lane & 7, kq = lane >> 3;
+    const int64_t row = (int64_t)b * p.L + row0;
+    const uint8_t *cp = p.c_q8 + (row + kq) * kDc + dim0 + 8 * sub;
+    const int sk = lane % kKeysW;
+    x.s = row0 + sk >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(p.c_scale + (row + sk) * (kDc / KDT_Q8_GROUP) + dim0 / KDT_Q8_GROUP) +
+                                 lane / kKeysW)
+                         : 0x7f7f7f7fu;
+#pragma unroll
+    for (int t = 0; t < Codes<kTiles>::kSets; ++t)
+#pragma unroll
+        for (int q = 0; q < kTiles; ++q)
+            x.c[t][q] = row0 + kq + 4 * t >= 0 ? __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc + 64 * q)) : make_uint2(0u, 0u);
+}
+
+// Widen and store: `dst` is the shared-memory address of the warp's first key's row in the first tile.
+template <int kTiles, bool kNanKeys>
+__device__ __forceinline__ void store_codes(const Codes<kTiles> &x, uint32_t dst, uint32_t tile_bytes, int lane) {
+    constexpr int kKeysW = 4 * Codes<kTiles>::kSets;
+    const int sub = lane & 7, kq = lane >> 3;
+    const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;
+    uint32_t byte[4], f[4];
+    bool high = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        byte[k] = (x.s >> (8 * k)) & 255u;
+        f[k] = kNanKeys && byte[k] == (uint32_t)q8::kNaN ? 0x7fc0u : q8::factor(byte[k]);
+        high |= byte[k] > q8::kHighByte && byte[k] != (uint32_t)q8::kNaN;
+    }
+    const uint32_t fa = f[0] | (f[1] << 16), fb = f[2] | (f[3] << 16);
+    // key kq + 4 t: swizzle (sub ^ key % 8), the same for all even t and for all odd t
+    const uint32_t d0 = dst + kq * 128 + ((sub ^ kq) << 4), d1 = d0 ^ 64u;
+#pragma unroll
+    for (int t = 0; t < Codes<kTiles>::kSets; ++t)
+#pragma unroll
+        for (int q = 0; q < kTiles; ++q) {
+            const uint32_t fk = __shfl_sync(0xffffffffu, (q & 1) ? fb : fa, 4 * t + kq + (q >> 1) * kKeysW);
+            const uint4 v = q8::widen8(x.c[t][q], __byte_perm(fk, 0u, pick));
+            st_shared_v4(((t & 1) ? d1 : d0) + 512 * t + q * tile_bytes, v.x, v.y, v.z, v.w);
+        }
+    if (__any_sync(0xffffffffu, high)) {                   // some scale above 2^7: a second product
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = byte[k] == (uint32_t)q8::kNaN ? 0x3f80u : q8::factor_high(byte[k]);
+        const uint32_t ha = h[0] | (h[1] << 16), hb = h[2] | (h[3] << 16);
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+            const int t = k / kTiles, q = k % kTiles;
+            const uint32_t fk = __byte_perm(__shfl_sync(0xffffffffu, (q & 1) ? hb : ha, 4 * t + kq + (q >> 1) * kKeysW), 0u, pick);
+            const uint32_t a = ((t & 1) ? d1 : d0) + 512 * t + q * tile_bytes;
+            uint32_t v[4];
+            ld_shared_v4(a, v);
+            st_shared_v4(a, q8::mul_bf16x2(v[0], fk), q8::mul_bf16x2(v[1], fk), q8::mul_bf16x2(v[2], fk), q8::mul_bf16x2(v[3], fk));
+        }
+    }
+}
+
+template <bool kQ8>
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     verify_tc_kernel(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs,
                      const __grid_constant__ CUtensorMap map_kpe, const __grid_constant__ CUtensorMap map_qpe,
                      const TcParams p) {
@@ -685,7 +786,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kNK; ++i) { mbar_init(&bar.kfull[i], 1); mbar_init(&bar.kempty[i], 1); }
+        constexpr int kFills = kQ8 ? 2 * kWidenWarps : 1;     // arrivals that fill a latent slot
+        for (int i = 0; i < kNK; ++i) { mbar_init(&bar.kfull[i], kFills); mbar_init(&bar.kempty[i], 1); }
         for (int i = 0; i < kNR; ++i) { mbar_init(&bar.rfull[i], 1); mbar_init(&bar.rempty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar.sfull[i], 1); mbar_init(&bar.sempty[i], 16); }
         mbar_init(&bar.qpe_full, 1);
@@ -702,7 +804,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&bar.staged[i][0], 4);
             mbar_init(&bar.staged[i][1], 4);
         }
-        for (int i = 0; i < kNV; ++i) { mbar_init(&bar.vfull[i], 1); mbar_init(&bar.vempty[i], 1); }
+        for (int i = 0; i < kNV; ++i) { mbar_init(&bar.vfull[i], kFills); mbar_init(&bar.vempty[i], 1); }
         mbar_init(&bar.go, 1);
         mbar_init(&bar.rescaled, 2);
         for (int i = 0; i < 2; ++i) {
@@ -734,10 +836,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     // Every role walks the same sequence of items of this cluster's work range; per-block
     // state (ring slots, buffers, parities) follows the cluster-wide block counter g.
     const int cl = blockIdx.x >> 2, ncl = gridDim.x >> 2;
-    const WorkIter w0 = {cl, bar.work_wleft, bar.work_u0, bar.work_kb0, bar.work_left, 0};
-    const int G = bar.work_count;                  // key blocks of this cluster
+    // (read where a role starts: kept across the register hand-over they would spill)
+    auto first_work = [&]() { return WorkIter{cl, bar.work_wleft, bar.work_u0, bar.work_kb0, bar.work_left, 0}; };
 
-    if (s_role) {
+    // Roles. Warps 0-3 issue, load and copy; 4-11 are softmax (S-CTA), correction and epilogue
+    // (O-CTA); 12-15 widen the 8-bit cache. (The outer branch is by warpgroup: a warpgroup changes
+    // its register share as one.)
+    if (warp < 4) {
+        if constexpr (kQ8) set_regs<kRegsQ8[0]>();
+        const int G = bar.work_count;                  // key blocks of this cluster
+        if (s_role) {
         // =============================== S-CTA ===============================
         unsigned char *qpe_tile = smem + kOffQpe;
         unsigned char *kring = smem + kOffKRing;
@@ -752,7 +860,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (elect_one() && G > 0) {
                 RingPos kr, rr;
                 bool going = true;
-                WorkIter w = w0;
+                WorkIter w = first_work();
                 Item it;
                 int ii = 0;
                 while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
@@ -784,7 +892,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                                     tma_prefetch_2d(&map_qpe, 0, (int)((int64_t)nx.b * p.rows_seq + r0 + k * kRows));
                             }
                         }
-                        for (int c = 0; c < kKChunks && going; ++c) {
+                        for (int c = 0; !kQ8 && c < kKChunks && going; ++c) {
                             if (kr.n >= kNK &&
                                 !(going = wait_or_abort(bar, &bar.kempty[kr.slot], kr.phase ^ 1, p.err, -2)))
                                 break;
@@ -808,7 +916,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int u = 0; u < kKChunks * G; ++u) ring_advance<kNK>(kr);
                     for (int u = 0; u < G; ++u) ring_advance<kNR>(rr);
                 }
-                ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
+                if (!kQ8) ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
                 ring_drain<kNR>(bar.rempty, rr, bar.wait_ns);
                 if (ii > 0) mbar_wait(&bar.qpe_empty, (uint32_t)(ii - 1) & 1, bar.wait_ns);
             }
@@ -826,7 +934,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 volatile int *seen_mine = &bar.kseen[par];
                 volatile int *seen_other = &bar.kseen[par ^ 1];
                 bool ok = true;
-                WorkIter w = w0;
+                WorkIter w = first_work();
                 Item it;
                 int ii = 0, g = 0;
                 while (ok && next_item(p, w, cl, ncl, it)) {
@@ -859,7 +967,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                                 }
                                 if (!ok) break;
                             }
-                            if (!(ok = wait_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5))) break;
+                            if (!(ok = kQ8 ? wait_cluster_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5)
+                                           : wait_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5)))
+                                break;
                             *seen_mine = u;
                             tc_fence_after();
                             KDT_TC_TRACE(kEvKFull, u);
@@ -875,7 +985,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                                     mma_ts_pair(d, acol + 32 * t + 8 * kk, bdesc0 + (uint64_t)((t * kKSub + kk * 32) >> 4),
                                                 idesc, (t > 0 || kk > 0) ? 1u : acc0);
                             KDT_TC_TRACE(kEvKIssued, u);
-                            mma_commit_pair(&bar.kempty[slot], kMaskAll);   // slot free: S-CTAs and their loaders
+                            mma_commit_pair(&bar.kempty[slot], kQ8 ? kMaskS : kMaskAll);   // slot free: S-CTAs and their loaders
                         }
                         if (!ok) break;
                         const int rslot = g % kNR;
@@ -915,7 +1025,211 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                 }
             }
-        } else if (warp >= 4) {
+        }
+        } else {
+        // =============================== O-CTA ===============================
+        unsigned char *pbase = smem + kOffP;
+        unsigned char *vbase = smem + kOffV;
+        if (warp == 0) {
+            // ------- TMA producer: this CTA's 128 of each 256 latent columns of V -------
+            // (8-bit cache: the widening warps fill the ring)
+            if (!kQ8 && elect_one() && G > 0) {
+                tma_prefetch_desc(&map_vs);
+                RingPos vr;
+                bool going = true;
+                WorkIter w = first_work();
+                Item it;
+                while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
+                    for (int j = 0; j < it.nb && going; ++j) {
+                        const int key0 = it.key_base + (it.kb0 + j) * kKeys;
+                        for (int h = 0; h < kVChunks; ++h) {
+                            if (vr.n >= kNV &&
+                                !(going = wait_or_abort(bar, &bar.vempty[vr.slot], vr.phase ^ 1, p.err, -8)))
+                                break;
+                            if (leader) mbar_arrive_expect_tx(&bar.vfull[vr.slot], 2 * kVSlotBytes);
+                            // chunk h of the pair spans 2 kVSubPerChunk sub-tiles of latent dims, the
+                            // first kVSubPerChunk from O-CTA 0, the rest from O-CTA 1: one request
+                            tma_load_4d_pair(vbase + vr.slot * kVSlotBytes, &map_vs, map_to_rank(&bar.vfull[vr.slot], lead_rank),
+                                             0, key0, (2 * h + kpair) * kVSubPerChunk, it.b);
+                            KDT_TC_TRACE(kEvVIssue, vr.n);
+                            ring_advance<kNV>(vr);
+                        }
+                    }
+                }
+                ring_drain<kNV>(bar.vempty, vr, bar.wait_ns);
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (leader): O += P V for 256 rows --------------------
+            if (leader && elect_one() && G > 0) {
+                const uint32_t idesc = idesc_bf16_f32(2 * kRows, 128 * kVSubPerChunk, 0, 1);
+                RingPos vr;
+                uint32_t rs_phase = 0, sync_phase = 0;
+                bool ok = true;
+                WorkIter w = first_work();
+                Item it;
+                int ii = 0, g = 0;
+                while (ok && next_item(p, w, cl, ncl, it)) {
+                    // the previous item's epilogue has read O out of tensor memory
+                    if (ii > 0 && !(ok = wait_cluster_or_abort(bar, &bar.o_free, (uint32_t)(ii - 1) & 1, p.err, -28)))
+                        break;
+                    KDT_TC_TRACE(kEvOFree, ii);
+                    for (int j = 0; j < it.nb && ok; ++j, ++g) {
+                        const int ps = g % kNP;
+                        if (!(ok = wait_cluster_or_abort(bar, &bar.pready[ps], (uint32_t)(g / kNP) & 1, p.err, -9))) break;
+                        KDT_TC_TRACE(kEvOMmaStart, g);
+                        const uint32_t n0 = *reinterpret_cast<volatile uint32_t *>(&bar.need[0][ps]);
+                        const uint32_t n1 = *reinterpret_cast<volatile uint32_t *>(&bar.need[1][ps]);
+                        if (n0 | n1) {
+                            // let every P.V issued so far finish, then hand O to the CTAs whose
+                            // rows need the rescale (the others count as done at once)
+                            mma_commit_pair(&bar.sync_bar, 0x4);
+                            if (!(ok = wait_or_abort(bar, &bar.sync_bar, sync_phase, p.err, -15))) break;
+                            sync_phase ^= 1;
+                            tc_fence_before();
+                            for (uint32_t k = 0; k < 2; ++k) {
+                                if (k == 0 ? n0 : n1) {
+                                    st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), (uint32_t)ps);
+                                    mbar_arrive_remote(&bar.go, 2 + k);      // release: command first
+                                } else {
+                                    mbar_arrive(&bar.rescaled);
+                                }
+                            }
+                            if (!(ok = wait_cluster_or_abort(bar, &bar.rescaled, rs_phase, p.err, -16))) break;
+                            rs_phase ^= 1;
+                        }
+                        tc_fence_after();
+                        const uint64_t adesc0 = sdesc_sw128(smem_u32(pbase + ps * kPSlotBytes), 16, 1024);
+                        const uint32_t acc0 = j > 0 ? 1u : 0u;
+                        for (int h = 0; h < kVChunks; ++h) {
+                            if (!(ok = kQ8 ? wait_cluster_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10)
+                                           : wait_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10)))
+                                break;
+                            tc_fence_after();
+                            KDT_TC_TRACE(kEvVFull, vr.n);
+                            const uint64_t bdesc0 = sdesc_sw128(smem_u32(vbase + vr.slot * kVSlotBytes), kVSub, 1024);
+                            const uint32_t dcol = tmem + 128 * kVSubPerChunk * h;
+#pragma unroll
+                            for (int kk = 0; kk < kKeys / 16; ++kk)   // the item's first block starts O afresh
+                                mma_ss_pair(dcol, adesc0 + (uint64_t)(((kk >> 2) * (kPBytes / 2) + (kk & 3) * 32) >> 4),
+                                            bdesc0 + (uint64_t)((kk * 2048) >> 4), idesc, kk > 0 ? 1u : acc0);
+                            mma_commit_pair(&bar.vempty[vr.slot], kMaskO);   // slot free in both O-CTAs
+                            ring_advance<kNV>(vr);
+                        }
+                        if (!ok) break;
+                        KDT_TC_TRACE(kEvOMmaIssued, g);
+                        // P slot ps of both O-CTAs is free again: tell both S-CTAs
+                        mma_commit_pair(&bar.pempty[ps], kMaskS);
+                    }
+                    if (!ok) break;
+                    // the item's P.V is complete once this arrives; the epilogues then read O
+                    mma_commit_pair(&bar.o_done, kMaskO);
+                    for (uint32_t k = 0; k < 2; ++k) {   // end the correction loop of this item
+                        st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), kCmdDone);
+                        mbar_arrive_remote(&bar.go, 2 + k);
+                    }
+                    ++ii;
+                }
+                if (!ok) {   // release the correction warps of an item left unfinished
+                    for (uint32_t k = 0; k < 2; ++k) {
+                        st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), kCmdDone);
+                        mbar_arrive_remote(&bar.go, 2 + k);
+                    }
+                }
+                drain_mmas(bar, kMaskO);
+            }
+        } else if (warp == 3) {
+            // ------- key loader: S-CTA k's half of each key block, into its shared memory -------
+            // Multicast to that one CTA with pair semantics: the bytes complete on the S
+            // leader's barrier, which counts both S-CTAs' halves.
+            if (elect_one() && G > 0) {
+                if (!kQ8) tma_prefetch_desc(&map_ks);
+                tma_prefetch_desc(&map_kpe);
+                const uint16_t dst_mask = (uint16_t)(1u << kpair);
+                unsigned char *kring = smem + kOffKRing;     // same offsets as in the S-CTA
+                unsigned char *rring = smem + kOffRRing;
+                RingPos kr, rr;
+                bool going = true;
+                // L2 prefetch cursor, kKvPrefetchBlocks blocks ahead of the loads: the clusters
+                // on one sequence ask for each block at about the same time, so without it every
+                // one of them waits for the same DRAM fetch
+                WorkIter wp = first_work();
+                Item ip;
+                int jp = 0;
+                bool pf = next_item(p, wp, cl, ncl, ip);
+                auto prefetch_block = [&]() {
+                    if (!pf) return;
+                    const int pk0 = ip.key_base + (ip.kb0 + jp) * kKeys + kpair * kHalfKeys;
+                    if (kQ8) {
+                        const int lo = max(pk0, 0), n = pk0 + kHalfKeys - lo;    // the leading block may start before row 0
+                        if (n > 0) {
+                            const int64_t row = (int64_t)ip.b * p.L + lo;
+                            prefetch_l2_bulk(p.c_q8 + row * kDc, (uint32_t)n * kDc);
+                            prefetch_l2_bulk(p.c_scale + row * (kDc / KDT_Q8_GROUP), (uint32_t)n * (kDc / KDT_Q8_GROUP));
+                        }
+                    } else {
+                        for (int c = 0; c < kKChunks; ++c) tma_prefetch_4d(&map_ks, 0, pk0, kKSubPerChunk * c, ip.b);
+                    }
+                    tma_prefetch_3d(&map_kpe, 0, pk0, ip.b);
+                    if (++jp == ip.nb) {
+                        jp = 0;
+                        pf = next_item(p, wp, cl, ncl, ip);
+                    }
+                };
+                for (int k = 0; k < kKvPrefetchBlocks; ++k) prefetch_block();
+                WorkIter w = first_work();
+                Item it;
+                while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
+                    for (int j = 0; j < it.nb && going; ++j) {
+                        prefetch_block();
+                        const int key0 = it.key_base + (it.kb0 + j) * kKeys + kpair * kHalfKeys;   // S-CTA k's 64 keys
+                        for (int c = 0; !kQ8 && c < kKChunks && going; ++c) {   // latent sub-tiles [kKSubPerChunk c, +kKSubPerChunk)
+                            if (kr.n >= kNK &&
+                                !(going = wait_or_abort(bar, &bar.kempty[kr.slot], kr.phase ^ 1, p.err, -21)))
+                                break;
+                            tma_load_4d_pair_mc(kring + kr.slot * kKSlotBytes, &map_ks,
+                                                map_to_rank(&bar.kfull[kr.slot], 0), 0, key0, kKSubPerChunk * c, it.b, dst_mask);
+                            KDT_TC_TRACE(kEvKIssue, kr.n);
+                            ring_advance<kNK>(kr);
+                        }
+                        if (!going) break;
+                        if (rr.n >= kNR &&
+                            !(going = wait_or_abort(bar, &bar.rempty[rr.slot], rr.phase ^ 1, p.err, -21)))
+                            break;
+                        tma_load_3d_pair_mc(rring + rr.slot * kKSub, &map_kpe, map_to_rank(&bar.rfull[rr.slot], 0), 0,
+                                            key0, it.b, dst_mask);
+                        ring_advance<kNR>(rr);
+                    }
+                }
+                // every copy this CTA issued has landed and been read before it may exit
+                if (!kQ8) ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
+                ring_drain<kNR>(bar.rempty, rr, bar.wait_ns);
+            }
+        } else if (warp == 2) {
+            // ---------------- P watcher: P of each block landed, and does O need a rescale? --
+            for (int g = 0; g < G; ++g) {
+                const int ps = g % kNP;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.pfull[ps], kPTx);   // P + alpha of block g
+                if (!warp_wait(bar, &bar.pfull[ps], (uint32_t)(g / kNP) & 1, p.err, -11)) break;
+                if (lane == 0) KDT_TC_TRACE(kEvCorrIn, g);
+                // factors other than 1 only occur once a row has a running maximum, i.e. not in
+                // the first block of an item, whose P.V starts O afresh
+                const float4 a4 = reinterpret_cast<const float4 *>(pbase + ps * kPSlotBytes + kPBytes)[lane];
+                const bool need = __any_sync(0xffffffffu, a4.x != 1.f || a4.y != 1.f || a4.z != 1.f || a4.w != 1.f);
+                if (lane == 0) {
+                    mbar_arrive_remote_cta(&bar.sfree[g % kNS], (uint32_t)kpair);   // its staging slot is reusable
+                    st_cluster_u32(map_to_rank(&bar.need[kpair][ps], lead_rank), need ? 1u : 0u);
+                    mbar_arrive_remote(&bar.pready[ps], lead_rank);                 // release: flag first
+                }
+                __syncwarp();
+            }
+        }
+        }
+    } else if (!kQ8 || warp < 12) {
+        if constexpr (kQ8) set_regs<kRegsQ8[1]>();
+        const int G = bar.work_count;                  // key blocks of this cluster
+        if (s_role) {
+        const uint32_t tmem_q = tmem;                 // Q_nope: columns [0, 256)
+        const uint32_t tmem_s0 = tmem + 256;          // score buffers at 256 and 384
             // ---------------- per item: Q_nope -> TMEM, softmax, statistics -----------------
             // Eight warps: warp w serves the 32 rows of TMEM lane quadrant (w % 4); warps 4-7
             // take keys 0..63 of each block, warps 8-11 keys 64..127.
@@ -942,10 +1256,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t wq[32];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            wq[4 * k] = v[8 * h + k].x;
-                            wq[4 * k + 1] = v[8 * h + k].y;
-                            wq[4 * k + 2] = v[8 * h + k].z;
-                            wq[4 * k + 3] = v[8 * h + k].w;
+                            const uint4 e = kQ8 ? q8::reorder8(v[8 * h + k]) : v[8 * h + k];
+                            wq[4 * k] = e.x;
+                            wq[4 * k + 1] = e.y;
+                            wq[4 * k + 2] = e.z;
+                            wq[4 * k + 3] = e.w;
                         }
                         tmem_st32(tmem_lane_addr(tmem_q, warp, (4 * half + 2 * r2 + h) * 32), wq);
                     }
@@ -955,7 +1270,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0 && !withhold) mbar_arrive_remote_cta(&bar.q_ready, lead_rank);
             };
-            WorkIter w = w0;
+            WorkIter w = first_work();
             Item it;
             int ii = 0, g = 0;
             bool have = next_item(p, w, cl, ncl, it);
@@ -1037,8 +1352,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                         unsigned char *slot_base = smem + kOffPStage + ss * kPSlotBytes;
                         unsigned char *stage_row = slot_base + half * (kPBytes / 2) + row * 128;
                         // an all-visible half has finite scores, so m_run is finite here
-                        l_run += masked ? stage_p_row<true>(x, p.scale_log2, m_run, stage_row, row)
-                                        : stage_p_row<false>(x, p.scale_log2, m_run, stage_row, row);
+                        l_run += masked ? stage_p_row<true, kQ8>(x, p.scale_log2, m_run, stage_row, row)
+                                        : stage_p_row<false, kQ8>(x, p.scale_log2, m_run, stage_row, row);
                         // the rescale factors follow the second half of P, which carries them
                         if (half == 1) reinterpret_cast<float *>(slot_base + kPBytes)[row] = alpha;
                         fence_proxy_async_smem();                  // staging visible to the copy engine
@@ -1097,193 +1412,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = warp_wait(bar, &bar.stats_empty[sb], (uint32_t)(i_last >> 1) & 1, p.err, -27) && ok;
                 }
             }
-        }
-    } else {
-        // =============================== O-CTA ===============================
+        } else if (warp < 4 + kEpiWarps) {
         unsigned char *pbase = smem + kOffP;
-        unsigned char *vbase = smem + kOffV;
         const float2 *stats_s = reinterpret_cast<const float2 *>(smem + kOffStats);
-        if (warp == 0) {
-            // ------- TMA producer: this CTA's 128 of each 256 latent columns of V -------
-            if (elect_one() && G > 0) {
-                tma_prefetch_desc(&map_vs);
-                RingPos vr;
-                bool going = true;
-                WorkIter w = w0;
-                Item it;
-                while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
-                    for (int j = 0; j < it.nb && going; ++j) {
-                        const int key0 = it.key_base + (it.kb0 + j) * kKeys;
-                        for (int h = 0; h < kVChunks; ++h) {
-                            if (vr.n >= kNV &&
-                                !(going = wait_or_abort(bar, &bar.vempty[vr.slot], vr.phase ^ 1, p.err, -8)))
-                                break;
-                            if (leader) mbar_arrive_expect_tx(&bar.vfull[vr.slot], 2 * kVSlotBytes);
-                            // chunk h of the pair spans 2 kVSubPerChunk sub-tiles of latent dims, the
-                            // first kVSubPerChunk from O-CTA 0, the rest from O-CTA 1: one request
-                            tma_load_4d_pair(vbase + vr.slot * kVSlotBytes, &map_vs, map_to_rank(&bar.vfull[vr.slot], lead_rank),
-                                             0, key0, (2 * h + kpair) * kVSubPerChunk, it.b);
-                            KDT_TC_TRACE(kEvVIssue, vr.n);
-                            ring_advance<kNV>(vr);
-                        }
-                    }
-                }
-                ring_drain<kNV>(bar.vempty, vr, bar.wait_ns);
-            }
-        } else if (warp == 1) {
-            // ---------------- MMA issuer (leader): O += P V for 256 rows --------------------
-            if (leader && elect_one() && G > 0) {
-                const uint32_t idesc = idesc_bf16_f32(2 * kRows, 128 * kVSubPerChunk, 0, 1);
-                RingPos vr;
-                uint32_t rs_phase = 0, sync_phase = 0;
-                bool ok = true;
-                WorkIter w = w0;
-                Item it;
-                int ii = 0, g = 0;
-                while (ok && next_item(p, w, cl, ncl, it)) {
-                    // the previous item's epilogue has read O out of tensor memory
-                    if (ii > 0 && !(ok = wait_cluster_or_abort(bar, &bar.o_free, (uint32_t)(ii - 1) & 1, p.err, -28)))
-                        break;
-                    KDT_TC_TRACE(kEvOFree, ii);
-                    for (int j = 0; j < it.nb && ok; ++j, ++g) {
-                        const int ps = g % kNP;
-                        if (!(ok = wait_cluster_or_abort(bar, &bar.pready[ps], (uint32_t)(g / kNP) & 1, p.err, -9))) break;
-                        KDT_TC_TRACE(kEvOMmaStart, g);
-                        const uint32_t n0 = *reinterpret_cast<volatile uint32_t *>(&bar.need[0][ps]);
-                        const uint32_t n1 = *reinterpret_cast<volatile uint32_t *>(&bar.need[1][ps]);
-                        if (n0 | n1) {
-                            // let every P.V issued so far finish, then hand O to the CTAs whose
-                            // rows need the rescale (the others count as done at once)
-                            mma_commit_pair(&bar.sync_bar, 0x4);
-                            if (!(ok = wait_or_abort(bar, &bar.sync_bar, sync_phase, p.err, -15))) break;
-                            sync_phase ^= 1;
-                            tc_fence_before();
-                            for (uint32_t k = 0; k < 2; ++k) {
-                                if (k == 0 ? n0 : n1) {
-                                    st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), (uint32_t)ps);
-                                    mbar_arrive_remote(&bar.go, 2 + k);      // release: command first
-                                } else {
-                                    mbar_arrive(&bar.rescaled);
-                                }
-                            }
-                            if (!(ok = wait_cluster_or_abort(bar, &bar.rescaled, rs_phase, p.err, -16))) break;
-                            rs_phase ^= 1;
-                        }
-                        tc_fence_after();
-                        const uint64_t adesc0 = sdesc_sw128(smem_u32(pbase + ps * kPSlotBytes), 16, 1024);
-                        const uint32_t acc0 = j > 0 ? 1u : 0u;
-                        for (int h = 0; h < kVChunks; ++h) {
-                            if (!(ok = wait_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10))) break;
-                            tc_fence_after();
-                            KDT_TC_TRACE(kEvVFull, vr.n);
-                            const uint64_t bdesc0 = sdesc_sw128(smem_u32(vbase + vr.slot * kVSlotBytes), kVSub, 1024);
-                            const uint32_t dcol = tmem + 128 * kVSubPerChunk * h;
-#pragma unroll
-                            for (int kk = 0; kk < kKeys / 16; ++kk)   // the item's first block starts O afresh
-                                mma_ss_pair(dcol, adesc0 + (uint64_t)(((kk >> 2) * (kPBytes / 2) + (kk & 3) * 32) >> 4),
-                                            bdesc0 + (uint64_t)((kk * 2048) >> 4), idesc, kk > 0 ? 1u : acc0);
-                            mma_commit_pair(&bar.vempty[vr.slot], kMaskO);   // slot free in both O-CTAs
-                            ring_advance<kNV>(vr);
-                        }
-                        if (!ok) break;
-                        KDT_TC_TRACE(kEvOMmaIssued, g);
-                        // P slot ps of both O-CTAs is free again: tell both S-CTAs
-                        mma_commit_pair(&bar.pempty[ps], kMaskS);
-                    }
-                    if (!ok) break;
-                    // the item's P.V is complete once this arrives; the epilogues then read O
-                    mma_commit_pair(&bar.o_done, kMaskO);
-                    for (uint32_t k = 0; k < 2; ++k) {   // end the correction loop of this item
-                        st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), kCmdDone);
-                        mbar_arrive_remote(&bar.go, 2 + k);
-                    }
-                    ++ii;
-                }
-                if (!ok) {   // release the correction warps of an item left unfinished
-                    for (uint32_t k = 0; k < 2; ++k) {
-                        st_cluster_u32(map_to_rank(&bar.cmd, 2 + k), kCmdDone);
-                        mbar_arrive_remote(&bar.go, 2 + k);
-                    }
-                }
-                drain_mmas(bar, kMaskO);
-            }
-        } else if (warp == 3) {
-            // ------- key loader: S-CTA k's half of each key block, into its shared memory -------
-            // Multicast to that one CTA with pair semantics: the bytes complete on the S
-            // leader's barrier, which counts both S-CTAs' halves.
-            if (elect_one() && G > 0) {
-                tma_prefetch_desc(&map_ks);
-                tma_prefetch_desc(&map_kpe);
-                const uint16_t dst_mask = (uint16_t)(1u << kpair);
-                unsigned char *kring = smem + kOffKRing;     // same offsets as in the S-CTA
-                unsigned char *rring = smem + kOffRRing;
-                RingPos kr, rr;
-                bool going = true;
-                // L2 prefetch cursor, kKvPrefetchBlocks blocks ahead of the loads: the clusters
-                // on one sequence ask for each block at about the same time, so without it every
-                // one of them waits for the same DRAM fetch
-                WorkIter wp = w0;
-                Item ip;
-                int jp = 0;
-                bool pf = next_item(p, wp, cl, ncl, ip);
-                auto prefetch_block = [&]() {
-                    if (!pf) return;
-                    const int pk0 = ip.key_base + (ip.kb0 + jp) * kKeys + kpair * kHalfKeys;
-                    for (int c = 0; c < kKChunks; ++c) tma_prefetch_4d(&map_ks, 0, pk0, kKSubPerChunk * c, ip.b);
-                    tma_prefetch_3d(&map_kpe, 0, pk0, ip.b);
-                    if (++jp == ip.nb) {
-                        jp = 0;
-                        pf = next_item(p, wp, cl, ncl, ip);
-                    }
-                };
-                for (int k = 0; k < kKvPrefetchBlocks; ++k) prefetch_block();
-                WorkIter w = w0;
-                Item it;
-                while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
-                    for (int j = 0; j < it.nb && going; ++j) {
-                        prefetch_block();
-                        const int key0 = it.key_base + (it.kb0 + j) * kKeys + kpair * kHalfKeys;   // S-CTA k's 64 keys
-                        for (int c = 0; c < kKChunks && going; ++c) {   // latent sub-tiles [kKSubPerChunk c, +kKSubPerChunk)
-                            if (kr.n >= kNK &&
-                                !(going = wait_or_abort(bar, &bar.kempty[kr.slot], kr.phase ^ 1, p.err, -21)))
-                                break;
-                            tma_load_4d_pair_mc(kring + kr.slot * kKSlotBytes, &map_ks,
-                                                map_to_rank(&bar.kfull[kr.slot], 0), 0, key0, kKSubPerChunk * c, it.b, dst_mask);
-                            KDT_TC_TRACE(kEvKIssue, kr.n);
-                            ring_advance<kNK>(kr);
-                        }
-                        if (!going) break;
-                        if (rr.n >= kNR &&
-                            !(going = wait_or_abort(bar, &bar.rempty[rr.slot], rr.phase ^ 1, p.err, -21)))
-                            break;
-                        tma_load_3d_pair_mc(rring + rr.slot * kKSub, &map_kpe, map_to_rank(&bar.rfull[rr.slot], 0), 0,
-                                            key0, it.b, dst_mask);
-                        ring_advance<kNR>(rr);
-                    }
-                }
-                // every copy this CTA issued has landed and been read before it may exit
-                ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
-                ring_drain<kNR>(bar.rempty, rr, bar.wait_ns);
-            }
-        } else if (warp == 2) {
-            // ---------------- P watcher: P of each block landed, and does O need a rescale? --
-            for (int g = 0; g < G; ++g) {
-                const int ps = g % kNP;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.pfull[ps], kPTx);   // P + alpha of block g
-                if (!warp_wait(bar, &bar.pfull[ps], (uint32_t)(g / kNP) & 1, p.err, -11)) break;
-                if (lane == 0) KDT_TC_TRACE(kEvCorrIn, g);
-                // factors other than 1 only occur once a row has a running maximum, i.e. not in
-                // the first block of an item, whose P.V starts O afresh
-                const float4 a4 = reinterpret_cast<const float4 *>(pbase + ps * kPSlotBytes + kPBytes)[lane];
-                const bool need = __any_sync(0xffffffffu, a4.x != 1.f || a4.y != 1.f || a4.z != 1.f || a4.w != 1.f);
-                if (lane == 0) {
-                    mbar_arrive_remote_cta(&bar.sfree[g % kNS], (uint32_t)kpair);   // its staging slot is reusable
-                    st_cluster_u32(map_to_rank(&bar.need[kpair][ps], lead_rank), need ? 1u : 0u);
-                    mbar_arrive_remote(&bar.pready[ps], lead_rank);                 // release: flag first
-                }
-                __syncwarp();
-            }
-        } else if (warp >= 4 && warp < 4 + kEpiWarps) {
             // ---------------- correction (rare rescale) and epilogue, per item ----------------
             // Warp w serves the 32 rows of TMEM lane quadrant (w % 4) and the columns
             // [col0, col0 + kEpiGroupCols); named barrier 1 counts these warps. They sleep on
@@ -1292,7 +1423,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const int col0 = ((warp - 4) >> 2) * kEpiGroupCols;
             bool ok = true;
             uint32_t e = 0;                                     // `go` events so far
-            WorkIter w = w0;
+            WorkIter w = first_work();
             Item it;
             int ii = 0;
             while (ok && next_item(p, w, cl, ncl, it)) {
@@ -1339,6 +1470,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int R = (it.rt0 + kpair) * kRows + row;
                 const int64_t grow = (int64_t)it.b * p.rows_seq + R;
+                const bool b16 = kQ8 && it.whole && p.out_bf16;   // final rows in bf16 (orow unused then)
                 float *orow, *lrow;
                 if (it.whole) {
                     orow = p.out + grow * kDc;
@@ -1349,7 +1481,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     lrow = p.part_lse + k;
                 }
                 const float2 st = stats_s[sb * kRows + row];
-                const float inv = st.y > 0.f ? 1.f / st.y : 0.f;
+                const float inv = kQ8 ? (st.y == 0.f ? 0.f : 1.f / st.y)      // (a NaN goes on)
+                                      : (st.y > 0.f ? 1.f / st.y : 0.f);
                 // Each thread holds one row; the rows go out through a per-warp transpose in
                 // shared memory so that every store instruction writes whole 32-byte sectors
                 // (eight rows x 64 bytes). 16-byte slot q of staged row r sits at
@@ -1367,24 +1500,33 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q) {
+                            constexpr int k1 = kQ8 ? 2 : 1, k2 = kQ8 ? 1 : 2;      // widening's order of the dims
                             *reinterpret_cast<float4 *>(stg + lane * kEpiCols + ((q ^ ((lane >> 1) & 3)) << 2)) =
-                                make_float4(__uint_as_float(r[16 * hh + 4 * q]) * inv, __uint_as_float(r[16 * hh + 4 * q + 1]) * inv,
-                                            __uint_as_float(r[16 * hh + 4 * q + 2]) * inv,
+                                make_float4(__uint_as_float(r[16 * hh + 4 * q]) * inv, __uint_as_float(r[16 * hh + 4 * q + k1]) * inv,
+                                            __uint_as_float(r[16 * hh + 4 * q + k2]) * inv,
                                             __uint_as_float(r[16 * hh + 4 * q + 3]) * inv);
+                        }
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int rr = 8 * i + rsub;
                             const float4 v =
                                 *reinterpret_cast<const float4 *>(stg + rr * kEpiCols + ((qsub ^ ((rr >> 1) & 3)) << 2));
-                            if (rr < rows_ok)
-                                *reinterpret_cast<float4 *>(orow0 + (int64_t)rr * kDc + c * 32 + hh * 16 + 4 * qsub) = v;
+                            if (rr < rows_ok) {
+                                if (kQ8 && b16)
+                                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) +
+                                                               (grow - lane + rr) * kDc + col0 + c * 32 + hh * 16 + 4 * qsub) =
+                                        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                                else
+                                    *reinterpret_cast<float4 *>(orow0 + (int64_t)rr * kDc + c * 32 + hh * 16 + 4 * qsub) = v;
+                            }
                         }
                         __syncwarp();
                     }
                 }
-                if (col0 == 0 && R < p.rows_seq && lrow) *lrow = st.y > 0.f ? 0.6931471805599453f * (st.x + log2f(st.y)) : -INFINITY;
+                if (col0 == 0 && R < p.rows_seq && lrow)
+                    *lrow = (kQ8 ? st.y != 0.f : st.y > 0.f) ? 0.6931471805599453f * (st.x + log2f(st.y)) : -INFINITY;
                 // O may be overwritten and the statistics buffer refilled
                 tc_fence_before();
                 __syncwarp();
@@ -1395,6 +1537,61 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvEpiOut, ii);
                 ++ii;
             }
+        }
+    } else {
+        if constexpr (kQ8) {
+        set_regs<kRegsQ8[3]>();
+        // ---------------- widening: this CTA's half of every latent chunk -----------------------
+        const int ww = warp - 12;
+        unsigned char *ring = smem + (s_role ? kOffKRing : kOffV);
+        WorkIter w = first_work();
+        Item it;
+        if (s_role) {      // chunk c of a block: its 64 keys x dims 256 c .. + 256, four [64 x 64] tiles
+            Codes<4> x;
+            RingPos r;
+            bool have = next_item(p, w, cl, ncl, it), ok = true;
+            auto load = [&](int j, int c) {
+                load_codes(p, it.b, it.key_base + (it.kb0 + j) * kKeys + kpair * kHalfKeys + 16 * ww, 256 * c, lane, x);
+            };
+            if (have) load(0, 0);
+            while (have && ok) {
+                const int nb = it.nb;
+                for (int k = 0; k < kKChunks * nb && ok; ++k) {
+                    if (r.n >= kNK && !(ok = warp_wait(bar, &bar.kempty[r.slot], r.phase ^ 1, p.err, -30))) break;
+                    store_codes<4, true>(x, smem_u32(ring + r.slot * kKSlotBytes) + 16 * ww * 128, kKSub, lane);
+                    fence_proxy_async_all();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(&bar.kfull[r.slot], lead_rank);
+                    ring_advance<kNK>(r);
+                    if (k + 1 < kKChunks * nb) load((k + 1) / kKChunks, (k + 1) % kKChunks);
+                    else if ((have = next_item(p, w, cl, ncl, it))) load(0, 0);
+                }
+            }
+            // the releases of the last chunks have arrived before this CTA may leave
+            if (ok) ring_drain<kNK>(bar.kempty, r, bar.wait_ns);
+        } else {           // chunk h of a block: 128 keys x this CTA's 128 dims, two [128 x 64] tiles
+            Codes<2> x;
+            RingPos r;
+            bool have = next_item(p, w, cl, ncl, it), ok = true;
+            auto load = [&](int j, int h) {
+                load_codes(p, it.b, it.key_base + (it.kb0 + j) * kKeys + 32 * ww, (2 * h + kpair) * 64 * kVSubPerChunk, lane, x);
+            };
+            if (have) load(0, 0);
+            while (have && ok) {
+                const int nb = it.nb;
+                for (int k = 0; k < kVChunks * nb && ok; ++k) {
+                    if (r.n >= kNV && !(ok = warp_wait(bar, &bar.vempty[r.slot], r.phase ^ 1, p.err, -31))) break;
+                    store_codes<2, false>(x, smem_u32(ring + r.slot * kVSlotBytes) + 32 * ww * 128, kVSub, lane);
+                    fence_proxy_async_all();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(&bar.vfull[r.slot], lead_rank);
+                    ring_advance<kNV>(r);
+                    if (k + 1 < kVChunks * nb) load((k + 1) / kVChunks, (k + 1) % kVChunks);
+                    else if ((have = next_item(p, w, cl, ncl, it))) load(0, 0);
+                }
+            }
+            if (ok) ring_drain<kNV>(bar.vempty, r, bar.wait_ns);
+        }
         }
     }
 
@@ -1421,6 +1618,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 // the unit's 256 (one warp per row, 16 columns per lane): the normalised partial states
 // (o_k, lse_k) of the pieces combine exactly as the log-sum-exp merge of disjoint key
 // sets, o = sum_k e^(lse_k - M) o_k / sum_k e^(lse_k - M) with M the largest lse_k.
+template <bool kQ8>
 __global__ void __launch_bounds__(256) merge_pieces_kernel(const TcParams p, int C) {
     __shared__ int s_valid, s_n, s_b, s_rt0;
     __shared__ int s_slot[kMaxClusters + 1];
@@ -1474,8 +1672,10 @@ __global__ void __launch_bounds__(256) merge_pieces_kernel(const TcParams p, int
     // their rows of o weighted and summed (independent loads)
     const int n = s_n;
     float M = -INFINITY;
+    bool nan = false;                                         // some piece of the row is NaN (8-bit cache)
     for (int base = 0; base < n; base += 32) {
         const float l = base + lane < n ? p.part_lse[(int64_t)s_slot[base + lane] * (2 * kRows) + r] : -INFINITY;
+        if (kQ8) nan |= __any_sync(0xffffffffu, l != l);
         float m = l;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -1507,13 +1707,23 @@ __global__ void __launch_bounds__(256) merge_pieces_kernel(const TcParams p, int
             }
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (kQ8 && nan) sum = __uint_as_float(0x7fffffffu);
+    const bool some = kQ8 ? sum != 0.f : sum > 0.f;
+    const float inv = some ? 1.f / sum : 0.f;
     const int64_t grow = (int64_t)s_b * p.rows_seq + R;
-    float4 *dst = reinterpret_cast<float4 *>(p.out + grow * kDc);
+    if (kQ8 && p.out_bf16) {
+        uint2 *dst = reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + grow * kDc);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        dst[lane + 32 * q] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
-    if (lane == 0 && p.lse) p.lse[grow] = sum > 0.f ? M + logf(sum) : -INFINITY;
+        for (int q = 0; q < 4; ++q)
+            dst[lane + 32 * q] =
+                make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
+    } else {
+        float4 *dst = reinterpret_cast<float4 *>(p.out + grow * kDc);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            dst[lane + 32 * q] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+    }
+    if (lane == 0 && p.lse) p.lse[grow] = some ? M + logf(sum) : -INFINITY;
 }
 
 }  // namespace
@@ -1521,7 +1731,9 @@ __global__ void __launch_bounds__(256) merge_pieces_kernel(const TcParams p, int
 int tc_rows_per_unit() { return 2 * kRows; }
 int tc_keys_per_block() { return kKeys; }
 
-int tc_max_clusters() {
+namespace {
+
+template <bool kQ8> int max_clusters() {
     static std::atomic<int> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return sm_count() / 4 > 0 ? sm_count() / 4 : 1;
@@ -1530,7 +1742,7 @@ int tc_max_clusters() {
     if (n > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kQ8 ? kThreadsQ8 : kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1539,8 +1751,8 @@ int tc_max_clusters() {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(verify_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, verify_tc_kernel, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, verify_tc_kernel<kQ8>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();    // clear the query's error; plan with the SM count instead
         const int f = sm_count() / 4;
         return f < 1 ? 1 : (f > kMaxClusters ? kMaxClusters : f);
@@ -1549,6 +1761,11 @@ int tc_max_clusters() {
     cached[slot].store(n, std::memory_order_relaxed);
     return n;
 }
+
+}  // namespace
+
+int tc_max_clusters() { return max_clusters<false>(); }
+int tc_q8_max_clusters() { return max_clusters<true>(); }
 
 namespace {
 
@@ -1585,10 +1802,12 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims
 }  // namespace
 
 
-cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) {
+namespace {
+
+template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
     CUtensorMap map_ks, map_vs, map_kpe, map_qpe;
     const cuuint64_t L = (cuuint64_t)vp.L;
-    {
+    if (!kQ8) {
         // c_kv viewed as [B][8 dim-blocks][L keys][64]: a box of (64, n keys, m blocks)
         // lands as m consecutive [n x 64] 128B-swizzled sub-tiles.
         cuuint64_t dims[4] = {64, L, (cuuint64_t)(kDc / 64), (cuuint64_t)vp.B};
@@ -1603,6 +1822,7 @@ cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) {
         cuuint64_t strides[2] = {(cuuint64_t)kDr * 2, L * kDr * 2};
         cuuint32_t box[3] = {64, kHalfKeys, 1};
         if (!make_map(&map_kpe, vp.k_pe, 3, dims, strides, box)) return cudaErrorInvalidValue;
+        if (kQ8) map_ks = map_vs = map_kpe;                        // unused: the latents come through registers
     }
     {
         cuuint64_t dims[2] = {(cuuint64_t)kDr, (cuuint64_t)vp.rows_total};
@@ -1632,9 +1852,13 @@ cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) {
     p.wait_ns = vp.wait_ns ? vp.wait_ns : kWaitLimit;
     p.fault = vp.fault;
     p.sched = vp.tc_sched;
+    p.c_q8 = static_cast<const uint8_t *>(vp.c_kv);
+    p.c_scale = vp.c_scale;
+    p.L = vp.L;
+    p.out_bf16 = vp.out_bf16;
     const int C = vp.tc_clusters;
     if (C < 1 || C > kMaxClusters || (C > 1 && (!p.part_o || !p.part_lse || !p.sched))) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // Programmatic dependent launch: this kernel overlaps the visibility kernel launched
     // just before it in the same call (it waits for it before reading the bits), and the
@@ -1644,12 +1868,12 @@ cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) {
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(4 * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kQ8 ? kThreadsQ8 : kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = vp.overlap_vis ? 1 : 0;
-    if ((e = cudaLaunchKernelEx(&cfg, verify_tc_kernel, map_ks, map_vs, map_kpe, map_qpe, p)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, verify_tc_kernel<kQ8>, map_ks, map_vs, map_kpe, map_qpe, p)) != cudaSuccess) return e;
     if (C > 1) {
         cudaLaunchConfig_t mc = {};
         mc.gridDim = dim3((unsigned)(C - 1), 2 * kRows / 8);
@@ -1657,9 +1881,14 @@ cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) {
         mc.stream = s;
         mc.attrs = pdl;
         mc.numAttrs = 1;
-        e = cudaLaunchKernelEx(&mc, merge_pieces_kernel, p, C);
+        e = cudaLaunchKernelEx(&mc, merge_pieces_kernel<kQ8>, p, C);
     }
     return e;
 }
+
+}  // namespace
+
+cudaError_t launch_verify_tc(const VerifyParams &vp, cudaStream_t s) { return launch<false>(vp, s); }
+cudaError_t launch_verify_tc_q8(const VerifyParams &vp, cudaStream_t s) { return launch<true>(vp, s); }
 
 }  // namespace kdt

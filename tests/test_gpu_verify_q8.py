@@ -100,7 +100,8 @@ CASES = [(1, 1, [0]), (1, 64, [0, 1, 126, 127, 128, 129, 1000]), (9, 8, [37, 37]
          (33, 3, [65, 600]), (64, 64, [200]), (70, 1, [130, 0]), (1, 128, [9000]), (2, 1024, [70])]
 
 
-@pytest.mark.parametrize("impl,splits", [("auto", 0), ("q8_rows", 0), ("q8_rows", 1), ("q8_rows", 5)])
+@pytest.mark.parametrize("impl,splits", [("auto", 0), ("q8_rows", 0), ("q8_rows", 1), ("q8_rows", 5), ("tcgen05", 0),
+                                         ("tcgen05", 1), ("tcgen05", 3)])
 @pytest.mark.parametrize("T,H,prefix", CASES)
 def test_parity(kdt, T, H, prefix, impl, splits):
     import torch
@@ -110,7 +111,7 @@ def test_parity(kdt, T, H, prefix, impl, splits):
     _check(d, got, 2.0 ** -8 if bf16 else 2.0 ** -24)
 
 
-@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+@pytest.mark.parametrize("impl", ["tcgen05", "q8_rows"])
 def test_caller_bits_and_rows_that_see_nothing(kdt, impl):
     d = _inputs(11, 40, 6, [0, 0, 130])
     rng = np.random.RandomState(3)
@@ -120,7 +121,7 @@ def test_caller_bits_and_rows_that_see_nothing(kdt, impl):
     _check(d, _call(kdt, d, see=see, impl=impl, num_splits=3), 2.0 ** -24, see=see)
 
 
-@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+@pytest.mark.parametrize("impl", ["tcgen05", "q8_rows"])
 @pytest.mark.parametrize("T,H", [(12, 4), (64, 64)])
 def test_nan_reaches_exactly_the_rows_that_see_it(kdt, impl, T, H):
     """NaN in a tree node's codes (its group flagged) and an infinity in another's rope key:
@@ -146,7 +147,7 @@ def test_nan_reaches_exactly_the_rows_that_see_it(kdt, impl, T, H):
     assert np.isnan(out[0]).all() and np.isnan(lse[0]).all()
 
 
-@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+@pytest.mark.parametrize("impl", ["tcgen05", "q8_rows"])
 def test_outlier_keys_raise_the_reference(kdt, impl):
     """Keys far larger than the rest, late in the sequence, in several blocks: the running
     reference rises block after block and old sums are rescaled."""
@@ -158,7 +159,7 @@ def test_outlier_keys_raise_the_reference(kdt, impl):
     _check(d, _call(kdt, d, impl=impl), 2.0 ** -24)
 
 
-@pytest.mark.parametrize("impl", ["auto", "q8_rows"])
+@pytest.mark.parametrize("impl", ["tcgen05", "q8_rows"])
 def test_scales_over_the_whole_range(kdt, impl):
     """Scale bytes from the smallest to above 2^7 (where widening takes a second product)."""
     import torch

@@ -99,7 +99,7 @@ def _verify(kdt, **kw):
 def test_verify_q8_refusals(kdt):
     K = kdt.kdt
     assert kdt.lib().kdt_verify_attn_q8(None, None, 0, None) == K.KDT_ERR_NULL_ARG
-    for kw in (dict(D_c=256), dict(D_r=32), dict(out_dtype=2), dict(impl=1), dict(impl=3), dict(impl=9), dict(impl=-1)):
+    for kw in (dict(D_c=256), dict(D_r=32), dict(out_dtype=2), dict(impl=1), dict(impl=3), dict(impl=5), dict(impl=-1)):
         assert _verify(kdt, **kw) == K.KDT_ERR_UNSUPPORTED, kw
     for kw in (dict(B=-1), dict(B=65536), dict(T=0), dict(T=4097), dict(H=0), dict(H=1025), dict(max_kv_len=8),
                dict(max_kv_len=101), dict(num_splits=-1), dict(q_nope=0x10008), dict(q_pe=0x10402), dict(c_q8=0x20008),
@@ -111,7 +111,7 @@ def test_verify_q8_refusals(kdt):
         assert _verify(kdt, **{kw: None}) == K.KDT_ERR_NULL_ARG, kw
     assert _verify(kdt, vis=0x90000) == K.KDT_ERR_NULL_ARG                      # both mask inputs
     assert _verify(kdt) == K.KDT_ERR_WORKSPACE
-    need = kdt.verify_attn_q8_workspace_size(2, 9, 8, 46)
+    need = kdt.verify_attn_q8_workspace_size(2, 9, 8, 46)          # the visibility bits
     assert need > 0
     assert _verify(kdt, ws=(0x100000, need - 1)) == K.KDT_ERR_WORKSPACE
     assert _verify(kdt, ws=(0x100010, need)) == K.KDT_ERR_WORKSPACE
@@ -120,9 +120,15 @@ def test_verify_q8_refusals(kdt):
 
 def test_verify_q8_plan(kdt):
     p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows")
-    # 72 rows a sequence are two 64-row tiles of one 128-key block each
-    assert p["impl"] == "q8_rows" and p["ctas"] == 4 and p["num_launches"] == 3
-    assert p["workspace_bytes"] >= 2 * 9 * 4 + 2 * 4 * 64 * 513 * 4
+    # 72 rows a sequence are two 64-row tiles of one 128-key block each: nothing to cut
+    assert p["impl"] == "q8_rows" and p["ctas"] == 4 and p["num_launches"] == 2
+    assert 2 * 9 * 4 <= p["workspace_bytes"] <= 256
+    p = kdt.verify_attn_q8_plan(2, 9, 8, 129, impl="q8_rows")
+    assert p["ctas"] == 8 and p["num_launches"] == 3 and p["workspace_bytes"] >= 2 * 8 * 64 * 513 * 4
+    # rows a sequence choose the kernel: 64 heads of one token, 64 heads of a tree
+    assert kdt.verify_attn_q8_plan(4, 1, 64, 5000)["impl"] == "q8_rows"
+    p = kdt.verify_attn_q8_plan(4, 64, 64, 5000)
+    assert p["impl"] == "tcgen05" and p["ctas"] == 4 * p["num_splits"]
     p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows", num_splits=1, bits=True)
     assert p["ctas"] == 1 and p["num_launches"] == 1 and p["workspace_bytes"] == 0
     with pytest.raises(kdt.KdtError):
