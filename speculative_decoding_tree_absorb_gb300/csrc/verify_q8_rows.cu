@@ -547,11 +547,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             const bool nan = b0 == (uint32_t)q8::kNaN || b1 == (uint32_t)q8::kNaN || b2 == (uint32_t)q8::kNaN ||
                              b3 == (uint32_t)q8::kNaN;
             if (nan) sh.bad[g & 1][k0 + lane] = 1u;
+            // two keys a lane at a time: their shuffles, their products, their stores (a shuffle between two
+            // stores would wait for the first one's values)
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const uint32_t dst = ((t & 1) ? krow1 : krow0) + 512 * t;
-                sts(dst, q8::widen8(a[t], __byte_perm(__shfl_sync(0xffffffffu, fa, 4 * t + kq), 0u, pick)));
-                sts(dst + kKTile, q8::widen8(b[t], __byte_perm(__shfl_sync(0xffffffffu, fb, 4 * t + kq), 0u, pick)));
+            for (int t0 = 0; t0 < 8; t0 += 2) {
+                uint32_t f[4];
+                uint4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = __shfl_sync(0xffffffffu, k & 1 ? fb : fa, 4 * (t0 + (k >> 1)) + kq);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = q8::widen8(k & 1 ? b[t0 + (k >> 1)] : a[t0 + (k >> 1)], __byte_perm(f[k], 0u, pick));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sts((k >> 1 ? krow1 : krow0) + 512 * (t0 + (k >> 1)) + (k & 1) * kKTile, v[k]);
             }
             // some scale above 2^7: a second product
             if (__any_sync(0xffffffffu, max(max(b0, b1), max(b2, b3)) > q8::kHighByte)) {

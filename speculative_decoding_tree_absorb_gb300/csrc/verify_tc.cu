@@ -43,13 +43,13 @@
 //    O (fp32) far from overflow; a smaller one rescales often on caches with
 //    outlier keys (a few times larger than the rest), and every rescale drains the
 //    P.V pipe.
-//  * The same kernel runs over the 8-bit latent cache (kQ8): there is no TMA for latents
-//    then. Four more warps a CTA load codes to registers, widen them to bf16 (exact: e4m3
-//    times a power of two) and store the same swizzled tiles into the same rings: in an
-//    S-CTA its 64 keys of each key chunk, in an O-CTA its 128 columns of each value chunk.
-//    Widening leaves each four dims in the order (0, 2, 1, 3): Q is loaded in that order and
-//    O written back from it. A CTA widens 32 k codes a block (about 800 instructions a warp
-//    in the 3700 clocks a block takes), so the widening hides behind the MMAs. A NaN group
+//  * The same kernel runs over the 8-bit latent cache (kQ8): the latents' TMA then brings
+//    codes, and four more warps a CTA widen them to bf16 (exact: e4m3 times a power of two)
+//    into the same swizzled tiles of the same rings: in an S-CTA its 64 keys of each key
+//    chunk, in an O-CTA its 128 columns of each value chunk. Widening leaves each four dims
+//    in the order (0, 2, 1, 3): Q is loaded in that order and O written back from it. A CTA
+//    widens 32 k codes a block (about 900 instructions a warp in the 3700 clocks a block
+//    takes), so the widening hides behind the MMAs. A NaN group
 //    gives NaN keys, so that rows which see it become NaN, and zero values, so that it does
 //    not reach rows from which it is hidden.
 //  * Every wait is bounded; on a lost arrival the kernel records a status in the
@@ -114,7 +114,7 @@ constexpr int kThreads = 384;          // 12 warps
 // 8-bit cache: warps 12-15 widen. The launch gives each of the four warpgroups 128 registers a
 // thread; they trade (issuers and loaders, two of softmax, widening).
 constexpr int kThreadsQ8 = 512;
-constexpr int kRegsQ8[4] = {72, 168, 168, 104};
+constexpr int kRegsQ8[4] = {96, 168, 168, 80};
 static_assert(kRegsQ8[0] + kRegsQ8[1] + kRegsQ8[2] + kRegsQ8[3] <= 4 * 128, "the warpgroups' shares exceed the launch's registers");
 constexpr int kWidenWarps = 4;
 constexpr int kQPrefetchBlocks = 6;               // blocks before an item's end that warm L2 with the next Q
@@ -169,6 +169,17 @@ constexpr int kOffEpi = kOffStats + 2 * kRows * 8;          // O: epilogue trans
 constexpr int kSEnd = kOffLSum + kRows * 4;
 constexpr int kOEnd = kOffEpi + kEpiWarps * 32 * kEpiCols * 4;
 constexpr int kTileBytes = kSEnd > kOEnd ? kSEnd : kOEnd;
+// 8-bit cache: raw pieces [64 keys x 64 dims] of codes. An S-CTA keeps them in the room of two rope
+// slots (its rope ring then has two), an O-CTA behind its other parts.
+constexpr int kNRQ8 = 2;
+constexpr int kRaw = 4;                                     // slots: three pieces (12 KB) in flight
+constexpr int kRawBytes = 64 * 64;
+constexpr int kOffRawS = kOffRRing + kNRQ8 * kKSub;
+constexpr int kOffRawO = (kOEnd + 127) / 128 * 128;
+static_assert(kRaw * kRawBytes <= (kNR - kNRQ8) * kKSub, "raw pieces in the rope ring's room");
+constexpr int kQ8End = kOffRawO + kRaw * kRawBytes;
+constexpr int kSmemBytesQ8 = (kSEnd > kQ8End ? kSEnd : kQ8End) + 1024;
+static_assert(kSmemBytesQ8 + 2048 <= 227 * 1024, "shared memory budget");
 constexpr int kSmemBytes = kTileBytes + 1024;               // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
@@ -204,6 +215,9 @@ struct Barriers {
     uint64_t o_free;               // O leader: both O-CTAs' epilogues have read O (one arrival a warp)
     uint64_t sync_bar;             // leader: MMA thread's own completion probe (mid-stream)
     uint64_t drain;                // completion of all MMAs of the pair before TMEM is read or freed
+    // 8-bit cache
+    uint64_t rawfull[kRaw];        // a raw piece landed (transaction bytes)
+    uint64_t rawempty[kRaw];       // the widening warps have read it
     uint32_t need[2][kNP];         // leader: per-CTA "some row of O needs a rescale" per P slot
     uint32_t cmd;                  // each O-CTA: correction command
     int kseen[2];                  // S leader: latest latent chunk use each MMA issuer saw land
@@ -471,6 +485,37 @@ __device__ __forceinline__ bool warp_wait_cluster(Barriers &bar, uint64_t *b, ui
     return __all_sync(0xffffffffu, wait_cluster_or_abort(bar, b, parity, err, code));
 }
 
+// The same for waits that mostly find the phase complete: the abort flag is read only after a miss.
+__device__ __forceinline__ bool quick_warp_wait(Barriers &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    return warp_wait(bar, b, parity, err, code);
+}
+
+// 8-bit cache: the requests for a CTA's raw pieces of codes, made in order by one thread, up to
+// kRaw pieces ahead of the widening warps.
+struct RawRequests {
+    int n = 0, slot = 0;
+    uint32_t phase = 1;
+    // the eight pieces of block j of item it
+    __device__ __forceinline__ bool block(Barriers &bar, const CUtensorMap &map, uint32_t raw, bool s_role, int kpair, const Item &it,
+                                          int j, int32_t *err) {
+        const int key0 = it.key_base + (it.kb0 + j) * kKeys;
+        for (int q = 0; q < 8; ++q) {
+            if (n >= kRaw && !wait_or_abort(bar, &bar.rawempty[slot], phase, err, -32)) return false;
+            mbar_arrive_expect_tx(&bar.rawfull[slot], kRawBytes);
+            // S-CTA: its 64 keys of dim tile q; O-CTA: of its dim tiles (two a chunk), one half of the keys
+            const int key = key0 + (s_role ? kpair : q & 1) * kHalfKeys, tile = s_role ? q : 2 * (2 * (q >> 2) + kpair) + ((q >> 1) & 1);
+            tma_load_4d_at(raw + slot * kRawBytes, &map, &bar.rawfull[slot], 0, key, tile, it.b);
+            ++n;
+            if (++slot == kRaw) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        return true;
+    }
+};
+
 // Copy `bytes` (multiple of 16) from this CTA's shared memory to the same-layout
 // buffer in CTA `rank`, completing as transaction bytes on that CTA's barrier.
 __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_local, const void *src, uint32_t bytes,
@@ -641,71 +686,37 @@ template <int kN> __device__ __forceinline__ void set_regs() {
     if constexpr (kN < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
 }
 
-// One warp's share of a chunk, 16 sets of 8 codes a lane: kTiles tiles of 64 dims, 16 / kTiles
-// groups of four keys (8 lanes a key, 8 codes a lane: one 16-byte chunk of a tile's row).
-template <int kTiles> struct Codes {
-    static constexpr int kSets = 16 / kTiles;        // groups of four keys
-    uint2 c[kSets][kTiles];
-    uint32_t s;    // scale bytes of two tiles: of key `lane`, or (four tiles) of key lane % 16, tiles 2 (lane / 16) and + 1
-};
-
-// Load keys row0 .. of sequence b, dims dim0 .. (row0: the warp's first key, may be negative:
-// rows before 0 give zeros).
-template <int kTiles>
-__device__ __forceinline__ void load_codes(const TcParams &p, int b, int row0, int dim0, int lane, Codes<kTiles> &x) {
-    constexpr int kKeysW = 4 * Codes<kTiles>::kSets;     // keys of the warp: 16 or 32
+// One warp's share of a raw piece (64 keys x 64 dims): 16 keys, four at a time -- 8 lanes a key, 8
+// codes a lane, one 16-byte chunk of the bf16 tile's row. `bytes`: the two scale bytes of a key in
+// these dims, held by lane src0 + (key of the 16). NaN groups become nan_bits.
+__device__ __forceinline__ void widen_piece(uint32_t raw, uint32_t dst, uint32_t bytes, int src0, uint32_t nan_bits, int lane) {
     const int sub = lane & 7, kq = lane >> 3;
-    const int64_t row = (int64_t)b * p.L + row0;
-    const uint8_t *cp = p.c_q8 + (row + kq) * kDc + dim0 + 8 * sub;
-    const int sk = lane % kKeysW;
-    x.s = row0 + sk >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(p.c_scale + (row + sk) * (kDc / KDT_Q8_GROUP) + dim0 / KDT_Q8_GROUP) +
-                                 lane / kKeysW)
-                         : 0x7f7f7f7fu;
+    const uint32_t b0 = bytes & 255u, b1 = (bytes >> 8) & 255u, n = (uint32_t)q8::kNaN;
+    const uint32_t f = (b0 == n ? nan_bits : q8::factor(b0)) | ((b1 == n ? nan_bits : q8::factor(b1)) << 16);
+    const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;        // this lane's group of the two
+    // key kq + 4 t: swizzle sub ^ key % 8, the same for all even t and for all odd t
+    const uint32_t d0 = dst + kq * 128 + ((sub ^ kq) << 4), d1 = d0 ^ 64u, r0 = raw + kq * 64 + sub * 8;
+    uint32_t fk[4];
+    uint2 c[4];
 #pragma unroll
-    for (int t = 0; t < Codes<kTiles>::kSets; ++t)
+    for (int t = 0; t < 4; ++t) c[t] = ld_shared_v2(r0 + t * 256);
 #pragma unroll
-        for (int q = 0; q < kTiles; ++q)
-            x.c[t][q] = row0 + kq + 4 * t >= 0 ? __ldg(reinterpret_cast<const uint2 *>(cp + 4 * t * kDc + 64 * q)) : make_uint2(0u, 0u);
-}
-
-// Widen and store: `dst` is the shared-memory address of the warp's first key's row in the first tile.
-template <int kTiles, bool kNanKeys>
-__device__ __forceinline__ void store_codes(const Codes<kTiles> &x, uint32_t dst, uint32_t tile_bytes, int lane) {
-    constexpr int kKeysW = 4 * Codes<kTiles>::kSets;
-    const int sub = lane & 7, kq = lane >> 3;
-    const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;
-    uint32_t byte[4], f[4];
-    bool high = false;
+    for (int t = 0; t < 4; ++t) fk[t] = __byte_perm(__shfl_sync(0xffffffffu, f, src0 + 4 * t + kq), 0u, pick);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        byte[k] = (x.s >> (8 * k)) & 255u;
-        f[k] = kNanKeys && byte[k] == (uint32_t)q8::kNaN ? 0x7fc0u : q8::factor(byte[k]);
-        high |= byte[k] > q8::kHighByte && byte[k] != (uint32_t)q8::kNaN;
+    for (int t = 0; t < 4; ++t) {
+        const uint4 v = q8::widen8(c[t], fk[t]);
+        st_shared_v4(((t & 1) ? d1 : d0) + 512 * t, v.x, v.y, v.z, v.w);
     }
-    const uint32_t fa = f[0] | (f[1] << 16), fb = f[2] | (f[3] << 16);
-    // key kq + 4 t: swizzle (sub ^ key % 8), the same for all even t and for all odd t
-    const uint32_t d0 = dst + kq * 128 + ((sub ^ kq) << 4), d1 = d0 ^ 64u;
-#pragma unroll
-    for (int t = 0; t < Codes<kTiles>::kSets; ++t)
-#pragma unroll
-        for (int q = 0; q < kTiles; ++q) {
-            const uint32_t fk = __shfl_sync(0xffffffffu, (q & 1) ? fb : fa, 4 * t + kq + (q >> 1) * kKeysW);
-            const uint4 v = q8::widen8(x.c[t][q], __byte_perm(fk, 0u, pick));
-            st_shared_v4(((t & 1) ? d1 : d0) + 512 * t + q * tile_bytes, v.x, v.y, v.z, v.w);
-        }
-    if (__any_sync(0xffffffffu, high)) {                   // some scale above 2^7: a second product
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = byte[k] == (uint32_t)q8::kNaN ? 0x3f80u : q8::factor_high(byte[k]);
-        const uint32_t ha = h[0] | (h[1] << 16), hb = h[2] | (h[3] << 16);
+    const bool high = (b0 > q8::kHighByte && b0 != n) || (b1 > q8::kHighByte && b1 != n);
+    if (__any_sync(0xffffffffu, high)) {                       // some scale above 2^7: a second product
+        const uint32_t h = (b0 == n ? 0x3f80u : q8::factor_high(b0)) | ((b1 == n ? 0x3f80u : q8::factor_high(b1)) << 16);
 #pragma unroll 1
-        for (int k = 0; k < 16; ++k) {
-            const int t = k / kTiles, q = k % kTiles;
-            const uint32_t fk = __byte_perm(__shfl_sync(0xffffffffu, (q & 1) ? hb : ha, 4 * t + kq + (q >> 1) * kKeysW), 0u, pick);
-            const uint32_t a = ((t & 1) ? d1 : d0) + 512 * t + q * tile_bytes;
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t g = __byte_perm(__shfl_sync(0xffffffffu, h, src0 + 4 * t + kq), 0u, pick);
+            const uint32_t a = ((t & 1) ? d1 : d0) + 512 * t;
             uint32_t v[4];
             ld_shared_v4(a, v);
-            st_shared_v4(a, q8::mul_bf16x2(v[0], fk), q8::mul_bf16x2(v[1], fk), q8::mul_bf16x2(v[2], fk), q8::mul_bf16x2(v[3], fk));
+            st_shared_v4(a, q8::mul_bf16x2(v[0], g), q8::mul_bf16x2(v[1], g), q8::mul_bf16x2(v[2], g), q8::mul_bf16x2(v[3], g));
         }
     }
 }
@@ -715,6 +726,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
     verify_tc_kernel(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs,
                      const __grid_constant__ CUtensorMap map_kpe, const __grid_constant__ CUtensorMap map_qpe,
                      const TcParams p) {
+    constexpr int kRopeSlots = kQ8 ? kNRQ8 : kNR;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -788,7 +800,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
     if (threadIdx.x == 0) {
         constexpr int kFills = kQ8 ? 2 * kWidenWarps : 1;     // arrivals that fill a latent slot
         for (int i = 0; i < kNK; ++i) { mbar_init(&bar.kfull[i], kFills); mbar_init(&bar.kempty[i], 1); }
-        for (int i = 0; i < kNR; ++i) { mbar_init(&bar.rfull[i], 1); mbar_init(&bar.rempty[i], 1); }
+        for (int i = 0; i < kRopeSlots; ++i) { mbar_init(&bar.rfull[i], 1); mbar_init(&bar.rempty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar.sfull[i], 1); mbar_init(&bar.sempty[i], 16); }
         mbar_init(&bar.qpe_full, 1);
         mbar_init(&bar.qpe_empty, 1);
@@ -813,6 +825,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         }
         mbar_init(&bar.o_done, 1);
         mbar_init(&bar.o_free, 2 * kEpiWarps);
+        if (kQ8)
+            for (int i = 0; i < kRaw; ++i) { mbar_init(&bar.rawfull[i], 1); mbar_init(&bar.rawempty[i], kWidenWarps); }
         bar.kseen[0] = bar.kseen[1] = -1;
         mbar_init(&bar.sync_bar, 1);
         // one drain commit per MMA issuer that runs: two in the S leader (one for a single
@@ -859,24 +873,33 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
             // next use is armed once the pair's MMAs have released it.
             if (elect_one() && G > 0) {
                 RingPos kr, rr;
+                RawRequests raws;
+                if (kQ8) tma_prefetch_desc(&map_ks);
                 bool going = true;
                 WorkIter w = first_work();
                 Item it;
                 int ii = 0;
                 while (going && !aborted(bar) && next_item(p, w, cl, ncl, it)) {
                     // this CTA's Q_pe tile is free once the previous item's rope MMAs read it
-                    if (ii > 0 && !(going = wait_or_abort(bar, &bar.qpe_empty, (uint32_t)(ii - 1) & 1, p.err, -24)))
-                        break;
-                    if (leader) mbar_arrive_expect_tx(&bar.qpe_full, 2 * kQpeBytes);
-                    tma_load_2d_pair(qpe_tile, &map_qpe, map_to_rank(&bar.qpe_full, lead_rank), 0,
-                                     (int)((int64_t)it.b * p.rows_seq + (it.rt0 + kpair) * kRows));
-                    KDT_TC_TRACE(kEvQpeIssued, ii);
+                    // (8-bit cache: the P copier loads it, this thread must not wait for MMAs)
+                    if (!kQ8) {
+                        if (ii > 0 && !(going = wait_or_abort(bar, &bar.qpe_empty, (uint32_t)(ii - 1) & 1, p.err, -24)))
+                            break;
+                        if (leader) mbar_arrive_expect_tx(&bar.qpe_full, 2 * kQpeBytes);
+                        tma_load_2d_pair(qpe_tile, &map_qpe, map_to_rank(&bar.qpe_full, lead_rank), 0,
+                                         (int)((int64_t)it.b * p.rows_seq + (it.rt0 + kpair) * kRows));
+                        KDT_TC_TRACE(kEvQpeIssued, ii);
+                    }
                     ++ii;
                     // a few blocks before the item ends, warm L2 with the next item's rows of Q
                     // (the pair's 256 rows are contiguous): its load then sits between two
                     // items on the tensor pipes' critical path
                     const int j_pf = it.nb > kQPrefetchBlocks ? it.nb - kQPrefetchBlocks : 0;
-                    for (int j = 0; leader && j < it.nb && going; ++j) {
+                    for (int j = 0; (leader || kQ8) && j < it.nb && going; ++j) {
+                        if (kQ8) {
+                            if (!(going = raws.block(bar, map_ks, smem_u32(smem) + kOffRawS, true, kpair, it, j, p.err))) break;
+                            if (!leader) continue;
+                        }
                         if (j == j_pf) {
                             WorkIter wn = w;
                             Item nx;
@@ -901,11 +924,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                             ring_advance<kNK>(kr);
                         }
                         if (!going) break;
-                        if (rr.n >= kNR &&
+                        if (rr.n >= kRopeSlots &&
                             !(going = wait_or_abort(bar, &bar.rempty[rr.slot], rr.phase ^ 1, p.err, -2)))
                             break;
                         mbar_arrive_expect_tx(&bar.rfull[rr.slot], 2 * kKSub);
-                        ring_advance<kNR>(rr);
+                        ring_advance<kRopeSlots>(rr);
                     }
                 }
                 // drain (both S-CTAs): the MMA commits for the last uses of every slot mean
@@ -914,10 +937,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                     kr = RingPos{};
                     rr = RingPos{};
                     for (int u = 0; u < kKChunks * G; ++u) ring_advance<kNK>(kr);
-                    for (int u = 0; u < G; ++u) ring_advance<kNR>(rr);
+                    for (int u = 0; u < G; ++u) ring_advance<kRopeSlots>(rr);
                 }
                 if (!kQ8) ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
-                ring_drain<kNR>(bar.rempty, rr, bar.wait_ns);
+                ring_drain<kRopeSlots>(bar.rempty, rr, bar.wait_ns);
                 if (ii > 0) mbar_wait(&bar.qpe_empty, (uint32_t)(ii - 1) & 1, bar.wait_ns);
             }
         } else if (warp == 1 || warp == 2) {
@@ -967,9 +990,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                                 }
                                 if (!ok) break;
                             }
-                            if (!(ok = kQ8 ? wait_cluster_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5)
-                                           : wait_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5)))
-                                break;
+                            if (!(ok = wait_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5))) break;
                             *seen_mine = u;
                             tc_fence_after();
                             KDT_TC_TRACE(kEvKFull, u);
@@ -988,8 +1009,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                             mma_commit_pair(&bar.kempty[slot], kQ8 ? kMaskS : kMaskAll);   // slot free: S-CTAs and their loaders
                         }
                         if (!ok) break;
-                        const int rslot = g % kNR;
-                        if (!(ok = wait_or_abort(bar, &bar.rfull[rslot], (uint32_t)(g / kNR) & 1, p.err, -5))) break;
+                        const int rslot = g % kRopeSlots;
+                        if (!(ok = wait_or_abort(bar, &bar.rfull[rslot], (uint32_t)(g / kRopeSlots) & 1, p.err, -5))) break;
                         tc_fence_after();
                         KDT_TC_TRACE(kEvRFull, g);
                         const uint64_t qdesc0 = sdesc_sw128(smem_u32(qpe_tile), 16, 1024);
@@ -1010,6 +1031,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         } else if (warp == 3) {
             // ---------------- P copier: each half of P to the O-CTA once staged ---------------
             if (elect_one()) {
+                // 8-bit cache: also Q_pe of each item. Once the last block of an item is staged its
+                // rope MMAs have run, so the tile is free for the next item's
+                WorkIter w = first_work();
+                Item it;
+                int left = 0;                                  // blocks of the item still to copy
+                auto load_qpe = [&]() {
+                    if (!next_item(p, w, cl, ncl, it)) return;
+                    left = it.nb;
+                    if (leader) mbar_arrive_expect_tx(&bar.qpe_full, 2 * kQpeBytes);
+                    tma_load_2d_pair(smem + kOffQpe, &map_qpe, map_to_rank(&bar.qpe_full, lead_rank), 0,
+                                     (int)((int64_t)it.b * p.rows_seq + (it.rt0 + kpair) * kRows));
+                };
+                if (kQ8 && G > 0) load_qpe();
                 for (int g = 0; g < G; ++g) {
                     const int ss = g % kNS, ps = g % kNP;
                     const uint32_t par = (uint32_t)(g / kNS) & 1;
@@ -1023,6 +1057,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                         if (h == 0) KDT_TC_TRACE(kEvSoftmaxSent, g);
                     }
                     if (!ok) break;
+                    if (kQ8 && --left == 0) load_qpe();
                 }
             }
         }
@@ -1032,7 +1067,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         unsigned char *vbase = smem + kOffV;
         if (warp == 0) {
             // ------- TMA producer: this CTA's 128 of each 256 latent columns of V -------
-            // (8-bit cache: the widening warps fill the ring)
+            if (kQ8 && elect_one() && G > 0) {             // codes; the widening warps fill the ring
+                tma_prefetch_desc(&map_ks);
+                RawRequests raws;
+                bool going = true;
+                WorkIter w = first_work();
+                Item it;
+                while (going && !aborted(bar) && next_item(p, w, cl, ncl, it))
+                    for (int j = 0; j < it.nb && going; ++j)
+                        going = raws.block(bar, map_ks, smem_u32(smem) + kOffRawO, false, kpair, it, j, p.err);
+            }
             if (!kQ8 && elect_one() && G > 0) {
                 tma_prefetch_desc(&map_vs);
                 RingPos vr;
@@ -1101,9 +1145,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                         const uint64_t adesc0 = sdesc_sw128(smem_u32(pbase + ps * kPSlotBytes), 16, 1024);
                         const uint32_t acc0 = j > 0 ? 1u : 0u;
                         for (int h = 0; h < kVChunks; ++h) {
-                            if (!(ok = kQ8 ? wait_cluster_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10)
-                                           : wait_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10)))
-                                break;
+                            if (!(ok = wait_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10))) break;
                             tc_fence_after();
                             KDT_TC_TRACE(kEvVFull, vr.n);
                             const uint64_t bdesc0 = sdesc_sw128(smem_u32(vbase + vr.slot * kVSlotBytes), kVSub, 1024);
@@ -1192,17 +1234,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                             ring_advance<kNK>(kr);
                         }
                         if (!going) break;
-                        if (rr.n >= kNR &&
+                        if (rr.n >= kRopeSlots &&
                             !(going = wait_or_abort(bar, &bar.rempty[rr.slot], rr.phase ^ 1, p.err, -21)))
                             break;
                         tma_load_3d_pair_mc(rring + rr.slot * kKSub, &map_kpe, map_to_rank(&bar.rfull[rr.slot], 0), 0,
                                             key0, it.b, dst_mask);
-                        ring_advance<kNR>(rr);
+                        ring_advance<kRopeSlots>(rr);
                     }
                 }
                 // every copy this CTA issued has landed and been read before it may exit
                 if (!kQ8) ring_drain<kNK>(bar.kempty, kr, bar.wait_ns);
-                ring_drain<kNR>(bar.rempty, rr, bar.wait_ns);
+                ring_drain<kRopeSlots>(bar.rempty, rr, bar.wait_ns);
             }
         } else if (warp == 2) {
             // ---------------- P watcher: P of each block landed, and does O need a rescale? --
@@ -1542,56 +1584,84 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         if constexpr (kQ8) {
         set_regs<kRegsQ8[3]>();
         // ---------------- widening: this CTA's half of every latent chunk -----------------------
+        // Codes come by TMA in raw pieces of 64 keys x 64 dims, eight a block: an S-CTA's are the
+        // eight dim tiles of its 64 keys, an O-CTA's its four dim tiles of either half of the 128
+        // keys; four pieces make a chunk of the bf16 ring. Every warp takes 16 keys of every piece.
+        // The loop over pieces is rolled and small on purpose: loads to registers two chunks ahead
+        // need it unrolled, and that code ran at the speed of instruction fetches (a block took
+        // 10 k clocks against the 3.7 k of its MMAs).
         const int ww = warp - 12;
-        unsigned char *ring = smem + (s_role ? kOffKRing : kOffV);
+        const uint32_t ring = smem_u32(smem) + (s_role ? kOffKRing : kOffV);
+        const uint32_t slot_bytes = s_role ? kKSlotBytes : kVSlotBytes, nslots = s_role ? kNK : kNV;
+        uint64_t *full = s_role ? bar.kfull : bar.vfull, *empty = s_role ? bar.kempty : bar.vempty;
+        const uint32_t nan_bits = s_role ? 0x7fc0u : 0u;       // NaN keys, zero values
+        const int total = 8 * bar.work_count;                  // pieces
+        const uint32_t raw = smem_u32(smem) + (s_role ? kOffRawS : kOffRawO);
+        bool ok = true;
+        // scale bytes, a block ahead: 16 keys of the warp (lane % 16), for each half of the lanes the
+        // dims (S) or the keys (O) of one half of the pieces; two words of four bytes
         WorkIter w = first_work();
         Item it;
-        if (s_role) {      // chunk c of a block: its 64 keys x dims 256 c .. + 256, four [64 x 64] tiles
-            Codes<4> x;
-            RingPos r;
-            bool have = next_item(p, w, cl, ncl, it), ok = true;
-            auto load = [&](int j, int c) {
-                load_codes(p, it.b, it.key_base + (it.kb0 + j) * kKeys + kpair * kHalfKeys + 16 * ww, 256 * c, lane, x);
-            };
-            if (have) load(0, 0);
-            while (have && ok) {
-                const int nb = it.nb;
-                for (int k = 0; k < kKChunks * nb && ok; ++k) {
-                    if (r.n >= kNK && !(ok = warp_wait(bar, &bar.kempty[r.slot], r.phase ^ 1, p.err, -30))) break;
-                    store_codes<4, true>(x, smem_u32(ring + r.slot * kKSlotBytes) + 16 * ww * 128, kKSub, lane);
-                    fence_proxy_async_all();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(&bar.kfull[r.slot], lead_rank);
-                    ring_advance<kNK>(r);
-                    if (k + 1 < kKChunks * nb) load((k + 1) / kKChunks, (k + 1) % kKChunks);
-                    else if ((have = next_item(p, w, cl, ncl, it))) load(0, 0);
+        int j = 0;
+        bool have = next_item(p, w, cl, ncl, it);
+        auto load_scales = [&]() {
+            const int x = lane >> 4, key = it.key_base + (it.kb0 + j) * kKeys + (s_role ? kpair : x) * kHalfKeys + 16 * ww + (lane & 15);
+            uint2 v = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);    // (rows before 0: the codes are zeros)
+            if (key >= 0) {
+                const uint32_t *sp = reinterpret_cast<const uint32_t *>(p.c_scale + ((int64_t)it.b * p.L + key) * (kDc / KDT_Q8_GROUP));
+                v.x = __ldg(sp + (s_role ? 2 * x : kpair));
+                v.y = __ldg(sp + (s_role ? 2 * x + 1 : 2 + kpair));
+            }
+            if (++j == it.nb) {
+                j = 0;
+                have = next_item(p, w, cl, ncl, it);
+            }
+            return v;
+        };
+        uint2 sn = make_uint2(0u, 0u), sc = sn;
+        if (have) sn = load_scales();
+        int rslot = 0, slot = 0;
+        uint32_t rphase = 0, phase = 0;
+        bool refill = false;                                   // the ring's slots have been used before
+#pragma unroll 1
+        for (int n = 0; n < total && ok; ++n) {
+            const int q = n & 7;
+            if (q == 0) {
+                sc = sn;
+                if (have) sn = load_scales();
+            }
+            if ((q & 3) == 0 && refill) ok = quick_warp_wait(bar, &empty[slot], phase ^ 1, p.err, -30);
+            ok = ok && quick_warp_wait(bar, &bar.rawfull[rslot], rphase, p.err, -31);
+            if (!ok) break;
+            const uint32_t dst = ring + slot * slot_bytes +
+                                 (s_role ? (q & 3) * kKSub + 16 * ww * 128
+                                         : ((q >> 1) & 1) * kVSub + (64 * (q & 1) + 16 * ww) * 128);
+            const uint32_t word = (s_role ? (q >> 1) & 1 : q >> 2) ? sc.y : sc.x;
+            const uint32_t bytes = (s_role ? q & 1 : (q >> 1) & 1) ? word >> 16 : word & 0xffffu;
+            widen_piece(raw + rslot * kRawBytes + 16 * ww * 64, dst, bytes, 16 * (s_role ? q >> 2 : q & 1), nan_bits, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.rawempty[rslot]);
+            if (++rslot == kRaw) {
+                rslot = 0;
+                rphase ^= 1;
+            }
+            if ((q & 3) == 3) {                                // a chunk of the ring is complete
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_cta(&full[slot], lead_rank);
+                if (++slot == (int)nslots) {
+                    slot = 0;
+                    phase ^= 1;
+                    refill = true;
                 }
             }
-            // the releases of the last chunks have arrived before this CTA may leave
-            if (ok) ring_drain<kNK>(bar.kempty, r, bar.wait_ns);
-        } else {           // chunk h of a block: 128 keys x this CTA's 128 dims, two [128 x 64] tiles
-            Codes<2> x;
-            RingPos r;
-            bool have = next_item(p, w, cl, ncl, it), ok = true;
-            auto load = [&](int j, int h) {
-                load_codes(p, it.b, it.key_base + (it.kb0 + j) * kKeys + 32 * ww, (2 * h + kpair) * 64 * kVSubPerChunk, lane, x);
-            };
-            if (have) load(0, 0);
-            while (have && ok) {
-                const int nb = it.nb;
-                for (int k = 0; k < kVChunks * nb && ok; ++k) {
-                    if (r.n >= kNV && !(ok = warp_wait(bar, &bar.vempty[r.slot], r.phase ^ 1, p.err, -31))) break;
-                    store_codes<2, false>(x, smem_u32(ring + r.slot * kVSlotBytes) + 32 * ww * 128, kVSub, lane);
-                    fence_proxy_async_all();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(&bar.vfull[r.slot], lead_rank);
-                    ring_advance<kNV>(r);
-                    if (k + 1 < kVChunks * nb) load((k + 1) / kVChunks, (k + 1) % kVChunks);
-                    else if ((have = next_item(p, w, cl, ncl, it))) load(0, 0);
-                }
-            }
-            if (ok) ring_drain<kNV>(bar.vempty, r, bar.wait_ns);
         }
+        // the releases of the last chunks, and the copies in flight, have arrived before this CTA may leave
+        if (ok)
+            for (int k = 0; k < (int)nslots && k < 2 * bar.work_count; ++k) {
+                const int u = 2 * bar.work_count - 1 - k;      // chunk use
+                mbar_wait(&empty[u % (int)nslots], (uint32_t)(u / (int)nslots) & 1, bar.wait_ns);
+            }
         }
     }
 
@@ -1743,7 +1813,7 @@ template <bool kQ8> int max_clusters() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
     cfg.blockDim = dim3(kQ8 ? kThreadsQ8 : kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = kQ8 ? kSmemBytesQ8 : kSmemBytes;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 4;
@@ -1751,7 +1821,8 @@ template <bool kQ8> int max_clusters() {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+    if (cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kQ8 ? kSmemBytesQ8 : kSmemBytes) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, verify_tc_kernel<kQ8>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();    // clear the query's error; plan with the SM count instead
         const int f = sm_count() / 4;
@@ -1789,13 +1860,14 @@ EncodeTiledFn encode_fn() {
 }
 
 bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-              const cuuint32_t *box) {
+              const cuuint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint32_t es[4] = {1, 1, 1, 1};
     memset(m, 0, sizeof(*m));
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, type, rank, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1807,7 +1879,16 @@ namespace {
 template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
     CUtensorMap map_ks, map_vs, map_kpe, map_qpe;
     const cuuint64_t L = (cuuint64_t)vp.L;
-    if (!kQ8) {
+    if (kQ8) {
+        // codes viewed as [B][8 dim-blocks][L keys][64]: a box lands as [64 keys][64 codes], rows before
+        // row 0 as zeros
+        cuuint64_t dims[4] = {64, L, (cuuint64_t)(kDc / 64), (cuuint64_t)vp.B};
+        cuuint64_t strides[3] = {(cuuint64_t)kDc, 64, L * kDc};
+        cuuint32_t box[4] = {64, kHalfKeys, 1, 1};
+        if (!make_map(&map_ks, vp.c_kv, 4, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+        map_vs = map_ks;                                           // unused
+    } else {
         // c_kv viewed as [B][8 dim-blocks][L keys][64]: a box of (64, n keys, m blocks)
         // lands as m consecutive [n x 64] 128B-swizzled sub-tiles.
         cuuint64_t dims[4] = {64, L, (cuuint64_t)(kDc / 64), (cuuint64_t)vp.B};
@@ -1822,7 +1903,6 @@ template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
         cuuint64_t strides[2] = {(cuuint64_t)kDr * 2, L * kDr * 2};
         cuuint32_t box[3] = {64, kHalfKeys, 1};
         if (!make_map(&map_kpe, vp.k_pe, 3, dims, strides, box)) return cudaErrorInvalidValue;
-        if (kQ8) map_ks = map_vs = map_kpe;                        // unused: the latents come through registers
     }
     {
         cuuint64_t dims[2] = {(cuuint64_t)kDr, (cuuint64_t)vp.rows_total};
@@ -1858,7 +1938,8 @@ template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
     p.out_bf16 = vp.out_bf16;
     const int C = vp.tc_clusters;
     if (C < 1 || C > kMaxClusters || (C > 1 && (!p.part_o || !p.part_lse || !p.sched))) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kQ8 ? kSmemBytesQ8 : kSmemBytes);
     if (e != cudaSuccess) return e;
     // Programmatic dependent launch: this kernel overlaps the visibility kernel launched
     // just before it in the same call (it waits for it before reading the bits), and the
@@ -1869,7 +1950,7 @@ template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(4 * C));
     cfg.blockDim = dim3(kQ8 ? kThreadsQ8 : kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = kQ8 ? kSmemBytesQ8 : kSmemBytes;
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = vp.overlap_vis ? 1 : 0;
