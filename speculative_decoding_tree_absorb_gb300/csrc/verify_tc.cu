@@ -111,12 +111,13 @@ constexpr int kRows = 128;             // query rows per CTA (the pair's MMA has
 constexpr int kKeys = 128;             // keys per block (S MMA N, P.V K)
 constexpr int kHalfKeys = kKeys / 2;   // keys of a block held by one S-CTA
 constexpr int kThreads = 384;          // 12 warps
-// 8-bit cache: warps 12-15 widen. The launch gives each of the four warpgroups 128 registers a
-// thread; they trade (issuers and loaders, two of softmax, widening).
-constexpr int kThreadsQ8 = 512;
-constexpr int kRegsQ8[4] = {96, 168, 168, 80};
-static_assert(kRegsQ8[0] + kRegsQ8[1] + kRegsQ8[2] + kRegsQ8[3] <= 4 * 128, "the warpgroups' shares exceed the launch's registers");
-constexpr int kWidenWarps = 4;
+// 8-bit cache: warps 12-19 widen. The launch gives each of the five warpgroups 96 registers a
+// thread; they trade: issuers and loaders, two of softmax, two of widening.
+constexpr int kThreadsQ8 = 640;
+constexpr int kRegsLaunchQ8 = 96, kRegsIssueQ8 = 64, kRegsSoftQ8 = 136, kRegsWidenQ8 = 72;
+static_assert(kRegsIssueQ8 + 2 * kRegsSoftQ8 + 2 * kRegsWidenQ8 <= 5 * kRegsLaunchQ8,
+              "the warpgroups' shares exceed the launch's registers");
+constexpr int kWidenWarps = 8;
 constexpr int kQPrefetchBlocks = 6;               // blocks before an item's end that warm L2 with the next Q
 constexpr uint32_t kQPrefetchChunk = 32768;       // bytes per L2 prefetch request
 constexpr int kKvPrefetchBlocks = 4;              // key blocks the L2 prefetch runs ahead of the loads
@@ -169,11 +170,12 @@ constexpr int kOffEpi = kOffStats + 2 * kRows * 8;          // O: epilogue trans
 constexpr int kSEnd = kOffLSum + kRows * 4;
 constexpr int kOEnd = kOffEpi + kEpiWarps * 32 * kEpiCols * 4;
 constexpr int kTileBytes = kSEnd > kOEnd ? kSEnd : kOEnd;
-// 8-bit cache: raw pieces [64 keys x 64 dims] of codes. An S-CTA keeps them in the room of two rope
-// slots (its rope ring then has two), an O-CTA behind its other parts.
+// 8-bit cache: raw pieces of codes, 8 KB each, four a block -- in an S-CTA two dim tiles of its 64 keys,
+// in an O-CTA one dim tile of 128 keys. An S-CTA keeps them in the room of two rope slots (its rope
+// ring then has two), an O-CTA behind its other parts.
 constexpr int kNRQ8 = 2;
-constexpr int kRaw = 4;                                     // slots: three pieces (12 KB) in flight
-constexpr int kRawBytes = 64 * 64;
+constexpr int kRaw = 2;                                     // slots, one for each set of widening warps
+constexpr int kRawBytes = 128 * 64;
 constexpr int kOffRawS = kOffRRing + kNRQ8 * kKSub;
 constexpr int kOffRawO = (kOEnd + 127) / 128 * 128;
 static_assert(kRaw * kRawBytes <= (kNR - kNRQ8) * kKSub, "raw pieces in the rope ring's room");
@@ -491,26 +493,21 @@ __device__ __forceinline__ bool quick_warp_wait(Barriers &bar, uint64_t *b, uint
     return warp_wait(bar, b, parity, err, code);
 }
 
-// 8-bit cache: the requests for a CTA's raw pieces of codes, made in order by one thread, up to
-// kRaw pieces ahead of the widening warps.
+// 8-bit cache: the requests for a CTA's raw pieces of codes, made in order by one thread as the
+// widening warps have taken the piece before out of the slot.
 struct RawRequests {
-    int n = 0, slot = 0;
-    uint32_t phase = 1;
-    // the eight pieces of block j of item it
+    uint32_t n = 0;
+    // the four pieces of block j of item it
     __device__ __forceinline__ bool block(Barriers &bar, const CUtensorMap &map, uint32_t raw, bool s_role, int kpair, const Item &it,
                                           int j, int32_t *err) {
-        const int key0 = it.key_base + (it.kb0 + j) * kKeys;
-        for (int q = 0; q < 8; ++q) {
-            if (n >= kRaw && !wait_or_abort(bar, &bar.rawempty[slot], phase, err, -32)) return false;
+        const int key0 = it.key_base + (it.kb0 + j) * kKeys + (s_role ? kpair * kHalfKeys : 0);
+        for (int q = 0; q < 4; ++q, ++n) {
+            const uint32_t slot = n % kRaw, use = n / kRaw;
+            if (use > 0 && !wait_or_abort(bar, &bar.rawempty[slot], (use - 1) & 1, err, -32)) return false;
             mbar_arrive_expect_tx(&bar.rawfull[slot], kRawBytes);
-            // S-CTA: its 64 keys of dim tile q; O-CTA: of its dim tiles (two a chunk), one half of the keys
-            const int key = key0 + (s_role ? kpair : q & 1) * kHalfKeys, tile = s_role ? q : 2 * (2 * (q >> 2) + kpair) + ((q >> 1) & 1);
-            tma_load_4d_at(raw + slot * kRawBytes, &map, &bar.rawfull[slot], 0, key, tile, it.b);
-            ++n;
-            if (++slot == kRaw) {
-                slot = 0;
-                phase ^= 1;
-            }
+            // S-CTA: dim tiles 2 q and 2 q + 1; O-CTA: tile q % 2 of its two in value chunk q / 2
+            tma_load_4d_at(raw + slot * kRawBytes, &map, &bar.rawfull[slot], 0, key0,
+                           s_role ? 2 * q : 2 * (2 * (q >> 1) + kpair) + (q & 1), it.b);
         }
         return true;
     }
@@ -682,43 +679,29 @@ __device__ __forceinline__ uint32_t tmem_lane_addr(uint32_t base, int warp, uint
 // ---- widening (8-bit cache) ------------------------------------------------------------------
 // Registers a warpgroup takes for its role.
 template <int kN> __device__ __forceinline__ void set_regs() {
-    if constexpr (kN > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
-    if constexpr (kN < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+    if constexpr (kN > kRegsLaunchQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+    if constexpr (kN < kRegsLaunchQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
 }
 
-// One warp's share of a raw piece (64 keys x 64 dims): 16 keys, four at a time -- 8 lanes a key, 8
-// codes a lane, one 16-byte chunk of the bf16 tile's row. `bytes`: the two scale bytes of a key in
-// these dims, held by lane src0 + (key of the 16). NaN groups become nan_bits.
-__device__ __forceinline__ void widen_piece(uint32_t raw, uint32_t dst, uint32_t bytes, int src0, uint32_t nan_bits, int lane) {
-    const int sub = lane & 7, kq = lane >> 3;
-    const uint32_t b0 = bytes & 255u, b1 = (bytes >> 8) & 255u, n = (uint32_t)q8::kNaN;
-    const uint32_t f = (b0 == n ? nan_bits : q8::factor(b0)) | ((b1 == n ? nan_bits : q8::factor(b1)) << 16);
-    const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;        // this lane's group of the two
-    // key kq + 4 t: swizzle sub ^ key % 8, the same for all even t and for all odd t
-    const uint32_t d0 = dst + kq * 128 + ((sub ^ kq) << 4), d1 = d0 ^ 64u, r0 = raw + kq * 64 + sub * 8;
-    uint32_t fk[4];
-    uint2 c[4];
+// Two scale bytes as a pair of bf16 factors; a NaN group gives nan_bits.
+__device__ __forceinline__ uint32_t factor_pair(uint32_t bytes, uint32_t nan_bits) {
+    const uint32_t b0 = bytes & 255u, b1 = bytes >> 8, n = (uint32_t)q8::kNaN;
+    return (b0 == n ? nan_bits : q8::factor(b0)) | ((b1 == n ? nan_bits : q8::factor(b1)) << 16);
+}
+
+__device__ __forceinline__ uint32_t factor_high_pair(uint32_t bytes) {
+    const uint32_t b0 = bytes & 255u, b1 = bytes >> 8, n = (uint32_t)q8::kNaN;
+    return (b0 == n ? 0x3f80u : q8::factor_high(b0)) | ((b1 == n ? 0x3f80u : q8::factor_high(b1)) << 16);
+}
+
+__device__ __forceinline__ bool any_high(uint32_t word) {      // some scale byte above 2^7, NaN apart
+    bool h = false;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) c[t] = ld_shared_v2(r0 + t * 256);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) fk[t] = __byte_perm(__shfl_sync(0xffffffffu, f, src0 + 4 * t + kq), 0u, pick);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const uint4 v = q8::widen8(c[t], fk[t]);
-        st_shared_v4(((t & 1) ? d1 : d0) + 512 * t, v.x, v.y, v.z, v.w);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t b = (word >> (8 * k)) & 255u;
+        h |= b > q8::kHighByte && b != (uint32_t)q8::kNaN;
     }
-    const bool high = (b0 > q8::kHighByte && b0 != n) || (b1 > q8::kHighByte && b1 != n);
-    if (__any_sync(0xffffffffu, high)) {                       // some scale above 2^7: a second product
-        const uint32_t h = (b0 == n ? 0x3f80u : q8::factor_high(b0)) | ((b1 == n ? 0x3f80u : q8::factor_high(b1)) << 16);
-#pragma unroll 1
-        for (int t = 0; t < 4; ++t) {
-            const uint32_t g = __byte_perm(__shfl_sync(0xffffffffu, h, src0 + 4 * t + kq), 0u, pick);
-            const uint32_t a = ((t & 1) ? d1 : d0) + 512 * t;
-            uint32_t v[4];
-            ld_shared_v4(a, v);
-            st_shared_v4(a, q8::mul_bf16x2(v[0], g), q8::mul_bf16x2(v[1], g), q8::mul_bf16x2(v[2], g), q8::mul_bf16x2(v[3], g));
-        }
-    }
+    return h;
 }
 
 template <bool kQ8>
@@ -826,7 +809,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         mbar_init(&bar.o_done, 1);
         mbar_init(&bar.o_free, 2 * kEpiWarps);
         if (kQ8)
-            for (int i = 0; i < kRaw; ++i) { mbar_init(&bar.rawfull[i], 1); mbar_init(&bar.rawempty[i], kWidenWarps); }
+            for (int i = 0; i < kRaw; ++i) { mbar_init(&bar.rawfull[i], 1); mbar_init(&bar.rawempty[i], kWidenWarps / 2); }
         bar.kseen[0] = bar.kseen[1] = -1;
         mbar_init(&bar.sync_bar, 1);
         // one drain commit per MMA issuer that runs: two in the S leader (one for a single
@@ -857,7 +840,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
     // (O-CTA); 12-15 widen the 8-bit cache. (The outer branch is by warpgroup: a warpgroup changes
     // its register share as one.)
     if (warp < 4) {
-        if constexpr (kQ8) set_regs<kRegsQ8[0]>();
+        if constexpr (kQ8) set_regs<kRegsIssueQ8>();
         const int G = bar.work_count;                  // key blocks of this cluster
         if (s_role) {
         // =============================== S-CTA ===============================
@@ -1068,14 +1051,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         if (warp == 0) {
             // ------- TMA producer: this CTA's 128 of each 256 latent columns of V -------
             if (kQ8 && elect_one() && G > 0) {             // codes; the widening warps fill the ring
-                tma_prefetch_desc(&map_ks);
+                tma_prefetch_desc(&map_vs);
                 RawRequests raws;
                 bool going = true;
                 WorkIter w = first_work();
                 Item it;
                 while (going && !aborted(bar) && next_item(p, w, cl, ncl, it))
                     for (int j = 0; j < it.nb && going; ++j)
-                        going = raws.block(bar, map_ks, smem_u32(smem) + kOffRawO, false, kpair, it, j, p.err);
+                        going = raws.block(bar, map_vs, smem_u32(smem) + kOffRawO, false, kpair, it, j, p.err);
             }
             if (!kQ8 && elect_one() && G > 0) {
                 tma_prefetch_desc(&map_vs);
@@ -1267,7 +1250,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         }
         }
     } else if (!kQ8 || warp < 12) {
-        if constexpr (kQ8) set_regs<kRegsQ8[1]>();
+        if constexpr (kQ8) set_regs<kRegsSoftQ8>();
         const int G = bar.work_count;                  // key blocks of this cluster
         if (s_role) {
         const uint32_t tmem_q = tmem;                 // Q_nope: columns [0, 256)
@@ -1582,30 +1565,38 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         }
     } else {
         if constexpr (kQ8) {
-        set_regs<kRegsQ8[3]>();
+        set_regs<kRegsWidenQ8>();
         // ---------------- widening: this CTA's half of every latent chunk -----------------------
-        // Codes come by TMA in raw pieces of 64 keys x 64 dims, eight a block: an S-CTA's are the
-        // eight dim tiles of its 64 keys, an O-CTA's its four dim tiles of either half of the 128
-        // keys; four pieces make a chunk of the bf16 ring. Every warp takes 16 keys of every piece.
-        // The loop over pieces is rolled and small on purpose: loads to registers two chunks ahead
-        // need it unrolled, and that code ran at the speed of instruction fetches (a block took
-        // 10 k clocks against the 3.7 k of its MMAs).
-        const int ww = warp - 12;
+        // Codes come by TMA in raw pieces, four a block; warps 12-15 take pieces 0 and 2, warps 16-19
+        // pieces 1 and 3, so that both work on the same chunk of the bf16 ring (two pieces). A warp
+        // has 16 keys of both tiles of a piece (S) or 32 keys of its one tile (O): eight sets of four
+        // keys, 8 lanes a key, 8 codes a lane -- one 16-byte chunk of the bf16 tile's row. It takes
+        // its codes to registers and gives the slot back at once: the next piece lands while this one
+        // is widened. The loop is rolled and small on purpose: register loads two chunks ahead need
+        // it unrolled, and that code ran at the speed of instruction fetches (10 k clocks a block).
+        const int ww = (warp - 12) & 3, par = (warp - 12) >> 2, sub = lane & 7, kq = lane >> 3;
         const uint32_t ring = smem_u32(smem) + (s_role ? kOffKRing : kOffV);
         const uint32_t slot_bytes = s_role ? kKSlotBytes : kVSlotBytes, nslots = s_role ? kNK : kNV;
         uint64_t *full = s_role ? bar.kfull : bar.vfull, *empty = s_role ? bar.kempty : bar.vempty;
         const uint32_t nan_bits = s_role ? 0x7fc0u : 0u;       // NaN keys, zero values
-        const int total = 8 * bar.work_count;                  // pieces
-        const uint32_t raw = smem_u32(smem) + (s_role ? kOffRawS : kOffRawO);
+        // sets 0-3 and 4-7: the two tiles (S), or keys 0-15 and 16-31 of the warp's (O)
+        const uint32_t raw = smem_u32(smem) + (s_role ? kOffRawS : kOffRawO) + par * kRawBytes + ((s_role ? 16 : 32) * ww + kq) * 64 + sub * 8;
+        const uint32_t raw_step = s_role ? 4096 : 1024, dst_step = s_role ? kKSub : 2048;
+        // in the chunk: this warp's first key's row of its first tile, this lane's swizzled 16 bytes
+        // (keys kq + 4 t: sub ^ key % 8 is the same for all even t and for all odd t)
+        const uint32_t at = (s_role ? 2 * par * kKSub + 16 * ww * 128 : par * kVSub + 32 * ww * 128) + kq * 128 + ((sub ^ kq) << 4);
+        const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;    // this lane's group of a tile's two
+        const int total = 4 * bar.work_count;                  // pieces
         bool ok = true;
-        // scale bytes, a block ahead: 16 keys of the warp (lane % 16), for each half of the lanes the
-        // dims (S) or the keys (O) of one half of the pieces; two words of four bytes
+        // scale bytes, a block ahead, two words of four bytes: S-CTA, of key lane % 16 of the warp's
+        // and the dims of pieces 2 (lane / 16) and + 1; O-CTA, of key lane and the CTA's two chunks
         WorkIter w = first_work();
         Item it;
         int j = 0;
         bool have = next_item(p, w, cl, ncl, it);
         auto load_scales = [&]() {
-            const int x = lane >> 4, key = it.key_base + (it.kb0 + j) * kKeys + (s_role ? kpair : x) * kHalfKeys + 16 * ww + (lane & 15);
+            const int x = lane >> 4, key = it.key_base + (it.kb0 + j) * kKeys +
+                                           (s_role ? kpair * kHalfKeys + 16 * ww + (lane & 15) : 32 * ww + lane);
             uint2 v = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);    // (rows before 0: the codes are zeros)
             if (key >= 0) {
                 const uint32_t *sp = reinterpret_cast<const uint32_t *>(p.c_scale + ((int64_t)it.b * p.L + key) * (kDc / KDT_Q8_GROUP));
@@ -1620,43 +1611,60 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         };
         uint2 sn = make_uint2(0u, 0u), sc = sn;
         if (have) sn = load_scales();
-        int rslot = 0, slot = 0;
-        uint32_t rphase = 0, phase = 0;
+        uint32_t slot = 0, phase = 0, rphase = 0;
         bool refill = false;                                   // the ring's slots have been used before
 #pragma unroll 1
-        for (int n = 0; n < total && ok; ++n) {
-            const int q = n & 7;
-            if (q == 0) {
+        for (int n = par; n < total; n += 2) {
+            const int q = n & 3;
+            if (q == par) {
                 sc = sn;
                 if (have) sn = load_scales();
             }
-            if ((q & 3) == 0 && refill) ok = quick_warp_wait(bar, &empty[slot], phase ^ 1, p.err, -30);
-            ok = ok && quick_warp_wait(bar, &bar.rawfull[rslot], rphase, p.err, -31);
-            if (!ok) break;
-            const uint32_t dst = ring + slot * slot_bytes +
-                                 (s_role ? (q & 3) * kKSub + 16 * ww * 128
-                                         : ((q >> 1) & 1) * kVSub + (64 * (q & 1) + 16 * ww) * 128);
-            const uint32_t word = (s_role ? (q >> 1) & 1 : q >> 2) ? sc.y : sc.x;
-            const uint32_t bytes = (s_role ? q & 1 : (q >> 1) & 1) ? word >> 16 : word & 0xffffu;
-            widen_piece(raw + rslot * kRawBytes + 16 * ww * 64, dst, bytes, 16 * (s_role ? q >> 2 : q & 1), nan_bits, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.rawempty[rslot]);
-            if (++rslot == kRaw) {
-                rslot = 0;
-                rphase ^= 1;
+            if (!(ok = quick_warp_wait(bar, &bar.rawfull[par], rphase, p.err, -31))) break;
+            rphase ^= 1;
+            uint2 c[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c[k] = ld_shared_v2(raw + (k >> 2) * raw_step + (k & 3) * 256);
+            // the piece's scale word; S: one half a tile, O: the half of its tile for all sets
+            const uint32_t word = (s_role ? q & 1 : q >> 1) ? sc.y : sc.x;
+            const uint32_t lo = !s_role && (q & 1) ? word >> 16 : word & 0xffffu, hi = s_role ? word >> 16 : lo;
+            const uint32_t fa = factor_pair(lo, nan_bits), fb = factor_pair(hi, nan_bits);
+            const uint32_t src = kq + (s_role ? 16 * (q >> 1) : 0), src_step = s_role ? 0 : 16;
+            uint32_t f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                f[k] = __byte_perm(__shfl_sync(0xffffffffu, k < 4 ? fa : fb, src + (k >> 2) * src_step + 4 * (k & 3)), 0u, pick);
+            __syncwarp();                                      // every lane has its codes
+            if (lane == 0) mbar_arrive(&bar.rawempty[par]);
+            if (refill && !(ok = quick_warp_wait(bar, &empty[slot], phase ^ 1, p.err, -30))) break;
+            const uint32_t d0 = ring + slot * slot_bytes + at, d1 = d0 ^ 64u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint4 v = q8::widen8(c[k], f[k]);
+                st_shared_v4(((k & 1) ? d1 : d0) + (k >> 2) * dst_step + (k & 3) * 512, v.x, v.y, v.z, v.w);
             }
-            if ((q & 3) == 3) {                                // a chunk of the ring is complete
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote_cta(&full[slot], lead_rank);
-                if (++slot == (int)nslots) {
-                    slot = 0;
-                    phase ^= 1;
-                    refill = true;
+            if (__any_sync(0xffffffffu, any_high(word))) {     // some scale above 2^7: a second product
+                const uint32_t ha = factor_high_pair(lo), hb = factor_high_pair(hi);
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t g = __byte_perm(
+                        __shfl_sync(0xffffffffu, k < 4 ? ha : hb, src + (k >> 2) * src_step + 4 * (k & 3)), 0u, pick);
+                    const uint32_t a = ((k & 1) ? d1 : d0) + (k >> 2) * dst_step + (k & 3) * 512;
+                    uint32_t v[4];
+                    ld_shared_v4(a, v);
+                    st_shared_v4(a, q8::mul_bf16x2(v[0], g), q8::mul_bf16x2(v[1], g), q8::mul_bf16x2(v[2], g), q8::mul_bf16x2(v[3], g));
                 }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_cta(&full[slot], lead_rank);
+            if (++slot == nslots) {
+                slot = 0;
+                phase ^= 1;
+                refill = true;
+            }
         }
-        // the releases of the last chunks, and the copies in flight, have arrived before this CTA may leave
+        // the releases of the last chunks have arrived before this CTA may leave
         if (ok)
             for (int k = 0; k < (int)nslots && k < 2 * bar.work_count; ++k) {
                 const int u = 2 * bar.work_count - 1 - k;      // chunk use
@@ -1880,14 +1888,14 @@ template <bool kQ8> cudaError_t launch(const VerifyParams &vp, cudaStream_t s) {
     CUtensorMap map_ks, map_vs, map_kpe, map_qpe;
     const cuuint64_t L = (cuuint64_t)vp.L;
     if (kQ8) {
-        // codes viewed as [B][8 dim-blocks][L keys][64]: a box lands as [64 keys][64 codes], rows before
-        // row 0 as zeros
+        // codes viewed as [B][8 dim-blocks][L keys][64]: a box of (64, n keys, m blocks) lands as
+        // m consecutive [n][64 codes], rows before row 0 as zeros
         cuuint64_t dims[4] = {64, L, (cuuint64_t)(kDc / 64), (cuuint64_t)vp.B};
         cuuint64_t strides[3] = {(cuuint64_t)kDc, 64, L * kDc};
-        cuuint32_t box[4] = {64, kHalfKeys, 1, 1};
-        if (!make_map(&map_ks, vp.c_kv, 4, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE))
+        cuuint32_t box_k[4] = {64, kHalfKeys, 2, 1}, box_v[4] = {64, kKeys, 1, 1};
+        if (!make_map(&map_ks, vp.c_kv, 4, dims, strides, box_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !make_map(&map_vs, vp.c_kv, 4, dims, strides, box_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE))
             return cudaErrorInvalidValue;
-        map_vs = map_ks;                                           // unused
     } else {
         // c_kv viewed as [B][8 dim-blocks][L keys][64]: a box of (64, n keys, m blocks)
         // lands as m consecutive [n x 64] 128B-swizzled sub-tiles.
