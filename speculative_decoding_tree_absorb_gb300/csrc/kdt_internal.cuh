@@ -121,6 +121,14 @@ cudaError_t launch_vc_proj(const float *o, const void *w_vc, int R, int H, int D
 
 // K5: tree-verify attention over the 8-bit latent cache (kdt_verify_attn_q8), everything
 // validated on the host.
+// Where a CTA's share of the work starts, left by the attention kernel for the merge: in positions
+// of the (row tile, key block) list, with the tile that position is in.
+struct Q8Share {
+    int64_t start, t0, t1;     // the tile's positions [t0, t1)
+    int64_t row0;              // its first query row over all sequences
+    int rows;                  // its rows
+};
+
 struct Q8Params {
     int B, T, H, W;            // W = ceil(T/32) visibility words per query
     int rows_seq;              // T * H
@@ -138,6 +146,7 @@ struct Q8Params {
     float *lse;
     float *part_o, *part_lse;  // [2 * ctas][kQ8Rows] piece states (unused with one CTA)
     int32_t *err;
+    Q8Share *shares;           // [ctas + 1]
     int ctas;
     bool pieces;               // tiles may be cut between CTAs: a second kernel joins their pieces
     bool overlap_vis;          // launched right behind this call's visibility kernel

@@ -91,10 +91,8 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
         off = align_up(off + prow * kDc * sizeof(float));
         p.pl_off = off;
         off = align_up(off + prow * sizeof(float));
-        if (tc) {
-            p.sched_off = off;
-            off = align_up(off + kTcSchedWords * sizeof(int64_t));
-        }
+        p.sched_off = off;
+        off = align_up(off + (tc ? kTcSchedWords * sizeof(int64_t) : (size_t)(p.splits + 1) * sizeof(Q8Share)));
     }
     p.ws_bytes = off;
     p.launches = (a->parent ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
@@ -203,6 +201,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     q.err = a->err;
     q.ctas = p.ctas;
     q.pieces = p.pieces;
+    q.shares = reinterpret_cast<Q8Share *>(ws + p.sched_off);
     q.overlap_vis = a->parent != nullptr;
     return launch_verify_q8_rows(q, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }

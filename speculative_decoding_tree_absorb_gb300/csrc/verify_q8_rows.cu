@@ -77,6 +77,10 @@ struct Bars {
     int work[4];                // this CTA's share: blocks, first sequence, tile, block
 };
 
+// Visibility words of a block's tree keys: up to 64 nodes (those of the tile's rows, from node i0
+// on), kVisWords words each from word w0 on (128 keys touch at most five).
+constexpr int kVisWords = 5;
+
 struct Shared {
     Bars bar;
     alignas(16) float nm[kRowsT];   // minus the reference (read as float4)
@@ -86,6 +90,7 @@ struct Shared {
     alignas(16) float inv[kRowsT];
     float red[4][kRowsT];       // per key quadrant
     uint32_t bad[2][kKeysB];    // keys with a NaN group, by block parity
+    uint32_t vis[kRowsT * kVisWords];
 };
 
 __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
@@ -177,7 +182,8 @@ __device__ __forceinline__ bool advance(const Q8Params &p, Item &it) {
 }
 
 // Positions: sequence-major, tile-major, block order; W of them. CTA c takes
-// [W c / C, W (c + 1) / C). One warp finds its share's first item {left, b, rt, kb}.
+// [W c / C, W (c + 1) / C). One warp finds its share's first item {left, b, rt, kb}, and leaves for the
+// merge where the share starts and which tile that is in.
 __device__ __forceinline__ void find_share(const Q8Params &p, int64_t C, int64_t c, int lane, int *out) {
     int64_t W = 0;
     for (int b = lane; b < p.B; b += 32) W += (int64_t)p.tiles_seq * blocks_of(p, b);
@@ -187,6 +193,11 @@ __device__ __forceinline__ void find_share(const Q8Params &p, int64_t C, int64_t
     if (lane == 0) {
         out[0] = (int)(s1 - s0);
         out[1] = out[2] = out[3] = 0;
+        if (p.pieces) {
+            p.shares[c].start = s0;
+            p.shares[c].t0 = p.shares[c].t1 = s0;             // (an empty share behind the last position)
+            if (c == C - 1) p.shares[C].start = W;
+        }
     }
     __syncwarp();
     int64_t before = 0;
@@ -203,9 +214,16 @@ __device__ __forceinline__ void find_share(const Q8Params &p, int64_t C, int64_t
         const int64_t at = before + incl - w;
         const bool hit = s0 >= at && s0 < at + w;
         if (hit) {
+            const int rt = (int)((s0 - at) / nb);
             out[1] = b;
-            out[2] = (int)((s0 - at) / nb);
-            out[3] = (int)((s0 - at) % nb);
+            out[2] = rt;
+            out[3] = (int)(s0 - at - (int64_t)rt * nb);
+            if (p.pieces) {
+                p.shares[c].t0 = at + (int64_t)rt * nb;
+                p.shares[c].t1 = p.shares[c].t0 + nb;
+                p.shares[c].row0 = (int64_t)b * p.rows_seq + (int64_t)rt * kRowsT;
+                p.shares[c].rows = min(kRowsT, p.rows_seq - rt * kRowsT);
+            }
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
         if (__any_sync(0xffffffffu, hit)) break;
@@ -216,15 +234,15 @@ __device__ __forceinline__ void find_share(const Q8Params &p, int64_t C, int64_t
 // Which of the 32 rows from row0 on see tree key t (t < 0: a prefix key, all of them; t >= T:
 // behind the tree, none): bit r for row row0 + r, whose query is node (row0 + r) / H. Rows at or
 // beyond rows_seq get any value.
-__device__ __forceinline__ uint32_t seen_by(const Q8Params &p, const Item &it, int t, int row0) {
+__device__ __forceinline__ uint32_t seen_by(const Q8Params &p, const uint32_t *words, int i0, int w0, int t, int row0) {
     if (t < 0) return ~0u;
     if (t >= p.T) return 0u;
     uint32_t see = 0u;
     int i = row0 / p.H, left = p.H - (row0 - i * p.H);
-    for (int r = 0; r < 32 && i < p.T; ++i) {                // one node at a time: `left` rows of it
-        const uint32_t bits = __ldg(p.vis + ((int64_t)it.b * p.T + i) * p.W + (t >> 5));
+    const uint32_t *word = words + (i - i0) * kVisWords + (t >> 5) - w0;
+    for (int r = 0; r < 32 && i < p.T; ++i, word += kVisWords) {     // one node at a time: `left` rows of it
         const int n = min(left, 32 - r);
-        if ((bits >> (t & 31)) & 1u) see |= (0xffffffffu >> (32 - n)) << r;
+        if ((*word >> (t & 31)) & 1u) see |= (0xffffffffu >> (32 - n)) << r;
         r += n;
         left = p.H;
     }
@@ -301,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         const int srow = (int)threadIdx.x - 32 * kSoft0;
         const uint32_t prow = smem + kOffR + key * 128;
         bool ok = true, vis_ready = false;
-        // this thread's 32 scores of the block at key0, scaled, plus off[row]; -inf where hidden
-        auto scores = [&](int key0, const float *off, float (&x)[32]) {
+        // this thread's 32 scores of the block, scaled, plus off[row]; -inf where hidden
+        auto scores = [&](const float *off, bool masked, uint32_t see, float (&x)[32]) {
             uint32_t raw[32];
             tmem_ld32(lane_addr(tmem + kColS, warp, 32 * half), raw);
             tmem_wait_ld();
@@ -318,12 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
 #pragma unroll
                 for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(0x7fffffffu);
             }
-            if (key0 + kKeysB > it.P) {                      // the block holds tree keys, or rows behind them
-                if (!vis_ready) {
-                    griddep_wait();
-                    vis_ready = true;
-                }
-                const uint32_t see = seen_by(p, it, key0 + key - it.P, it.rt * kRowsT + 32 * half);
+            if (masked) {
 #pragma unroll
                 for (int r = 0; r < 32; ++r) x[r] = (see >> r) & 1u ? x[r] : -INFINITY;
             }
@@ -367,15 +380,34 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             barrier_or<1, 256>(false);
             bool fail = false;
             for (int j = 0; j < it.nb; ++j, ++g) {
+                // which rows see this thread's key, when the block holds tree keys, or rows behind them
                 const int key0 = (it.kb + j) * kKeysB;
+                const bool masked = key0 + kKeysB > it.P;
+                uint32_t see = ~0u;
+                if (masked) {
+                    if (!vis_ready) {
+                        griddep_wait();
+                        vis_ready = true;
+                    }
+                    const int i0 = it.rt * kRowsT / p.H, w0 = max(key0 - it.P, 0) >> 5;
+                    for (int e = srow; e < kRowsT * kVisWords; e += 32 * kSoftWarps) {
+                        const int i = i0 + e / kVisWords, wd = w0 + e % kVisWords;
+                        sh.vis[e] = i < p.T && wd < p.W ? __ldg(p.vis + ((int64_t)it.b * p.T + i) * p.W + wd) : 0u;
+                    }
+                    barrier_or<1, 256>(false);
+                    see = seen_by(p, sh.vis, i0, w0, key0 + key - it.P, it.rt * kRowsT + 32 * half);
+                }
                 ok = ok && warp_wait(bar, &bar.sfull, g & 1, p.err, -41);
                 float x[32];                                 // score - reference
-                const float *off = sh.nm;                    // (+inf for a row without a reference yet)
+                // minus the reference, +inf for a row without one yet; an item's first block goes straight
+                // to the maxima
+                const float *off = j > 0 ? sh.nm : sh.zero;
                 bool raised = false;
+                if (j == 0 && (fail = barrier_or<1, 256>(!ok))) break;
                 if (ok) tc_fence_after();
 #pragma unroll 1
                 for (;;) {
-                    if (ok) scores(key0, off, x);
+                    if (ok) scores(off, masked, see, x);
                     if (off == sh.nm) {
                         if (raised) break;
                         float top = -INFINITY;
@@ -467,25 +499,51 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             }
             barrier_or<1, 256>(false);
             tc_fence_after();
-            const int dim = (key & ~3) | ((key & 1) << 1) | ((key >> 1) & 1);    // widening's order of the dims
             const int rows = min(32, p.rows_seq - it.rt * kRowsT - 32 * half);   // of this warp's 32 (may be <= 0)
+            // A thread has one dim of 32 rows. Four lanes exchange 4 x 4 values (two rounds), so that
+            // each holds the four dims of one row and a store instruction covers four rows (stores of
+            // single values took 11 k clocks an item); widening's order of the dims is undone on the way.
+            const bool up2 = lane & 2, up1 = lane & 1;
+            // 16 rows at a time, a small loop: the code of an item's end is mostly fetched anew
 #pragma unroll 1
-            for (int q = 0; q < kPairs; ++q) {
-                uint32_t o[32];
-                tmem_ld32(lane_addr(tmem, warp, kRowsT * q + 32 * half), o);
+            for (int e = 0; e < 2 * kPairs; ++e) {
+                const int q = e >> 1, r0 = 16 * (e & 1);
+                uint32_t o[16];
+                tmem_ld16(lane_addr(tmem, warp, kRowsT * q + 32 * half + r0), o);
                 tmem_wait_ld();
-                const int64_t at = (first + 32 * half) * kDc + 128 * q + dim;
-                if (whole && kBf16Out) {
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at;
+                const int64_t at = (first + 32 * half + r0 + (lane & 3)) * kDc + 128 * q + 32 * (warp & 3) + (lane & ~3);
+                // round by round for all four groups of rows: a store's branch between two groups would
+                // make their shuffles wait for one another
+                float keep[8], got[8];                       // own dim of rows 2 up2 and + 1, and lane ^ 2's dim of them
 #pragma unroll
-                    for (int r = 0; r < 32; ++r)
-                        if (r < rows) dst[r * kDc] = __float2bfloat16_rn(__uint_as_float(o[r]) * sh.inv[32 * half + r]);
-                } else {
-                    float *dst = (whole ? static_cast<float *>(p.out) : p.part_o) + at;
-#pragma unroll
-                    for (int r = 0; r < 32; ++r)
-                        if (r < rows) dst[r * kDc] = __uint_as_float(o[r]) * sh.inv[32 * half + r];
+                for (int m = 0; m < 4; ++m) {
+                    const float4 iv = *reinterpret_cast<const float4 *>(sh.inv + 32 * half + r0 + 4 * m);
+                    const float v0 = __uint_as_float(o[4 * m]) * iv.x, v1 = __uint_as_float(o[4 * m + 1]) * iv.y,
+                                v2 = __uint_as_float(o[4 * m + 2]) * iv.z, v3 = __uint_as_float(o[4 * m + 3]) * iv.w;
+                    got[2 * m] = __shfl_xor_sync(0xffffffffu, up2 ? v0 : v2, 2);
+                    got[2 * m + 1] = __shfl_xor_sync(0xffffffffu, up2 ? v1 : v3, 2);
+                    keep[2 * m] = up2 ? v2 : v0;
+                    keep[2 * m + 1] = up2 ? v3 : v1;
                 }
+                float4 w[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float b0 = __shfl_xor_sync(0xffffffffu, up1 ? keep[2 * m] : keep[2 * m + 1], 1);
+                    const float b1 = __shfl_xor_sync(0xffffffffu, up1 ? got[2 * m] : got[2 * m + 1], 1);
+                    const float own = up1 ? keep[2 * m + 1] : keep[2 * m], far = up1 ? got[2 * m + 1] : got[2 * m];
+                    // row 2 up2 + up1; the four lanes hold dims 0, 2, 1, 3
+                    const float e0 = up1 ? b0 : own, e1 = up1 ? own : b0, f0 = up1 ? b1 : far, f1 = up1 ? far : b1;
+                    w[m] = make_float4(up2 ? f0 : e0, up2 ? e0 : f0, up2 ? f1 : e1, up2 ? e1 : f1);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (r0 + 4 * m + (lane & 3) < rows) {
+                        if (whole && kBf16Out)
+                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 4 * m * kDc) =
+                                make_uint2(q8::pack_bf16(w[m].x, w[m].y), q8::pack_bf16(w[m].z, w[m].w));
+                        else
+                            *reinterpret_cast<float4 *>((whole ? static_cast<float *>(p.out) : p.part_o) + at + 4 * m * kDc) = w[m];
+                    }
             }
             tc_fence_before();
             __syncwarp();
@@ -691,44 +749,130 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the tiles that a share boundary cut: CTA (tile, y) takes rows 8 y ..
-// + 8, a warp a row. The tile spans positions [t0, t1), the shares meeting it are c_a .. c_b
-// (one: it was written whole), each with a normalised state (o, lse): o = sum_k e^(lse_k -
-// M) o_k / sum_k e^(lse_k - M). A NaN in a piece's lse reaches the row.
+// Joins the pieces of the tiles that a share boundary cut. CTA (c - 1, y) serves boundary c (where
+// share c begins) when it is the first inside its tile, rows kMergeRows y .. of it, two warps a row
+// (256 columns each: with many pieces the loads of one row are a chain, and more of them in flight
+// is what counts). The shares meeting the tile, c - 1 and on, each left a normalised state (o, lse):
+// o = sum_k e^(lse_k - M) o_k / sum_k e^(lse_k - M). A NaN in a piece's lse reaches the row. The
+// shares' bounds are read, not computed again: the 64-bit divisions for them took 30 us.
+constexpr int kMergeRows = 4;
+
 template <bool kBf16Out>
-__global__ void __launch_bounds__(256) merge_q8_rows_kernel(const Q8Params p) {
+__global__ void __launch_bounds__(64 * kMergeRows) merge_q8_rows_kernel(const Q8Params p) {
     griddep_wait();
-    const int tile = blockIdx.x, b = tile / p.tiles_seq, rt = tile % p.tiles_seq;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t C = p.ctas;
-    int64_t tot = 0, bef = 0;
-    for (int k = lane; k < p.B; k += 32) {
-        const int64_t w = (int64_t)p.tiles_seq * blocks_of(p, k);
-        tot += w;
-        if (k < b) bef += w;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        tot += __shfl_xor_sync(0xffffffffu, tot, off);
-        bef += __shfl_xor_sync(0xffffffffu, bef, off);
-    }
-    const int64_t W = tot;
-    const int nblk = blocks_of(p, b);
-    const int64_t t0 = bef + (int64_t)rt * nblk, t1 = t0 + nblk;
-    const int64_t ca = ((t0 + 1) * C - 1) / W, cb = (t1 * C - 1) / W;      // shares of positions t0 and t1 - 1
-    if (ca == cb) return;
-    const int row = blockIdx.y * 8 + warp, r = rt * kRowsT + row;
-    if (r >= p.rows_seq) return;
-    // share c's slot: 2c when the share starts at or after t0 (the tile is its first item), else 2c + 1
-    auto slot = [&](int64_t c) -> int64_t {
-        const int64_t s = W * c / C;
-        return c > cb || s == W * (c + 1) / C ? -1 : (s >= t0 ? 2 * c : 2 * c + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.ctas, c = blockIdx.x + 1;
+    const Q8Share sh = p.shares[c];
+    const int64_t before = p.shares[c - 1].start;
+    if (sh.start == sh.t0 || before > sh.t0) return;          // between two tiles, or not the first inside this one
+    const int row = blockIdx.y * kMergeRows + (warp >> 1), col = 256 * (warp & 1) + 4 * lane;
+    if (row >= sh.rows) return;
+    // share k's slot: 2k when it starts in the tile (which is its first item then), else 2k + 1; -1: it does
+    // not meet the tile, or is empty
+    auto slot = [&](int k) {
+        if (k >= C) return -1;
+        const int64_t a = p.shares[k].start, e = p.shares[k + 1].start;
+        return a >= sh.t1 || a == e ? -1 : (a >= sh.t0 ? 2 * k : 2 * k + 1);
     };
+    // two passes over the shares, 32 at a time: the largest lse, then the weighted sums
     float M = -INFINITY;
     bool nan = false;
-    for (int64_t base = ca; base <= cb; base += 32) {
-        const int64_t sl = slot(base + lane);
-        const float v = sl >= 0 ? p.part_lse[sl * kRowsT + row] : -INFINITY;
+    for (int base = c - 1; base < C && p.shares[base].start < sh.t1; base += 32) {
+        const int sl = slot(base + lane);
+        const float v = sl >= 0 ? p.part_lse[(int64_t)sl * kRowsT + row] : -INFINITY;
+        nan |= v != v;
+        M = fmaxf(M, v);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    nan = __any_sync(0xffffffffu, nan);
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float S = nan ? __uint_as_float(0x7fffffffu) : 0.f;
+    if (M > -INFINITY)
+        for (int base = c - 1; base < C && p.shares[base].start < sh.t1; base += 32) {
+            const int sl = slot(base + lane);
+            const float v = sl >= 0 ? p.part_lse[(int64_t)sl * kRowsT + row] : -INFINITY;
+            const float wt = v == -INFINITY ? 0.f : __expf(v - M);
+            float ws = wt;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+            S += ws;
+            // the pieces that count (weight 0: no visible key, no such share), their loads independent
+            uint32_t live = __ballot_sync(0xffffffffu, wt != 0.f);
+            while (live) {
+                float4 a[4], d[4];
+                float wk[4];
+                int n = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wk[u] = 0.f;
+                    if (!live) continue;                      // (uniform)
+                    const int k = __ffs(live) - 1;
+                    live &= live - 1;
+                    wk[u] = __shfl_sync(0xffffffffu, wt, k);
+                    const float4 *src =
+                        reinterpret_cast<const float4 *>(p.part_o + ((int64_t)__shfl_sync(0xffffffffu, sl, k) * kRowsT + row) * kDc + col);
+                    a[u] = src[0];
+                    d[u] = src[32];
+                    n = u + 1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u >= n) break;
+                    acc[0] = make_float4(fmaf(wk[u], a[u].x, acc[0].x), fmaf(wk[u], a[u].y, acc[0].y), fmaf(wk[u], a[u].z, acc[0].z),
+                                         fmaf(wk[u], a[u].w, acc[0].w));
+                    acc[1] = make_float4(fmaf(wk[u], d[u].x, acc[1].x), fmaf(wk[u], d[u].y, acc[1].y), fmaf(wk[u], d[u].z, acc[1].z),
+                                         fmaf(wk[u], d[u].w, acc[1].w));
+                }
+            }
+        }
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const int64_t grow = sh.row0 + row;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 v = make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
+        if (kBf16Out)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + grow * kDc + col + 128 * h) =
+                make_uint2(q8::pack_bf16(v.x, v.y), q8::pack_bf16(v.z, v.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + grow * kDc + col + 128 * h) = v;
+    }
+    if (col == 0 && p.lse) p.lse[grow] = S == 0.f ? -INFINITY : M + logf(S);
+}
+
+// The same for few tiles cut into many pieces (one short batch over a long cache): CTA (tile, row),
+// its eight warps take every eighth piece with all 512 columns, and meet in shared memory.
+template <bool kBf16Out>
+__global__ void __launch_bounds__(256) merge_q8_deep_kernel(const Q8Params p) {
+    griddep_wait();
+    __shared__ float part[8][kDc];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.ctas;
+    const int b = blockIdx.x / p.tiles_seq, rt = blockIdx.x % p.tiles_seq, row = blockIdx.y;
+    const int64_t grow = (int64_t)b * p.rows_seq + (int64_t)rt * kRowsT + row;
+    if (rt * kRowsT + row >= p.rows_seq) return;
+    // the first share that starts inside the tile
+    int c = -1;
+    for (int base = 1; base < C && c < 0; base += 32) {
+        const int k = base + lane;
+        const bool in = k < C && p.shares[k].row0 == grow - row && p.shares[k].start > p.shares[k].t0 &&
+                        p.shares[k].start < p.shares[k].t1;
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        if (m) c = base + __ffs(m) - 1;
+    }
+    if (c < 0) return;                                        // not cut
+    const int64_t t0 = p.shares[c].t0, t1 = p.shares[c].t1;
+    auto slot = [&](int k) {
+        if (k >= C) return -1;
+        const int64_t a = p.shares[k].start, e = p.shares[k + 1].start;
+        return a >= t1 || a == e ? -1 : (a >= t0 ? 2 * k : 2 * k + 1);
+    };
+    // the share before may be empty: the tile's first piece is the last non-empty one's
+    int first = c - 1;
+    while (first > 0 && p.shares[first].start == p.shares[first + 1].start) --first;
+    float M = -INFINITY;
+    bool nan = false;
+    for (int base = first; base < C && p.shares[base].start < t1; base += 32) {
+        const int sl = slot(base + lane);
+        const float v = sl >= 0 ? p.part_lse[(int64_t)sl * kRowsT + row] : -INFINITY;
         nan |= v != v;
         M = fmaxf(M, v);
     }
@@ -740,43 +884,46 @@ __global__ void __launch_bounds__(256) merge_q8_rows_kernel(const Q8Params p) {
     for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     float S = nan ? __uint_as_float(0x7fffffffu) : 0.f;
     if (M > -INFINITY)
-        for (int64_t base = ca; base <= cb; base += 32) {
-            const int64_t sl = slot(base + lane);
-            const float v = sl >= 0 ? p.part_lse[sl * kRowsT + row] : -INFINITY;
+        for (int base = first; base < C && p.shares[base].start < t1; base += 32) {
+            const int sl = slot(base + lane);
+            const float v = sl >= 0 ? p.part_lse[(int64_t)sl * kRowsT + row] : -INFINITY;
             const float wt = v == -INFINITY ? 0.f : __expf(v - M);
             float ws = wt;
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
             S += ws;
-            const int cnt = (int)min((int64_t)32, cb - base + 1);
-#pragma unroll 4
-            for (int k = 0; k < cnt; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wt, k);
-                const int64_t sk = __shfl_sync(0xffffffffu, sl, k);
-                if (sk < 0 || wk == 0.f) continue;           // the same for the whole warp
-                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (sk * kRowsT + row) * kDc) + lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 v4 = src[32 * q];
-                    acc[q].x = fmaf(wk, v4.x, acc[q].x);
-                    acc[q].y = fmaf(wk, v4.y, acc[q].y);
-                    acc[q].z = fmaf(wk, v4.z, acc[q].z);
-                    acc[q].w = fmaf(wk, v4.w, acc[q].w);
+            for (int u = 0; u < 4; ++u) {
+                const float wk = __shfl_sync(0xffffffffu, wt, warp + 8 * u);
+                const int sk = __shfl_sync(0xffffffffu, sl, warp + 8 * u);
+                if (wk != 0.f) {
+                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + ((int64_t)sk * kRowsT + row) * kDc) + lane;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 d = src[32 * q];
+                        acc[q] = make_float4(fmaf(wk, d.x, acc[q].x), fmaf(wk, d.y, acc[q].y), fmaf(wk, d.z, acc[q].z), fmaf(wk, d.w, acc[q].w));
+                    }
                 }
             }
         }
-    const float inv = S == 0.f ? 0.f : 1.f / S;
-    const int64_t grow = (int64_t)b * p.rows_seq + r;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 v = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
-        if (kBf16Out)
-            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + grow * kDc)[32 * q + lane] =
-                make_uint2(q8::pack_bf16(v.x, v.y), q8::pack_bf16(v.z, v.w));
-        else
-            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + grow * kDc)[32 * q + lane] = v;
+    for (int q = 0; q < 4; ++q) reinterpret_cast<float4 *>(part[warp])[32 * q + lane] = acc[q];
+    __syncthreads();
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 x = reinterpret_cast<const float2 *>(part[k])[threadIdx.x];
+        v.x += x.x;
+        v.y += x.y;
     }
-    if (lane == 0 && p.lse) p.lse[grow] = S == 0.f ? -INFINITY : M + logf(S);
+    v.x *= inv;
+    v.y *= inv;
+    if (kBf16Out)
+        reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + grow * kDc)[threadIdx.x] = q8::pack_bf16(v.x, v.y);
+    else
+        reinterpret_cast<float2 *>(static_cast<float *>(p.out) + grow * kDc)[threadIdx.x] = v;
+    if (threadIdx.x == 0 && p.lse) p.lse[grow] = S == 0.f ? -INFINITY : M + logf(S);
 }
 
 template <bool kBf16Out> cudaError_t launch(const Q8Params &p, cudaStream_t s) {
@@ -797,12 +944,15 @@ template <bool kBf16Out> cudaError_t launch(const Q8Params &p, cudaStream_t s) {
     if ((e = cudaLaunchKernelEx(&cfg, verify_q8_rows_kernel<kBf16Out>, p)) != cudaSuccess) return e;
     if (p.pieces) {
         cudaLaunchConfig_t mc = {};
-        mc.gridDim = dim3((unsigned)((int64_t)p.B * p.tiles_seq), kRowsT / 8);
-        mc.blockDim = dim3(256);
+        // eight or more pieces a tile: their loads are what takes the time (two tiles of 65 pieces: 17 us against 28)
+        const int64_t tiles = (int64_t)p.B * p.tiles_seq;
+        const bool deep = tiles * 8 <= p.ctas;
+        mc.gridDim = deep ? dim3((unsigned)tiles, kRowsT) : dim3((unsigned)(p.ctas - 1), kRowsT / kMergeRows);
+        mc.blockDim = dim3(deep ? 256 : 64 * kMergeRows);
         mc.stream = s;
         mc.attrs = pdl;
         mc.numAttrs = 1;
-        e = cudaLaunchKernelEx(&mc, merge_q8_rows_kernel<kBf16Out>, p);
+        e = cudaLaunchKernelEx(&mc, deep ? merge_q8_deep_kernel<kBf16Out> : merge_q8_rows_kernel<kBf16Out>, p);
     }
     return e;
 }
