@@ -139,7 +139,8 @@ struct Q8Params {
     const uint8_t *c_q8, *c_scale;
     const __nv_bfloat16 *k_pe;
     const int32_t *prefix_len;
-    const uint32_t *vis;       // [B,T,W]
+    const uint32_t *vis;       // or, for T <= 32, parent
+    const int32_t *parent;       // [B,T,W]
     float scale_log2;          // scale * log2(e)
     void *out;                 // bf16 or float32
     bool out_bf16;

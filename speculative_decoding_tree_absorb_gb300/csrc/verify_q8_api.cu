@@ -15,14 +15,20 @@ struct Q8Plan {
     int impl = KDT_IMPL_Q8_ROWS;
     int ctas = 0, launches = 0;
     int tiles_seq = 0;
+    bool vis = false;                      // the visibility kernel finds the words first
     bool pieces = false;                   // a second kernel joins the pieces of what the split cut
     int splits = 0;                        // CTAs, or 4-CTA clusters, the work is shared among
     size_t vis_off = 0, po_off = 0, pl_off = 0, sched_off = 0, ws_bytes = 0;
 };
 
-// Kernel by rows a sequence: the 4-CTA cluster kernel takes 256 rows of a sequence at a time, the
-// rows kernel 64 on one SM.
-bool many_rows(int tiles, int units) { return tiles > 2 * units; }
+// Which kernel. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 4.0 us on one SM and
+// reads the cache again for every 64 rows; a cluster takes (256 rows, 128 keys) in 2.4 us on 4 SMs, but
+// its set-up, schedule and drain are longer: 45 us against 13. Measured, rows kernel / clusters, us:
+// 8 sequences of 8 k keys, 128 rows 54 / 84, 384 rows 103 / 115, 512 rows 129 / 117; 8 sequences of
+// 8 k keys and 4096 rows 876 / 567; one of 1000 keys and 4096 rows 40 / 60.
+bool rows_cheaper(int64_t pairs, int64_t unit_blocks) {
+    return 13.0 + 4.0 * (double)pairs / sm_count() < 45.0 + 2.4 * (double)unit_blocks / tc_q8_max_clusters();
+}
 
 kdt_status check_args(const kdt_verify_q8_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;
@@ -62,9 +68,11 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
     const int rows_seq = a->T * a->H;
     p.tiles_seq = (rows_seq + kQ8Rows - 1) / kQ8Rows;
     const int units_seq = (rows_seq + tc_rows_per_unit() - 1) / tc_rows_per_unit();
-    p.impl = a->impl != KDT_IMPL_AUTO ? a->impl : (many_rows(p.tiles_seq, units_seq) ? KDT_IMPL_TCGEN05 : KDT_IMPL_Q8_ROWS);
-    const bool tc = p.impl == KDT_IMPL_TCGEN05;
     const int nblk = (a->max_kv_len + kQ8Keys - 1) / kQ8Keys;
+    p.impl = a->impl != KDT_IMPL_AUTO ? a->impl
+             : rows_cheaper((int64_t)a->B * p.tiles_seq * nblk, (int64_t)a->B * units_seq * nblk) ? KDT_IMPL_Q8_ROWS
+                                                                                                  : KDT_IMPL_TCGEN05;
+    const bool tc = p.impl == KDT_IMPL_TCGEN05;
     int piece_rows;
     if (tc) {
         if ((int64_t)a->B * rows_seq > INT32_MAX || a->kv_row_stride > INT32_MAX) return KDT_ERR_BAD_SHAPE;
@@ -84,7 +92,8 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
     // a tile of one block is never cut
     p.pieces = p.splits > 1 && (tc || nblk > 1);
     size_t off = 0;
-    if (a->parent) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
+    p.vis = a->parent && (tc || a->T > 32);                   // the rows kernel walks a short tree itself
+    if (p.vis) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
     if (p.pieces) {
         const size_t prow = (size_t)2 * p.splits * piece_rows;
         p.po_off = off;
@@ -95,7 +104,7 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
         off = align_up(off + (tc ? kTcSchedWords * sizeof(int64_t) : (size_t)(p.splits + 1) * sizeof(Q8Share)));
     }
     p.ws_bytes = off;
-    p.launches = (a->parent ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
+    p.launches = (p.vis ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
     *out = p;
     return KDT_OK;
 }
@@ -136,7 +145,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
         return st;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const uint32_t *vis = a->vis;
-    if (a->parent) {
+    if (p.vis) {
         uint32_t *bits = reinterpret_cast<uint32_t *>(ws + p.vis_off);
         if (launch_build_visibility(a->parent, a->B, a->T, bits, a->err, stream) != cudaSuccess) return KDT_ERR_CUDA;
         vis = bits;
@@ -172,7 +181,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
         v.num_splits = p.splits;
         v.blocks_per_split = 0;
         v.err = a->err;
-        v.overlap_vis = a->parent != nullptr;
+        v.overlap_vis = p.vis;
         return launch_verify_tc_q8(v, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
     }
     Q8Params q = {};
@@ -192,6 +201,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     q.k_pe = static_cast<const __nv_bfloat16 *>(a->k_pe);
     q.prefix_len = a->prefix_len;
     q.vis = vis;
+    q.parent = p.vis ? nullptr : a->parent;
     q.scale_log2 = a->scale * 1.4426950408889634f;
     q.out = a->out;
     q.out_bf16 = a->out_dtype == KDT_BF16;
@@ -202,7 +212,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     q.ctas = p.ctas;
     q.pieces = p.pieces;
     q.shares = reinterpret_cast<Q8Share *>(ws + p.sched_off);
-    q.overlap_vis = a->parent != nullptr;
+    q.overlap_vis = p.vis;
     return launch_verify_q8_rows(q, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
 

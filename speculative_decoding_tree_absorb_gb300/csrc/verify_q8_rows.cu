@@ -249,6 +249,26 @@ __device__ __forceinline__ uint32_t seen_by(const Q8Params &p, const uint32_t *w
     return see;
 }
 
+// One warp finds the words of a tree of at most 32 nodes (one word a node) from its parents, lane i
+// those of node i's ancestors, for the tile's nodes from i0 on. It saves the launch of the visibility
+// kernel: XX us of YY for one short tree. A malformed entry ends its walks and is recorded, as there.
+__device__ __forceinline__ void walk_tree(const Q8Params &p, int b, int lane, int i0, uint32_t *words) {
+    const int par = lane < p.T ? __ldg(p.parent + (int64_t)b * p.T + lane) : -1;
+    uint32_t m = 0u;
+    int at = lane;
+    bool on = lane < p.T;
+    while (__any_sync(0xffffffffu, on)) {
+        const int up = __shfl_sync(0xffffffffu, par, at);
+        if (on) {
+            m |= 1u << at;
+            if (up < -1 || up >= at) record_error(p.err, (int32_t)((int64_t)b * p.T + at + 1));
+            on = up >= 0 && up < at;
+            at = on ? up : at;
+        }
+    }
+    if (lane >= i0) words[(lane - i0) * kVisWords] = m;
+}
+
 // x[r] of 32 lanes reduced over the lanes for all 32 r at once: lane r gets row r's result.
 // Step `off` exchanges the half of the array that the other lane keeps.
 template <typename Op>
@@ -390,6 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                         vis_ready = true;
                     }
                     const int i0 = it.rt * kRowsT / p.H, w0 = max(key0 - it.P, 0) >> 5;
+                    if (p.parent) {
+                        if (srow < 32) walk_tree(p, it.b, lane, i0, sh.vis);
+                    } else
                     for (int e = srow; e < kRowsT * kVisWords; e += 32 * kSoftWarps) {
                         const int i = i0 + e / kVisWords, wd = w0 + e % kVisWords;
                         sh.vis[e] = i < p.T && wd < p.W ? __ldg(p.vis + ((int64_t)it.b * p.T + i) * p.W + wd) : 0u;

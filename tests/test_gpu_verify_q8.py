@@ -225,7 +225,7 @@ def test_captured_graph_two_streams_and_fresh_inputs(kdt, T, H, prefix):
 
 def test_not_device_memory_is_refused(kdt):
     import torch
-    d = _inputs(71, 1, 8, [10])
+    d = _inputs(71, 33, 8, [10])            # a tree whose visibility takes a workspace
     pre = torch.tensor([10], dtype=torch.int32)
     with pytest.raises(kdt.KdtError) as e:
         kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre.pin_memory(),
@@ -236,3 +236,22 @@ def test_not_device_memory_is_refused(kdt):
                            parent=torch.from_numpy(d["parent"]).cuda(),
                            workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[128:])
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+@pytest.mark.parametrize("T", [9, 32, 33])
+def test_malformed_parents_are_recorded(kdt, T, impl):
+    import torch
+    d = _inputs(72, T, 4, [10, 0, 130])
+    good = d["parent"].copy()
+    d["parent"][1, 4], d["parent"][2, 6] = 4, -2            # its own parent; below -1
+    good[1, 4] = good[2, 6] = -1                            # a walk ends there
+    err = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    got = []
+    for par in (d["parent"], good):
+        got.append(kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre,
+                                      parent=torch.from_numpy(par).cuda(), max_kv_len=130 + T, impl=impl, err=err))
+        assert int(err.item()) == (T + 4 + 1 if par is not good else 0)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

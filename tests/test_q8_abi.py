@@ -110,25 +110,29 @@ def test_verify_q8_refusals(kdt):
     for kw in ("q_nope", "q_pe", "c_q8", "c_scale", "k_pe", "prefix_len", "out", "parent"):
         assert _verify(kdt, **{kw: None}) == K.KDT_ERR_NULL_ARG, kw
     assert _verify(kdt, vis=0x90000) == K.KDT_ERR_NULL_ARG                      # both mask inputs
-    assert _verify(kdt) == K.KDT_ERR_WORKSPACE
-    need = kdt.verify_attn_q8_workspace_size(2, 9, 8, 46)          # the visibility bits
+    assert kdt.verify_attn_q8_workspace_size(2, 32, 8, 69, impl="q8_rows", num_splits=1) == 0
+    need = kdt.verify_attn_q8_workspace_size(2, 33, 8, 70, impl="q8_rows", num_splits=1)   # the visibility bits
     assert need > 0
-    assert _verify(kdt, ws=(0x100000, need - 1)) == K.KDT_ERR_WORKSPACE
-    assert _verify(kdt, ws=(0x100010, need)) == K.KDT_ERR_WORKSPACE
+    kw = dict(T=33, max_kv_len=70, impl=4, num_splits=1)
+    assert _verify(kdt, **kw) == K.KDT_ERR_WORKSPACE
+    assert _verify(kdt, ws=(0x100000, need - 1), **kw) == K.KDT_ERR_WORKSPACE
+    assert _verify(kdt, ws=(0x100010, need), **kw) == K.KDT_ERR_WORKSPACE
     assert _verify(kdt, B=0) == K.KDT_OK
 
 
 def test_verify_q8_plan(kdt):
     p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows")
     # 72 rows a sequence are two 64-row tiles of one 128-key block each: nothing to cut
-    assert p["impl"] == "q8_rows" and p["ctas"] == 4 and p["num_launches"] == 2
-    assert 2 * 9 * 4 <= p["workspace_bytes"] <= 256
+    assert p["impl"] == "q8_rows" and p["ctas"] == 4 and p["num_launches"] == 1 and p["workspace_bytes"] == 0
+    p = kdt.verify_attn_q8_plan(2, 33, 2, 70, impl="q8_rows")      # more than 32 nodes: a kernel finds the visibility
+    assert p["ctas"] == 4 and p["num_launches"] == 2 and 2 * 33 * 2 * 4 <= p["workspace_bytes"] <= 768
     p = kdt.verify_attn_q8_plan(2, 9, 8, 129, impl="q8_rows")
-    assert p["ctas"] == 8 and p["num_launches"] == 3 and p["workspace_bytes"] >= 2 * 8 * 64 * 513 * 4
-    # rows a sequence choose the kernel: 64 heads of one token, 64 heads of a tree
+    assert p["ctas"] == 8 and p["num_launches"] == 2 and p["workspace_bytes"] >= 2 * 8 * 64 * 513 * 4
+    # the work chooses the kernel: 64 heads of one token, of a tree, of a tree over a short cache
     assert kdt.verify_attn_q8_plan(4, 1, 64, 5000)["impl"] == "q8_rows"
     p = kdt.verify_attn_q8_plan(4, 64, 64, 5000)
     assert p["impl"] == "tcgen05" and p["ctas"] == 4 * p["num_splits"]
+    assert kdt.verify_attn_q8_plan(2, 64, 64, 164)["impl"] == "q8_rows"
     p = kdt.verify_attn_q8_plan(2, 9, 8, 46, impl="q8_rows", num_splits=1, bits=True)
     assert p["ctas"] == 1 and p["num_launches"] == 1 and p["workspace_bytes"] == 0
     with pytest.raises(kdt.KdtError):
