@@ -36,6 +36,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 19;                  // sums of 2^44 weights then fit 63 bits
 constexpr int kFrac = 44;
 constexpr double kMargin = 4e-5;
+constexpr int kKeep = 32;                           // log-probabilities written at a time
+constexpr int kFewKids = 32;                        // children whose first tests are made in float32
 
 struct Exp2Table {
     uint64_t fix[129];                              // 2^{k/128} in units of 2^-46, k = -64 .. 64
@@ -108,6 +110,8 @@ struct Shared {
     Slot slot[2][kMaxCluster];                      // by exchange parity
     uint64_t exact[2][kMaxCluster];
     double z;
+    double keep_z[kKeep];                           // what the path's log-probabilities are made of
+    float keep_l[kKeep], keep_m[kKeep];
     float wz[kNW];
     float wm[kNW];
     uint64_t wx[kNW];                               // exact sums of the warps' parts
@@ -115,7 +119,7 @@ struct Shared {
     int n_child, decision, found;
 };
 
-__host__ __device__ constexpr size_t list_bytes(int T) { return ((size_t)T * 28 + 15) / 16 * 16; }
+__host__ __device__ constexpr size_t list_bytes(int T) { return ((size_t)T * 36 + 15) / 16 * 16; }
 
 // One cluster a sequence.
 template <typename E>
@@ -124,11 +128,13 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
     // children of the node at hand: exact weight (0 for a repeated token), node, token (INT32_MIN when
-    // it is none), logit, random number; and the tree's parents
+    // it is none), logit, random number; and the
+    // tree's parents, tokens and random numbers
     uint64_t *cw = reinterpret_cast<uint64_t *>(dyn);
     int32_t *cn = reinterpret_cast<int32_t *>(cw + p.T), *ct = cn + p.T;
     float *cl = reinterpret_cast<float *>(ct + p.T), *cu = cl + p.T;
-    int32_t *par = reinterpret_cast<int32_t *>(cu + p.T);
+    int32_t *par = reinterpret_cast<int32_t *>(cu + p.T), *tok = par + p.T;
+    float *un = reinterpret_cast<float *>(tok + p.T);
     E *row = reinterpret_cast<E *>(dyn + list_bytes(p.T));
     uint32_t rank, size;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -144,6 +150,8 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
     for (int i = tid; i < p.T; i += kNT) {
         const int32_t pa = p.parent[tb + i];
         par[i] = pa;
+        tok[i] = p.tok[tb + i];
+        un[i] = p.u_node[tb + i];
         if (rank == 0) {
             p.acc_nodes[tb + i] = -1;
             if (p.logp) p.logp[tb + i] = 0.f;
@@ -155,6 +163,16 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
     const int part = (p.slice / 16 + kNW - 1) / kNW * 16;
     const int w0 = min(warp * part, n), w1 = min(w0 + part, n);
 
+    // natural log of the probability of a token of logit l, M the row's maximum, z the sum of weights
+    auto log_p = [&](float l, float M, double z) {
+        return (float)(((double)l - (double)M) * p.inv_temp - (log(z) - kFrac * 0.69314718055994530942));
+    };
+    auto write_kept = [&](int first, int count) {              // by the warp of the thread that kept them
+        if (rank || warp || !p.logp) return;
+        __syncwarp();
+        if (lane < count) p.logp[tb + first + lane] = log_p(sh.keep_l[lane], sh.keep_m[lane], sh.keep_z[lane]);
+        __syncwarp();
+    };
     int node = 0, depth = 0;
     uint32_t step = 0;
     for (;;) {
@@ -171,11 +189,11 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
             }
             __syncwarp();
             for (int k = lane; k < c; k += 32) {
-                const int32_t t = p.tok[tb + cn[k]];
+                const int32_t t = tok[cn[k]];
                 const bool good = t >= 0 && t < p.V;
                 if (!good && rank == 0) record_error(p.err, (int32_t)(tb + cn[k] + 1));
                 ct[k] = good ? t : INT32_MIN;
-                cu[k] = p.u_node[tb + cn[k]];
+                cu[k] = un[cn[k]];
                 cl[k] = good ? as_f32(static_cast<const E *>(p.logits)[(tb + node) * p.row_stride + t]) : -INFINITY;
             }
             if (lane == 0) sh.n_child = c;
@@ -276,7 +294,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         if (warp == 0) {                                       // Z in units of the weights, the same in every CTA
             double s = 0.0;
             if (lane < (int)size && slots[lane].m > -INFINITY)
-                s = slots[lane].z * exp2(((double)slots[lane].m - (double)M) * ((double)p.c_hi + (double)p.c_lo) + (double)kFrac);
+                s = slots[lane].z * ((double)exp2f((slots[lane].m - M) * p.c_hi) * (double)(1ull << kFrac));
 #pragma unroll
             for (int off = kMaxCluster / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             if (lane == 0) sh.z = s;
@@ -295,8 +313,22 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         for (;;) {
             if (tid == 0) {
                 double rem = sh.z;
-                const double margin = exact ? -1.0 : kMargin * rem;
                 int d = -1;                                    // -1: none stands, -2: too close
+                // FP64 operations in a row take long here; float32 adds at most 3 roundings a child
+                if (!exact && nc <= kFewKids) {
+                    float left = (float)rem;
+                    const float margin = (float)kMargin * left;
+                    for (int k = 0; k < nc; ++k) {
+                        const float w = (float)cw[k], t = cu[k] * left;
+                        if (cw[k] == 0) continue;
+                        if (fabsf(t - w) <= margin || t < w) {
+                            d = fabsf(t - w) <= margin ? -2 : k;
+                            break;
+                        }
+                        left -= w;
+                    }
+                } else {
+                const double margin = exact ? -1.0 : kMargin * rem;
                 for (int k = 0; k < nc; ++k) {
                     const double w = (double)cw[k];
                     if (cw[k] == 0) continue;
@@ -311,6 +343,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
                     }
                     rem -= w;
                 }
+                }
                 sh.decision = d;
             }
             __syncthreads();
@@ -318,6 +351,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
             if (take >= 0 || exact) break;
             // exact sums of the warps' parts, children included
             uint64_t x = 0;
+#pragma unroll 4
             for (int i = w0 + lane; i < w1; i += 32) x += weight(as_f32(data[i]), M, p.c_hi, p.c_lo, sh.tab);
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -338,18 +372,19 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
             exact = true;
             if (take == -1) break;                             // no test was close: none stands
         }
-        // natural log of a token's probability, for the one thread that writes it
-        auto log_p = [&](float l) {
-            return (float)(((double)l - (double)M) * p.inv_temp - (log(sh.z) - kFrac * 0.69314718055994530942));
-        };
         if (rank == 0 && tid == 0) {
             p.acc_nodes[tb + depth] = node;
-            if (take >= 0 && p.logp) p.logp[tb + depth] = log_p(cl[take]);
+            if (take >= 0) {                                   // their FP64 log is off the walk's path
+                sh.keep_z[depth % kKeep] = sh.z;
+                sh.keep_l[depth % kKeep] = cl[take];
+                sh.keep_m[depth % kKeep] = M;
+            }
         }
         ++step;
         if (take >= 0) {
             node = cn[take];
             ++depth;
+            if (depth % kKeep == 0) write_kept(depth - kKeep, kKeep);
             __syncthreads();                                   // the children's arrays are rewritten next
             continue;
         }
@@ -425,10 +460,11 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
                 if (acc > t) break;
             }
             p.bonus[b] = v0 + i;
-            if (p.logp) p.logp[tb + depth] = log_p(as_f32(data[i]));
+            if (p.logp) p.logp[tb + depth] = log_p(as_f32(data[i]), M, sh.z);
         }
         break;
     }
+    write_kept(depth - depth % kKeep, depth % kKeep);
     tc::cluster_sync();        // no CTA leaves while another may still write to its shared memory
 }
 

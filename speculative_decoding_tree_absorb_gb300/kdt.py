@@ -231,9 +231,10 @@ def _row_stride(q):
     combined [B,T,H,576] query buffer)."""
     if q.is_contiguous():
         return 0
-    if q.stride(3) != 1 or q.stride(2) * q.shape[2] != q.stride(1) or q.stride(1) * q.shape[1] != q.stride(0):
+    s, n = q.stride(), q.shape
+    if s[3] != 1 or s[2] * n[2] != s[1] or s[1] * n[1] != s[0]:
         raise ValueError("query views must have a contiguous last dim and equally spaced (b,i,h) rows")
-    return int(q.stride(2))
+    return s[2]
 
 
 def plan(args: VerifyArgs) -> dict:
@@ -428,9 +429,10 @@ def tree_build(cand_tok, cand_lp, N, root_tok=None, stream=None):
 def _row_stride3(t, name):
     """Element stride between the (b,i) rows of a [B,T,d] view with a contiguous last dim and
     equally spaced rows (e.g. a slice of a combined [B,T,576] buffer)."""
-    if t.stride(2) != 1 or (t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.stride(1) * t.shape[1]):
+    s, n = t.stride(), t.shape
+    if s[2] != 1 or (n[0] > 1 and n[1] > 0 and s[0] != s[1] * n[1]):
         raise ValueError(f"{name} must be a [B,T,d] view with a contiguous last dim and equally spaced (b,i) rows")
-    return t.stride(1) if t.shape[1] > 1 else (t.stride(0) if t.shape[0] > 1 else t.shape[2])
+    return s[1] if n[1] > 1 else (s[0] if n[0] > 1 else n[2])
 
 
 def _check_q8_cache(c_q8, c_scale, k_pe):
@@ -546,8 +548,9 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
     """
     import torch
     B, L = _check_q8_cache(c_q8, c_scale, k_pe)
-    T, H = q_nope.shape[1], q_nope.shape[2]
-    if q_nope.shape != (B, T, H, 512) or q_pe.shape != (B, T, H, 64):
+    shape = q_nope.shape
+    T, H = shape[1], shape[2]
+    if shape != (B, T, H, 512) or q_pe.shape != (B, T, H, 64):
         raise ValueError("q_nope must be [B,T,H,512] and q_pe [B,T,H,64], B as in the cache")
     if q_nope.dtype != torch.bfloat16 or q_pe.dtype != torch.bfloat16:
         raise TypeError("queries must be bfloat16")
