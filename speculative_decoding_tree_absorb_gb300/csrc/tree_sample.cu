@@ -25,6 +25,8 @@
 //    pairs. Its error is below 2^-40 of the weight.
 #include <math.h>
 
+#include <atomic>
+
 #include "kdt_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -33,6 +35,7 @@ namespace {
 
 constexpr int kNT = 512, kNW = kNT / 32;            // threads, warps a CTA
 constexpr int kMaxCluster = 8;
+constexpr size_t kMostSmem = 220 * 1024;
 constexpr int kMaxVocab = 1 << 19;                  // sums of 2^44 weights then fit 63 bits
 constexpr int kFrac = 44;
 constexpr double kMargin = 4e-5;
@@ -468,11 +471,23 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
     tc::cluster_sync();        // no CTA leaves while another may still write to its shared memory
 }
 
-// CTAs a sequence: as many as the device holds at once for the batch, a power of two.
-int cluster_size(int B, int V) {
-    int c = kMaxCluster;
-    while (c > 1 && ((int64_t)B * c > sm_count() || V < 1024 * c)) c >>= 1;
-    return c;
+// Clusters of C CTAs that the device holds at once (a cluster lies within one GPC: 15 of 8, 36 of 4, 76 of 2).
+template <typename E> int resident(cudaLaunchConfig_t cfg, int C) {
+    static std::atomic<int> cached[64][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) dev = 0;
+    std::atomic<int> &slot = cached[dev & 63][C];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.dynamicSmemBytes = kMostSmem;
+    cfg.attrs[0].val.clusterDim.x = (unsigned)C;
+    if (cudaOccupancyMaxActiveClusters(&n, tree_sample_kernel<E>, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();                                    // clear the query's error
+        return sm_count() / C;
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
 }
 
 Exp2Table make_table() {
@@ -487,25 +502,28 @@ Exp2Table make_table() {
 }
 
 template <typename E> cudaError_t launch(SampleParams p, int B, cudaStream_t s) {
-    const int C = cluster_size(B, p.V);
-    p.slice = ((p.V + C - 1) / C + 15) / 16 * 16;
-    const size_t lists = list_bytes(p.T), slice = (size_t)p.slice * sizeof(E);
-    constexpr size_t kMost = 220 * 1024;
-    p.cache = lists + slice <= kMost;
-    const size_t smem = lists + (p.cache ? slice : 0);
-    cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.x = kMaxCluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(B * C));
     cfg.blockDim = dim3(kNT);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    // CTAs a sequence: as many as the device holds at once for the batch, of 1024 tokens or more each
+    // (16 gave one sequence of 32000 tokens nothing, and only 7 such clusters are held)
+    int C = kMaxCluster;
+    while (C > 1 && (p.V < 1024 * C || B > resident<E>(cfg, C))) C >>= 1;
+    p.slice = ((p.V + C - 1) / C + 15) / 16 * 16;
+    const size_t lists = list_bytes(p.T), slice = (size_t)p.slice * sizeof(E);
+    p.cache = lists + slice <= kMostSmem;
+    const size_t smem = lists + (p.cache ? slice : 0);
+    at[0].val.clusterDim.x = (unsigned)C;
+    cfg.gridDim = dim3((unsigned)(B * C));
+    cfg.dynamicSmemBytes = smem;
     static const Exp2Table table = make_table();
     return cudaLaunchKernelEx(&cfg, tree_sample_kernel<E>, p, table);
 }
