@@ -77,6 +77,13 @@ struct Bars {
     int work[4];                // this CTA's share: blocks, first sequence, tile, block
 };
 
+// One warp's part of an item's outputs on its way out: 32 dims of 8 rows in bf16, of 4 in float32.
+union Stage {
+    __nv_bfloat16 h[8][32];
+    float f[4][32];
+    uint4 all[32];
+};
+
 // Visibility words of a block's tree keys: up to 64 nodes (those of the tile's rows, from node i0
 // on), kVisWords words each from word w0 on (128 keys touch at most five).
 constexpr int kVisWords = 5;
@@ -91,6 +98,7 @@ struct Shared {
     float red[4][kRowsT];       // per key quadrant
     uint32_t bad[2][kKeysB];    // keys with a NaN group, by block parity
     uint32_t vis[kRowsT * kVisWords];
+    Stage stage[kSoftWarps];
 };
 
 __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
@@ -522,51 +530,50 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             }
             barrier_or<1, 256>(false);
             tc_fence_after();
+            Stage &stage = sh.stage[warp - kSoft0];
             const int rows = min(32, p.rows_seq - it.rt * kRowsT - 32 * half);   // of this warp's 32 (may be <= 0)
-            // A thread has one dim of 32 rows. Four lanes exchange 4 x 4 values (two rounds), so that
-            // each holds the four dims of one row and a store instruction covers four rows (stores of
-            // single values took 11 k clocks an item); widening's order of the dims is undone on the way.
-            const bool up2 = lane & 2, up1 = lane & 1;
+            // A thread has one dim of 32 rows; 512 bytes of shared memory a warp turn them into 16-byte pieces of
+            // rows, with widening's order of the dims undone on the way in (an exchange by shuffles took
+            // 5.6 k clocks an item, stores of single values 11 k)
+            const int dim = (lane & ~3) | ((lane & 1) << 1) | ((lane >> 1) & 1);
             // 16 rows at a time, a small loop: the code of an item's end is mostly fetched anew
 #pragma unroll 1
             for (int e = 0; e < 2 * kPairs; ++e) {
-                const int q = e >> 1, r0 = 16 * (e & 1);
+                const int r0 = 16 * (e & 1);
                 uint32_t o[16];
-                tmem_ld16(lane_addr(tmem, warp, kRowsT * q + 32 * half + r0), o);
+                tmem_ld16(lane_addr(tmem, warp, kRowsT * (e >> 1) + 32 * half + r0), o);
                 tmem_wait_ld();
-                const int64_t at = (first + 32 * half + r0 + (lane & 3)) * kDc + 128 * q + 32 * (warp & 3) + (lane & ~3);
-                // round by round for all four groups of rows: a store's branch between two groups would
-                // make their shuffles wait for one another
-                float keep[8], got[8];                       // own dim of rows 2 up2 and + 1, and lane ^ 2's dim of them
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float4 iv = *reinterpret_cast<const float4 *>(sh.inv + 32 * half + r0 + 4 * m);
-                    const float v0 = __uint_as_float(o[4 * m]) * iv.x, v1 = __uint_as_float(o[4 * m + 1]) * iv.y,
-                                v2 = __uint_as_float(o[4 * m + 2]) * iv.z, v3 = __uint_as_float(o[4 * m + 3]) * iv.w;
-                    got[2 * m] = __shfl_xor_sync(0xffffffffu, up2 ? v0 : v2, 2);
-                    got[2 * m + 1] = __shfl_xor_sync(0xffffffffu, up2 ? v1 : v3, 2);
-                    keep[2 * m] = up2 ? v2 : v0;
-                    keep[2 * m + 1] = up2 ? v3 : v1;
+                    o[4 * m] = __float_as_uint(__uint_as_float(o[4 * m]) * iv.x);
+                    o[4 * m + 1] = __float_as_uint(__uint_as_float(o[4 * m + 1]) * iv.y);
+                    o[4 * m + 2] = __float_as_uint(__uint_as_float(o[4 * m + 2]) * iv.z);
+                    o[4 * m + 3] = __float_as_uint(__uint_as_float(o[4 * m + 3]) * iv.w);
                 }
-                float4 w[4];
+                const int64_t at = (first + 32 * half + r0) * kDc + 128 * (e >> 1) + 32 * (warp & 3);
+                if (whole && kBf16Out) {
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at + (lane >> 2) * kDc + 8 * (lane & 3);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float b0 = __shfl_xor_sync(0xffffffffu, up1 ? keep[2 * m] : keep[2 * m + 1], 1);
-                    const float b1 = __shfl_xor_sync(0xffffffffu, up1 ? got[2 * m] : got[2 * m + 1], 1);
-                    const float own = up1 ? keep[2 * m + 1] : keep[2 * m], far = up1 ? got[2 * m + 1] : got[2 * m];
-                    // row 2 up2 + up1; the four lanes hold dims 0, 2, 1, 3
-                    const float e0 = up1 ? b0 : own, e1 = up1 ? own : b0, f0 = up1 ? b1 : far, f1 = up1 ? far : b1;
-                    w[m] = make_float4(up2 ? f0 : e0, up2 ? e0 : f0, up2 ? f1 : e1, up2 ? e1 : f1);
-                }
+                    for (int g8 = 0; g8 < 16; g8 += 8) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (r0 + 4 * m + (lane & 3) < rows) {
-                        if (whole && kBf16Out)
-                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 4 * m * kDc) =
-                                make_uint2(q8::pack_bf16(w[m].x, w[m].y), q8::pack_bf16(w[m].z, w[m].w));
-                        else
-                            *reinterpret_cast<float4 *>((whole ? static_cast<float *>(p.out) : p.part_o) + at + 4 * m * kDc) = w[m];
+                        for (int r = 0; r < 8; ++r) stage.h[r][dim] = __float2bfloat16_rn(__uint_as_float(o[g8 + r]));
+                        __syncwarp();
+                        if (r0 + g8 + (lane >> 2) < rows) *reinterpret_cast<uint4 *>(dst + g8 * kDc) = stage.all[lane];
+                        __syncwarp();
                     }
+                } else {
+                    float *dst = (whole ? static_cast<float *>(p.out) : p.part_o) + at + (lane >> 3) * kDc + 4 * (lane & 7);
+#pragma unroll
+                    for (int g4 = 0; g4 < 16; g4 += 4) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) stage.f[r][dim] = __uint_as_float(o[g4 + r]);
+                        __syncwarp();
+                        if (r0 + g4 + (lane >> 3) < rows)
+                            *reinterpret_cast<uint4 *>(dst + g4 * kDc) = stage.all[lane];
+                        __syncwarp();
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
