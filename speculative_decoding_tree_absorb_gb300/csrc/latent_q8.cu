@@ -16,6 +16,7 @@ namespace kdt {
 namespace {
 
 constexpr int kWarps = 8;                           // warps a CTA
+constexpr int kWriters = 4, kReaders = 5;           // CTAs an SM when there are rows enough
 constexpr int kHalf = kDr / 2;
 
 // Frequencies of the rotation in turns: pos * w_j / 2 pi as a fixed-point fraction of a turn
@@ -38,15 +39,19 @@ struct WriteParams {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+template <bool kOnce, typename V> __device__ __forceinline__ V once(const V *p) {
+    return kOnce ? __ldcs(p) : __ldg(p);
+}
+
 // A lane's 16 latent elements of a row, as kPieces pieces of kPer consecutive ones: piece q
 // starts at element q * 32 * kPer + lane * kPer, so every warp load is contiguous.
 template <typename E> struct Row;
 template <> struct Row<float> {
     static constexpr int kPer = 4, kPieces = 4;
     float4 v[4];
-    __device__ __forceinline__ void load(const float *p, int lane) {
+    template <bool kOnce> __device__ __forceinline__ void load(const float *p, int lane) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = __ldcs(reinterpret_cast<const float4 *>(p) + 32 * q + lane);
+        for (int q = 0; q < 4; ++q) v[q] = once<kOnce>(reinterpret_cast<const float4 *>(p) + 32 * q + lane);
     }
     __device__ __forceinline__ void get(float (&x)[16]) const {
 #pragma unroll
@@ -61,9 +66,9 @@ template <> struct Row<float> {
 template <> struct Row<__nv_bfloat16> {
     static constexpr int kPer = 8, kPieces = 2;
     uint4 v[2];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int lane) {
+    template <bool kOnce> __device__ __forceinline__ void load(const __nv_bfloat16 *p, int lane) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) v[q] = __ldcs(reinterpret_cast<const uint4 *>(p) + 32 * q + lane);
+        for (int q = 0; q < 2; ++q) v[q] = once<kOnce>(reinterpret_cast<const uint4 *>(p) + 32 * q + lane);
     }
     __device__ __forceinline__ void get(float (&x)[16]) const {
 #pragma unroll
@@ -82,96 +87,77 @@ template <> struct Row<__nv_bfloat16> {
 // group of 32 is 32 / kPer neighbouring lanes of one piece, its largest magnitude a few
 // shuffles (taken over the bit patterns, so infinities and NaN come out on top).
 template <typename E>
-__global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const WriteParams p,
+__global__ void __launch_bounds__(32 * kWarps, kWriters) latent_write_kernel(const WriteParams p,
                                                                    const __grid_constant__ TurnFreqs fr) {
     using R = Row<E>;
     constexpr int kLanes = KDT_Q8_GROUP / R::kPer;        // lanes that share a group
     const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)p.B * p.T, step = (int64_t)gridDim.x * kWarps;
-    float g[16];
-    if (p.gamma) {
-        R gr;
-        gr.load(static_cast<const E *>(p.gamma), lane);
-        gr.get(g);
-    }
     const uint64_t freq = fr.f[lane];
-    struct Next {
-        R c;
-        E k0, k1;
-        int32_t pos;
-        int64_t dst;                                      // cache row over all sequences, -1 = none
-    };
-    auto fetch = [&](int64_t n, Next &x) {
-        x.dst = -1;
-        if (n >= rows) return;
+    for (int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); n < rows; n += step) {
         const int b = (int)(n / p.T), i = (int)(n - (int64_t)b * p.T);
-        if (p.n_rows && i >= p.n_rows[b]) return;
-        const int64_t row = (int64_t)p.prefix_len[b] + i;
-        if (row < 0 || row >= p.L) return;
-        x.dst = (int64_t)b * p.L + row;
-        x.c.load(static_cast<const E *>(p.c) + n * p.c_stride, lane);
+        if (p.n_rows && i >= p.n_rows[b]) continue;
+        R c;
+        c.template load<true>(static_cast<const E *>(p.c) + n * p.c_stride, lane);
         const E *k = static_cast<const E *>(p.k) + n * p.k_stride;
-        x.k0 = k[lane];
-        x.k1 = k[lane + kHalf];
-        x.pos = p.pos ? p.pos[n] : 0;
-    };
-    int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    Next cur, nxt;
-    fetch(n, cur);
-    for (; n < rows; n += step) {
-        fetch(n + step, nxt);
-        if (cur.dst >= 0) {
-            float y[16];
-            cur.c.get(y);
-            if (p.gamma) {
-                float ss = 0.f;
+        const E ka = k[lane], kb = k[lane + kHalf];
+        const int32_t pos = p.pos ? p.pos[n] : 0;
+        const int64_t row = (int64_t)p.prefix_len[b] + i;
+        if (row < 0 || row >= p.L) continue;
+        const int64_t dst = (int64_t)b * p.L + row;
+        float y[16];
+        c.get(y);
+        if (p.gamma) {
+            R gr;                                     // from L1 for each row: 16 registers less
+            gr.template load<false>(static_cast<const E *>(p.gamma), lane);
+            float ss = 0.f;
 #pragma unroll
-                for (int t = 0; t < 16; ++t) ss = fmaf(y[t], y[t], ss);
+            for (int t = 0; t < 16; ++t) ss = fmaf(y[t], y[t], ss);
 #pragma unroll
-                for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                const float r = 1.f / sqrtf(ss * (1.f / kDc) + p.eps);
+            for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            const float r = 1.f / sqrtf(ss * (1.f / kDc) + p.eps);
+            float g[16];
+            gr.get(g);
 #pragma unroll
-                for (int t = 0; t < 16; ++t) y[t] = y[t] * r * g[t];
-            }
-            uint8_t *codes = p.c_q8 + cur.dst * kDc;
-            uint8_t *scales = p.c_scale + cur.dst * (kDc / KDT_Q8_GROUP);
-#pragma unroll
-            for (int q = 0; q < R::kPieces; ++q) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int t = 0; t < R::kPer; ++t)
-                    top = max(top, __float_as_uint(y[R::kPer * q + t]) & 0x7fffffffu);
-#pragma unroll
-                for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int byte = q8::scale_byte(top);
-                const float inv = q8::inverse_scale(byte);     // 0 for a group that reads as NaN
-                uint32_t w[R::kPer / 4];
-#pragma unroll
-                for (int t = 0; t < R::kPer / 4; ++t) {
-                    const float *z = &y[R::kPer * q + 4 * t];
-                    w[t] = byte == q8::kNaN ? 0u : q8::encode4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
-                }
-                if constexpr (R::kPer == 4)
-                    reinterpret_cast<uint32_t *>(codes)[32 * q + lane] = w[0];
-                else
-                    reinterpret_cast<uint2 *>(codes)[32 * q + lane] = make_uint2(w[0], w[1]);
-                if (lane % kLanes == 0) scales[q * (32 / kLanes) + lane / kLanes] = (uint8_t)byte;
-            }
-            float k0 = to_f32(cur.k0), k1 = to_f32(cur.k1);
-            if (p.pos) {
-                // the angle in turns, exact modulo 1, rounded to 32 bits: within [-1/2, 1/2)
-                const int32_t turn = (int32_t)(((uint64_t)(int64_t)cur.pos * freq + 0x80000000ull) >> 32);
-                float s, c;
-                sincospif((float)turn * 4.656612873077393e-10f, &s, &c);     // 2^-31: half turns
-                const float r0 = __fsub_rn(__fmul_rn(k0, c), __fmul_rn(k1, s));
-                k1 = __fadd_rn(__fmul_rn(k1, c), __fmul_rn(k0, s));
-                k0 = r0;
-            }
-            __nv_bfloat16 *kd = p.k_pe + cur.dst * kDr;
-            kd[lane] = __float2bfloat16_rn(k0);
-            kd[lane + kHalf] = __float2bfloat16_rn(k1);
+            for (int t = 0; t < 16; ++t) y[t] = y[t] * r * g[t];
         }
-        cur = nxt;
+        uint8_t *codes = p.c_q8 + dst * kDc;
+        uint8_t *scales = p.c_scale + dst * (kDc / KDT_Q8_GROUP);
+#pragma unroll
+        for (int q = 0; q < R::kPieces; ++q) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int t = 0; t < R::kPer; ++t)
+                top = max(top, __float_as_uint(y[R::kPer * q + t]) & 0x7fffffffu);
+#pragma unroll
+            for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const int byte = q8::scale_byte(top);
+            const float inv = q8::inverse_scale(byte);     // 0 for a group that reads as NaN
+            uint32_t w[R::kPer / 4];
+#pragma unroll
+            for (int t = 0; t < R::kPer / 4; ++t) {
+                const float *z = &y[R::kPer * q + 4 * t];
+                w[t] = byte == q8::kNaN ? 0u : q8::encode4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
+            }
+            if constexpr (R::kPer == 4)
+                reinterpret_cast<uint32_t *>(codes)[32 * q + lane] = w[0];
+            else
+                reinterpret_cast<uint2 *>(codes)[32 * q + lane] = make_uint2(w[0], w[1]);
+            if (lane % kLanes == 0) scales[q * (32 / kLanes) + lane / kLanes] = (uint8_t)byte;
+        }
+        float k0 = to_f32(ka), k1 = to_f32(kb);
+        if (p.pos) {
+            // the angle in turns, exact modulo 1, rounded to 32 bits: within [-1/2, 1/2)
+            const int32_t turn = (int32_t)(((uint64_t)(int64_t)pos * freq + 0x80000000ull) >> 32);
+            float s, c;
+            sincospif((float)turn * 4.656612873077393e-10f, &s, &c);     // 2^-31: half turns
+            const float r0 = __fsub_rn(__fmul_rn(k0, c), __fmul_rn(k1, s));
+            k1 = __fadd_rn(__fmul_rn(k1, c), __fmul_rn(k0, s));
+            k0 = r0;
+        }
+        __nv_bfloat16 *kd = p.k_pe + dst * kDr;
+        kd[lane] = __float2bfloat16_rn(k0);
+        kd[lane + kHalf] = __float2bfloat16_rn(k1);
     }
 }
 
@@ -270,11 +256,10 @@ __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const ReadPara
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs for `rows` rows: a warp a row until the device is full (kFull CTAs an SM), then
+// CTAs for `rows` rows: a warp a row until the device is full (`full` CTAs an SM), then
 // resident warps take several rows each.
-constexpr int kFull = 5;
-int grid_for(int64_t rows) {
-    const int64_t ctas = (rows + kWarps - 1) / kWarps, most = (int64_t)sm_count() * kFull;
+int grid_for(int64_t rows, int full) {
+    const int64_t ctas = (rows + kWarps - 1) / kWarps, most = (int64_t)sm_count() * full;
     return (int)(ctas < most ? ctas : most);
 }
 
@@ -314,7 +299,7 @@ kdt_status kdt_latent_write_q8(const kdt_latent_write_args *a, cudaStream_t stre
     const WriteParams p = {a->c,    a->k,       a->gamma, cs, ks, a->pos, a->prefix_len, a->n_rows,
                            a->c_q8, a->c_scale, static_cast<__nv_bfloat16 *>(a->k_pe), a->kv_row_stride,
                            a->B,    a->T,       a->eps};
-    const int grid = grid_for((int64_t)a->B * a->T);
+    const int grid = grid_for((int64_t)a->B * a->T, kWriters);
     if (a->dtype == KDT_F32)
         latent_write_kernel<float><<<grid, 32 * kWarps, 0, stream>>>(p, fr);
     else
@@ -336,7 +321,7 @@ kdt_status kdt_latent_read_q8(const uint8_t *c_q8, const uint8_t *c_scale, const
     if (st != KDT_OK) return st;
     const ReadParams p = {c_q8, c_scale, static_cast<const __nv_bfloat16 *>(k_pe), kv_row_stride, B, R, start, n_rows,
                           c, k};
-    const int grid = grid_for((int64_t)B * R);
+    const int grid = grid_for((int64_t)B * R, kReaders);
     if (dtype == KDT_F32)
         latent_read_kernel<float><<<grid, 32 * kWarps, 0, stream>>>(p);
     else
