@@ -44,14 +44,15 @@
 //    outlier keys (a few times larger than the rest), and every rescale drains the
 //    P.V pipe.
 //  * The same kernel runs over the 8-bit latent cache (kQ8): the latents' TMA then brings
-//    codes, and four more warps a CTA widen them to bf16 (exact: e4m3 times a power of two)
+//    codes, and eight more warps a CTA widen them to bf16 (exact: e4m3 times a power of two)
 //    into the same swizzled tiles of the same rings: in an S-CTA its 64 keys of each key
 //    chunk, in an O-CTA its 128 columns of each value chunk. Widening leaves each four dims
-//    in the order (0, 2, 1, 3): Q is loaded in that order and O written back from it. A CTA
-//    widens 32 k codes a block (about 900 instructions a warp in the 3700 clocks a block
-//    takes), so the widening hides behind the MMAs. A NaN group
-//    gives NaN keys, so that rows which see it become NaN, and zero values, so that it does
-//    not reach rows from which it is hidden.
+//    in the order (0, 2, 1, 3): Q is loaded in that order and O written back from it. It is
+//    what bounds the kernel: a CTA widens 32 k codes a block, about 900 instructions a warp
+//    that share the schedulers with the softmax, in 4.7 k clocks a block (566 us for 8
+//    sequences of 64 nodes and 64 heads over 8 k keys) against 3.4 k of the bf16 kernel, whose
+//    cache is twice as large. A NaN group gives NaN keys, so that rows which see it become
+//    NaN, and zero values, so that it does not reach rows from which it is hidden.
 //  * Every wait is bounded; on a lost arrival the kernel records a status in the
 //    caller's error word, drains its own in-flight copies and MMAs, frees TMEM and
 //    returns (no trap, no hang).
@@ -837,13 +838,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
     auto first_work = [&]() { return WorkIter{cl, bar.work_wleft, bar.work_u0, bar.work_kb0, bar.work_left, 0}; };
 
     // Roles. Warps 0-3 issue, load and copy; 4-11 are softmax (S-CTA), correction and epilogue
-    // (O-CTA); 12-15 widen the 8-bit cache. (The outer branch is by warpgroup: a warpgroup changes
-    // its register share as one.)
-    if (warp < 4) {
-        if constexpr (kQ8) set_regs<kRegsIssueQ8>();
+    // (O-CTA); 12-19 widen the 8-bit cache.
+    // =============================== S-CTA ===============================
+    auto s_issue = [&]() {
         const int G = bar.work_count;                  // key blocks of this cluster
-        if (s_role) {
-        // =============================== S-CTA ===============================
         unsigned char *qpe_tile = smem + kOffQpe;
         unsigned char *kring = smem + kOffKRing;
         unsigned char *rring = smem + kOffRRing;
@@ -1044,8 +1042,197 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                 }
             }
         }
-        } else {
-        // =============================== O-CTA ===============================
+    };
+    auto s_softmax = [&]() {
+        const int G = bar.work_count;
+        const uint32_t tmem_q = tmem;                 // Q_nope: columns [0, 256)
+        const uint32_t tmem_s0 = tmem + 256;          // score buffers at 256 and 384
+        // ---------------- per item: Q_nope -> TMEM, softmax, statistics -----------------
+        // Eight warps: warp w serves the 32 rows of TMEM lane quadrant (w % 4); warps 4-7
+        // take keys 0..63 of each block, warps 8-11 keys 64..127.
+        const int half = (warp - 4) >> 2;
+        const int row = 32 * (warp & 3) + lane;
+        float *rowmax_s = reinterpret_cast<float *>(smem + kOffRowMax);
+        float *lsum_s = reinterpret_cast<float *>(smem + kOffLSum);
+        bool ok = true;
+        bool fail = false;
+        bool vis_ready = false;                    // the visibility bits are known to be written
+        // Q_nope of an item's rows into tensor memory, 16 loads in flight per thread
+        auto load_q = [&](const Item &q, bool withhold) {
+            const int Rq = (q.rt0 + kpair) * kRows + row;
+            const bool valid = Rq < p.rows_seq;
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(p.q_nope + ((int64_t)q.b * p.rows_seq + Rq) * p.q_stride) + 32 * half;
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2) {
+                uint4 v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = valid ? __ldg(src + 16 * r2 + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t wq[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 e = kQ8 ? q8::reorder8(v[8 * h + k]) : v[8 * h + k];
+                        wq[4 * k] = e.x;
+                        wq[4 * k + 1] = e.y;
+                        wq[4 * k + 2] = e.z;
+                        wq[4 * k + 3] = e.w;
+                    }
+                    tmem_st32(tmem_lane_addr(tmem_q, warp, (4 * half + 2 * r2 + h) * 32), wq);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && !withhold) mbar_arrive_remote_cta(&bar.q_ready, lead_rank);
+        };
+        WorkIter w = first_work();
+        Item it;
+        int ii = 0, g = 0;
+        bool have = next_item(p, w, cl, ncl, it);
+        if (have) {
+            load_q(it, p.fault == 1);                  // the test hook leaves Q-ready one arrival short
+            if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvQReady, 0);
+        }
+        while (!fail && have) {
+            const int R = (it.rt0 + kpair) * kRows + row;
+            const int qi = min(R, p.rows_seq - 1) / p.H;
+            const uint32_t *visrow = p.vis + ((int64_t)it.b * p.T + qi) * p.W;
+            float m_run = -INFINITY;                           // log2 units, same in both halves
+            float l_run = 0.f;                                 // this half's share of the row sum
+            for (int j = 0; j < it.nb; ++j, ++g) {
+                // No warp leaves this loop on its own: every iteration meets the other seven
+                // at the named barrier, which ORs their failures.
+                const int buf = g & 1;
+                const int ss = g % kNS;                        // staging slot here
+                const int ps = g % kNP;                        // P slot in the O-CTA
+                ok = ok && warp_wait(bar, &bar.sfull[buf], (uint32_t)(g >> 1) & 1, p.err, -6);
+                float x[64];
+                float mx = -INFINITY;
+                bool masked = false;                            // block half holds hidden keys
+                if (ok) {
+                    tc_fence_after();
+                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxIn, g);
+                    uint32_t r0v[32], r1v[32];
+                    const uint32_t sbase = tmem_s0 + buf * kKeys + 64 * half;
+                    tmem_ld32(tmem_lane_addr(sbase, warp, 0), r0v);
+                    tmem_ld32(tmem_lane_addr(sbase, warp, 32), r1v);
+                    tmem_wait_ld();
+                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxLd, g);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {             // raw scores
+                        x[q] = __uint_as_float(r0v[q]);
+                        x[32 + q] = __uint_as_float(r1v[q]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_cta(&bar.sempty[buf], lead_rank);   // buffer may be overwritten
+                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxLoaded, g);
+                    const int key0 = it.key_base + (it.kb0 + j) * kKeys + 64 * half;
+                    masked = key0 < 0 || key0 + 64 > it.P;     // leading pad or tree keys
+                    if (masked) {   // scale now, hidden keys -inf (also right for scale 0)
+                        // the bits may come from the visibility kernel launched just before
+                        // this one: wait for it before the first window with tree keys
+                        if (!vis_ready && key0 + 64 > it.P) {
+                            griddep_wait();
+                            vis_ready = true;
+                        }
+                        const uint64_t vm = vis_mask64(visrow, p.W, key0, it.P);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = ((vm >> c) & 1ull) ? x[c] * p.scale_log2 : -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) mx = fmaxf(mx, x[c]);
+                    } else {        // all visible: raw scores kept, the scale goes into the exponent
+                        mx = scaled_max64(x, p.scale_log2);
+                    }
+                    rowmax_s[(buf * 2 + half) * kRows + row] = mx;
+                }
+                if (barrier_or<2, 256>(!ok)) {
+                    fail = true;
+                    break;
+                }
+                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxMax, g);
+                mx = fmaxf(mx, rowmax_s[(buf * 2 + (half ^ 1)) * kRows + row]);
+                float alpha = 1.f;
+                if (mx > m_run + kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY)) {
+                    alpha = (m_run == -INFINITY) ? 1.f : fast_exp2(m_run - mx);
+                    m_run = mx;
+                    l_run *= alpha;
+                }
+                // the O-CTA's P slot is free once P.V of block g - kNP has run; this CTA's
+                // staging slot once the copy of block g - kNS has landed
+                ok = (g < kNP || warp_wait(bar, &bar.pempty[ps], (uint32_t)((g / kNP) - 1) & 1, p.err, -7)) &&
+                     (g < kNS || warp_wait(bar, &bar.sfree[ss], (uint32_t)((g / kNS) - 1) & 1, p.err, -19));
+                if (ok) {
+                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxSlot, g);
+                    unsigned char *slot_base = smem + kOffPStage + ss * kPSlotBytes;
+                    unsigned char *stage_row = slot_base + half * (kPBytes / 2) + row * 128;
+                    // an all-visible half has finite scores, so m_run is finite here
+                    l_run += masked ? stage_p_row<true, kQ8>(x, p.scale_log2, m_run, stage_row, row)
+                                    : stage_p_row<false, kQ8>(x, p.scale_log2, m_run, stage_row, row);
+                    // the rescale factors follow the second half of P, which carries them
+                    if (half == 1) reinterpret_cast<float *>(slot_base + kPBytes)[row] = alpha;
+                    fence_proxy_async_smem();                  // staging visible to the copy engine
+                    __syncwarp();
+                    // hand the rows to the copy thread without waiting for the other warps
+                    if (lane == 0) mbar_arrive(&bar.staged[ss][half]);
+                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxStaged, g);
+                }
+            }
+            if (fail) break;
+            // this item's statistics for the O-CTA epilogue: (m, l), l over both halves
+            if (half == 1) lsum_s[row] = l_run;
+            if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvItemEnd0, ii);
+            if (warp == 8 && lane == 0) KDT_TC_TRACE(kEvItemEnd1, ii);
+            fail = barrier_or<2, 256>(!ok);
+            if (fail) break;
+            if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvItemBar, ii);
+            const int sb = ii & 1;                            // statistics buffer of this item
+            if (half == 0) {
+                // the O-CTA has read this buffer's previous contents (item ii - 2)
+                ok = ii < 2 || warp_wait(bar, &bar.stats_empty[sb], (uint32_t)((ii >> 1) - 1) & 1, p.err, -26);
+                if (ok) {
+                    const uint32_t dst = map_to_rank(smem + kOffStats + (sb * kRows + row) * 8, o_rank);
+                    st_cluster_f32(dst, m_run);
+                    st_cluster_f32(dst + 4, l_run + lsum_s[row]);
+                    // every lane releases its own two stores: no fence on this path
+                    mbar_arrive_remote(&bar.stats_full[sb], o_rank);
+                }
+                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvStatsSent, ii);
+            }
+            ++ii;
+            // the next item's Q_nope: tensor memory is free, every MMA of this item ran
+            // before its last scores could be read
+            have = next_item(p, w, cl, ncl, it);
+            if (have && ok) {
+                load_q(it, false);
+                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvQReady, ii);
+            }
+            // lsum_s is rewritten at the end of the next item only after this barrier
+            fail = barrier_or<2, 256>(!ok);
+        }
+        // The O pair's MMA commits (pempty), the O-CTA's watcher (sfree) and its epilogue
+        // (stats_empty) arrive here; the arrivals still due are consumed before this CTA
+        // may leave, so none can land in the shared memory of a CTA that later runs here.
+        if (!fail && ok && warp == 4) {
+            for (int ps = 0; ps < kNP && ps < G; ++ps) {
+                const int g_last = ps + ((G - 1 - ps) / kNP) * kNP;
+                ok = warp_wait(bar, &bar.pempty[ps], (uint32_t)(g_last / kNP) & 1, p.err, -18) && ok;
+            }
+            for (int ss = 0; ss < kNS && ss < G; ++ss) {
+                const int g_last = ss + ((G - 1 - ss) / kNS) * kNS;
+                ok = warp_wait(bar, &bar.sfree[ss], (uint32_t)(g_last / kNS) & 1, p.err, -20) && ok;
+            }
+            for (int sb = 0; sb < 2 && sb < ii; ++sb) {
+                const int i_last = sb + ((ii - 1 - sb) / 2) * 2;
+                ok = warp_wait(bar, &bar.stats_empty[sb], (uint32_t)(i_last >> 1) & 1, p.err, -27) && ok;
+            }
+        }
+    };
+    // =============================== O-CTA ===============================
+    auto o_issue = [&]() {
+        const int G = bar.work_count;
         unsigned char *pbase = smem + kOffP;
         unsigned char *vbase = smem + kOffV;
         if (warp == 0) {
@@ -1248,323 +1435,153 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                 __syncwarp();
             }
         }
-        }
-    } else if (!kQ8 || warp < 12) {
-        if constexpr (kQ8) set_regs<kRegsSoftQ8>();
-        const int G = bar.work_count;                  // key blocks of this cluster
-        if (s_role) {
-        const uint32_t tmem_q = tmem;                 // Q_nope: columns [0, 256)
-        const uint32_t tmem_s0 = tmem + 256;          // score buffers at 256 and 384
-            // ---------------- per item: Q_nope -> TMEM, softmax, statistics -----------------
-            // Eight warps: warp w serves the 32 rows of TMEM lane quadrant (w % 4); warps 4-7
-            // take keys 0..63 of each block, warps 8-11 keys 64..127.
-            const int half = (warp - 4) >> 2;
-            const int row = 32 * (warp & 3) + lane;
-            float *rowmax_s = reinterpret_cast<float *>(smem + kOffRowMax);
-            float *lsum_s = reinterpret_cast<float *>(smem + kOffLSum);
-            bool ok = true;
-            bool fail = false;
-            bool vis_ready = false;                    // the visibility bits are known to be written
-            // Q_nope of an item's rows into tensor memory, 16 loads in flight per thread
-            auto load_q = [&](const Item &q, bool withhold) {
-                const int Rq = (q.rt0 + kpair) * kRows + row;
-                const bool valid = Rq < p.rows_seq;
-                const uint4 *src =
-                    reinterpret_cast<const uint4 *>(p.q_nope + ((int64_t)q.b * p.rows_seq + Rq) * p.q_stride) + 32 * half;
-#pragma unroll
-                for (int r2 = 0; r2 < 2; ++r2) {
-                    uint4 v[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = valid ? __ldg(src + 16 * r2 + k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t wq[32];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint4 e = kQ8 ? q8::reorder8(v[8 * h + k]) : v[8 * h + k];
-                            wq[4 * k] = e.x;
-                            wq[4 * k + 1] = e.y;
-                            wq[4 * k + 2] = e.z;
-                            wq[4 * k + 3] = e.w;
-                        }
-                        tmem_st32(tmem_lane_addr(tmem_q, warp, (4 * half + 2 * r2 + h) * 32), wq);
-                    }
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && !withhold) mbar_arrive_remote_cta(&bar.q_ready, lead_rank);
-            };
-            WorkIter w = first_work();
-            Item it;
-            int ii = 0, g = 0;
-            bool have = next_item(p, w, cl, ncl, it);
-            if (have) {
-                load_q(it, p.fault == 1);                  // the test hook leaves Q-ready one arrival short
-                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvQReady, 0);
-            }
-            while (!fail && have) {
-                const int R = (it.rt0 + kpair) * kRows + row;
-                const int qi = min(R, p.rows_seq - 1) / p.H;
-                const uint32_t *visrow = p.vis + ((int64_t)it.b * p.T + qi) * p.W;
-                float m_run = -INFINITY;                           // log2 units, same in both halves
-                float l_run = 0.f;                                 // this half's share of the row sum
-                for (int j = 0; j < it.nb; ++j, ++g) {
-                    // No warp leaves this loop on its own: every iteration meets the other seven
-                    // at the named barrier, which ORs their failures.
-                    const int buf = g & 1;
-                    const int ss = g % kNS;                        // staging slot here
-                    const int ps = g % kNP;                        // P slot in the O-CTA
-                    ok = ok && warp_wait(bar, &bar.sfull[buf], (uint32_t)(g >> 1) & 1, p.err, -6);
-                    float x[64];
-                    float mx = -INFINITY;
-                    bool masked = false;                            // block half holds hidden keys
-                    if (ok) {
-                        tc_fence_after();
-                        if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxIn, g);
-                        uint32_t r0v[32], r1v[32];
-                        const uint32_t sbase = tmem_s0 + buf * kKeys + 64 * half;
-                        tmem_ld32(tmem_lane_addr(sbase, warp, 0), r0v);
-                        tmem_ld32(tmem_lane_addr(sbase, warp, 32), r1v);
-                        tmem_wait_ld();
-                        if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxLd, g);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) {             // raw scores
-                            x[q] = __uint_as_float(r0v[q]);
-                            x[32 + q] = __uint_as_float(r1v[q]);
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote_cta(&bar.sempty[buf], lead_rank);   // buffer may be overwritten
-                        if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxLoaded, g);
-                        const int key0 = it.key_base + (it.kb0 + j) * kKeys + 64 * half;
-                        masked = key0 < 0 || key0 + 64 > it.P;     // leading pad or tree keys
-                        if (masked) {   // scale now, hidden keys -inf (also right for scale 0)
-                            // the bits may come from the visibility kernel launched just before
-                            // this one: wait for it before the first window with tree keys
-                            if (!vis_ready && key0 + 64 > it.P) {
-                                griddep_wait();
-                                vis_ready = true;
-                            }
-                            const uint64_t vm = vis_mask64(visrow, p.W, key0, it.P);
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) x[c] = ((vm >> c) & 1ull) ? x[c] * p.scale_log2 : -INFINITY;
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) mx = fmaxf(mx, x[c]);
-                        } else {        // all visible: raw scores kept, the scale goes into the exponent
-                            mx = scaled_max64(x, p.scale_log2);
-                        }
-                        rowmax_s[(buf * 2 + half) * kRows + row] = mx;
-                    }
-                    if (barrier_or<2, 256>(!ok)) {
-                        fail = true;
-                        break;
-                    }
-                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxMax, g);
-                    mx = fmaxf(mx, rowmax_s[(buf * 2 + (half ^ 1)) * kRows + row]);
-                    float alpha = 1.f;
-                    if (mx > m_run + kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY)) {
-                        alpha = (m_run == -INFINITY) ? 1.f : fast_exp2(m_run - mx);
-                        m_run = mx;
-                        l_run *= alpha;
-                    }
-                    // the O-CTA's P slot is free once P.V of block g - kNP has run; this CTA's
-                    // staging slot once the copy of block g - kNS has landed
-                    ok = (g < kNP || warp_wait(bar, &bar.pempty[ps], (uint32_t)((g / kNP) - 1) & 1, p.err, -7)) &&
-                         (g < kNS || warp_wait(bar, &bar.sfree[ss], (uint32_t)((g / kNS) - 1) & 1, p.err, -19));
-                    if (ok) {
-                        if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxSlot, g);
-                        unsigned char *slot_base = smem + kOffPStage + ss * kPSlotBytes;
-                        unsigned char *stage_row = slot_base + half * (kPBytes / 2) + row * 128;
-                        // an all-visible half has finite scores, so m_run is finite here
-                        l_run += masked ? stage_p_row<true, kQ8>(x, p.scale_log2, m_run, stage_row, row)
-                                        : stage_p_row<false, kQ8>(x, p.scale_log2, m_run, stage_row, row);
-                        // the rescale factors follow the second half of P, which carries them
-                        if (half == 1) reinterpret_cast<float *>(slot_base + kPBytes)[row] = alpha;
-                        fence_proxy_async_smem();                  // staging visible to the copy engine
-                        __syncwarp();
-                        // hand the rows to the copy thread without waiting for the other warps
-                        if (lane == 0) mbar_arrive(&bar.staged[ss][half]);
-                        if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxStaged, g);
-                    }
-                }
-                if (fail) break;
-                // this item's statistics for the O-CTA epilogue: (m, l), l over both halves
-                if (half == 1) lsum_s[row] = l_run;
-                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvItemEnd0, ii);
-                if (warp == 8 && lane == 0) KDT_TC_TRACE(kEvItemEnd1, ii);
-                fail = barrier_or<2, 256>(!ok);
-                if (fail) break;
-                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvItemBar, ii);
-                const int sb = ii & 1;                            // statistics buffer of this item
-                if (half == 0) {
-                    // the O-CTA has read this buffer's previous contents (item ii - 2)
-                    ok = ii < 2 || warp_wait(bar, &bar.stats_empty[sb], (uint32_t)((ii >> 1) - 1) & 1, p.err, -26);
-                    if (ok) {
-                        const uint32_t dst = map_to_rank(smem + kOffStats + (sb * kRows + row) * 8, o_rank);
-                        st_cluster_f32(dst, m_run);
-                        st_cluster_f32(dst + 4, l_run + lsum_s[row]);
-                        // every lane releases its own two stores: no fence on this path
-                        mbar_arrive_remote(&bar.stats_full[sb], o_rank);
-                    }
-                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvStatsSent, ii);
-                }
-                ++ii;
-                // the next item's Q_nope: tensor memory is free, every MMA of this item ran
-                // before its last scores could be read
-                have = next_item(p, w, cl, ncl, it);
-                if (have && ok) {
-                    load_q(it, false);
-                    if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvQReady, ii);
-                }
-                // lsum_s is rewritten at the end of the next item only after this barrier
-                fail = barrier_or<2, 256>(!ok);
-            }
-            // The O pair's MMA commits (pempty), the O-CTA's watcher (sfree) and its epilogue
-            // (stats_empty) arrive here; the arrivals still due are consumed before this CTA
-            // may leave, so none can land in the shared memory of a CTA that later runs here.
-            if (!fail && ok && warp == 4) {
-                for (int ps = 0; ps < kNP && ps < G; ++ps) {
-                    const int g_last = ps + ((G - 1 - ps) / kNP) * kNP;
-                    ok = warp_wait(bar, &bar.pempty[ps], (uint32_t)(g_last / kNP) & 1, p.err, -18) && ok;
-                }
-                for (int ss = 0; ss < kNS && ss < G; ++ss) {
-                    const int g_last = ss + ((G - 1 - ss) / kNS) * kNS;
-                    ok = warp_wait(bar, &bar.sfree[ss], (uint32_t)(g_last / kNS) & 1, p.err, -20) && ok;
-                }
-                for (int sb = 0; sb < 2 && sb < ii; ++sb) {
-                    const int i_last = sb + ((ii - 1 - sb) / 2) * 2;
-                    ok = warp_wait(bar, &bar.stats_empty[sb], (uint32_t)(i_last >> 1) & 1, p.err, -27) && ok;
-                }
-            }
-        } else if (warp < 4 + kEpiWarps) {
+    };
+    auto o_epilogue = [&]() {
         unsigned char *pbase = smem + kOffP;
         const float2 *stats_s = reinterpret_cast<const float2 *>(smem + kOffStats);
-            // ---------------- correction (rare rescale) and epilogue, per item ----------------
-            // Warp w serves the 32 rows of TMEM lane quadrant (w % 4) and the columns
-            // [col0, col0 + kEpiGroupCols); named barrier 1 counts these warps. They sleep on
-            // `go` until the MMA thread hands O over for a rescale or ends the item.
-            const int row = 32 * (warp & 3) + lane;
-            const int col0 = ((warp - 4) >> 2) * kEpiGroupCols;
-            bool ok = true;
-            uint32_t e = 0;                                     // `go` events so far
-            WorkIter w = first_work();
-            Item it;
-            int ii = 0;
-            while (ok && next_item(p, w, cl, ncl, it)) {
-                for (;; ++e) {
-                    ok = warp_wait_cluster(bar, &bar.go, e & 1, p.err, -12);
-                    if (barrier_or<1, 32 * kEpiWarps>(!ok)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t cmd = *reinterpret_cast<volatile uint32_t *>(&bar.cmd);
-                    if (cmd == kCmdDone) {
-                        ++e;
-                        break;
-                    }
-                    // every P.V before the block in P slot `cmd` has completed: rescale this
-                    // CTA's rows of O by that block's factors (rows that need none multiply by 1)
-                    const float a = reinterpret_cast<const float *>(pbase + (cmd % kNP) * kPSlotBytes + kPBytes)[row];
-                    tc_fence_after();
-                    for (int c = 0; c < kEpiGroupCols / 32; ++c) {
-                        uint32_t r[32];
-                        const uint32_t addr = tmem_lane_addr(tmem, warp, col0 + c * 32);
-                        tmem_ld32(addr, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * a);
-                        tmem_st32(addr, r);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    barrier_or<1, 32 * kEpiWarps>(false);  // every warp's stores done
-                    if (threadIdx.x == 128) mbar_arrive_remote(&bar.rescaled, lead_rank);
-                }
-                if (!ok) break;
-                // epilogue of the item: o = O / l, lse = ln2 (m + log2 l); whole units write the
-                // final rows, pieces their partial state
-                const int sb = ii & 1;
-                ok = warp_wait(bar, &bar.o_done, (uint32_t)ii & 1, p.err, -13) &&
-                     warp_wait_cluster(bar, &bar.stats_full[sb], (uint32_t)(ii >> 1) & 1, p.err, -14);
+        // ---------------- correction (rare rescale) and epilogue, per item ----------------
+        // Warp w serves the 32 rows of TMEM lane quadrant (w % 4) and the columns
+        // [col0, col0 + kEpiGroupCols); named barrier 1 counts these warps. They sleep on
+        // `go` until the MMA thread hands O over for a rescale or ends the item.
+        const int row = 32 * (warp & 3) + lane;
+        const int col0 = ((warp - 4) >> 2) * kEpiGroupCols;
+        bool ok = true;
+        uint32_t e = 0;                                     // `go` events so far
+        WorkIter w = first_work();
+        Item it;
+        int ii = 0;
+        while (ok && next_item(p, w, cl, ncl, it)) {
+            for (;; ++e) {
+                ok = warp_wait_cluster(bar, &bar.go, e & 1, p.err, -12);
                 if (barrier_or<1, 32 * kEpiWarps>(!ok)) {
                     ok = false;
                     break;
                 }
-                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvEpiIn, ii);
-                tc_fence_after();
-                const int R = (it.rt0 + kpair) * kRows + row;
-                const int64_t grow = (int64_t)it.b * p.rows_seq + R;
-                const bool b16 = kQ8 && it.whole && p.out_bf16;   // final rows in bf16 (orow unused then)
-                float *orow, *lrow;
-                if (it.whole) {
-                    orow = p.out + grow * kDc;
-                    lrow = p.lse ? p.lse + grow : nullptr;
-                } else {
-                    const int64_t k = (int64_t)it.slot * (2 * kRows) + kpair * kRows + row;
-                    orow = p.part_o + k * kDc;
-                    lrow = p.part_lse + k;
+                const uint32_t cmd = *reinterpret_cast<volatile uint32_t *>(&bar.cmd);
+                if (cmd == kCmdDone) {
+                    ++e;
+                    break;
                 }
-                const float2 st = stats_s[sb * kRows + row];
-                const float inv = kQ8 ? (st.y == 0.f ? 0.f : 1.f / st.y)      // (a NaN goes on)
-                                      : (st.y > 0.f ? 1.f / st.y : 0.f);
-                // Each thread holds one row; the rows go out through a per-warp transpose in
-                // shared memory so that every store instruction writes whole 32-byte sectors
-                // (eight rows x 64 bytes). 16-byte slot q of staged row r sits at
-                // q ^ ((r >> 1) & 3), which keeps both the row-wise writes and the
-                // sector-wise reads at the minimum number of shared-memory wavefronts.
-                static_assert(kEpiCols == 16, "the transpose below stages 16 columns");
-                float *stg = reinterpret_cast<float *>(smem + kOffEpi) + (warp - 4) * 32 * kEpiCols;
-                const int rsub = lane >> 2, qsub = lane & 3;      // read side: row 8i + rsub, slot qsub
-                float *orow0 = orow - (int64_t)lane * kDc + col0; // row 0 of this warp's 32, its first column
-                const int rows_ok = p.rows_seq - (R - lane);      // rows of the 32 that exist
+                // every P.V before the block in P slot `cmd` has completed: rescale this
+                // CTA's rows of O by that block's factors (rows that need none multiply by 1)
+                const float a = reinterpret_cast<const float *>(pbase + (cmd % kNP) * kPSlotBytes + kPBytes)[row];
+                tc_fence_after();
                 for (int c = 0; c < kEpiGroupCols / 32; ++c) {
                     uint32_t r[32];
-                    tmem_ld32(tmem_lane_addr(tmem, warp, col0 + c * 32), r);
+                    const uint32_t addr = tmem_lane_addr(tmem, warp, col0 + c * 32);
+                    tmem_ld32(addr, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            constexpr int k1 = kQ8 ? 2 : 1, k2 = kQ8 ? 1 : 2;      // widening's order of the dims
-                            *reinterpret_cast<float4 *>(stg + lane * kEpiCols + ((q ^ ((lane >> 1) & 3)) << 2)) =
-                                make_float4(__uint_as_float(r[16 * hh + 4 * q]) * inv, __uint_as_float(r[16 * hh + 4 * q + k1]) * inv,
-                                            __uint_as_float(r[16 * hh + 4 * q + k2]) * inv,
-                                            __uint_as_float(r[16 * hh + 4 * q + 3]) * inv);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int rr = 8 * i + rsub;
-                            const float4 v =
-                                *reinterpret_cast<const float4 *>(stg + rr * kEpiCols + ((qsub ^ ((rr >> 1) & 3)) << 2));
-                            if (rr < rows_ok) {
-                                if (kQ8 && b16)
-                                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) +
-                                                               (grow - lane + rr) * kDc + col0 + c * 32 + hh * 16 + 4 * qsub) =
-                                        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                                else
-                                    *reinterpret_cast<float4 *>(orow0 + (int64_t)rr * kDc + c * 32 + hh * 16 + 4 * qsub) = v;
-                            }
-                        }
-                        __syncwarp();
-                    }
+                    for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * a);
+                    tmem_st32(addr, r);
                 }
-                if (col0 == 0 && R < p.rows_seq && lrow)
-                    *lrow = (kQ8 ? st.y != 0.f : st.y > 0.f) ? 0.6931471805599453f * (st.x + log2f(st.y)) : -INFINITY;
-                // O may be overwritten and the statistics buffer refilled
+                tmem_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_remote(&bar.o_free, lead_rank);
-                    mbar_arrive_remote_cta(&bar.stats_empty[sb], (uint32_t)kpair);
-                }
-                if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvEpiOut, ii);
-                ++ii;
+                barrier_or<1, 32 * kEpiWarps>(false);  // every warp's stores done
+                if (threadIdx.x == 128) mbar_arrive_remote(&bar.rescaled, lead_rank);
             }
+            if (!ok) break;
+            // epilogue of the item: o = O / l, lse = ln2 (m + log2 l); whole units write the
+            // final rows, pieces their partial state
+            const int sb = ii & 1;
+            ok = warp_wait(bar, &bar.o_done, (uint32_t)ii & 1, p.err, -13) &&
+                 warp_wait_cluster(bar, &bar.stats_full[sb], (uint32_t)(ii >> 1) & 1, p.err, -14);
+            if (barrier_or<1, 32 * kEpiWarps>(!ok)) {
+                ok = false;
+                break;
+            }
+            if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvEpiIn, ii);
+            tc_fence_after();
+            const int R = (it.rt0 + kpair) * kRows + row;
+            const int64_t grow = (int64_t)it.b * p.rows_seq + R;
+            const bool b16 = kQ8 && it.whole && p.out_bf16;   // final rows in bf16 (orow unused then)
+            float *orow, *lrow;
+            if (it.whole) {
+                orow = p.out + grow * kDc;
+                lrow = p.lse ? p.lse + grow : nullptr;
+            } else {
+                const int64_t k = (int64_t)it.slot * (2 * kRows) + kpair * kRows + row;
+                orow = p.part_o + k * kDc;
+                lrow = p.part_lse + k;
+            }
+            const float2 st = stats_s[sb * kRows + row];
+            const float inv = kQ8 ? (st.y == 0.f ? 0.f : 1.f / st.y)      // (a NaN goes on)
+                                  : (st.y > 0.f ? 1.f / st.y : 0.f);
+            // Each thread holds one row; the rows go out through a per-warp transpose in
+            // shared memory so that every store instruction writes whole 32-byte sectors
+            // (eight rows x 64 bytes). 16-byte slot q of staged row r sits at
+            // q ^ ((r >> 1) & 3), which keeps both the row-wise writes and the
+            // sector-wise reads at the minimum number of shared-memory wavefronts.
+            static_assert(kEpiCols == 16, "the transpose below stages 16 columns");
+            float *stg = reinterpret_cast<float *>(smem + kOffEpi) + (warp - 4) * 32 * kEpiCols;
+            const int rsub = lane >> 2, qsub = lane & 3;      // read side: row 8i + rsub, slot qsub
+            float *orow0 = orow - (int64_t)lane * kDc + col0; // row 0 of this warp's 32, its first column
+            const int rows_ok = p.rows_seq - (R - lane);      // rows of the 32 that exist
+            for (int c = 0; c < kEpiGroupCols / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tmem_lane_addr(tmem, warp, col0 + c * 32), r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        constexpr int k1 = kQ8 ? 2 : 1, k2 = kQ8 ? 1 : 2;      // widening's order of the dims
+                        *reinterpret_cast<float4 *>(stg + lane * kEpiCols + ((q ^ ((lane >> 1) & 3)) << 2)) =
+                            make_float4(__uint_as_float(r[16 * hh + 4 * q]) * inv, __uint_as_float(r[16 * hh + 4 * q + k1]) * inv,
+                                        __uint_as_float(r[16 * hh + 4 * q + k2]) * inv,
+                                        __uint_as_float(r[16 * hh + 4 * q + 3]) * inv);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + rsub;
+                        const float4 v =
+                            *reinterpret_cast<const float4 *>(stg + rr * kEpiCols + ((qsub ^ ((rr >> 1) & 3)) << 2));
+                        if (rr < rows_ok) {
+                            if (kQ8 && b16)
+                                *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) +
+                                                           (grow - lane + rr) * kDc + col0 + c * 32 + hh * 16 + 4 * qsub) =
+                                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                            else
+                                *reinterpret_cast<float4 *>(orow0 + (int64_t)rr * kDc + c * 32 + hh * 16 + 4 * qsub) = v;
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (col0 == 0 && R < p.rows_seq && lrow)
+                *lrow = (kQ8 ? st.y != 0.f : st.y > 0.f) ? 0.6931471805599453f * (st.x + log2f(st.y)) : -INFINITY;
+            // O may be overwritten and the statistics buffer refilled
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_remote(&bar.o_free, lead_rank);
+                mbar_arrive_remote_cta(&bar.stats_empty[sb], (uint32_t)kpair);
+            }
+            if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvEpiOut, ii);
+            ++ii;
         }
+    };
+    // The roles' order is each kernel's own: by CTA the bf16 kernel runs 2.5% faster than by warpgroup
+    // (417 against 428 us for 8 sequences of 64 nodes over 8 k keys); the 8-bit kernel has to branch by
+    // warpgroup, because a warpgroup changes its register share as one.
+    if constexpr (!kQ8) {
+        if (s_role) {
+            if (warp < 4) s_issue();
+            else s_softmax();
+        } else {
+            if (warp < 4) o_issue();
+            else if (warp < 4 + kEpiWarps) o_epilogue();
+        }
+    } else if (warp < 4) {
+        set_regs<kRegsIssueQ8>();
+        if (s_role) s_issue();
+        else o_issue();
+    } else if (warp < 12) {
+        set_regs<kRegsSoftQ8>();
+        if (s_role) s_softmax();
+        else if (warp < 4 + kEpiWarps) o_epilogue();
     } else {
-        if constexpr (kQ8) {
         set_regs<kRegsWidenQ8>();
         // ---------------- widening: this CTA's half of every latent chunk -----------------------
         // Codes come by TMA in raw pieces, four a block; warps 12-15 take pieces 0 and 2, warps 16-19
@@ -1670,7 +1687,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                 const int u = 2 * bar.work_count - 1 - k;      // chunk use
                 mbar_wait(&empty[u % (int)nslots], (uint32_t)(u / (int)nslots) & 1, bar.wait_ns);
             }
-        }
     }
 
     // ---- teardown ------------------------------------------------------------------------
