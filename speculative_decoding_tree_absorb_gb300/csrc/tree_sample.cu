@@ -23,6 +23,10 @@
 //    float32 numbers (an FP64 operation of one warp takes 16 clocks here): y log2(e) = n + k / 128
 //    + r, e^y = 2^n 2^{k/128} (1 + q + q^2/2 + ...), q = r ln 2 <= 0.0028, the leading terms as
 //    pairs. Its error is below 2^-40 of the weight.
+//  * What bounds it is the chain of a step, not its bytes: about 3 us of loads, two block sums,
+//    the exchange and the tests, 1.2 us for 160000 tokens over 8 CTAs, and once a sequence
+//    12 us of weights and sums for the draw. Measured: 8 sequences, 64 nodes, 160000 tokens in
+//    bf16 (paths of up to 6) 50 us, one sequence, 9 nodes, 32000 tokens in float32 21 us.
 #include <math.h>
 
 #include <atomic>

@@ -30,6 +30,13 @@
 //  * A group of codes marked NaN is stored as zeros and its key flagged: the flag makes the
 //    key's visible scores NaN, so a row that sees it becomes NaN and a row that does not
 //    see it is untouched (0 * NaN never enters a product).
+//  * What bounds it: 64 rows a tile make the MMAs read shared memory for the whole of their
+//    time (4 KB of A and 2 KB of B for 48 clocks each), and there is room for one block of
+//    128 keys, so its stages follow one another: O^T's MMAs 1.7 k clocks, the last pair's
+//    widening 2.5-3 k (its stores share shared memory with those MMAs), the last scores
+//    0.6 k, softmax 1.2 k, hand-offs: 7.5 k clocks (3.9 us) a block. Measured: 64 single
+//    tokens of 64 heads over 1-8 k keys 92 us (196 MB of cache: 2.1 TB/s, tensor pipe 23%);
+//    3 sequences of 13 nodes and 16 heads over 5-32 k keys 70 us.
 //  * Every wait is bounded; one that runs out records a status in the error word and the
 //    kernel drains its MMAs, frees tensor memory and returns.
 #include <math.h>
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         // shared-memory place of key k0 + kq (key k0 + kq + 4 t follows at + 512 t), and this lane's
         // swizzled chunk for even and odd t (which flip bit 2 of the key)
         const uint32_t krow0 = smem + 2 * pair * kKTile + (k0 + kq) * 128 + ((sub ^ kq) << 4), krow1 = krow0 ^ 64;
-        const uint32_t pick = sub >> 2 ? 0x3232u : 0x1010u;  // the lane's group of a tile's two
+        const uint32_t pick = sub >> 2 ? 0x7632u : 0x5410u;  // the lane's group of a tile's two
         uint2 a[8], b[8];      // codes of key k0 + kq + 4 t in the pair's first and second tile
         uint32_t sc;           // the four scale bytes of key k0 + lane
         int j = 0;
@@ -627,25 +634,30 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         const uint32_t G = (uint32_t)bar.work[0];            // blocks of the share
         if (fill(p, it)) load();
         for (uint32_t g = 0; g < G; ++g) {
-            // the pair's space: read by O^T's MMAs of the block before
-            if (g > 0 && !warp_wait(bar, &bar.kempty[pair], (g - 1) & 1, p.err, -45)) break;
-            // a lane turns the scale bytes of its key into factors, a pair for each tile
+            // before the wait: a lane turns the scale bytes of its key into factors, and gets those of
+            // its eight keys (the first tile's in the low half)
             const uint32_t b0 = sc & 255u, b1 = (sc >> 8) & 255u, b2 = (sc >> 16) & 255u, b3 = sc >> 24;
-            const uint32_t fa = q8::factor(b0) | (q8::factor(b1) << 16), fb = q8::factor(b2) | (q8::factor(b3) << 16);
             const bool nan = b0 == (uint32_t)q8::kNaN || b1 == (uint32_t)q8::kNaN || b2 == (uint32_t)q8::kNaN ||
                              b3 == (uint32_t)q8::kNaN;
+            uint32_t f[8];
+            {
+                const uint32_t fa = q8::factor(b0) | (q8::factor(b1) << 16), fb = q8::factor(b2) | (q8::factor(b3) << 16);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    f[t] = __byte_perm(__shfl_sync(0xffffffffu, fa, 4 * t + kq), __shfl_sync(0xffffffffu, fb, 4 * t + kq), pick);
+            }
+            // the pair's space: read by O^T's MMAs of the block before
+            if (g > 0 && !warp_wait(bar, &bar.kempty[pair], (g - 1) & 1, p.err, -45)) break;
             if (nan) sh.bad[g & 1][k0 + lane] = 1u;
-            // two keys a lane at a time: their shuffles, their products, their stores (a shuffle between two
-            // stores would wait for the first one's values)
+            // two keys a lane at a time: their products, their stores
 #pragma unroll
             for (int t0 = 0; t0 < 8; t0 += 2) {
-                uint32_t f[4];
                 uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = __shfl_sync(0xffffffffu, k & 1 ? fb : fa, 4 * (t0 + (k >> 1)) + kq);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = q8::widen8(k & 1 ? b[t0 + (k >> 1)] : a[t0 + (k >> 1)], __byte_perm(f[k], 0u, pick));
+                for (int k = 0; k < 4; ++k) {
+                    const int t = t0 + (k >> 1);
+                    v[k] = q8::widen8(k & 1 ? b[t] : a[t], __byte_perm(f[t], 0u, k & 1 ? 0x3232u : 0x1010u));
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sts((k >> 1 ? krow1 : krow0) + 512 * (t0 + (k >> 1)) + (k & 1) * kKTile, v[k]);
             }
@@ -655,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 const uint32_t hb = q8::factor_high(b2) | (q8::factor_high(b3) << 16);
 #pragma unroll 1
                 for (int t = 0; t < 16; ++t) {
-                    const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, t < 8 ? ha : hb, 4 * (t & 7) + kq), 0u, pick);
+                    const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, t < 8 ? ha : hb, 4 * (t & 7) + kq), 0u,
+                                                   sub >> 2 ? 0x3232u : 0x1010u);
                     const uint32_t dst = ((t & 1) ? krow1 : krow0) + 512 * (t & 7) + (t >> 3) * kKTile;
                     uint4 v = lds(dst);
                     v.x = q8::mul_bf16x2(v.x, f);
