@@ -516,7 +516,7 @@ typedef struct {
     kdt_dtype out_dtype;    /* KDT_F32 or KDT_BF16 */
     float *lse;             /* device fp32 [B,T,H], or NULL */
     int32_t *err;           /* device int32 error word, or NULL (as for kdt_verify_attn) */
-    int impl;               /* KDT_IMPL_AUTO (by the rows T * H of a sequence), KDT_IMPL_TCGEN05 (256 rows
+    int impl;               /* KDT_IMPL_AUTO (the cheaper one for these sizes), KDT_IMPL_TCGEN05 (256 rows
                                at a time on 4-CTA clusters) or KDT_IMPL_Q8_ROWS (64 rows on one SM) */
     int num_splits;         /* 0 = automatic; else the CTAs the (64-row tile, 128-key block) pairs are cut
                                into equal shares for (at most one per pair), or the clusters (at most
@@ -532,7 +532,8 @@ typedef struct {
  * Exactly one of `parent` and `vis` is given; a row that sees no key gets out = 0 and
  * lse = -inf. A row that sees a NaN group or a non-finite k_pe gets NaN; a row from which
  * such a key is hidden is not affected by it, and rows of the cache at or beyond
- * prefix_len[b] + T are never read.
+ * prefix_len[b] + T are never read. prefix_len values are device data: the caller guarantees
+ * 0 <= prefix_len[b] <= max_kv_len - T.
  * `workspace` must hold kdt_verify_attn_q8_workspace_size(a) bytes (256-byte aligned);
  * its contents need no initialisation. Calls that may run at the same time, captured ones
  * included, need workspaces of their own.
@@ -562,8 +563,8 @@ kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
  * (a token that an earlier sibling drafted too counts once: the later one is never accepted).
  * When no child is accepted the bonus token is the least j with sum_{k <= j} w'_k >
  * u_bonus[b] * sum_k w'_k, where w' is w with the children's tokens set to 0.
- * Sums and comparisons are made in fixed point or 64 bits: the result does not depend on how
- * the work is split.
+ * A comparison that float32 sums leave in doubt, and every draw, is made in fixed point: the
+ * result does not depend on how the work is split.
  *   parent   device int32 [B,T], -1 <= parent[b,i] < i;  tok device int32 [B,T] (tok[b,0] unused)
  *   logits   device, row (b,i) at logits + (b*T + i) * row_stride elements, V of them used, of
  *            dtype; row_stride 0 = V. -inf is a token that cannot be drawn.

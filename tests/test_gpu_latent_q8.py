@@ -217,7 +217,7 @@ def test_far_rows_pass_32_bits(kdt):
     assert (pre == L - T + 3).all()
 
 
-@pytest.mark.parametrize("B,T", [(1, 1), (4, 64), (7, 300)])
+@pytest.mark.parametrize("B,T", [(1, 1), (4, 64), (7, 300), (2, 4096)])
 def test_compact_moves_the_path(kdt, B, T):
     import torch
     g = _gen(T)

@@ -223,6 +223,22 @@ def test_captured_graph_two_streams_and_fresh_inputs(kdt, T, H, prefix):
             assert torch.equal(o, outs[k]) and torch.equal(l, lses[k])
 
 
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+def test_far_sequences_pass_32_bits(kdt, impl):
+    """Code offsets of the last sequence are beyond 2^31 (and its queries few)."""
+    d = _inputs(81, 9, 4, [0, 3, 260], pad=2200000)
+    assert 2 * d["L"] * 512 > 2 ** 31
+    _check(d, _call(kdt, d, impl=impl), 0.0)
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+@pytest.mark.parametrize("T,H", [(1, 4), (6, 50)])
+def test_more_sequences_than_sms(kdt, impl, T, H):
+    rng = np.random.RandomState(3)
+    d = _inputs(82, T, H, [int(x) for x in rng.randint(0, 300, 170)])
+    _check(d, _call(kdt, d, impl=impl), 0.0)
+
+
 def test_not_device_memory_is_refused(kdt):
     import torch
     d = _inputs(71, 33, 8, [10])            # a tree whose visibility takes a workspace
