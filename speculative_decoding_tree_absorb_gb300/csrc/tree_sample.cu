@@ -23,10 +23,10 @@
 //    float32 numbers (an FP64 operation of one warp takes 16 clocks here): y log2(e) = n + k / 128
 //    + r, e^y = 2^n 2^{k/128} (1 + q + q^2/2 + ...), q = r ln 2 <= 0.0028, the leading terms as
 //    pairs. Its error is below 2^-40 of the weight.
-//  * What bounds it is the chain of a step, not its bytes: about 3 us of loads, two block sums,
-//    the exchange and the tests, 1.2 us for 160000 tokens over 8 CTAs, and once a sequence
-//    12 us of weights and sums for the draw. Measured: 8 sequences, 64 nodes, 160000 tokens in
-//    bf16 (paths of up to 6) 50 us, one sequence, 9 nodes, 32000 tokens in float32 21 us.
+//  * What bounds it is the chain of a step, not its bytes: about 2.5 us of loads, two block sums,
+//    the exchange and the tests, 0.8 us for 160000 tokens over 8 CTAs, and once a sequence
+//    8 us of weights and 3 of sums for the draw. Measured: 8 sequences, 64 nodes, 160000 tokens
+//    in bf16 (paths of up to 6) 41 us, one sequence, 9 nodes, 32000 tokens in float32 19 us.
 #include <math.h>
 
 #include <atomic>
@@ -39,17 +39,18 @@ namespace {
 
 constexpr int kNT = 512, kNW = kNT / 32;            // threads, warps a CTA
 constexpr int kMaxCluster = 8;
-constexpr size_t kMostSmem = 220 * 1024;
+constexpr size_t kMostSmem = 208 * 1024;            // beside Shared
 constexpr int kMaxVocab = 1 << 19;                  // sums of 2^44 weights then fit 63 bits
 constexpr int kFrac = 44;
 constexpr double kMargin = 4e-5;
 constexpr int kKeep = 32;                           // log-probabilities written at a time
 constexpr int kFewKids = 32;                        // children whose first tests are made in float32
 
+// 2^{k/128}, k = -64 .. 64, in units of 2^-45: hi * 2^45 + lo, hi a multiple of 2^-22 and 0 <= lo < 2^23.
 struct Exp2Table {
-    uint64_t fix[129];                              // 2^{k/128} in units of 2^-46, k = -64 .. 64
-    float hi[129], lo[129];                         // the same as a pair; lo in units of 2^-46
+    float hi[129], lo[129];
 };
+constexpr int kCopies = 16;                         // of the table in shared memory: a lane's reads meet no other's
 
 struct SampleParams {
     const int32_t *parent, *tok;
@@ -69,35 +70,41 @@ struct SampleParams {
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// round(2^44 e^{(l - m) / temperature}), l <= m finite (l may be -inf).
-__device__ __forceinline__ uint64_t weight(float l, float m, float c_hi, float c_lo, const Exp2Table &tab) {
+// round(2^44 e^{(l - m) / temperature}), l <= m finite (l may be -inf); tab is the lane's copy of the
+// table. Roundings to integers are sums with 1.5 * 2^23 (the integer is then in the low bits): conversions
+// run at a fraction of their rate. Without branches, so that several weights are under way at once.
+__device__ __forceinline__ uint64_t weight(float l, float m, float c_hi, float c_lo, const float2 *tab) {
+    constexpr float kMagic = 12582912.f;
+    constexpr int kMagicBits = 0x4b400000;
     const float d = __fsub_rn(l, m);
-    if (!(d > -INFINITY)) return 0;
     const float bb = __fsub_rn(d, l);
     const float dl = __fsub_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fadd_rn(m, bb));   // l - m = d + dl exactly
     const float p = __fmul_rn(d, c_hi);
     const float pl = __fadd_rn(__fmaf_rn(d, c_hi, -p), __fmaf_rn(d, c_lo, __fmul_rn(dl, c_hi)));
-    const float n = rintf(p);
-    if (n < -46.f) return 0;                        // below half a unit
-    const float f = __fsub_rn(p, n);                // exact
+    const float t = __fadd_rn(p, kMagic);
+    const int n = __float_as_int(t) - kMagicBits;
+    const float f = __fsub_rn(p, __fsub_rn(t, kMagic));                               // exact
     const float fh = __fadd_rn(f, pl), fl = __fsub_rn(pl, __fsub_rn(fh, f));         // |f| >= |pl| or both tiny
-    const float kf = rintf(__fmul_rn(fh, 128.f));
-    const int k = (int)kf + 64;
-    const float r = __fmaf_rn(kf, -0.0078125f, fh);                                   // exact
+    const float u = __fmaf_rn(fh, 128.f, kMagic);
+    const uint32_t k = min((uint32_t)(__float_as_int(u) - kMagicBits + 64), 128u);    // (beyond it: l = -inf)
+    const float r = __fmaf_rn(__fsub_rn(u, kMagic), -0.0078125f, fh);                 // exact
     constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957768e-09f;   // ln 2 as a pair
     const float q = __fmul_rn(r, kLn2Hi);
     const float ql = __fadd_rn(__fmaf_rn(r, kLn2Hi, -q), __fmaf_rn(r, kLn2Lo, __fmul_rn(fl, kLn2Hi)));
     // e^q - 1 - q
     const float s = __fmul_rn(__fmul_rn(q, q), __fmaf_rn(q, __fmaf_rn(q, 0.0416666679f, 0.166666672f), 0.5f));
-    const float th = tab.hi[k];
-    const float a = __fmul_rn(th, q);
-    const float b = __fadd_rn(__fmaf_rn(th, q, -a), __fmul_rn(th, __fadd_rn(ql, s)));
-    constexpr float kUnit = 70368744177664.f;                                         // 2^46
-    int64_t w = (int64_t)tab.fix[k] + __float2ll_rn(__fmul_rn(a, kUnit)) +
-                __float2ll_rn(__fmaf_rn(tab.lo[k], q, __fmul_rn(b, kUnit)));
-    const int shift = 46 - kFrac - (int)n;
-    w = (w + ((int64_t)1 << (shift - 1))) >> shift;
-    return (uint64_t)w;
+    const float2 th = tab[k * kCopies];
+    const float a = __fmul_rn(th.x, q);
+    const float b = __fadd_rn(__fmaf_rn(th.x, q, -a), __fmul_rn(th.x, __fadd_rn(__fmaf_rn(q, ql, ql), s)));
+    // in units of 2^-45: hi + lo + a + b, a in two parts
+    const float v = __fmaf_rn(a, 8388608.f, kMagic);
+    const float ra = __fmaf_rn(__fsub_rn(v, kMagic), -1.1920928955078125e-07f, a);    // exact
+    const int rest = __float2int_rn(__fmaf_rn(th.y, __fadd_rn(q, s), __fmul_rn(__fadd_rn(b, ra), 35184372088832.f)));
+    const int hi = __float_as_int(__fmaf_rn(th.x, 4194304.f, 8388608.f)) - 0x4b000000;
+    const int lo = __float_as_int(__fadd_rn(th.y, 8388608.f)) - 0x4b000000;
+    const int64_t w = (int64_t)hi * (1 << 23) + ((int64_t)(__float_as_int(v) - kMagicBits) * (1 << 22) + (int64_t)(lo + rest));
+    const int shift = 45 - kFrac - n;                // 1 .. 48
+    return p >= -47.f ? (uint64_t)((w + ((int64_t)1 << ((shift - 1) & 63))) >> (shift & 63)) : 0;   // below -45: half a unit
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -113,7 +120,7 @@ struct alignas(16) Slot {
 };
 
 struct Shared {
-    Exp2Table tab;
+    float2 tab[129 * kCopies];
     Slot slot[2][kMaxCluster];                      // by exchange parity
     uint64_t exact[2][kMaxCluster];
     double z;
@@ -149,11 +156,8 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
     const int b = blockIdx.x / size, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t tb = (int64_t)b * p.T;
     const int v0 = min((int)rank * p.slice, p.V), n = min(p.slice, p.V - v0);
-    for (int k = tid; k < 129; k += kNT) {
-        sh.tab.fix[k] = table.fix[k];
-        sh.tab.hi[k] = table.hi[k];
-        sh.tab.lo[k] = table.lo[k];
-    }
+    for (int k = tid; k < 129 * kCopies; k += kNT) sh.tab[k] = make_float2(table.hi[k / kCopies], table.lo[k / kCopies]);
+    const float2 *tab = sh.tab + lane % kCopies;
     for (int i = tid; i < p.T; i += kNT) {
         const int32_t pa = p.parent[tb + i];
         par[i] = pa;
@@ -165,14 +169,21 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
             if (pa < -1 || pa >= i) record_error(p.err, (int32_t)(tb + i + 1));
         }
     }
-    tc::cluster_sync();        // every CTA runs before another writes to its shared memory
+    tc::cluster_arrive();      // every CTA runs before another writes to its shared memory (waited for there)
+    __syncthreads();
     // a warp's part of the slice, in whole groups of 16 tokens
     const int part = (p.slice / 16 + kNW - 1) / kNW * 16;
     const int w0 = min(warp * part, n), w1 = min(w0 + part, n);
 
-    // natural log of the probability of a token of logit l, M the row's maximum, z the sum of weights
+    // natural log of the probability of a token of logit l, M the row's maximum, z the sum of weights. The
+    // FP64 log takes 2 k clocks: log z = log 2^e + logf(mantissa as float32) + the rest, to a unit of float32
     auto log_p = [&](float l, float M, double z) {
-        return (float)(((double)l - (double)M) * p.inv_temp - (log(z) - kFrac * 0.69314718055994530942));
+        const long long bits = __double_as_longlong(z);
+        const int e = (int)(bits >> 52) - 1023;
+        const double mant = __longlong_as_double((bits & 0xfffffffffffffll) | 0x3ff0000000000000ll);
+        const float mf = (float)mant;
+        const double log_mant = (double)logf(mf) + (double)__fdividef((float)(mant - (double)mf), mf);
+        return (float)(((double)l - (double)M) * p.inv_temp - (log_mant + (e - kFrac) * 0.69314718055994530942));
     };
     auto write_kept = [&](int first, int count) {              // by the warp of the thread that kept them
         if (rank || warp || !p.logp) return;
@@ -241,9 +252,9 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         for (int off = 16; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
         if (lane == 0) sh.wm[warp] = m;
         __syncthreads();                                       // also: the row and the children are in place
-        m = sh.wm[0];
+        m = sh.wm[lane % kNW];
 #pragma unroll
-        for (int k = 1; k < kNW; ++k) m = top(m, sh.wm[k]);
+        for (int off = kNW / 2; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
         const E *data = p.cache ? row : src;
         // -- the slice's sum relative to its maximum
         // (in float32 by vectors of 16 bytes and warps, then in 64 bits: off by at most 130 roundings)
@@ -278,6 +289,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         __syncthreads();
         // -- one exchange over the cluster
         Slot *slots = sh.slot[step & 1];
+        if (step == 0) tc::cluster_wait();
         if (warp == 0) {
             double s = lane < kNW ? (double)sh.wz[lane] : 0.0;
 #pragma unroll
@@ -287,8 +299,9 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
                                   (uint32_t)__double2loint(s), (uint32_t)__double2hiint(s));
         }
         tc::cluster_sync();
-        float M = slots[0].m;
-        for (uint32_t k = 1; k < size; ++k) M = top(M, slots[k].m);
+        float M = lane % kMaxCluster < (int)size ? slots[lane % kMaxCluster].m : -INFINITY;
+#pragma unroll
+        for (int off = kMaxCluster / 2; off >= 1; off >>= 1) M = top(M, __shfl_xor_sync(0xffffffffu, M, off));
         if (!(M > -INFINITY && M < INFINITY)) {                // no distribution: the walk ends here
             if (rank == 0 && tid == 0) {
                 record_error(p.err, (int32_t)(tb + node + 1));
@@ -308,8 +321,8 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         }
         // -- the children's weights; a repeated token counts once
         const int nc = sh.n_child;
-        for (int k = tid; k < nc; k += kNT) {
-            cw[k] = ct[k] < 0 ? 0 : weight(cl[k], M, p.c_hi, p.c_lo, sh.tab);
+        for (int k = tid >= 32 ? tid - 32 : kNT - 32 + tid; k < nc; k += kNT) {   // (warp 0 is at the sum)
+            cw[k] = ct[k] < 0 ? 0 : weight(cl[k], M, p.c_hi, p.c_lo, tab);
             for (int j = 0; j < k && cw[k]; ++j)
                 if (ct[j] == ct[k]) cw[k] = 0;
         }
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
             // exact sums of the warps' parts, children included
             uint64_t x = 0;
 #pragma unroll 4
-            for (int i = w0 + lane; i < w1; i += 32) x += weight(as_f32(data[i]), M, p.c_hi, p.c_lo, sh.tab);
+            for (int i = w0 + lane; i < w1; i += 32) x += weight(as_f32(data[i]), M, p.c_hi, p.c_lo, tab);
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
             if (lane == 0) sh.wx[warp] = x;
@@ -444,7 +457,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         auto left = [&](int i) -> uint64_t {                   // weight of slice token i, 0 for a child's
             for (int k = 0; k < nc; ++k)
                 if (ct[k] == v0 + i) return 0;
-            return weight(as_f32(data[i]), M, p.c_hi, p.c_lo, sh.tab);
+            return weight(as_f32(data[i]), M, p.c_hi, p.c_lo, tab);
         };
         uint64_t sum = 0;
         for (int i = e0; i < e1; ++i) sum += left(i);
@@ -497,10 +510,9 @@ template <typename E> int resident(cudaLaunchConfig_t cfg, int C) {
 Exp2Table make_table() {
     Exp2Table t;
     for (int k = 0; k < 129; ++k) {
-        const double e = exp2((k - 64) / 128.0), unit = 70368744177664.0;
-        t.fix[k] = (uint64_t)(e * unit + 0.5);
-        t.hi[k] = (float)e;
-        t.lo[k] = (float)((e - (double)t.hi[k]) * unit);
+        const uint64_t fix = (uint64_t)(exp2((k - 64) / 128.0) * 35184372088832.0 + 0.5);
+        t.hi[k] = (float)(fix >> 23) * 2.384185791015625e-07f;                        // 2^-22
+        t.lo[k] = (float)(fix & ((1 << 23) - 1));
     }
     return t;
 }
