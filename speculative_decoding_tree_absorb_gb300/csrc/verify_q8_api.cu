@@ -21,13 +21,14 @@ struct Q8Plan {
     size_t vis_off = 0, po_off = 0, pl_off = 0, sched_off = 0, ws_bytes = 0;
 };
 
-// Which kernel. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 4.0 us on one SM and
-// reads the cache again for every 64 rows; a cluster takes (256 rows, 128 keys) in 2.4 us on 4 SMs, but
-// its set-up, schedule and drain are longer: 45 us against 13. Measured, rows kernel / clusters, us:
-// 8 sequences of 8 k keys, 128 rows 54 / 84, 384 rows 103 / 115, 512 rows 129 / 117; 8 sequences of
-// 8 k keys and 4096 rows 876 / 567; one of 1000 keys and 4096 rows 40 / 60.
-bool rows_cheaper(int64_t pairs, int64_t unit_blocks) {
-    return 13.0 + 4.0 * (double)pairs / sm_count() < 45.0 + 2.4 * (double)unit_blocks / tc_q8_max_clusters();
+// Which kernel, by estimates in us. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 3.9
+// on one SM and 5.5 more for a tile's queries and output; a cluster takes (256 rows, 128 keys) in 2.25 on
+// 4 SMs and 10 more for a unit of rows, and its set-up, schedule and drain are longer. Measured, rows
+// kernel / clusters: 8 sequences of 8 k keys, 128 rows 51 / 83, 384 rows 99 / 114, 512 rows 125 / 116, 4096
+// rows 876 / 567; 43 of 2688 rows, 3 keys 129 / 206, 300 keys 217 / 273, 1000 keys 427 / 412; 2 of 4096 rows,
+// 2000 keys 80 / 85.
+bool rows_cheaper(int64_t tiles, int64_t units, int nblk) {
+    return 10.0 + tiles * (3.9 * nblk + 5.5) / sm_count() < 45.0 + units * (2.25 * nblk + 10.0) / tc_q8_max_clusters();
 }
 
 kdt_status check_args(const kdt_verify_q8_args *a) {
@@ -70,7 +71,7 @@ kdt_status make_plan(const kdt_verify_q8_args *a, Q8Plan *out) {
     const int units_seq = (rows_seq + tc_rows_per_unit() - 1) / tc_rows_per_unit();
     const int nblk = (a->max_kv_len + kQ8Keys - 1) / kQ8Keys;
     p.impl = a->impl != KDT_IMPL_AUTO ? a->impl
-             : rows_cheaper((int64_t)a->B * p.tiles_seq * nblk, (int64_t)a->B * units_seq * nblk) ? KDT_IMPL_Q8_ROWS
+             : rows_cheaper((int64_t)a->B * p.tiles_seq, (int64_t)a->B * units_seq, nblk) ? KDT_IMPL_Q8_ROWS
                                                                                                   : KDT_IMPL_TCGEN05;
     const bool tc = p.impl == KDT_IMPL_TCGEN05;
     int piece_rows;
