@@ -264,10 +264,25 @@ __device__ __forceinline__ uint32_t seen_by(const Q8Params &p, const uint32_t *w
     return see;
 }
 
+// Warms L2 with the queries of the item behind this one: they come from DRAM else, and their loads stand
+// between two items (43 sequences of 2688 rows over 3 keys: 131 -> 109 us).
+__device__ __forceinline__ void prefetch_next_q(const Q8Params &p, const Item &it) {
+    if (it.left <= it.nb || p.q_nope_stride > 2 * kDc || p.q_pe_stride > 2 * kDc) return;   // (rows far apart: left alone)
+    const bool wrap = it.rt + 1 == p.tiles_seq;
+    const int rt = wrap ? 0 : it.rt + 1, live = min(kRowsT, p.rows_seq - rt * kRowsT);
+    const int64_t row = (int64_t)(it.b + wrap) * p.rows_seq + rt * kRowsT;
+    const __nv_bfloat16 *q = p.q_nope + row * p.q_nope_stride;
+    for (int r = 0; r < live; r += 16) {
+        const int n = min(16, live - r) - 1;
+        prefetch_l2_bulk(q + r * p.q_nope_stride, (uint32_t)(n * p.q_nope_stride + kDc) * 2);
+    }
+    prefetch_l2_bulk(p.q_pe + row * p.q_pe_stride, (uint32_t)((live - 1) * p.q_pe_stride + kDr) * 2);
+}
+
 // One warp finds the words of a tree of at most 32 nodes (one word a node) from its parents, lane i
-// those of node i's ancestors, for the tile's nodes from i0 on. It saves the launch of the visibility
-// kernel (a short tree: 36 -> 31 us a call). A malformed entry ends its walks and is recorded, as there.
-__device__ __forceinline__ void walk_tree(const Q8Params &p, int b, int lane, int i0, uint32_t *words) {
+// node i's. It saves the launch of the visibility kernel (a short tree: 36 -> 31 us a call). A malformed
+// entry ends its walks and is recorded, as there.
+__device__ __forceinline__ uint32_t walk_tree(const Q8Params &p, int b, int lane) {
     const int par = lane < p.T ? __ldg(p.parent + (int64_t)b * p.T + lane) : -1;
     uint32_t m = 0u;
     int at = lane;
@@ -281,7 +296,7 @@ __device__ __forceinline__ void walk_tree(const Q8Params &p, int b, int lane, in
             at = on ? up : at;
         }
     }
-    if (lane >= i0) words[(lane - i0) * kVisWords] = m;
+    return m;
 }
 
 // x[r] of 32 lanes reduced over the lanes for all 32 r at once: lane r gets row r's result.
@@ -354,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         const int srow = (int)threadIdx.x - 32 * kSoft0;
         const uint32_t prow = smem + kOffR + key * 128;
         bool ok = true, vis_ready = false;
+        uint32_t tree = 0u;                                  // of sequence tree_b, in the first softmax warp
+        int tree_b = -1;
         // this thread's 32 scores of the block, scaled, plus off[row]; -inf where hidden
         auto scores = [&](const float *off, bool masked, uint32_t see, float (&x)[32]) {
             uint32_t raw[32];
@@ -380,25 +397,30 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         auto load_q = [&](const Item &q) {
             const int r0 = 8 * (warp - kSoft0), R0 = q.rt * kRowsT + r0, sub = lane & 7, kq = lane >> 3;
             const int64_t base = (int64_t)q.b * p.rows_seq + R0;
-#pragma unroll 4
-            for (int r = 0; r < 8; ++r) {
-                const bool live = R0 + r < p.rows_seq;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_nope + (base + r) * p.q_nope_stride);
-                const uint32_t dst = smem + kOffQ + (r0 + r) * 128;
+            // all loads first: their latency stands between two items
+            uint4 v[8][2], w[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = 32 * h + lane;             // 16-byte chunk of the row's 64
-                    const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    sts(dst + (c >> 3) * kQTile + (((c & 7) ^ ((r0 + r) & 7)) << 4), q8::reorder8(v));
-                }
+            for (int r = 0; r < 8; ++r) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_nope + (base + r) * p.q_nope_stride) + lane;
+                const bool live = R0 + r < p.rows_seq;
+                v[r][0] = live ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);      // 16-byte chunks of the row's 64
+                v[r][1] = live ? __ldg(src + 32) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[h] = R0 + 4 * h + kq < p.rows_seq
+                           ? __ldg(reinterpret_cast<const uint4 *>(p.q_pe + (base + 4 * h + kq) * p.q_pe_stride) + sub)
+                           : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    sts(smem + kOffQ + (r0 + r) * 128 + (4 * h + (lane >> 3)) * kQTile + (((lane & 7) ^ ((r0 + r) & 7)) << 4),
+                        q8::reorder8(v[r][h]));
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = 4 * h + kq;
-                const uint4 v = R0 + r < p.rows_seq
-                                    ? __ldg(reinterpret_cast<const uint4 *>(p.q_pe + (base + r) * p.q_pe_stride) + sub)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-                sts(smem + kOffQ + 8 * kQTile + (r0 + r) * 128 + ((sub ^ ((r0 + r) & 7)) << 4), v);
+                const int r = r0 + 4 * h + kq;
+                sts(smem + kOffQ + 8 * kQTile + r * 128 + ((sub ^ (r & 7)) << 4), w[h]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -426,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                     }
                     const int i0 = it.rt * kRowsT / p.H, w0 = max(key0 - it.P, 0) >> 5;
                     if (p.parent) {
-                        if (srow < 32) walk_tree(p, it.b, lane, i0, sh.vis);
+                        if (srow < 32) {
+                            if (it.b != tree_b) tree = walk_tree(p, it.b, lane);
+                            tree_b = it.b;
+                            if (lane >= i0) sh.vis[(lane - i0) * kVisWords] = tree;
+                        }
                     } else
                     for (int e = srow; e < kRowsT * kVisWords; e += 32 * kSoftWarps) {
                         const int i = i0 + e / kVisWords, wd = w0 + e % kVisWords;
@@ -763,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 for (int t = 0; t < 4; ++t) mma_ss(tmem + kColS, desc(rd + 2 * t), desc(qr + 2 * t), id_s, 1u);
                 mma_commit(&bar.sfull);
                 prefetch();
+                if (j == 0) prefetch_next_q(p, it);
                 if (!(ok = wait_for(bar, &bar.pfull, g & 1, p.err, -50))) break;
                 // the item before: its O^T has been read out
                 if (j == 0 && ii > 0 && !(ok = wait_for(bar, &bar.ofree, (ii - 1) & 1, p.err, -51))) break;
