@@ -530,10 +530,10 @@ typedef struct {
  * with float32 sums; scores, softmax statistics and the output's sums are float32, the
  * weights are rounded to bf16 for the second product, and the output once to out_dtype.
  * Exactly one of `parent` and `vis` is given; a row that sees no key gets out = 0 and
- * lse = -inf. A row that sees a NaN group or a non-finite k_pe gets NaN; a row from which
- * such a key is hidden is not affected by it, and rows of the cache at or beyond
- * prefix_len[b] + T are never read. prefix_len values are device data: the caller guarantees
- * 0 <= prefix_len[b] <= max_kv_len - T.
+ * lse = -inf. A row that sees a NaN group, or a k_pe that makes its score NaN or +inf, gets
+ * NaN (a score of -inf has weight 0); a row from which such a key is hidden is not affected
+ * by it, and rows of the cache at or beyond prefix_len[b] + T are never read. prefix_len
+ * values are device data: the caller guarantees 0 <= prefix_len[b] <= max_kv_len - T.
  * `workspace` must hold kdt_verify_attn_q8_workspace_size(a) bytes (256-byte aligned);
  * its contents need no initialisation. Calls that may run at the same time, captured ones
  * included, need workspaces of their own.

@@ -224,6 +224,25 @@ def test_captured_graph_two_streams_and_fresh_inputs(kdt, T, H, prefix):
 
 
 @pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+def test_infinite_rope_keys(kdt, impl):
+    """A key with an infinite rope value scores +inf or -inf by the sign of the row's query there: NaN, or
+    a key of weight 0."""
+    d = _inputs(84, 5, 4, [200])
+    d["kp"][0, 17, 3] = float("inf")
+    out, lse = _call(kdt, d, impl=impl)
+    up = (d["q"][0, ..., 512 + 3] > 0).cpu().numpy()
+    assert up.any() and (d["q"][0, ..., 512 + 3] < 0).any()
+    assert np.isnan(out[0][up]).all() and np.isnan(lse[0][up]).all()
+    # the others: as without the key
+    import torch
+    keep = torch.tensor([j for j in range(205) if j != 17], device="cuda")
+    e = dict(d, c8=d["c8"][:, keep].contiguous(), sc=d["sc"][:, keep].contiguous(), kp=d["kp"][:, keep].contiguous(),
+             prefix=[199])
+    without = _call(kdt, e, impl=impl)
+    _check(e, (np.where(up[..., None], without[0][0], out[0])[None], np.where(up, without[1][0], lse[0])[None]), 0.0)
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
 def test_far_sequences_pass_32_bits(kdt, impl):
     """Code offsets of the last sequence are beyond 2^31 (and its queries few)."""
     d = _inputs(81, 9, 4, [0, 3, 260], pad=2200000)
