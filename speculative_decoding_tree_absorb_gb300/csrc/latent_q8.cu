@@ -96,14 +96,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWriters) latent_write_kernel(con
     using R = Row<E>;
     constexpr int kLanes = KDT_Q8_GROUP / R::kPer;        // lanes that share a group
     const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)p.B * p.T, step = (int64_t)gridDim.x * kWarps;
+    const uint32_t rows = (uint32_t)p.B * p.T, step = gridDim.x * kWarps;      // (below 2^31: 32-bit divisions)
     const uint64_t freq = fr.f[lane];
-    for (int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); n < rows; n += step) {
-        const int b = (int)(n / p.T), i = (int)(n - (int64_t)b * p.T);
+    for (uint32_t n = blockIdx.x * kWarps + (threadIdx.x >> 5); n < rows; n += step) {
+        const int b = (int)(n / (uint32_t)p.T), i = (int)(n - (uint32_t)b * p.T);
         if (p.n_rows && i >= p.n_rows[b]) continue;
         R c;
-        c.template load<true>(static_cast<const E *>(p.c) + n * p.c_stride, lane);
-        const E *k = static_cast<const E *>(p.k) + n * p.k_stride;
+        c.template load<true>(static_cast<const E *>(p.c) + (int64_t)n * p.c_stride, lane);
+        const E *k = static_cast<const E *>(p.k) + (int64_t)n * p.k_stride;
         const E ka = k[lane], kb = k[lane + kHalf];
         const int32_t pos = p.pos ? p.pos[n] : 0;
         const int64_t row = (int64_t)p.prefix_len[b] + i;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWriters) latent_write_kernel(con
             for (int t = 0; t < 16; ++t) ss = fmaf(y[t], y[t], ss);
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float r = 1.f / sqrtf(ss * (1.f / kDc) + p.eps);
+            const float r = __frsqrt_rn(fmaf(ss, 1.f / kDc, p.eps));
             float g[16];
             gr.get(g);
 #pragma unroll
@@ -180,17 +180,17 @@ template <typename E>
 __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const ReadParams p) {
     constexpr int kPer = 16 / sizeof(E), kPieces = 16 / kPer;
     const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)p.B * p.R, step = (int64_t)gridDim.x * kWarps;
+    const uint32_t rows = (uint32_t)p.B * p.R, step = gridDim.x * kWarps;      // (below 2^31: 32-bit divisions)
     struct Next {
         uint32_t w[4];
         uint8_t s[kPieces];
         uint32_t k;
         bool live;
     };
-    auto fetch = [&](int64_t n, Next &x) {
+    auto fetch = [&](uint32_t n, Next &x) {
         x.live = false;
         if (n >= rows) return;
-        const int b = (int)(n / p.R), i = (int)(n - (int64_t)b * p.R);
+        const int b = (int)(n / (uint32_t)p.R), i = (int)(n - (uint32_t)b * p.R);
         if (p.n_rows && i >= p.n_rows[b]) return;
         x.live = true;
         const int64_t row = (int64_t)(p.start ? p.start[b] : 0) + i;
@@ -219,14 +219,14 @@ __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const ReadPara
         }
         if (p.k) x.k = __ldcs(reinterpret_cast<const uint32_t *>(p.k_pe + src * kDr) + lane);
     };
-    int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    uint32_t n = blockIdx.x * kWarps + (threadIdx.x >> 5);
     Next cur, nxt;
     fetch(n, cur);
     for (; n < rows; n += step) {
         fetch(n + step, nxt);
         if (cur.live) {
             if (p.c) {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<E *>(p.c) + n * kDc);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<E *>(p.c) + (int64_t)n * kDc);
 #pragma unroll
                 for (int q = 0; q < kPieces; ++q) {
                     const float s = q8::scale_value(cur.s[q]);
@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const ReadPara
             }
             if (p.k) {
                 if constexpr (sizeof(E) == 2)
-                    reinterpret_cast<uint32_t *>(p.k)[n * (kDr / 2) + lane] = cur.k;
+                    reinterpret_cast<uint32_t *>(p.k)[(int64_t)n * (kDr / 2) + lane] = cur.k;
                 else
-                    reinterpret_cast<float2 *>(p.k)[n * (kDr / 2) + lane] =
+                    reinterpret_cast<float2 *>(p.k)[(int64_t)n * (kDr / 2) + lane] =
                         make_float2(__uint_as_float(cur.k << 16), __uint_as_float(cur.k & 0xffff0000u));
             }
         }
