@@ -74,15 +74,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Codes (0, 2) and (1, 3) of a word as pairs of bf16 bit patterns times 2^-120. A pair has the
-// codes in the low bytes of its halves: 16 x moves exponent and mantissa to bits 4..10 and the
-// sign to bit 11, and 0xf0 times the sign bit moves it on to bit 15 (2048 + 0xf0 * 128 = 2^15).
-// That is two logic operations and two multiply-adds, on different pipes, against a byte
-// permute, a shift and two logic operations for a pair in order.
+// Codes (0, 2) and (1, 3) of a word as pairs of bf16 bit patterns times 2^-120. The byte permute
+// puts each code in the low byte of its half and copies of its sign in the high byte: 16 times
+// that has the sign in bit 15 and exponent and mantissa in bits 4..10, and the rest (more signs,
+// and what the lower half carries into the upper one's low bits) is masked away.
 __device__ __forceinline__ void spread(uint32_t w, uint32_t &even, uint32_t &odd) {
-    const uint32_t e = w & 0x00ff00ffu, o = __byte_perm(w, 0u, 0x4341);
-    even = e * 16u + (e & 0x00800080u) * 0xf0u;
-    odd = o * 16u + (o & 0x00800080u) * 0xf0u;
+    asm("prmt.b32 %0, %1, 0, 0xa280;" : "=r"(even) : "r"(w));
+    asm("prmt.b32 %0, %1, 0, 0xb391;" : "=r"(odd) : "r"(w));
+    even = (even * 16u) & 0x87f087f0u;
+    odd = (odd * 16u) & 0x87f087f0u;
+}
+
+// factor() of two scale bytes as a pair, when both are below 128 (no NaN, nothing for factor_high()).
+__device__ __forceinline__ uint32_t low_factors(uint32_t b0, uint32_t b1) {
+    return (b0 | b1 << 16) * 128u + 120u * 128u * 0x10001u;
 }
 
 // Eight codes to eight bf16 values, each four in the order (0, 2, 1, 3); f holds the factor twice.

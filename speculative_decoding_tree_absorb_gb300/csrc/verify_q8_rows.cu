@@ -663,11 +663,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             // before the wait: a lane turns the scale bytes of its key into factors, and gets those of
             // its eight keys (the first tile's in the low half)
             const uint32_t b0 = sc & 255u, b1 = (sc >> 8) & 255u, b2 = (sc >> 16) & 255u, b3 = sc >> 24;
-            const bool nan = b0 == (uint32_t)q8::kNaN || b1 == (uint32_t)q8::kNaN || b2 == (uint32_t)q8::kNaN ||
-                             b3 == (uint32_t)q8::kNaN;
+            const bool plain = !__any_sync(0xffffffffu, sc & 0x80808080u);         // mostly: no scale above 1, no NaN
+            const bool nan = !plain && (b0 == (uint32_t)q8::kNaN || b1 == (uint32_t)q8::kNaN || b2 == (uint32_t)q8::kNaN ||
+                                        b3 == (uint32_t)q8::kNaN);
             uint32_t f[8];
             {
-                const uint32_t fa = q8::factor(b0) | (q8::factor(b1) << 16), fb = q8::factor(b2) | (q8::factor(b3) << 16);
+                uint32_t fa, fb;
+                if (plain) {
+                    fa = q8::low_factors(b0, b1);
+                    fb = q8::low_factors(b2, b3);
+                } else {
+                    fa = q8::factor(b0) | (q8::factor(b1) << 16);
+                    fb = q8::factor(b2) | (q8::factor(b3) << 16);
+                }
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
                     f[t] = __byte_perm(__shfl_sync(0xffffffffu, fa, 4 * t + kq), __shfl_sync(0xffffffffu, fb, 4 * t + kq), pick);
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 for (int k = 0; k < 4; ++k) sts((k >> 1 ? krow1 : krow0) + 512 * (t0 + (k >> 1)) + (k & 1) * kKTile, v[k]);
             }
             // some scale above 2^7: a second product
-            if (__any_sync(0xffffffffu, max(max(b0, b1), max(b2, b3)) > q8::kHighByte)) {
+            if (!plain && __any_sync(0xffffffffu, max(max(b0, b1), max(b2, b3)) > q8::kHighByte)) {
                 const uint32_t ha = q8::factor_high(b0) | (q8::factor_high(b1) << 16);
                 const uint32_t hb = q8::factor_high(b2) | (q8::factor_high(b3) << 16);
 #pragma unroll 1

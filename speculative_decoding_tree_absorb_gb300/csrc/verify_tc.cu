@@ -1645,7 +1645,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
             // the piece's scale word; S: one half a tile, O: the half of its tile for all sets
             const uint32_t word = (s_role ? q & 1 : q >> 1) ? sc.y : sc.x;
             const uint32_t lo = !s_role && (q & 1) ? word >> 16 : word & 0xffffu, hi = s_role ? word >> 16 : lo;
-            const uint32_t fa = factor_pair(lo, nan_bits), fb = factor_pair(hi, nan_bits);
+            const bool plain = !__any_sync(0xffffffffu, word & 0x80808080u);       // mostly: no scale above 1, no NaN
+            uint32_t fa, fb;
+            if (plain) {
+                fa = q8::low_factors(lo & 255u, lo >> 8);
+                fb = q8::low_factors(hi & 255u, hi >> 8);
+            } else {
+                fa = factor_pair(lo, nan_bits);
+                fb = factor_pair(hi, nan_bits);
+            }
             const uint32_t src = kq + (s_role ? 16 * (q >> 1) : 0), src_step = s_role ? 0 : 16;
             uint32_t f[8];
 #pragma unroll
@@ -1660,7 +1668,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                 const uint4 v = q8::widen8(c[k], f[k]);
                 st_shared_v4(((k & 1) ? d1 : d0) + (k >> 2) * dst_step + (k & 3) * 512, v.x, v.y, v.z, v.w);
             }
-            if (__any_sync(0xffffffffu, any_high(word))) {     // some scale above 2^7: a second product
+            if (!plain && __any_sync(0xffffffffu, any_high(word))) {     // some scale above 2^7: a second product
                 const uint32_t ha = factor_high_pair(lo), hb = factor_high_pair(hi);
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
