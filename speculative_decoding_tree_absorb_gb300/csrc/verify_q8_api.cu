@@ -21,14 +21,14 @@ struct Q8Plan {
     size_t vis_off = 0, po_off = 0, pl_off = 0, sched_off = 0, ws_bytes = 0;
 };
 
-// Which kernel, by estimates in us. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 3.9
-// on one SM and 4.5 more for a tile's queries and output; a cluster takes (256 rows, 128 keys) in 2.25 on
+// Which kernel, by estimates in us. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 3.7
+// on one SM and 4.5 more for a tile's queries and output; a cluster takes (256 rows, 128 keys) in 2.05 on
 // 4 SMs and 10 more for a unit of rows, and its set-up, schedule and drain are longer. Measured, rows
-// kernel / clusters: 8 sequences of 8 k keys, 128 rows 51 / 84, 384 rows 97 / 115, 512 rows 123 / 119, 4096
-// rows 876 / 567; 43 of 2688 rows, 3 keys 107 / 207, 300 keys 203 / 272, 1000 keys 417 / 413; 2 of 4096 rows,
-// 2000 keys 81 / 85.
+// kernel / clusters: 8 sequences of 8 k keys, 128 rows 50 / 83, 384 rows 95 / 112, 512 rows 119 / 116, 4096
+// rows 791 / 530; 43 of 2688 rows, 3 keys 105 / 206, 300 keys 198 / 274, 1000 keys 404 / 403; 2 of 4096 rows,
+// 2000 keys 79 / 84.
 bool rows_cheaper(int64_t tiles, int64_t units, int nblk) {
-    return 10.0 + tiles * (3.9 * nblk + 4.5) / sm_count() < 45.0 + units * (2.25 * nblk + 10.0) / tc_q8_max_clusters();
+    return 10.0 + tiles * (3.7 * nblk + 4.5) / sm_count() < 45.0 + units * (2.05 * nblk + 10.0) / tc_q8_max_clusters();
 }
 
 kdt_status check_args(const kdt_verify_q8_args *a) {
