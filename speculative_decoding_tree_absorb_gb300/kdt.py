@@ -232,8 +232,9 @@ def _row_stride(q):
     if q.is_contiguous():
         return 0
     s, n = q.stride(), q.shape
-    if s[3] != 1 or s[2] * n[2] != s[1] or s[1] * n[1] != s[0]:
-        raise ValueError("query views must have a contiguous last dim and equally spaced (b,i,h) rows")
+    # (rows of an expanded view have stride 0, which the library takes for "contiguous")
+    if s[3] != 1 or s[2] < n[3] or s[2] * n[2] != s[1] or s[1] * n[1] != s[0]:
+        raise ValueError("query views must have a contiguous last dim and equally spaced (b,i,h) rows that do not overlap")
     return s[2]
 
 
@@ -428,11 +429,14 @@ def tree_build(cand_tok, cand_lp, N, root_tok=None, stream=None):
 
 def _row_stride3(t, name):
     """Element stride between the (b,i) rows of a [B,T,d] view with a contiguous last dim and
-    equally spaced rows (e.g. a slice of a combined [B,T,576] buffer)."""
+    equally spaced rows (e.g. a slice of a combined [B,T,576] buffer). Rows that overlap are
+    refused: an expanded view's stride of 0 means "contiguous" to the library."""
     s, n = t.stride(), t.shape
-    if s[2] != 1 or (n[0] > 1 and n[1] > 0 and s[0] != s[1] * n[1]):
-        raise ValueError(f"{name} must be a [B,T,d] view with a contiguous last dim and equally spaced (b,i) rows")
-    return s[1] if n[1] > 1 else (s[0] if n[0] > 1 else n[2])
+    stride = s[1] if n[1] > 1 else (s[0] if n[0] > 1 else n[2])
+    if s[2] != 1 or stride < n[2] or (n[0] > 1 and n[1] > 1 and s[0] != s[1] * n[1]):
+        raise ValueError(f"{name} must be a [B,T,d] view with a contiguous last dim and equally spaced (b,i) rows "
+                         "that do not overlap")
+    return stride
 
 
 def _check_q8_cache(c_q8, c_scale, k_pe):

@@ -205,3 +205,40 @@ def test_tree_sample_refusals(kdt):
         args.update(kw)
         with pytest.raises(ValueError):
             kdt.tree_sample(**args)
+
+
+def test_expanded_views_are_refused(kdt):
+    """One row shown as many has a row stride of 0 (rows that overlap: one below their width), which the
+    library would read as "contiguous": from memory that holds a single row."""
+    import torch
+    bf = torch.bfloat16
+    c8, sc = torch.zeros(2, 8, 512, dtype=torch.uint8), torch.zeros(2, 8, 16, dtype=torch.uint8)
+    kp, pre = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, dtype=torch.int32)
+    c, k = torch.zeros(2, 3, 512), torch.zeros(2, 3, 64)
+    one = torch.zeros(1, 1, 576)
+    for kw in (dict(c=one[..., :512].expand(2, 3, 512)), dict(k=one[..., 512:].expand(2, 3, 64)),
+               dict(c=torch.zeros(5 * 256 + 512).as_strided((2, 3, 512), (768, 256, 1))),
+               dict(k=torch.zeros(400).as_strided((2, 3, 64), (96, 32, 1)))):
+        with pytest.raises(ValueError):
+            kdt.latent_write_q8(**{**dict(c=c, k=k, c_q8=c8, c_scale=sc, k_pe=kp, prefix_len=pre), **kw})
+    with pytest.raises(ValueError):                                  # one sequence: only the row stride tells
+        kdt.latent_write_q8(one[..., :512].expand(1, 3, 512), k[:1], c8[:1], sc[:1], kp[:1], pre[:1])
+    par, u = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    row = torch.zeros(1, 1, 10)
+    for lg, b in ((row.expand(2, 3, 10), 2), (row.expand(1, 3, 10), 1), (row.expand(2, 1, 10), 2)):
+        t = lg.shape[1]
+        with pytest.raises(ValueError):
+            kdt.tree_sample(par[:b, :t].contiguous(), par[:b, :t].contiguous(), lg, u[:b, :t].contiguous(), u[:b, 0].contiguous())
+    q, par = torch.zeros(2, 3, 4, 576, dtype=bf), torch.zeros(2, 3, dtype=torch.int32)
+    q1 = q[:1, :1, :1]
+    for kw in (dict(q_nope=q1[..., :512].expand(2, 3, 4, 512)), dict(q_pe=q1[..., 512:].expand(2, 3, 4, 64))):
+        args = {**dict(q_nope=q[..., :512], q_pe=q[..., 512:]), **kw}
+        with pytest.raises(ValueError):
+            kdt.verify_attn_q8(args["q_nope"], args["q_pe"], c8, sc, kp, pre, parent=par)
+        with pytest.raises(ValueError):
+            kdt.make_args(args["q_nope"], args["q_pe"], torch.zeros(2, 8, 512, dtype=bf), kp, pre, parent=par)
+    # single rows and slices of a combined buffer are taken as they lie
+    from speculative_decoding_tree_absorb_gb300.kdt import _row_stride, _row_stride3
+    assert _row_stride3(one[..., :512], "c") == 512 and _row_stride3(torch.zeros(2, 3, 576)[..., :512], "c") == 576
+    assert _row_stride3(torch.zeros(2, 3, 576)[:, 1:2, :512], "c") == 3 * 576
+    assert _row_stride(q[..., :512]) == 576 and _row_stride(q1[..., :512]) == 0
