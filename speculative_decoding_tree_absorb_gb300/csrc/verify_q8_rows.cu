@@ -39,6 +39,7 @@
 //    3 sequences of 13 nodes and 16 heads over 5-32 k keys 70 us.
 //  * Every wait is bounded; one that runs out records a status in the error word and the
 //    kernel drains its MMAs, frees tensor memory and returns.
+#include <float.h>
 #include <math.h>
 
 #include "kdt_internal.cuh"
@@ -66,6 +67,9 @@ constexpr int kOffQ = kOffR + kKTile;               // nine Q tiles
 constexpr int kSmem = kOffQ + 9 * kQTile + 1024;    // + alignment slack
 constexpr uint32_t kColS = 256;                     // S^T columns; O^T tile q at 64 q
 constexpr float kRaise = 20.f;                      // log2 units
+// Minus the reference of a row that has seen no score yet but -inf: large enough that any other score
+// votes for a rise (but one of -FLT_MAX itself), and finite, so that -inf stays -inf, of weight 0.
+constexpr float kNoReference = FLT_MAX;
 constexpr uint64_t kWait = 200000000ull;            // ns
 constexpr int kAhead = 3;                           // blocks the L2 prefetch runs ahead
 
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
             float l = 0.f;                                   // of row `lane` of the 32, over this warp's keys
             if (srow < kRowsT) {
                 sh.m[srow] = -INFINITY;
-                sh.nm[srow] = INFINITY;
+                sh.nm[srow] = kNoReference;
             }
             barrier_or<1, 256>(false);
             bool fail = false;
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 }
                 ok = ok && warp_wait(bar, &bar.sfull, g & 1, p.err, -41);
                 float x[32];                                 // score - reference
-                // minus the reference, +inf for a row without one yet; an item's first block goes straight
+                // minus the reference, kNoReference for a row without one; an item's first block goes straight
                 // to the maxima
                 const float *off = j > 0 ? sh.nm : sh.zero;
                 bool raised = false;

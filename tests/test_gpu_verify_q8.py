@@ -290,3 +290,51 @@ def test_malformed_parents_are_recorded(kdt, T, impl):
         assert int(err.item()) == (T + 4 + 1 if par is not good else 0)
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def _scored_minus_inf(d, keys):
+    """Infinite rope values at these cache rows of every sequence, against queries that are all negative
+    there: each of those keys scores -inf for each row."""
+    d["q"][..., 512 + 3] = -(d["q"][..., 512 + 3].abs() + 0.5)
+    d["kp"][:, list(keys), 3] = float("inf")
+
+
+def _without(d, keys):
+    """The same problem without these prefix rows."""
+    import torch
+    keep = torch.tensor([j for j in range(d["L"]) if j not in set(keys)], device="cuda")
+    return dict(d, c8=d["c8"][:, keep].contiguous(), sc=d["sc"][:, keep].contiguous(), kp=d["kp"][:, keep].contiguous(),
+                prefix=[p - len(keys) for p in d["prefix"]])
+
+
+# prefix, rows that score -inf: all of the first block, of the first two, of the last whole block, all but one row
+MINUS_INF = [(383, range(0, 128)), (383, range(0, 256)), (384, range(0, 129)), (700, range(130, 700)), (640, range(1, 640))]
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 5])
+@pytest.mark.parametrize("T,H", [(1, 4), (9, 8), (40, 8)])
+@pytest.mark.parametrize("prefix,keys", MINUS_INF)
+def test_blocks_that_score_minus_inf_have_weight_0_in_the_rows_kernel(kdt, prefix, keys, T, H, splits):
+    """Whole 128-key blocks whose every score is -inf, an item's first block among them: as without these keys,
+    however the work is cut."""
+    d = _inputs(91, T, H, [prefix])
+    _scored_minus_inf(d, keys)
+    _check(_without(d, keys), _call(kdt, d, impl="q8_rows", num_splits=splits), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_nothing_but_minus_inf_in_the_rows_kernel(kdt, splits):
+    """A token whose own key scores -inf behind a block of finite ones, and one whose every key does: what is
+    left of the keys, and a row of zeros with lse -inf."""
+    no = np.zeros((1, 1, 1), dtype=bool)
+    d = _inputs(92, 1, 4, [128])
+    _scored_minus_inf(d, [128])
+    _check(d, _call(kdt, d, impl="q8_rows", num_splits=splits), 2.0 ** -24, see=no)
+    for prefix in (0, 128, 383):
+        d = _inputs(93, 1, 4, [prefix])
+        _scored_minus_inf(d, range(prefix + 1))
+        _check(dict(d, prefix=[0]), _call(kdt, d, impl="q8_rows", num_splits=splits), 0.0, see=no)
+    # a NaN among them is not lost
+    d["kp"][0, 200, 5] = float("nan")
+    out, lse = _call(kdt, d, impl="q8_rows", num_splits=splits)
+    assert np.isnan(out).all() and np.isnan(lse).all()
