@@ -1168,9 +1168,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                     if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxSlot, g);
                     unsigned char *slot_base = smem + kOffPStage + ss * kPSlotBytes;
                     unsigned char *stage_row = slot_base + half * (kPBytes / 2) + row * 128;
-                    // an all-visible half has finite scores, so m_run is finite here
+                    // an all-visible half has finite scores, so m_run is finite here -- but for the 8-bit
+                    // cache's infinite rope keys: where m_run is -inf all its scores are -inf (p = 0) or NaN
                     l_run += masked ? stage_p_row<true, kQ8>(x, p.scale_log2, m_run, stage_row, row)
-                                    : stage_p_row<false, kQ8>(x, p.scale_log2, m_run, stage_row, row);
+                                    : stage_p_row<false, kQ8>(x, p.scale_log2, kQ8 && m_run == -INFINITY ? 0.f : m_run,
+                                                                stage_row, row);
                     // the rescale factors follow the second half of P, which carries them
                     if (half == 1) reinterpret_cast<float *>(slot_base + kPBytes)[row] = alpha;
                     fence_proxy_async_smem();                  // staging visible to the copy engine

@@ -338,3 +338,28 @@ def test_nothing_but_minus_inf_in_the_rows_kernel(kdt, splits):
     d["kp"][0, 200, 5] = float("nan")
     out, lse = _call(kdt, d, impl="q8_rows", num_splits=splits)
     assert np.isnan(out).all() and np.isnan(lse).all()
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 5])
+@pytest.mark.parametrize("T,H", [(1, 4), (9, 8), (40, 8)])
+@pytest.mark.parametrize("prefix,keys", MINUS_INF)
+def test_blocks_that_score_minus_inf_have_weight_0_in_the_cluster_kernel(kdt, prefix, keys, T, H, splits):
+    """The same there, whose blocks end at the last tree row: halves of 64 keys without a mask, all -inf."""
+    d = _inputs(91, T, H, [prefix])
+    _scored_minus_inf(d, keys)
+    _check(_without(d, keys), _call(kdt, d, impl="tcgen05", num_splits=splits), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_nothing_but_minus_inf_in_the_cluster_kernel(kdt, splits):
+    no = np.zeros((1, 1, 1), dtype=bool)
+    d = _inputs(92, 1, 4, [128])
+    _scored_minus_inf(d, [128])
+    _check(d, _call(kdt, d, impl="tcgen05", num_splits=splits), 2.0 ** -24, see=no)
+    for prefix in (0, 128, 383):
+        d = _inputs(93, 1, 4, [prefix])
+        _scored_minus_inf(d, range(prefix + 1))
+        _check(dict(d, prefix=[0]), _call(kdt, d, impl="tcgen05", num_splits=splits), 0.0, see=no)
+    d["kp"][0, 200, 5] = float("nan")
+    out, lse = _call(kdt, d, impl="tcgen05", num_splits=splits)
+    assert np.isnan(out).all() and np.isnan(lse).all()
