@@ -316,6 +316,15 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
                  : "memory");
 }
 
+// Store a word to a shared::cluster address and complete its 4 bytes on the mbarrier at `bar` of the same
+// CTA, without waiting for either: the completion is a release at cluster scope (an arrival with that
+// scope first waits for all of the thread's memory operations).
+__device__ __forceinline__ void st_async_u32(uint32_t addr, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+                 "r"(bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }

@@ -221,6 +221,7 @@ struct Barriers {
     // 8-bit cache
     uint64_t rawfull[kRaw];        // a raw piece landed (transaction bytes)
     uint64_t rawempty[kRaw];       // the widening warps have read it
+    uint32_t told[kWidenWarps];    // leader: what the other CTA's widening warps store to say so (never read)
     uint32_t need[2][kNP];         // leader: per-CTA "some row of O needs a rescale" per P slot
     uint32_t cmd;                  // each O-CTA: correction command
     int kseen[2];                  // S leader: latest latent chunk use each MMA issuer saw land
@@ -474,6 +475,13 @@ __device__ __forceinline__ bool wait_cluster_or_abort(Barriers &bar, uint64_t *b
     if (mbar_wait_cluster(b, parity, bar.wait_ns)) return true;
     set_abort(bar, err, code);
     return false;
+}
+
+// A latent tile of the pair: TMA brings it, or (8-bit cache) both CTAs' widening warps store it, and
+// the other CTA's stores need cluster scope before an MMA issued here reads them.
+template <bool kQ8>
+__device__ __forceinline__ bool wait_tile_or_abort(Barriers &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+    return kQ8 ? wait_cluster_or_abort(bar, b, parity, err, code) : wait_or_abort(bar, b, parity, err, code);
 }
 
 // Warp-uniform waits: every lane polls, and the warp proceeds only if all lanes saw
@@ -782,7 +790,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
         }
     }
     if (threadIdx.x == 0) {
-        constexpr int kFills = kQ8 ? 2 * kWidenWarps : 1;     // arrivals that fill a latent slot
+        // arrivals that fill a latent slot (8-bit cache: the leader's widening warps, and 4 bytes from each of the other CTA's)
+        constexpr int kFills = kQ8 ? kWidenWarps : 1;
         for (int i = 0; i < kNK; ++i) { mbar_init(&bar.kfull[i], kFills); mbar_init(&bar.kempty[i], 1); }
         for (int i = 0; i < kRopeSlots; ++i) { mbar_init(&bar.rfull[i], 1); mbar_init(&bar.rempty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar.sfull[i], 1); mbar_init(&bar.sempty[i], 16); }
@@ -971,7 +980,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                                 }
                                 if (!ok) break;
                             }
-                            if (!(ok = wait_or_abort(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5))) break;
+                            if (!(ok = wait_tile_or_abort<kQ8>(bar, &bar.kfull[slot], (uint32_t)(u / kNK) & 1, p.err, -5))) break;
                             *seen_mine = u;
                             tc_fence_after();
                             KDT_TC_TRACE(kEvKFull, u);
@@ -1317,7 +1326,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                         const uint64_t adesc0 = sdesc_sw128(smem_u32(pbase + ps * kPSlotBytes), 16, 1024);
                         const uint32_t acc0 = j > 0 ? 1u : 0u;
                         for (int h = 0; h < kVChunks; ++h) {
-                            if (!(ok = wait_or_abort(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10))) break;
+                            if (!(ok = wait_tile_or_abort<kQ8>(bar, &bar.vfull[vr.slot], vr.phase, p.err, -10))) break;
                             tc_fence_after();
                             KDT_TC_TRACE(kEvVFull, vr.n);
                             const uint64_t bdesc0 = sdesc_sw128(smem_u32(vbase + vr.slot * kVSlotBytes), kVSub, 1024);
@@ -1684,7 +1693,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_cta(&full[slot], lead_rank);
+            // Chunk done, each lane's stores fenced for the MMAs. The leader's own warps arrive; the other CTA's
+            // complete four bytes each, which publishes their stores at cluster scope and holds nothing up
+            // (tree step 538 us; an arrival with a release at cluster scope 711, one by a thread that
+            // collects the CTA's warps 582; at CTA scope, too little for another CTA's stores, 531).
+            if (lane == 0) {
+                if (!leader) st_async_u32(map_to_rank(&bar.told[warp - 12], lead_rank), 1u, map_to_rank(&full[slot], lead_rank));
+                else if (warp == 12) mbar_arrive_expect_tx(&full[slot], 4 * kWidenWarps);
+                else mbar_arrive(&full[slot]);
+            }
             if (++slot == nslots) {
                 slot = 0;
                 phase ^= 1;

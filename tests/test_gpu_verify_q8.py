@@ -363,3 +363,24 @@ def test_nothing_but_minus_inf_in_the_cluster_kernel(kdt, splits):
     d["kp"][0, 200, 5] = float("nan")
     out, lse = _call(kdt, d, impl="tcgen05", num_splits=splits)
     assert np.isnan(out).all() and np.isnan(lse).all()
+
+
+@pytest.mark.parametrize("T,H,prefix", [(64, 64, [900, 2100, 1500, 77]), (9, 128, [4000, 12])])
+def test_cluster_kernel_repeats_its_bits(kdt, T, H, prefix):
+    """Both CTAs of a pair widen the tiles that one CTA's MMAs read: in every one of many runs, alone and with
+    other work on the device, the result is the same bit for bit."""
+    import torch
+    d = _inputs(95, T, H, prefix)
+    _check(d, _call(kdt, d, impl="tcgen05"), 2.0 ** -24)
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    par = torch.from_numpy(d["parent"]).cuda()
+    args = (d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre)
+    out, lse = kdt.verify_attn_q8(*args, parent=par, max_kv_len=max(prefix) + T, impl="tcgen05")
+    side, junk = torch.cuda.Stream(), torch.empty(1 << 26, device="cuda")
+    for k in range(60):
+        if k % 2:
+            with torch.cuda.stream(side):
+                junk.add_(1.0)
+        o, l = kdt.verify_attn_q8(*args, parent=par, max_kv_len=max(prefix) + T, impl="tcgen05")
+        assert torch.equal(o, out) and torch.equal(l, lse), k
+    torch.cuda.synchronize()
