@@ -35,8 +35,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Merge the S partial states of one row (partial s at part_o[(s*stride + k)*512],
-// part_lse[s*stride + k]) into out_row / lse_out. One warp.
-__device__ __forceinline__ void merge_row(const float *__restrict__ part_o, const float *__restrict__ part_lse, int S,
+// part_lse[s*stride + k]) into out_row / lse_out. One warp. (The partials are no read-only data: the
+// kernel that writes them may overlap the merge.)
+__device__ __forceinline__ void merge_row(const float *part_o, const float *part_lse, int S,
                                           int64_t stride, int64_t k, float *__restrict__ out_row, float *lse_out) {
     const int lane = threadIdx.x & 31;
     const float ls = lane < S ? part_lse[(int64_t)lane * stride + k] : -INFINITY;
@@ -52,7 +53,7 @@ __device__ __forceinline__ void merge_row(const float *__restrict__ part_o, cons
         const float4 *src = reinterpret_cast<const float4 *>(part_o + ((int64_t)s * stride + k) * kDc);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 v = __ldg(src + lane + 32 * c);
+            const float4 v = __ldcg(src + lane + 32 * c);
             acc[c].x = fmaf(ws, v.x, acc[c].x);
             acc[c].y = fmaf(ws, v.y, acc[c].y);
             acc[c].z = fmaf(ws, v.z, acc[c].z);
@@ -67,8 +68,8 @@ __device__ __forceinline__ void merge_row(const float *__restrict__ part_o, cons
     if (lane == 0 && lse_out) *lse_out = wsum > 0.f ? M + logf(wsum) : -INFINITY;
 }
 
-__global__ void __launch_bounds__(kWarpsPerCta * 32) merge_splits_kernel(const float *__restrict__ part_o,
-                                                                         const float *__restrict__ part_lse,
+__global__ void __launch_bounds__(kWarpsPerCta * 32) merge_splits_kernel(const float *part_o,
+                                                                         const float *part_lse,
                                                                          int S, int64_t rows,
                                                                          float *__restrict__ out,
                                                                          float *__restrict__ lse) {

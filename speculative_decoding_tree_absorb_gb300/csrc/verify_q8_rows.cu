@@ -457,10 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                             tree_b = it.b;
                             if (lane >= i0) sh.vis[(lane - i0) * kVisWords] = tree;
                         }
-                    } else
+                    } else                               // (from L2: written while this kernel ran)
                     for (int e = srow; e < kRowsT * kVisWords; e += 32 * kSoftWarps) {
                         const int i = i0 + e / kVisWords, wd = w0 + e % kVisWords;
-                        sh.vis[e] = i < p.T && wd < p.W ? __ldg(p.vis + ((int64_t)it.b * p.T + i) * p.W + wd) : 0u;
+                        sh.vis[e] = i < p.T && wd < p.W ? __ldcg(p.vis + ((int64_t)it.b * p.T + i) * p.W + wd) : 0u;
                     }
                     barrier_or<1, 256>(false);
                     see = seen_by(p, sh.vis, i0, w0, key0 + key - it.P, it.rt * kRowsT + 32 * half);

@@ -596,7 +596,8 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // Visibility of keys [key0, key0 + 64) for one query row as a 64-bit mask (bit c: key
 // key0 + c): keys before 0 are padding (hidden), prefix keys [0, P) are visible, and tree
 // key P + t is visible when bit t of the row's packed ancestor bits is set. The tree part
-// of a window spans at most three 32-bit words.
+// of a window spans at most three 32-bit words. Read from L2: the kernel that writes them may
+// overlap this one, so they are no read-only data.
 __device__ __forceinline__ uint64_t vis_mask64(const uint32_t *visrow, int W, int key0, int P) {
     uint64_t m = 0;
     const int p_lo = max(key0, 0) - key0, p_hi = min(key0 + 64, P) - key0;   // prefix keys, as c
@@ -608,9 +609,9 @@ __device__ __forceinline__ uint64_t vis_mask64(const uint32_t *visrow, int W, in
     if (c_lo < 64) {
         const int ta = key0 + c_lo - P;                                        // its tree index (>= 0)
         const int wi = ta >> 5, sh = ta & 31;
-        const uint64_t w0 = wi < W ? __ldg(visrow + wi) : 0u;
-        const uint64_t w1 = wi + 1 < W ? __ldg(visrow + wi + 1) : 0u;
-        const uint64_t w2 = wi + 2 < W ? __ldg(visrow + wi + 2) : 0u;
+        const uint64_t w0 = wi < W ? __ldcg(visrow + wi) : 0u;
+        const uint64_t w1 = wi + 1 < W ? __ldcg(visrow + wi + 1) : 0u;
+        const uint64_t w2 = wi + 2 < W ? __ldcg(visrow + wi + 2) : 0u;
         const uint64_t bits = ((w0 | (w1 << 32)) >> sh) | (sh ? (w2 << (64 - sh)) : 0ull);   // tree bits ta..ta+63
         m |= bits << c_lo;
     }
@@ -1822,7 +1823,7 @@ __global__ void __launch_bounds__(256) merge_pieces_kernel(const TcParams p, int
                 reinterpret_cast<const float4 *>(p.part_o + ((int64_t)s_slot[base + k] * (2 * kRows) + r) * kDc);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float4 v = __ldg(src + lane + 32 * q);
+                const float4 v = __ldcg(src + lane + 32 * q);      // (written while this kernel waited)
                 acc[q] = make_float4(fmaf(wk, v.x, acc[q].x), fmaf(wk, v.y, acc[q].y), fmaf(wk, v.z, acc[q].z),
                                      fmaf(wk, v.w, acc[q].w));
             }

@@ -384,3 +384,24 @@ def test_cluster_kernel_repeats_its_bits(kdt, T, H, prefix):
         o, l = kdt.verify_attn_q8(*args, parent=par, max_kv_len=max(prefix) + T, impl="tcgen05")
         assert torch.equal(o, out) and torch.equal(l, lse), k
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+@pytest.mark.parametrize("T,H", [(64, 8), (150, 2)])
+def test_each_call_sees_its_own_tree(kdt, impl, T, H):
+    """Calls in a row on one workspace with two trees in turn: the attention starts while the visibility
+    kernel of its call still writes the words over those of the call before."""
+    import torch
+    d = _inputs(96, T, H, [40, 3, 300])
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    chain = np.tile(np.arange(T, dtype=np.int32) - 1, (3, 1))
+    par = [torch.from_numpy(x).cuda() for x in (d["parent"], chain)]
+    ws = torch.empty(kdt.verify_attn_q8_workspace_size(3, T, H, 300 + T, impl=impl), dtype=torch.uint8, device="cuda")
+    args = (d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre)
+    outs = [kdt.verify_attn_q8(*args, parent=par[k % 2], max_kv_len=300 + T, impl=impl, workspace=ws, scale=SCALE)
+            for k in range(30)]
+    torch.cuda.synchronize()
+    for k, tree in enumerate((d["parent"], chain)):
+        _check(dict(d, parent=tree), [x.double().cpu().numpy() for x in outs[k]], 2.0 ** -24)
+    for k in range(2, 30):
+        assert torch.equal(outs[k][0], outs[k % 2][0]) and torch.equal(outs[k][1], outs[k % 2][1])
