@@ -3,6 +3,8 @@
 Every computation runs in the library's CUDA kernels; this module passes device
 pointers (``tensor.data_ptr()``) and the current CUDA stream, and allocates
 output and workspace tensors with torch when the caller does not pass them.
+Functions that take ``stream`` run on that torch stream instead, which must have
+waited for the current one; what they allocate is recorded on it.
 There is no CPU fallback: if libkdt.so is missing, importing the library raises.
 """
 from __future__ import annotations
@@ -190,6 +192,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _kept(t, stream):
+    """A new tensor that a call uses on ``stream`` (None: the current one): its memory belongs to the current
+    stream, which must not hand it out again while another one still uses it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    import torch
+    return _kept(torch.empty(shape, dtype=dtype, device=device), stream)
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -253,7 +268,7 @@ def build_visibility(parent, err=None, stream=None):
     """parent int32 [B,T] (cuda) -> packed bits uint32-as-int32 tensor [B,T,ceil(T/32)]."""
     import torch
     B, T = parent.shape
-    vis = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=parent.device)
+    vis = _empty((B, T, (T + 31) // 32), torch.int32, parent.device, stream)
     _check(lib().kdt_build_visibility(_ptr(parent), B, T, _ptr(vis), _ptr(err), _stream_ptr(stream)),
            "kdt_build_visibility")
     return vis
@@ -271,14 +286,14 @@ def verify_attn(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=None, 
     B, T, H = q_nope.shape[:3]
     dev = q_nope.device
     if out is None:
-        out = torch.empty((B, T, H, q_nope.shape[3]), dtype=torch.float32, device=dev)
+        out = _empty((B, T, H, q_nope.shape[3]), torch.float32, dev, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = _empty((B, T, H), torch.float32, dev, stream)
     a = make_args(q_nope, q_pe, c_kv, k_pe, prefix_len, parent=parent, vis=vis, max_kv_len=max_kv_len,
                   scale=scale, out=out, lse=lse, err=err, impl=impl, num_splits=num_splits)
     need = workspace_size(a)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().kdt_verify_attn(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream_ptr(stream)),
            "kdt_verify_attn")
@@ -309,7 +324,7 @@ def verify_attn_host(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=N
                   scale=scale, out=out, lse=lse, err=err, impl=impl, num_splits=num_splits)
     need = host_buffer_size(a, n_chunks)
     if dev_buf is None and need > 0:
-        dev_buf = torch.empty(need, dtype=torch.uint8, device=dev)
+        dev_buf = _empty(need, torch.uint8, dev, None if streams is None else streams[0])   # (where all of it ends)
     nbytes = 0 if dev_buf is None else dev_buf.numel() * dev_buf.element_size()
     if streams is None:
         streams = (torch.cuda.current_stream(dev), torch.cuda.Stream(dev), torch.cuda.Stream(dev))
@@ -325,9 +340,9 @@ def merge_attn_states(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     D = o_a.shape[-1]
     rows = lse_a.numel()
     if out is None:
-        out = torch.empty_like(o_a)
+        out = _kept(torch.empty_like(o_a), stream)
     if lse is None:
-        lse = torch.empty_like(lse_a)
+        lse = _kept(torch.empty_like(lse_a), stream)
     _check(lib().kdt_merge_attn_states(_ptr(o_a), _ptr(lse_a), _ptr(o_b), _ptr(lse_b), rows, D, _ptr(out),
                                        _ptr(lse), _stream_ptr(stream)), "kdt_merge_attn_states")
     return out, lse
@@ -343,7 +358,7 @@ def vc_up_proj(o, w_vc, out=None, err=None, stream=None):
         raise ValueError("w_vc must be [H, D_c, D_v] matching o [..., H, D_c]")
     R = o.numel() // (H * D_c) if o.numel() else 0
     if out is None:
-        out = torch.empty(tuple(o.shape[:-1]) + (D_v,), dtype=torch.float32, device=o.device)
+        out = _empty(tuple(o.shape[:-1]) + (D_v,), torch.float32, o.device, stream)
     _check(lib().kdt_vc_up_proj(_ptr(o), _ptr(w_vc), _dtype_code(w_vc), R, H, D_c, D_v, _ptr(out), _ptr(err),
                                 _stream_ptr(stream)), "kdt_vc_up_proj")
     return out
@@ -396,9 +411,9 @@ def tree_accept(parent, tok, target, err=None, stream=None):
     import torch
     B, T = parent.shape
     dev = parent.device
-    acc = torch.empty((B, T), dtype=torch.int32, device=dev)
-    n = torch.empty(B, dtype=torch.int32, device=dev)
-    bonus = torch.empty(B, dtype=torch.int32, device=dev)
+    acc = _empty((B, T), torch.int32, dev, stream)
+    n = _empty(B, torch.int32, dev, stream)
+    bonus = _empty(B, torch.int32, dev, stream)
     _check(lib().kdt_tree_accept(_ptr(parent), _ptr(tok), _ptr(target), B, T, _ptr(acc), _ptr(n), _ptr(bonus),
                                  _ptr(err), _stream_ptr(stream)), "kdt_tree_accept")
     return acc, n, bonus
@@ -418,10 +433,8 @@ def tree_build(cand_tok, cand_lp, N, root_tok=None, stream=None):
     import torch
     B, D, K = cand_lp.shape
     dev = cand_lp.device
-    parent = torch.empty((B, N + 1), dtype=torch.int32, device=dev)
-    tok = torch.empty_like(parent)
-    depth = torch.empty_like(parent)
-    score = torch.empty((B, N + 1), dtype=torch.float32, device=dev)
+    parent, tok, depth = (_empty((B, N + 1), torch.int32, dev, stream) for _ in range(3))
+    score = _empty((B, N + 1), torch.float32, dev, stream)
     _check(lib().kdt_tree_build(_ptr(cand_tok), _ptr(cand_lp), B, D, K, int(N), _ptr(root_tok), _ptr(parent),
                                 _ptr(tok), _ptr(depth), _ptr(score), _stream_ptr(stream)), "kdt_tree_build")
     return parent, tok, depth, score
@@ -494,9 +507,9 @@ def latent_read_q8(c_q8, c_scale, k_pe, start, R, *, n_rows=None, dtype=None, ou
     dtype = dtype or (out_c.dtype if out_c is not None else torch.bfloat16)
     _int32_of(start, B, "start"), _int32_of(n_rows, B, "n_rows")
     if out_c is None:
-        out_c = torch.empty((B, R, 512), dtype=dtype, device=c_q8.device)
+        out_c = _empty((B, R, 512), dtype, c_q8.device, stream)
     if out_k is None:
-        out_k = torch.empty((B, R, 64), dtype=dtype, device=c_q8.device)
+        out_k = _empty((B, R, 64), dtype, c_q8.device, stream)
     for t, d in ((out_c, 512), (out_k, 64)):
         if t.shape != (B, R, d) or t.dtype != dtype or not t.is_contiguous():
             raise ValueError("out_c and out_k must be contiguous [B,R,512] and [B,R,64] tensors of dtype")
@@ -562,11 +575,11 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
     if vis is not None and (vis.numel() != B * T * ((T + 31) // 32) or vis.element_size() != 4 or not vis.is_contiguous()):
         raise ValueError("vis must be a contiguous 32-bit [B,T,ceil(T/32)] tensor")
     if out is None:
-        out = torch.empty((B, T, H, 512), dtype=out_dtype or torch.float32, device=q_nope.device)
+        out = _empty((B, T, H, 512), out_dtype or torch.float32, q_nope.device, stream)
     elif out.shape != (B, T, H, 512) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
         raise ValueError("out must be a contiguous [B,T,H,512] tensor of out_dtype")
     if lse is None and want_lse:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=q_nope.device)
+        lse = _empty((B, T, H), torch.float32, q_nope.device, stream)
     elif lse is not None and (lse.numel() != B * T * H or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [B,T,H] tensor")
     a = VerifyQ8Args(B, T, H, 512, 64, q_nope.data_ptr(), _row_stride(q_nope), q_pe.data_ptr(), _row_stride(q_pe),
@@ -577,7 +590,7 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
                      IMPLS[impl] if isinstance(impl, str) else int(impl), int(num_splits))
     if workspace is None:
         need = int(lib().kdt_verify_attn_q8_workspace_size(ctypes.byref(a)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device) if need else None
+        workspace = _empty(need, torch.uint8, q_nope.device, stream) if need else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().kdt_verify_attn_q8(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream_ptr(stream)),
            "kdt_verify_attn_q8")
@@ -599,10 +612,10 @@ def tree_sample(parent, tok, logits, u_node, u_bonus, *, temperature=1.0, err=No
         if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
     dev = logits.device
-    acc = torch.empty((B, T), dtype=torch.int32, device=dev)
-    n = torch.empty(B, dtype=torch.int32, device=dev)
-    bonus = torch.empty(B, dtype=torch.int32, device=dev)
-    logp = torch.empty((B, T), dtype=torch.float32, device=dev) if want_logp else None
+    acc = _empty((B, T), torch.int32, dev, stream)
+    n = _empty(B, torch.int32, dev, stream)
+    bonus = _empty(B, torch.int32, dev, stream)
+    logp = _empty((B, T), torch.float32, dev, stream) if want_logp else None
     _check(lib().kdt_tree_sample(_ptr(parent), _ptr(tok), _ptr(logits), _dtype_code(logits), B, T, V, row_stride,
                                  float(temperature), _ptr(u_node), _ptr(u_bonus), _ptr(acc), _ptr(n), _ptr(bonus),
                                  _ptr(logp), _ptr(err), _stream_ptr(stream)), "kdt_tree_sample")

@@ -405,3 +405,27 @@ def test_each_call_sees_its_own_tree(kdt, impl, T, H):
         _check(dict(d, parent=tree), [x.double().cpu().numpy() for x in outs[k]], 2.0 ** -24)
     for k in range(2, 30):
         assert torch.equal(outs[k][0], outs[k % 2][0]) and torch.equal(outs[k][1], outs[k % 2][1])
+
+
+@pytest.mark.parametrize("T,H,prefix", [(40, 16, [3000, 700])])
+def test_a_busy_side_stream_keeps_its_workspace_and_outputs(kdt, T, H, prefix):
+    """A call queued on a stream that is still busy: what the call allocated is not handed out to the current
+    stream before it has run."""
+    import torch
+    d = _inputs(97, T, H, prefix)
+    want = _call(kdt, d)
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    par = torch.from_numpy(d["parent"]).cuda()
+    need = kdt.verify_attn_q8_workspace_size(2, T, H, max(prefix) + T)
+    side, a = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            a = (a @ a).clamp_(-1, 1)
+    out, lse = kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre, parent=par, scale=SCALE,
+                                  max_kv_len=max(prefix) + T, stream=side)
+    junk = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), want[0]) and np.array_equal(lse.double().cpu().numpy(), want[1])
+    del junk

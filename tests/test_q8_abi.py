@@ -242,3 +242,48 @@ def test_expanded_views_are_refused(kdt):
     assert _row_stride3(one[..., :512], "c") == 512 and _row_stride3(torch.zeros(2, 3, 576)[..., :512], "c") == 576
     assert _row_stride3(torch.zeros(2, 3, 576)[:, 1:2, :512], "c") == 3 * 576
     assert _row_stride(q[..., :512]) == 576 and _row_stride(q1[..., :512]) == 0
+
+
+class _FakeLib:
+    """Entry points that succeed and compute nothing."""
+
+    def __getattr__(self, name):
+        return (lambda *a: 4096) if name.endswith("_size") else (lambda *a: 0)
+
+
+def test_tensors_made_here_are_kept_for_the_stream_they_are_used_on(kdt, monkeypatch):
+    """With ``stream=`` the call's own workspace and outputs belong to the current stream's allocator: each
+    is recorded on the stream that uses it, or their memory could be handed out while it still runs."""
+    import torch
+    from types import SimpleNamespace
+    kept = []
+    monkeypatch.setattr(kdt.kdt, "lib", _FakeLib)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: kept.append((self.data_ptr(), s)))
+    side = SimpleNamespace(cuda_stream=0x99)
+    B, T, H, V, bf = 2, 3, 4, 10, torch.bfloat16
+    made, plain = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(plain(*a, **k)) or made[-1])
+    c8, sc = torch.zeros(B, 8, 512, dtype=torch.uint8), torch.zeros(B, 8, 16, dtype=torch.uint8)
+    kp, i32 = torch.zeros(B, 8, 64, dtype=bf), torch.zeros(B, T, dtype=torch.int32)
+    q, u = torch.zeros(B, T, H, 576, dtype=bf), torch.zeros(B, T)
+    pre, o, lse = i32[:, 0].contiguous(), torch.zeros(B, T, H, 512), torch.zeros(B, T, H)
+    calls = [
+        lambda s: kdt.verify_attn_q8(q[..., :512], q[..., 512:], c8, sc, kp, pre, parent=i32, stream=s),
+        lambda s: kdt.verify_attn(q[..., :512], q[..., 512:], torch.zeros(B, 8, 512, dtype=bf), kp, pre, parent=i32, stream=s),
+        lambda s: kdt.latent_read_q8(c8, sc, kp, None, 4, stream=s),
+        lambda s: kdt.tree_sample(i32, i32, torch.zeros(B, T, V), u, u[:, 0].contiguous(), stream=s),
+        lambda s: kdt.build_visibility(i32, stream=s),
+        lambda s: kdt.vc_up_proj(o, torch.zeros(H, 512, 128, dtype=bf), stream=s),
+        lambda s: kdt.tree_accept(i32, i32, i32, stream=s),
+        lambda s: kdt.tree_build(torch.zeros(B, 2, 4, dtype=torch.int32), torch.zeros(B, 2, 4), 5, stream=s),
+        lambda s: kdt.merge_attn_states(o, lse, o, lse, stream=s),
+    ]
+    monkeypatch.setattr(torch, "empty_like", lambda t, **k: torch.empty(t.shape, dtype=t.dtype))
+    for k, call in enumerate(calls):
+        made.clear(), kept.clear()
+        call(side)
+        assert made and sorted(kept) == sorted((t.data_ptr(), side) for t in made), k
+    mine = dict(out=o, lse=lse, workspace=torch.zeros(8192, dtype=torch.uint8))         # the caller's own: left alone
+    kept.clear()
+    kdt.verify_attn_q8(q[..., :512], q[..., 512:], c8, sc, kp, pre, parent=i32, stream=side, **mine)
+    assert not kept
