@@ -124,7 +124,8 @@ typedef struct {
     const void *k_pe;       /* [B,L,64]  rope keys, same row indexing */
     int64_t kv_row_stride;  /* L: rows per sequence in c_kv/k_pe, >= max_kv_len */
     const int32_t *prefix_len; /* device [B]: shared-prefix length; tree node t at row prefix_len[b]+t */
-    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T (sizes the grid, no sync) */
+    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T (sizes the grid, no
+                               sync); below 2^31 - 256 */
     const int32_t *parent;  /* device [B,T] parent array, or NULL */
     const uint32_t *vis;    /* device [B,T,ceil(T/32)] packed visibility bits, or NULL */
     float scale;            /* score scale, e.g. 1/sqrt(192) */
@@ -508,7 +509,7 @@ typedef struct {
     const void *k_pe;
     int64_t kv_row_stride;  /* L: rows per sequence, >= max_kv_len */
     const int32_t *prefix_len; /* device [B]; tree node t at row prefix_len[b] + t */
-    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T */
+    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T; below 2^31 - 256 */
     const int32_t *parent;  /* device [B,T] parent array, or NULL */
     const uint32_t *vis;    /* device [B,T,ceil(T/32)] packed visibility bits, or NULL */
     float scale;

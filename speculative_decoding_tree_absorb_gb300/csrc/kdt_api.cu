@@ -95,7 +95,8 @@ kdt_status check_args(const kdt_verify_args *a) {
     if (a->B == 0) return KDT_OK;
     if (!a->q_nope || !a->q_pe || !a->c_kv || !a->k_pe || !a->prefix_len || !a->out) return KDT_ERR_NULL_ARG;
     if ((a->parent == nullptr) == (a->vis == nullptr)) return KDT_ERR_NULL_ARG;
-    if (a->max_kv_len < a->T || (int64_t)a->max_kv_len > a->kv_row_stride) return KDT_ERR_BAD_SHAPE;
+    if (a->max_kv_len < a->T || a->max_kv_len > kMaxKv || (int64_t)a->max_kv_len > a->kv_row_stride)
+        return KDT_ERR_BAD_SHAPE;
     if (!aligned16(a->q_nope) || !aligned16(a->q_pe) || !aligned16(a->c_kv) || !aligned16(a->k_pe) ||
         !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
         return KDT_ERR_BAD_SHAPE;

@@ -28,6 +28,7 @@ __device__ __forceinline__ void record_error(int32_t *err, int32_t v) {
 }
 constexpr int kMaxSplits = 32;
 constexpr int kMaxT = 4096;
+constexpr int kMaxKv = INT32_MAX - 256;        // keys of a sequence: round-ups to blocks stay in 32 bits
 
 // Everything an attention kernel needs, already validated on the host.
 struct VerifyParams {

@@ -43,7 +43,8 @@ kdt_status check_args(const kdt_verify_q8_args *a) {
     if (!a->q_nope || !a->q_pe || !a->c_q8 || !a->c_scale || !a->k_pe || !a->prefix_len || !a->out)
         return KDT_ERR_NULL_ARG;
     if ((a->parent == nullptr) == (a->vis == nullptr)) return KDT_ERR_NULL_ARG;
-    if (a->max_kv_len < a->T || (int64_t)a->max_kv_len > a->kv_row_stride) return KDT_ERR_BAD_SHAPE;
+    if (a->max_kv_len < a->T || a->max_kv_len > kMaxKv || (int64_t)a->max_kv_len > a->kv_row_stride)
+        return KDT_ERR_BAD_SHAPE;
     for (const void *p : {a->q_nope, a->q_pe, (const void *)a->c_q8, (const void *)a->c_scale, a->k_pe,
                           (const void *)a->out})
         if (!aligned(p, 16)) return KDT_ERR_BAD_SHAPE;

@@ -287,3 +287,22 @@ def test_tensors_made_here_are_kept_for_the_stream_they_are_used_on(kdt, monkeyp
     kept.clear()
     kdt.verify_attn_q8(q[..., :512], q[..., 512:], c8, sc, kp, pre, parent=i32, stream=side, **mine)
     assert not kept
+
+
+def test_lengths_near_the_end_of_32_bits_are_refused(kdt):
+    """Rounded up to whole blocks they would pass 2^31: no plan with negative counts, for either cache."""
+    K = kdt.kdt
+    a = kdt.VerifyArgs()
+    a.B, a.T, a.H, a.D_c, a.D_r, a.dtype, a.scale = 2, 3, 4, 512, 64, 1, 1.0
+    for f in ("q_nope", "q_pe", "c_kv", "k_pe", "prefix_len", "parent", "out"):
+        setattr(a, f, 4096)
+    for n in (2 ** 31 - 1, 2 ** 31 - 127, 2 ** 31 - 256):
+        for impl in ("auto", "q8_rows", "tcgen05"):
+            with pytest.raises(kdt.KdtError) as e:
+                kdt.verify_attn_q8_plan(2, 3, 4, n, impl=impl)
+            assert e.value.status == K.KDT_ERR_BAD_SHAPE
+        a.kv_row_stride = a.max_kv_len = n
+        for a.impl in range(4):
+            with pytest.raises(kdt.KdtError):
+                kdt.plan(a)
+    assert kdt.verify_attn_q8_plan(2, 3, 4, 2 ** 31 - 257, impl="q8_rows")["ctas"] > 0
