@@ -472,6 +472,15 @@ def _int32_of(t, n, name):
     return t
 
 
+def _err_of(t):
+    """Address of an error word: four bytes are written there."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("err must be an int32 tensor of at least one element")
+    return t.data_ptr()
+
+
 def latent_write_q8(c, k, c_q8, c_scale, k_pe, prefix_len, *, gamma=None, eps=1e-6, pos=None, base=10000.0,
                     n_rows=None, stream=None):
     """Norm, rotate, quantise and store new rows of an 8-bit cache (kdt_latent_write_q8).
@@ -586,7 +595,7 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
                      c_q8.data_ptr(), c_scale.data_ptr(), k_pe.data_ptr(), L, prefix_len.data_ptr(),
                      L if max_kv_len is None else int(max_kv_len), None if parent is None else parent.data_ptr(),
                      None if vis is None else vis.data_ptr(), float(scale), out.data_ptr(), _dtype_code(out),
-                     None if lse is None else lse.data_ptr(), None if err is None else err.data_ptr(),
+                     None if lse is None else lse.data_ptr(), _err_of(err),
                      IMPLS[impl] if isinstance(impl, str) else int(impl), int(num_splits))
     if workspace is None:
         need = int(lib().kdt_verify_attn_q8_workspace_size(ctypes.byref(a)))
@@ -618,5 +627,5 @@ def tree_sample(parent, tok, logits, u_node, u_bonus, *, temperature=1.0, err=No
     logp = _empty((B, T), torch.float32, dev, stream) if want_logp else None
     _check(lib().kdt_tree_sample(_ptr(parent), _ptr(tok), _ptr(logits), _dtype_code(logits), B, T, V, row_stride,
                                  float(temperature), _ptr(u_node), _ptr(u_bonus), _ptr(acc), _ptr(n), _ptr(bonus),
-                                 _ptr(logp), _ptr(err), _stream_ptr(stream)), "kdt_tree_sample")
+                                 _ptr(logp), _err_of(err), _stream_ptr(stream)), "kdt_tree_sample")
     return acc, n, bonus, logp

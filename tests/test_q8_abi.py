@@ -306,3 +306,16 @@ def test_lengths_near_the_end_of_32_bits_are_refused(kdt):
             with pytest.raises(kdt.KdtError):
                 kdt.plan(a)
     assert kdt.verify_attn_q8_plan(2, 3, 4, 2 ** 31 - 257, impl="q8_rows")["ctas"] > 0
+
+
+def test_error_words_of_another_size_are_refused(kdt):
+    import torch
+    bf = torch.bfloat16
+    c8, sc = torch.zeros(2, 8, 512, dtype=torch.uint8), torch.zeros(2, 8, 16, dtype=torch.uint8)
+    kp, par, u = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    q = torch.zeros(2, 3, 4, 576, dtype=bf)
+    for err in (torch.zeros(4, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)):
+        with pytest.raises(ValueError, match="err"):
+            kdt.verify_attn_q8(q[..., :512], q[..., 512:], c8, sc, kp, par[:, 0].contiguous(), parent=par, err=err)
+        with pytest.raises(ValueError, match="err"):
+            kdt.tree_sample(par, par, torch.zeros(2, 3, 10), u, u[:, 0].contiguous(), err=err)
