@@ -429,3 +429,62 @@ def test_a_busy_side_stream_keeps_its_workspace_and_outputs(kdt, T, H, prefix):
     torch.cuda.synchronize()
     assert np.array_equal(out.double().cpu().numpy(), want[0]) and np.array_equal(lse.double().cpu().numpy(), want[1])
     del junk
+
+
+def _check_nodes(d, got, out_eps, see, nodes):
+    """_check for some nodes of each sequence: the others' rows are only required to be finite."""
+    out, lse = got
+    assert np.isfinite(out).all()
+    for b, P in enumerate(d["prefix"]):
+        N = P + d["T"]
+        c = oq.dequantise(d["c8"][b, :N].cpu().numpy(), d["sc"][b, :N].cpu().numpy())
+        k = d["kp"][b, :N].double().cpu().numpy()
+        q = d["q"][b, nodes].double().cpu().numpy()
+        ref_o, ref_l = oq.attention(q, c, k, P, see[b][nodes], SCALE)
+        for n, i in enumerate(nodes):
+            keys = np.concatenate([np.arange(P), P + np.flatnonzero(see[b][i])])
+            if not len(keys):
+                assert (out[b, i] == 0).all() and (lse[b, i] == -np.inf).all()
+                continue
+            kc = np.concatenate([c[keys], k[keys]], -1)
+            p = np.exp(SCALE * (q[n] @ kc.T) - ref_l[n][:, None])
+            ds = 576 * 2.0 ** -24 * SCALE * (np.abs(q[n]) @ np.abs(kc).T).max()
+            tol = (2.0 ** -8 + 2 * ds + 2.0 ** -20) * (p @ np.abs(c[keys])) + (out_eps + 2.0 ** -22) * np.abs(ref_o[n])
+            assert (np.abs(out[b, i] - ref_o[n]) <= tol).all(), (b, i, np.abs(out[b, i] - ref_o[n]).max())
+            tol = ds + (2.0 ** -20 + (len(keys) / 128 + 12) * 2.0 ** -24) * (1 + np.abs(ref_l[n]))
+            assert (np.abs(lse[b, i] - ref_l[n]) <= tol).all(), (b, i, np.abs(lse[b, i] - ref_l[n]).max())
+
+
+def _some_nodes(T, n=24):
+    """First and last nodes, those around words' and blocks' ends, and a few between."""
+    edge = [i + e for i in range(0, T, 128) for e in (-1, 0, 1, 31, 32)]
+    pick = np.random.RandomState(T).choice(T, min(T, n), replace=False).tolist()
+    return sorted({i for i in [T - 2] + edge[:15] + edge[-10:] + pick + [T - 1] if 0 <= i < T})
+
+
+WIDE = [(127, 3, [1, 300]), (128, 2, [0, 128]), (129, 5, [64, 70]), (200, 7, [0, 33, 500]), (513, 1, [127, 0]),
+        (1000, 3, [90]), (2500, 1, [5, 200]), (4096, 2, [130]), (4095, 1, [0])]
+
+
+@pytest.mark.parametrize("impl,splits", [("q8_rows", 0), ("q8_rows", 3), ("tcgen05", 0), ("tcgen05", 2), ("auto", 0)])
+@pytest.mark.parametrize("kind", ["random", "chain"])
+@pytest.mark.parametrize("T,H,prefix", WIDE)
+def test_wide_trees_and_prompt_chunks(kdt, T, H, prefix, kind, impl, splits):
+    """Trees over many visibility words and key blocks, up to the largest, and chains: a prompt's chunk."""
+    d = _inputs(T, T, H, prefix)
+    if kind == "chain":
+        d["parent"] = np.tile(np.arange(T, dtype=np.int32) - 1, (len(prefix), 1))
+    see = [oq.ancestors(p) for p in d["parent"]]
+    _check_nodes(d, _call(kdt, d, impl=impl, num_splits=splits), 2.0 ** -24, see, _some_nodes(T))
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+@pytest.mark.parametrize("T,H", [(161, 3), (1030, 2), (4096, 1)])
+def test_wide_caller_bits(kdt, impl, T, H):
+    """Any bits over many words, rows that see nothing among them."""
+    d = _inputs(T + 1, T, H, [0, 70])
+    rng = np.random.RandomState(T)
+    see = rng.rand(2, T, T) < 0.02
+    see[0, ::7] = False
+    see[0, 3, T - 1] = see[1, 5, T - 33] = True
+    _check_nodes(d, _call(kdt, d, see=see, impl=impl), 2.0 ** -24, see, _some_nodes(T))
