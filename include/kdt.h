@@ -572,7 +572,8 @@ kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
  *   u_node   device float32 [B,T], u_bonus device float32 [B]: numbers in [0, 1)
  *   acc_nodes, n_acc, bonus  out, as kdt_tree_accept's: they feed kdt_kv_compact(_q8)
  *   logp     device float32 [B,T] out, or NULL: entry k < n_acc is the log-probability (natural,
- *            under the target at this temperature) of the token emitted after path node k; 0 behind
+ *            under the target at this temperature) of the token emitted after path node k, off by at
+ *            most 2e-5 + 2^-23 of its size (the bonus token's: 3e-7 + 2^-23 of it); 0 behind
  *   err      device int32, or NULL: zeroed, then 1 + (b*T + i) of the first parent entry outside
  *            [-1, i) (skipped), child on the way whose token is outside [0, V) (never accepted), or
  *            node on the way whose logits have a NaN, a +inf or nothing but -inf (the walk ends

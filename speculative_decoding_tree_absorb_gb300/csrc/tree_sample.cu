@@ -14,8 +14,14 @@
 //    where they fit. A step is one pass for the slice's maximum and sum, one exchange of
 //    (maximum, sum) through distributed shared memory, and the children's tests, which every
 //    CTA makes alike from the same numbers.
-//  * The walk's sums use the fast exponential (relative error below 2^-18 for weights that
-//    count); a test closer than kMargin of Z is made again with the exact sums.
+//  * The walk's sums use the fast exponential and float32; a test closer than kMargin of Z is
+//    made again with the exact sums. The fast Z is off by at most 1.9e-5 of itself: 264 roundings
+//    in a row (V = 524288 in float32 with one CTA a sequence: 256 vectors a thread, 3 sums within
+//    one, 5 shuffles; bf16 140) give 1.58e-5; a weight 2^-|y| is off by 2^-22 and by
+//    2.1 2^-24 |y| (three roundings of y), with |y| at most 14.3 on average over the sum (V tokens
+//    of 2^-|y| beside the largest), 1.8e-6; the slices' factors 3e-7. A test in float32 adds
+//    three roundings a child, 5.8e-6 for kFewKids: together below kMargin. An accepted
+//    token's log-probability is made from the fast Z.
 //  * Drawing from the rest needs more: the threshold falls between two of V running sums, and
 //    with float32 weights (errors of 1e-7) neighbours of small probability would be mixed up.
 //    Weights are fixed-point numbers there, w = round(2^44 e^y): integer sums do not depend on
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kNT, 1) tree_sample_kernel(const SampleParams 
         for (int off = kNW / 2; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
         const E *data = p.cache ? row : src;
         // -- the slice's sum relative to its maximum
-        // (in float32 by vectors of 16 bytes and warps, then in 64 bits: off by at most 130 roundings)
+        // (in float32 by vectors of 16 bytes, threads and warps: at most 264 roundings in a row; then in 64 bits)
         float z = 0.f;
         if (m > -INFINITY && m < INFINITY) {
             auto term = [&](float x) { return ex2((x - m) * p.c_hi); };

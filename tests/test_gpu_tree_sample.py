@@ -227,3 +227,30 @@ def test_captured_and_replayed_beside_another_stream(kdt):
         torch.cuda.synchronize()
         _check(d, [x.cpu().numpy() for x in out] + [0])
         assert all(torch.equal(a, b) for a, b in zip(out, other))
+
+
+@pytest.mark.parametrize("dtype,B,temp", [("f32", 80, 1.0), ("bf16", 80, 0.3), ("f32", 2, 1.7)])
+def test_the_largest_vocabulary_in_a_large_batch(kdt, dtype, B, temp):
+    """524288 tokens with one CTA a sequence (and eight): the longest float32 sums there are. Many weights
+    of one size, so that their roundings count; a child's test just on either side of its border, from
+    within the fast sums' error to beyond the margin; and log-probabilities within the stated bounds."""
+    import torch
+    V, T = 524288, 2
+    d = _inputs(21, B, T, V, dtype, agree=1.0)
+    d["logits"] = d["logits"] * 0.2 + 1.0                    # of T rows each the first matters for the test
+    d["logits"][:, :, 5] = 9.0
+    d["parent"][:, 1], d["temp"] = 0, temp
+    for b in range(B):
+        d["logits"][b, 0, d["tok"][b, 1]] = 11.0 + 0.01 * (b % 7)
+        w = oq.sample_weights(d["logits"][b, 0].double().cpu().numpy(), temp)
+        off = [1e-7, 3e-6, 1e-5, 2e-5, 5e-5, 1e-3][b % 6] * (1 if b % 2 else -1)
+        d["u"][b, 1] = np.float32(w[d["tok"][b, 1]] / w.sum() * (1 + off))
+    got = _run(kdt, d)
+    assert got[4] == 0 and 0.2 * B < (got[1] == 2).sum() < 0.8 * B
+    for b in range(B):
+        path, want, lp = oq.tree_sample(d["parent"][b], d["tok"][b], lambda i: d["logits"][b, i].double().cpu().numpy(),
+                                        d["u"][b].astype(np.float64), float(d["ub"][b]), temp)
+        n = got[1][b]
+        assert got[0][b, :n].tolist() == path and got[2][b] == want
+        off = np.abs(got[3][b, :n] - lp)
+        assert (off[:-1] <= 2e-5 + 2.0 ** -23 * np.abs(lp[:-1])).all() and off[-1] <= 3e-7 + 2.0 ** -23 * abs(lp[-1]), (b, off)
