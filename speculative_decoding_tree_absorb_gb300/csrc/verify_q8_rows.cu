@@ -1026,9 +1026,10 @@ template <bool kBf16Out> cudaError_t launch(const Q8Params &p, cudaStream_t s) {
     if ((e = cudaLaunchKernelEx(&cfg, verify_q8_rows_kernel<kBf16Out>, p)) != cudaSuccess) return e;
     if (p.pieces) {
         cudaLaunchConfig_t mc = {};
-        // eight or more pieces a tile: their loads are what takes the time (two tiles of 65 pieces: 17 us against 28)
+        // sixteen or more pieces a tile: their loads are what takes the time. A call, a CTA a row / the other join, by
+        // pieces a tile: 152 42 / 56 us, 76 36 / 44, 64 31 / 39, 38 38 / 40, 17 50 / 52, 13 68 / 66, 8 46 / 42, 4 48 / 38
         const int64_t tiles = (int64_t)p.B * p.tiles_seq;
-        const bool deep = tiles * 8 <= p.ctas;
+        const bool deep = tiles * 16 <= p.ctas;
         mc.gridDim = deep ? dim3((unsigned)tiles, kRowsT) : dim3((unsigned)(p.ctas - 1), kRowsT / kMergeRows);
         mc.blockDim = dim3(deep ? 256 : 64 * kMergeRows);
         mc.stream = s;

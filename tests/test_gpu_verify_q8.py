@@ -488,3 +488,30 @@ def test_wide_caller_bits(kdt, impl, T, H):
     see[0, ::7] = False
     see[0, 3, T - 1] = see[1, 5, T - 33] = True
     _check_nodes(d, _call(kdt, d, see=see, impl=impl), 2.0 ** -24, see, _some_nodes(T))
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+def test_same_as_the_bf16_cache_by_element(kdt, impl):
+    """As test_same_as_the_bf16_cache, with each element's own bound: twice _check's, once for either kernel."""
+    import torch
+    d = _inputs(51, 16, 64, [500, 900])
+    out, lse = _call(kdt, d, impl=impl)
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    c, k = kdt.latent_read_q8(d["c8"], d["sc"], d["kp"], None, d["L"])
+    q = d["q"]
+    o2, l2 = (x.double().cpu().numpy() for x in kdt.verify_attn(
+        q[..., :512], q[..., 512:], c, k, pre, parent=torch.from_numpy(d["parent"]).cuda(), max_kv_len=916, scale=SCALE,
+        impl="tcgen05"))
+    for b, P in enumerate(d["prefix"]):
+        kc = torch.cat([c[b, :P + 16], k[b, :P + 16]], -1).double().cpu().numpy()
+        qb, see = q[b].double().cpu().numpy(), oq.ancestors(d["parent"][b])
+        for i in range(16):
+            keys = np.concatenate([np.arange(P), P + np.flatnonzero(see[i])])
+            s = SCALE * (qb[i] @ kc[keys].T)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            mag = (p / p.sum(-1, keepdims=True)) @ np.abs(kc[keys, :512])
+            ds = 576 * 2.0 ** -24 * SCALE * (np.abs(qb[i]) @ np.abs(kc[keys]).T).max()
+            tol = 2 * ((2.0 ** -8 + 2 * ds + 2.0 ** -20) * mag + (2.0 ** -24 + 2.0 ** -22) * np.abs(o2[b, i]))
+            assert (np.abs(out[b, i] - o2[b, i]) <= tol).all(), (b, i)
+            tol = 2 * (ds + (2.0 ** -20 + (len(keys) / 128 + 12) * 2.0 ** -24) * (1 + np.abs(l2[b, i])))
+            assert (np.abs(lse[b, i] - l2[b, i]) <= tol).all(), (b, i)
