@@ -515,3 +515,40 @@ def test_same_as_the_bf16_cache_by_element(kdt, impl):
             assert (np.abs(out[b, i] - o2[b, i]) <= tol).all(), (b, i)
             tol = 2 * (ds + (2.0 ** -20 + (len(keys) / 128 + 12) * 2.0 ** -24) * (1 + np.abs(l2[b, i])))
             assert (np.abs(lse[b, i] - l2[b, i]) <= tol).all(), (b, i)
+
+
+@pytest.mark.parametrize("impl,splits", [("auto", 0), ("q8_rows", 0), ("q8_rows", 700), ("tcgen05", 0)])
+@pytest.mark.parametrize("T,H,prefix", [(1, 64, [0, 1, 5]), (9, 8, [130, 3, 0, 300]), (40, 20, [70])])
+def test_a_bound_far_above_the_lengths(kdt, T, H, prefix, impl, splits):
+    """max_kv_len left at the cache's size: the split is planned for many more blocks than there are."""
+    import torch
+    d = _inputs(98, T, H, prefix, pad=30000)
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    out, lse = kdt.verify_attn_q8(d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre,
+                                  parent=torch.from_numpy(d["parent"]).cuda(), scale=SCALE, impl=impl, num_splits=splits)
+    _check(d, (out.double().cpu().numpy(), lse.double().cpu().numpy()), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 2.0])
+def test_other_scales(kdt, impl, scale, monkeypatch):
+    """A scale of 0 (the plain mean), a negative and a large one. The bounds hold n 2^-24 |scale| sum |q||c|, so
+    a negative scale is checked as the positive one over the negated queries: the same scores."""
+    import sys
+    d = _inputs(99, 20, 8, [300, 2], amp=0.25)
+    for splits in (0, 1):
+        monkeypatch.setattr(sys.modules[__name__], "SCALE", scale)
+        got = _call(kdt, d, impl=impl, num_splits=splits)
+        monkeypatch.setattr(sys.modules[__name__], "SCALE", abs(scale))
+        _check(dict(d, q=-d["q"]) if scale < 0 else d, got, 2.0 ** -24)
+
+
+@pytest.mark.parametrize("impl", ["q8_rows", "tcgen05"])
+def test_queries_far_apart_and_a_cache_without_room_to_spare(kdt, impl):
+    """Query rows 2048 elements apart; the last sequence's last row is the cache's last."""
+    import torch
+    d = _inputs(100, 7, 12, [400, 130], pad=0)
+    wide = torch.full((2, 7, 12, 2048), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[..., 64:640] = d["q"]
+    d["q"] = wide[..., 64:640]
+    _check(d, _call(kdt, d, impl=impl), 2.0 ** -24)
