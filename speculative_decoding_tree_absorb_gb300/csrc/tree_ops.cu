@@ -129,13 +129,16 @@ __global__ void tree_accept_kernel(const int32_t *__restrict__ parent, const int
 // that move independently: the CTAs of a sequence's cluster take some columns each, and
 // prefix_len is advanced once all of them have read it. Entries outside the tree or the cache
 // are not copied. An 8-bit cache has a third array, c_scale (s_vec = 1 vector a row; else NULL
-// and 0). What bounds it is the latency of a chunk's loads: 96 sequences that move 119 rows of
-// 656 bytes each took 33 us with one CTA and shared memory, 13 us so.
-constexpr int kCompactThreads = 256, kCompactHold = 8, kCompactCluster = 8;
+// and 0). What bounds it is the latency of a chunk's loads, and for large batches the CTAs an SM
+// holds: only the vectors stay in registers (64 registers, four CTAs), places are found again, and
+// a batch that fills the device has one CTA a sequence. 96 sequences moving 119 rows of 656 bytes
+// take 15 us (33 with one CTA each and shared memory); 1024 of 256 nodes moving 5 rows of 1152
+// bytes 5.7 us (5.4 so, and 42 with eight CTAs each of 110 registers).
+constexpr int kCompactThreads = 256, kCompactHold = 8, kCompactCluster = 8, kCompactCtas = 4;
 constexpr int kCompactChunk = kCompactThreads * kCompactHold;      // vectors
 constexpr int kCompactMostBytes = 40 * 1024;                        // of a row's two arrays
 
-__global__ void __launch_bounds__(kCompactThreads)
+__global__ void __launch_bounds__(kCompactThreads, kCompactCtas)
     kv_compact_kernel(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec, int r_vec, int s_vec, int64_t L,
                       int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int T, int S, int update_prefix) {
     const int b = blockIdx.x / S, part = blockIdx.x % S, tid = threadIdx.x;
@@ -144,31 +147,41 @@ __global__ void __launch_bounds__(kCompactThreads)
     const int row_vec = c_vec + r_vec + s_vec, per = ((row_vec + S - 1) / S + 1) / 2 * 2;   // whole sectors
     const int e0 = min(part * per, row_vec), cols = min(per, row_vec - e0);
     const int chunk = cols > 0 ? kCompactChunk / cols : 0;              // rows at a time
+    auto vector_of = [&](int64_t node, int e) -> uint4 * {              // of tree node's cache row
+        const int64_t r = (int64_t)b * L + p0 + node;
+        if (e < c_vec) return c_kv + r * c_vec + e;
+        return e < c_vec + r_vec ? k_pe + r * r_vec + (e - c_vec) : c_scale + r;
+    };
     for (int k0 = 1; k0 < n && cols > 0; k0 += chunk) {
         const int total = min(chunk, n - k0) * cols;
         uint4 v[kCompactHold];
-        uint4 *to[kCompactHold];                                        // NULL: nothing to move
+        int src[kCompactHold];                                          // all asked for before any is used
 #pragma unroll
         for (int u = 0; u < kCompactHold; ++u) {
-            const int i = tid + u * kCompactThreads, t = i / cols, e = e0 + i - t * cols, k = k0 + t;
-            to[u] = nullptr;
-            if (i >= total) continue;
-            const int src = acc_nodes[(int64_t)b * T + k];
-            if (src <= k || src >= T || p0 + src >= L || p0 < 0) continue;
-            const int64_t rs = (int64_t)b * L + p0 + src, rd = (int64_t)b * L + p0 + k;
-            uint4 *base = e < c_vec ? c_kv + e : (e < c_vec + r_vec ? k_pe + (e - c_vec) : c_scale);
-            const int width = e < c_vec ? c_vec : (e < c_vec + r_vec ? r_vec : 1);
-            v[u] = base[rs * width];
-            to[u] = base + rd * width;
+            if (u * kCompactThreads >= total) break;                    // (the CTA as one)
+            src[u] = acc_nodes[(int64_t)b * T + k0 + min(tid + u * kCompactThreads, total - 1) / cols];
+        }
+        uint32_t live = 0;                                              // which of the vectors move
+#pragma unroll
+        for (int u = 0; u < kCompactHold; ++u) {
+            if (u * kCompactThreads >= total) break;
+            const int i = tid + u * kCompactThreads, t = i / cols;
+            const bool moves = i < total && src[u] > k0 + t && src[u] < T && p0 + src[u] < L && p0 >= 0;
+            if (moves) v[u] = *vector_of(src[u], e0 + i - t * cols);
+            live |= (moves ? 1u : 0u) << u;
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kCompactHold; ++u)
-            if (to[u]) *to[u] = v[u];
+        for (int u = 0; u < kCompactHold; ++u) {
+            if (u * kCompactThreads >= total) break;
+            const int i = tid + u * kCompactThreads, t = i / cols;
+            if ((live >> u) & 1u) *vector_of(k0 + t, e0 + i - t * cols) = v[u];
+        }
         __syncthreads();
     }
     if (update_prefix) {
-        tc::cluster_sync();
+        if (S > 1) tc::cluster_sync();
+        else __syncthreads();
         if (part == 0 && tid == 0) prefix_len[b] = (int32_t)(p0 + n);
     }
 }
@@ -176,10 +189,12 @@ __global__ void __launch_bounds__(kCompactThreads)
 kdt_status launch_kv_compact(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec, int r_vec, int s_vec, int B, int T,
                              int64_t L, int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc,
                              int update_prefix, cudaStream_t stream) {
-    // CTAs a sequence: enough for the longest path in one chunk, by pairs of columns
-    const int64_t need = ((int64_t)T * (c_vec + r_vec + s_vec) + kCompactChunk - 1) / kCompactChunk;
-    int S = 1;
-    while (S < kCompactCluster && S < need) S <<= 1;
+    // CTAs a sequence: enough for the longest path in one chunk, by pairs of columns, as long as the device
+    // holds the batch's at once (and two for the widest rows: kCompactChunk vectors are less than one)
+    const int row_vec = c_vec + r_vec + s_vec;
+    const int64_t need = ((int64_t)T * row_vec + kCompactChunk - 1) / kCompactChunk, held = (int64_t)kCompactCtas * sm_count();
+    int S = row_vec > kCompactChunk ? 2 : 1;
+    while (S < kCompactCluster && S < need && 2 * S * (int64_t)B <= held) S <<= 1;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)S;
@@ -189,7 +204,7 @@ kdt_status launch_kv_compact(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec
     cfg.blockDim = dim3(kCompactThreads);
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = S > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kv_compact_kernel, c_kv, k_pe, c_scale, c_vec, r_vec, s_vec, L, prefix_len,
                               acc_nodes, n_acc, T, S, update_prefix ? 1 : 0) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }

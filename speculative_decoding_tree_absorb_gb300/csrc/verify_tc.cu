@@ -49,7 +49,7 @@
 //    chunk, in an O-CTA its 128 columns of each value chunk. Widening leaves each four dims
 //    in the order (0, 2, 1, 3): Q is loaded in that order and O written back from it. It is
 //    what bounds the kernel: a CTA widens 32 k codes a block, about 700 instructions a warp
-//    that share the schedulers with the softmax, in 4.2 k clocks a block (532 us for 8
+//    that share the schedulers with the softmax, in 4.2 k clocks a block (538 us for 8
 //    sequences of 64 nodes and 64 heads over 8 k keys) against 3.4 k of the bf16 kernel, whose
 //    cache is twice as large. A NaN group gives NaN keys, so that rows which see it become
 //    NaN, and zero values, so that it does not reach rows from which it is hidden.

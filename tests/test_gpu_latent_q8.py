@@ -267,3 +267,36 @@ def test_write_and_read_in_a_captured_graph_on_another_stream(kdt):
         kdt.latent_write_q8(kv[..., :512], kv[..., 512:], *ref, pre)
         c, k = kdt.latent_read_q8(*ref, None, 6, dtype=torch.float32)
         assert torch.equal(c, out_c) and torch.equal(k, out_k)
+
+
+@pytest.mark.parametrize("B,T", [(1, 1024), (30, 256), (100, 256), (250, 300), (700, 40), (1300, 5)])
+def test_compaction_of_every_split(kdt, B, T):
+    """Batches that get eight CTAs a sequence, fewer and one: both caches' rows as copied one by one, rows
+    beside the path as they were, prefixes advanced; paths of any length, none and one among them."""
+    import torch
+    rng = np.random.RandomState(B)
+    L = T + 40
+    pre = rng.randint(0, 40, B).astype(np.int32)
+    n = np.minimum(rng.choice([0, 1, 2, 6, T // 2, T], B), T).astype(np.int32)
+    acc = np.full((B, T), -1, dtype=np.int32)
+    for b in range(B):
+        if n[b]:
+            acc[b, :n[b]] = np.concatenate([[0], 1 + np.sort(rng.choice(T - 1, n[b] - 1, replace=False))])
+    g = torch.Generator(device="cuda").manual_seed(B)
+    big = lambda d, t: torch.randint(-2 ** 15, 2 ** 15 - 1, (B, L, d), device="cuda", generator=g).to(torch.int16).view(t)
+    q8 = [big(256, torch.uint8), big(8, torch.uint8), big(64, torch.bfloat16)]
+    kv = [big(512, torch.bfloat16), big(64, torch.bfloat16)]
+    was = [x.clone().view(torch.uint8) for x in q8 + kv]
+    move = [(b, int(pre[b]) + k, int(pre[b]) + int(acc[b, k])) for b in range(B) for k in range(1, n[b])]
+    if move:
+        bb, to, at = (torch.tensor(x, device="cuda") for x in zip(*move))
+        for x in was:
+            x[bb, to] = x[bb, at]
+    dev = [torch.from_numpy(x).cuda() for x in (acc, n)]
+    p8, p16 = (torch.from_numpy(pre).cuda() for _ in range(2))
+    kdt.kv_compact_q8(*q8, p8, *dev)
+    kdt.kv_compact(*kv, p16, *dev)
+    torch.cuda.synchronize()
+    for x, w in zip(q8 + kv, was):
+        assert torch.equal(x.view(torch.uint8), w)
+    assert p8.tolist() == p16.tolist() == (pre + n).tolist()
