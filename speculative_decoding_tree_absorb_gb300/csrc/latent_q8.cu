@@ -6,11 +6,11 @@
 // Both kernels only stream: a warp takes whole rows, every load and store instruction of a
 // warp covers one contiguous stretch (16 bytes a lane where the row holds that much), and
 // the grid is sized so that a resident warp takes several rows. Reading keeps the next row's
-// loads in flight (48 registers, 40 warps an SM); writing has more to hold, and more warps
+// loads in flight (40 registers, 40 warps an SM); writing has more to hold, and more warps
 // were worth more than a row ahead in each (16 warps of 92 registers: 33 us, 32 of 64: 22 us).
 // Measured: 12 prompts of up to 4095 rows in float32 written in 22 us (79 MB: 3.6 TB/s; issue
-// slots 63%), 8 sequences of 8256 rows read in 20-23 us (119 MB: 5.2-5.9 TB/s; issue slots
-// 70%). Short calls take the 7-9 us of one launch and one row's chain of loads.
+// slots 58%), 8 sequences of 8256 rows read in 20-25 us (119 MB: 4.8-5.9 TB/s; issue slots
+// 67%). Short calls take the 7-9 us of one launch and one row's chain of loads.
 #include <cmath>
 
 #include "kdt_internal.cuh"

@@ -24,8 +24,8 @@ struct Q8Plan {
 // Which kernel, by estimates in us. The rows kernel takes a pair (64 rows of a sequence, 128 keys) in 3.7
 // on one SM and 4.5 more for a tile's queries and output; a cluster takes (256 rows, 128 keys) in 2.05 on
 // 4 SMs and 10 more for a unit of rows, and its set-up, schedule and drain are longer. Measured, rows
-// kernel / clusters: 8 sequences of 8 k keys, 128 rows 50 / 83, 384 rows 95 / 112, 512 rows 119 / 116, 4096
-// rows 791 / 530; 43 of 2688 rows, 3 keys 105 / 206, 300 keys 198 / 274, 1000 keys 404 / 403; 2 of 4096 rows,
+// kernel / clusters: 8 sequences of 8 k keys, 128 rows 47 / 84, 384 rows 95 / 113, 512 rows 119 / 117, 4096
+// rows 793 / 536; 43 of 2688 rows, 3 keys 105 / 205, 300 keys 199 / 269, 1000 keys 406 / 403; 2 of 4096 rows,
 // 2000 keys 79 / 84.
 bool rows_cheaper(int64_t tiles, int64_t units, int nblk) {
     return 10.0 + tiles * (3.7 * nblk + 4.5) / sm_count() < 45.0 + units * (2.05 * nblk + 10.0) / tc_q8_max_clusters();
