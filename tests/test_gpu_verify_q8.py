@@ -552,3 +552,30 @@ def test_queries_far_apart_and_a_cache_without_room_to_spare(kdt, impl):
     wide[..., 64:640] = d["q"]
     d["q"] = wide[..., 64:640]
     _check(d, _call(kdt, d, impl=impl), 2.0 ** -24)
+
+
+def test_a_given_stream_inside_a_capture(kdt):
+    """Capturing with ``stream=`` a side stream that joined the capture, workspace and outputs made by the call:
+    replays give what plain calls give."""
+    import torch
+    d = _inputs(101, 40, 16, [900, 30])
+    pre = torch.tensor(d["prefix"], dtype=torch.int32, device="cuda")
+    par = torch.from_numpy(d["parent"]).cuda()
+    args = (d["q"][..., :512], d["q"][..., 512:], d["c8"], d["sc"], d["kp"], pre)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=a):
+        b.wait_stream(a)
+        one = kdt.verify_attn_q8(*args, parent=par, max_kv_len=940, stream=b)
+        two = kdt.verify_attn_q8(*args, parent=par, max_kv_len=940, stream=a)
+        a.wait_stream(b)
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        d["q"].copy_(torch.randn(d["q"].shape, device="cuda", generator=g).to(torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = kdt.verify_attn_q8(*args, parent=par, max_kv_len=940)
+        torch.cuda.synchronize()
+        for got in (one, two):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
