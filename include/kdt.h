@@ -550,6 +550,151 @@ size_t kdt_verify_attn_q8_workspace_size(const kdt_verify_q8_args *a);
 kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
 
 /* ------------------------------------------------------------------------------
+ * A paged latent cache: rows of many requests in pages that requests get and give
+ * back as their lengths change, instead of one block of L rows each.
+ *
+ *   c_kv  bf16 [n_pages, page_size, 512], k_pe bf16 [n_pages, page_size, 64]; page_size a power
+ *         of two from 8 to 1024, n_pages * page_size below 2^31 - 256. Row `slot` of the cache is
+ *         row slot % page_size of page slot / page_size.
+ *   table int32 [B, W], row stride table_row_stride (0 = W): row j of sequence b lies in page
+ *         table[b, j / page_size]. Entries behind the pages a call needs are never read as
+ *         pages, whatever they hold.
+ * ------------------------------------------------------------------------------ */
+
+/* Arguments of kdt_page_assign. All arrays on the device. */
+typedef struct {
+    int B;                  /* requests, at most 16384 */
+    int W;                  /* entries of a table row: the most pages a request can hold */
+    int32_t *table;         /* [B, W], updated */
+    int64_t table_row_stride; /* 0 = W */
+    int32_t *held;          /* [B]: pages request b holds, updated */
+    int32_t *free_pages;    /* [n_pages] a stack: the first *n_free entries are the free pages, updated */
+    int32_t *n_free;        /* [1], updated */
+    int n_pages;
+    int page_size;
+    const int32_t *new_len; /* [B]: rows request b is to have room for (0 gives all its pages back) */
+    const int32_t *start;   /* [B] first row whose slot is asked for (used with T > 0) */
+    int T;                  /* rows a request whose slots are asked for, or 0 */
+    int32_t *slots;         /* [B, T] out: cache row of row start[b] + i, or -1 at or beyond new_len[b] */
+    int32_t *err;           /* device int32, or NULL: 0, else 1 + the first request that was refused */
+} kdt_page_args;
+
+/*
+ * kdt_page_assign -- every request to ceil(new_len / page_size) pages, and where its rows go.
+ * As if every surplus page were first put on the stack (requests in order, a request's pages in
+ * table order, the first one given ending uppermost) and then every missing page taken off it in
+ * the same order: a call that grows lengths and one that shrinks them back leave all state as it
+ * was. Entries of `table` behind a request's pages and of `free_pages` at or beyond *n_free keep
+ * what they held.
+ * A request that asks for more than W pages, has a negative length or a `held` outside [0, W], or
+ * comes when the pages free (those given back by all requests in this call included) no longer
+ * cover what it and the requests before it miss, is refused: it keeps what it has, its slots are
+ * -1, and `err` names the first such.
+ * Slots feed kdt_latent_write_paged; a call for decoding has start = the lengths before and T = 1.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE (sizes, page size, alignment, B*W or B*T > 2^31 - 1),
+ * KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_page_assign(const kdt_page_args *a, cudaStream_t stream);
+
+/* Arguments of kdt_latent_write_paged. */
+typedef struct {
+    int rows;               /* new rows, of all sequences */
+    int D_c, D_r;           /* must be 512 and 64 */
+    kdt_dtype dtype;        /* element type of c, k and gamma */
+    const void *c;          /* latent of row n: the 512 elements at c + n * c_row_stride */
+    int64_t c_row_stride;   /* elements, 0 = 512; else >= 512 and a multiple of 16 bytes */
+    const void *k;          /* its rope key, not yet rotated: 64 elements at k + n * k_row_stride */
+    int64_t k_row_stride;   /* elements, 0 = 64; else >= 64 */
+    const void *gamma;      /* [512] weight of the latent's RMS norm, or NULL: no norm */
+    float eps;              /* the norm's epsilon, >= 0 (used with gamma) */
+    const int32_t *pos;     /* device [rows] rotary positions, or NULL: k is written as it is */
+    double base;            /* angle base (theta), > 0 (used with pos) */
+    const int32_t *slots;   /* device [rows]: cache row of row n; one outside [0, n_slots) is not written */
+    void *c_kv;             /* bf16 [n_slots, 512] */
+    void *k_pe;             /* bf16 [n_slots, 64] */
+    int n_slots;            /* n_pages * page_size */
+} kdt_latent_write_paged_args;
+
+/*
+ * kdt_latent_write_paged -- norm, rotate and store new rows at their slots in one pass: the norm
+ * and rotation of kdt_latent_write_q8 in float32, each value rounded once to bf16. Slots of
+ * different rows must differ (of two rows with one slot, either or a mixture of both is kept).
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE (sizes, strides, alignment), KDT_ERR_UNSUPPORTED
+ * (D_c, D_r, dtype), KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_latent_write_paged(const kdt_latent_write_paged_args *a, cudaStream_t stream);
+
+/*
+ * kdt_kv_compact_paged -- kdt_kv_compact for a paged cache: the k-th node of the accepted path
+ * moves from row prefix_len[b] + acc_nodes[b,k] of its sequence to row prefix_len[b] + k; the same
+ * rules, with W * page_size in the place of L. Rows whose page is outside [0, n_pages) are not
+ * copied. dtype, D_c and D_r as for kdt_kv_compact.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE, KDT_ERR_UNSUPPORTED, KDT_ERR_NOT_DEVICE, KDT_ERR_CUDA.
+ */
+kdt_status kdt_kv_compact_paged(void *c_kv, void *k_pe, kdt_dtype dtype, int D_c, int D_r, int n_pages, int page_size,
+                                const int32_t *table, int W, int64_t table_row_stride, int B, int T, int32_t *prefix_len,
+                                const int32_t *acc_nodes, const int32_t *n_acc, int update_prefix, cudaStream_t stream);
+
+/* Arguments of kdt_verify_attn_paged. Sizes as for kdt_verify_attn, B*T*H below 2^31. */
+typedef struct {
+    int B, T, H;
+    int D_c, D_r;           /* must be 512 and 64 */
+    const void *q_nope;     /* bf16 [B,T,H,512] absorbed query */
+    int64_t q_nope_row_stride; /* elements between (b,i,h) rows; 0 = 512, else >= 512 and a multiple of 8 */
+    const void *q_pe;       /* bf16 [B,T,H,64] rotated rope query */
+    int64_t q_pe_row_stride;   /* 0 = 64, else >= 64 and a multiple of 8 */
+    const void *c_kv;       /* the cache */
+    const void *k_pe;
+    int n_pages, page_size;
+    const int32_t *table;   /* device [B, table_width] */
+    int table_width;
+    int64_t table_row_stride; /* 0 = table_width */
+    const int32_t *prefix_len; /* device [B]; tree node t at row prefix_len[b] + t */
+    const int32_t *n_rows;  /* device [B]: sequence b has tree nodes i < n_rows[b] only (a padded batch; 0: it is
+                               not there), or NULL: T. Rows of out and lse behind them are left as they were. */
+    int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T, <= table_width * page_size */
+    const int32_t *parent;  /* device [B,T] parent array, or NULL */
+    const uint32_t *vis;    /* device [B,T,ceil(T/32)] packed visibility bits, or NULL. With T = 1 both may be
+                               NULL: the row sees its prefix and itself */
+    float scale;
+    void *out;              /* [B,T,H,512] of out_dtype */
+    kdt_dtype out_dtype;    /* KDT_F32 or KDT_BF16 */
+    float *lse;             /* device fp32 [B,T,H], or NULL */
+    int32_t *err;           /* device int32 error word, or NULL: 0, or 1 + the index b*T + i of the first malformed
+                               parent entry, or 1 + B*T + b for a sequence b one of whose pages is outside
+                               [0, n_pages) (the lowest of these), or a negative code if an internal wait gave up */
+    int num_splits;         /* 0 = automatic; else the shares that the work is cut into (at most one for each
+                               block of keys, and one an SM) */
+} kdt_verify_paged_args;
+
+/*
+ * kdt_verify_attn_paged -- kdt_verify_attn over a paged latent cache: the same scores, mask,
+ * softmax, latent output and log-sum-exp, key j of sequence b read from the page the table names.
+ * T = 1 is plain decoding: one new token a sequence, whose row has been written before the call.
+ * Products run on the tensor cores in bf16 with float32 sums; scores, softmax statistics and the
+ * output's sums are float32, the weights are rounded to bf16 for the second product, and the output
+ * once to out_dtype. The work is split over the keys and joined by log-sum-exp.
+ * A row that sees no key gets out = 0 and lse = -inf. A row that sees a key whose score is NaN or
+ * +inf gets NaN (a score of -inf has weight 0), and infinite or NaN latents reach the rows that see
+ * them; a row from which such a key is hidden is not affected by it. Cache rows at or beyond
+ * prefix_len[b] + n_rows[b] never affect the result, and their pages are never looked up. Rows of a
+ * page outside [0, n_pages) read as zeros. prefix_len values are device data: the caller guarantees
+ * 0 <= prefix_len[b] <= max_kv_len - n_rows[b]; others are brought into that range.
+ * `workspace` must hold kdt_verify_attn_paged_workspace_size(a) bytes (256-byte aligned); its
+ * contents need no initialisation. Calls that may run at the same time, captured ones included,
+ * need workspaces of their own.
+ * Errors: those of kdt_verify_attn, for the same reasons.
+ */
+kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of workspace kdt_verify_attn_paged needs for these arguments (host-side fields only);
+ * 0 for arguments it would reject. */
+size_t kdt_verify_attn_paged_workspace_size(const kdt_verify_paged_args *a);
+
+/* What kdt_verify_attn_paged will launch for these arguments. */
+kdt_status kdt_verify_attn_paged_plan(const kdt_verify_paged_args *a, kdt_plan *plan);
+
+/* ------------------------------------------------------------------------------
  * Sampled acceptance, beside the greedy kdt_tree_accept.
  * ------------------------------------------------------------------------------ */
 
@@ -585,6 +730,45 @@ kdt_status kdt_tree_sample(const int32_t *parent, const int32_t *tok, const void
                            int V, int64_t row_stride, double temperature, const float *u_node, const float *u_bonus,
                            int32_t *acc_nodes, int32_t *n_acc, int32_t *bonus, float *logp, int32_t *err,
                            cudaStream_t stream);
+
+/* Arguments of kdt_sample. A setting is one number for all rows, or an array of one a row. */
+typedef struct {
+    int R, V;               /* rows, vocabulary (at most 524288) */
+    const void *logits;     /* device, row r at logits + r * row_stride elements, V of them used */
+    kdt_dtype dtype;
+    int64_t row_stride;     /* 0 = V */
+    const float *u;         /* device [R]: numbers in [0, 1) */
+    const float *temperature; /* device [R], or NULL: temperature_all. In [1e-3, 1e3], or 0: greedy */
+    double temperature_all;
+    const int32_t *top_k;   /* device [R], or NULL: top_k_all. <= 0 or > V: all tokens */
+    int top_k_all;
+    const float *top_p;     /* device [R], or NULL: top_p_all. >= 1: all of them */
+    double top_p_all;
+    const float *min_p;     /* device [R], or NULL: min_p_all. <= 0: all of them; above 1 counts as 1 */
+    double min_p_all;
+    int32_t *token;         /* device [R] out */
+    float *logp;            /* device [R] out, or NULL: natural log of the token's probability at this
+                               temperature, before the filters (0 for a greedy row) */
+    int32_t *err;           /* device int32, or NULL: 0, else 1 + the first row that has no token */
+} kdt_sample_args;
+
+/*
+ * kdt_sample -- one token a row from given random numbers, under temperature, top-k, top-p and
+ * min-p: the first token behind a prompt, a drafter's own tokens, plain decoding.
+ * With l the row's logits: w_j = e^{(l_j - max l) / temperature}, held to 2^-44 of the largest. In
+ * the order of falling logits (equal ones in index order) the row keeps
+ *   the first top_k tokens; of those the least number whose weights reach top_p times the sum of
+ *   the top_k's (at least one); and of those the ones with w >= min_p.
+ * The token is the least j such that the kept weights up to and including j, in index order, sum
+ * to more than u times the sum of all kept weights. temperature 0 gives the first token of the
+ * largest logit. Sums are in fixed point: the result does not depend on how the work is split.
+ * -inf is a token that cannot be drawn. A row whose logits have a NaN, a +inf or nothing but
+ * -inf, or whose settings are not numbers in their ranges, gets token -1 and logp 0.
+ * logp is off by at most 1e-6 + 2^-23 of its size.
+ * Errors: KDT_ERR_NULL_ARG, KDT_ERR_BAD_SHAPE, KDT_ERR_UNSUPPORTED (dtype), KDT_ERR_NOT_DEVICE,
+ * KDT_ERR_CUDA.
+ */
+kdt_status kdt_sample(const kdt_sample_args *a, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -157,6 +157,31 @@ constexpr int kQ8Rows = 64;    // query rows of a tile
 constexpr int kQ8Keys = 128;   // keys of a block
 cudaError_t launch_verify_q8_rows(const Q8Params &p, cudaStream_t s);
 
+// K6: tree-verify attention over a paged bf16 latent cache (kdt_verify_attn_paged), everything
+// validated on the host.
+struct PagedParams {
+    int B, T, H, W;            // W = ceil(T/32) visibility words per query
+    int rows_seq;              // T * H
+    int max_kv;                // the caller's bound on prefix_len[b] + T
+    const __nv_bfloat16 *q_nope, *q_pe;
+    int64_t q_nope_stride, q_pe_stride;
+    const __nv_bfloat16 *c_kv, *k_pe;
+    int n_pages, shift;        // pages of 2^shift rows
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *prefix_len, *n_rows;
+    const uint32_t *vis;       // [B,T,W], NULL with T = 1: the one row sees everything
+    float scale_log2;          // scale * log2(e)
+    void *out;                 // bf16 or float32
+    bool out_bf16;
+    float *lse;
+    int32_t *err;
+};
+cudaError_t launch_verify_paged(const PagedParams &p, cudaStream_t s);
+
+// log2 of a page size that the paged cache takes (8 .. 1024 rows), or -1.
+int page_shift(int page_size);
+
 // Per-device SM count (cached).
 int sm_count();
 

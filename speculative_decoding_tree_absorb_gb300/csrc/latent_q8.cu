@@ -13,21 +13,16 @@
 // 67%). Short calls take the 7-9 us of one launch and one row's chain of loads.
 #include <cmath>
 
-#include "kdt_internal.cuh"
+#include "latent_rows.cuh"
 #include "q8.cuh"
 
 namespace kdt {
 namespace {
 
+using namespace rows;
+
 constexpr int kWarps = 8;                           // warps a CTA
 constexpr int kWriters = 4, kReaders = 5;           // CTAs an SM when there are rows enough
-constexpr int kHalf = kDr / 2;
-
-// Frequencies of the rotation in turns: pos * w_j / 2 pi as a fixed-point fraction of a turn
-// with 64 fractional bits, so pos * f wraps to the exact angle modulo a full turn.
-struct TurnFreqs {
-    uint64_t f[kHalf];
-};
 
 struct WriteParams {
     const void *c, *k, *gamma;
@@ -38,53 +33,6 @@ struct WriteParams {
     int64_t L;
     int B, T;
     float eps;
-};
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <bool kOnce, typename V> __device__ __forceinline__ V once(const V *p) {
-    return kOnce ? __ldcs(p) : __ldg(p);
-}
-
-// A lane's 16 latent elements of a row, as kPieces pieces of kPer consecutive ones: piece q
-// starts at element q * 32 * kPer + lane * kPer, so every warp load is contiguous.
-template <typename E> struct Row;
-template <> struct Row<float> {
-    static constexpr int kPer = 4, kPieces = 4;
-    float4 v[4];
-    template <bool kOnce> __device__ __forceinline__ void load(const float *p, int lane) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = once<kOnce>(reinterpret_cast<const float4 *>(p) + 32 * q + lane);
-    }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            x[4 * q] = v[q].x;
-            x[4 * q + 1] = v[q].y;
-            x[4 * q + 2] = v[q].z;
-            x[4 * q + 3] = v[q].w;
-        }
-    }
-};
-template <> struct Row<__nv_bfloat16> {
-    static constexpr int kPer = 8, kPieces = 2;
-    uint4 v[2];
-    template <bool kOnce> __device__ __forceinline__ void load(const __nv_bfloat16 *p, int lane) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) v[q] = once<kOnce>(reinterpret_cast<const uint4 *>(p) + 32 * q + lane);
-    }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                x[8 * q + 2 * t] = __uint_as_float(w[t] << 16);
-                x[8 * q + 2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
-            }
-        }
-    }
 };
 
 // One warp a row. y = x r gamma in float32 (r from the row's sum of squares by shuffles); a
@@ -111,20 +59,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWriters) latent_write_kernel(con
         const int64_t dst = (int64_t)b * p.L + row;
         float y[16];
         c.get(y);
-        if (p.gamma) {
-            R gr;                                     // from L1 for each row: 16 registers less
-            gr.template load<false>(static_cast<const E *>(p.gamma), lane);
-            float ss = 0.f;
-#pragma unroll
-            for (int t = 0; t < 16; ++t) ss = fmaf(y[t], y[t], ss);
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float r = __frsqrt_rn(fmaf(ss, 1.f / kDc, p.eps));
-            float g[16];
-            gr.get(g);
-#pragma unroll
-            for (int t = 0; t < 16; ++t) y[t] = y[t] * r * g[t];
-        }
+        if (p.gamma) rms_norm(y, static_cast<const E *>(p.gamma), p.eps, lane);
         uint8_t *codes = p.c_q8 + dst * kDc;
         uint8_t *scales = p.c_scale + dst * (kDc / KDT_Q8_GROUP);
 #pragma unroll
@@ -150,15 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWriters) latent_write_kernel(con
             if (lane % kLanes == 0) scales[q * (32 / kLanes) + lane / kLanes] = (uint8_t)byte;
         }
         float k0 = to_f32(ka), k1 = to_f32(kb);
-        if (p.pos) {
-            // the angle in turns, exact modulo 1, rounded to 32 bits: within [-1/2, 1/2)
-            const int32_t turn = (int32_t)(((uint64_t)(int64_t)pos * freq + 0x80000000ull) >> 32);
-            float s, c;
-            sincospif((float)turn * 4.656612873077393e-10f, &s, &c);     // 2^-31: half turns
-            const float r0 = __fsub_rn(__fmul_rn(k0, c), __fmul_rn(k1, s));
-            k1 = __fadd_rn(__fmul_rn(k1, c), __fmul_rn(k0, s));
-            k0 = r0;
-        }
+        if (p.pos) rotate(k0, k1, pos, freq);
         __nv_bfloat16 *kd = p.k_pe + dst * kDr;
         kd[lane] = __float2bfloat16_rn(k0);
         kd[lane + kHalf] = __float2bfloat16_rn(k1);
@@ -293,13 +220,7 @@ kdt_status kdt_latent_write_q8(const kdt_latent_write_args *a, cudaStream_t stre
     const kdt_status st = check_on_current_device(
         {a->c, a->k, a->gamma, a->pos, a->prefix_len, a->n_rows, a->c_q8, a->c_scale, a->k_pe});
     if (st != KDT_OK) return st;
-    TurnFreqs fr = {};
-    if (a->pos)
-        for (int j = 0; j < kHalf; ++j) {
-            // base^(-2j/64) radians a position, as a fraction of a turn (whole turns drop out)
-            const double t = pow(a->base, -(double)j / kHalf) * 0.15915494309189533577;
-            fr.f[j] = (uint64_t)((t - floor(t)) * 18446744073709551616.0);
-        }
+    const TurnFreqs fr = a->pos ? turn_freqs(a->base) : TurnFreqs{};
     const WriteParams p = {a->c,    a->k,       a->gamma, cs, ks, a->pos, a->prefix_len, a->n_rows,
                            a->c_q8, a->c_scale, static_cast<__nv_bfloat16 *>(a->k_pe), a->kv_row_stride,
                            a->B,    a->T,       a->eps};

@@ -138,17 +138,32 @@ constexpr int kCompactThreads = 256, kCompactHold = 8, kCompactCluster = 8, kCom
 constexpr int kCompactChunk = kCompactThreads * kCompactHold;      // vectors
 constexpr int kCompactMostBytes = 40 * 1024;                        // of a row's two arrays
 
+// Where a sequence's rows lie: in the dense block (table NULL), or in pages of 2^shift rows named by its row of the
+// table. L bounds a sequence's rows in both.
+struct Pages {
+    const int32_t *table = nullptr;
+    int64_t stride = 0;
+    int shift = 0, n_pages = 0;
+};
+
+template <bool kPaged>
 __global__ void __launch_bounds__(kCompactThreads, kCompactCtas)
     kv_compact_kernel(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec, int r_vec, int s_vec, int64_t L,
-                      int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int T, int S, int update_prefix) {
+                      int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc, int T, int S, int update_prefix,
+                      const Pages pages) {
     const int b = blockIdx.x / S, part = blockIdx.x % S, tid = threadIdx.x;
     const int64_t p0 = prefix_len[b];
     const int n = min(max(n_acc[b], 0), T);
     const int row_vec = c_vec + r_vec + s_vec, per = ((row_vec + S - 1) / S + 1) / 2 * 2;   // whole sectors
     const int e0 = min(part * per, row_vec), cols = min(per, row_vec - e0);
     const int chunk = cols > 0 ? kCompactChunk / cols : 0;              // rows at a time
-    auto vector_of = [&](int64_t node, int e) -> uint4 * {              // of tree node's cache row
-        const int64_t r = (int64_t)b * L + p0 + node;
+    // tree node's cache row, -1 when it has none
+    auto row_of = [&](int64_t node) -> int64_t {
+        if (!kPaged) return (int64_t)b * L + p0 + node;
+        const int32_t page = pages.table[b * pages.stride + ((p0 + node) >> pages.shift)];
+        return page < 0 || page >= pages.n_pages ? -1 : ((int64_t)page << pages.shift) + ((p0 + node) & ((1 << pages.shift) - 1));
+    };
+    auto vector_of = [&](int64_t r, int e) -> uint4 * {
         if (e < c_vec) return c_kv + r * c_vec + e;
         return e < c_vec + r_vec ? k_pe + r * r_vec + (e - c_vec) : c_scale + r;
     };
@@ -166,8 +181,12 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas)
         for (int u = 0; u < kCompactHold; ++u) {
             if (u * kCompactThreads >= total) break;
             const int i = tid + u * kCompactThreads, t = i / cols;
-            const bool moves = i < total && src[u] > k0 + t && src[u] < T && p0 + src[u] < L && p0 >= 0;
-            if (moves) v[u] = *vector_of(src[u], e0 + i - t * cols);
+            bool moves = i < total && src[u] > k0 + t && src[u] < T && p0 + src[u] < L && p0 >= 0;
+            if (moves) {
+                const int64_t from = row_of(src[u]);
+                if (kPaged) moves = from >= 0 && row_of(k0 + t) >= 0;
+                if (moves) v[u] = *vector_of(from, e0 + i - t * cols);
+            }
             live |= (moves ? 1u : 0u) << u;
         }
         __syncthreads();
@@ -175,7 +194,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas)
         for (int u = 0; u < kCompactHold; ++u) {
             if (u * kCompactThreads >= total) break;
             const int i = tid + u * kCompactThreads, t = i / cols;
-            if ((live >> u) & 1u) *vector_of(k0 + t, e0 + i - t * cols) = v[u];
+            if ((live >> u) & 1u) *vector_of(row_of(k0 + t), e0 + i - t * cols) = v[u];
         }
         __syncthreads();
     }
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas)
 
 kdt_status launch_kv_compact(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec, int r_vec, int s_vec, int B, int T,
                              int64_t L, int32_t *prefix_len, const int32_t *acc_nodes, const int32_t *n_acc,
-                             int update_prefix, cudaStream_t stream) {
+                             int update_prefix, cudaStream_t stream, const Pages &pages = Pages()) {
     // CTAs a sequence: enough for the longest path in one chunk, by pairs of columns, as long as the device
     // holds the batch's at once (and two for the widest rows: kCompactChunk vectors are less than one)
     const int row_vec = c_vec + r_vec + s_vec;
@@ -205,8 +224,9 @@ kdt_status launch_kv_compact(uint4 *c_kv, uint4 *k_pe, uint4 *c_scale, int c_vec
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kv_compact_kernel, c_kv, k_pe, c_scale, c_vec, r_vec, s_vec, L, prefix_len,
-                              acc_nodes, n_acc, T, S, update_prefix ? 1 : 0) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, pages.table ? kv_compact_kernel<true> : kv_compact_kernel<false>, c_kv, k_pe, c_scale, c_vec,
+                              r_vec, s_vec, L, prefix_len, acc_nodes, n_acc, T, S, update_prefix ? 1 : 0,
+                              pages) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ best-first builder --
@@ -536,6 +556,35 @@ kdt_status kdt_kv_compact_q8(uint8_t *c_q8, uint8_t *c_scale, void *k_pe, int B,
     return launch_kv_compact(reinterpret_cast<uint4 *>(c_q8), static_cast<uint4 *>(k_pe),
                              reinterpret_cast<uint4 *>(c_scale), kDc / 16, kDr * 2 / 16, 1, B, T, kv_row_stride,
                              prefix_len, acc_nodes, n_acc, update_prefix, stream);
+}
+
+kdt_status kdt_kv_compact_paged(void *c_kv, void *k_pe, kdt_dtype dtype, int D_c, int D_r, int n_pages, int page_size,
+                                const int32_t *table, int W, int64_t table_row_stride, int B, int T, int32_t *prefix_len,
+                                const int32_t *acc_nodes, const int32_t *n_acc, int update_prefix, cudaStream_t stream) {
+    const int shift = page_shift(page_size);
+    const int64_t stride = table_row_stride ? table_row_stride : W;
+    if (B < 0 || T < 1 || T > kMaxT || D_c < 1 || D_r < 1 || n_pages < 1 || W < 1 || stride < W || shift < 0 ||
+        (int64_t)n_pages << shift > INT32_MAX || (int64_t)W << shift < T)
+        return KDT_ERR_BAD_SHAPE;
+    if (dtype != KDT_F32 && dtype != KDT_BF16) return KDT_ERR_UNSUPPORTED;
+    const int esz = dtype == KDT_F32 ? 4 : 2;
+    if (((int64_t)D_c * esz) % 16 || ((int64_t)D_r * esz) % 16) return KDT_ERR_BAD_SHAPE;
+    if (((int64_t)D_c * esz + (int64_t)D_r * esz) > kCompactMostBytes) return KDT_ERR_BAD_SHAPE;
+    if (B == 0) return KDT_OK;
+    if (!c_kv || !k_pe || !table || !prefix_len || !acc_nodes || !n_acc) return KDT_ERR_NULL_ARG;
+    if (!aligned16(c_kv) || !aligned16(k_pe)) return KDT_ERR_BAD_SHAPE;
+    for (const void *p : {(const void *)table, (const void *)prefix_len, (const void *)acc_nodes, (const void *)n_acc})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KDT_ERR_BAD_SHAPE;
+    const kdt_status st = check_on_current_device({c_kv, k_pe, table, prefix_len, acc_nodes, n_acc});
+    if (st != KDT_OK) return st;
+    Pages pages;
+    pages.table = table;
+    pages.stride = stride;
+    pages.shift = shift;
+    pages.n_pages = n_pages;
+    return launch_kv_compact(static_cast<uint4 *>(c_kv), static_cast<uint4 *>(k_pe), nullptr, D_c * esz / 16,
+                             D_r * esz / 16, 0, B, T, (int64_t)W << shift, prefix_len, acc_nodes, n_acc, update_prefix,
+                             stream, pages);
 }
 
 }  // extern "C"

@@ -1,0 +1,139 @@
+// C ABI of the attention over a paged latent cache: argument checks, plan and launches. See
+// include/kdt.h for the contract.
+#include <math.h>
+
+#include "kdt_internal.cuh"
+
+namespace kdt {
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct PagedPlan {
+    int ctas = 0, launches = 0, splits = 0;
+    bool vis = false;                      // the visibility kernel finds the words first
+    size_t vis_off = 0, ws_bytes = 0;
+};
+
+kdt_status check_args(const kdt_verify_paged_args *a) {
+    if (!a) return KDT_ERR_NULL_ARG;
+    if (a->B < 0 || a->B > 65535 || a->T < 1 || a->T > kMaxT || a->H < 1 || a->H > 1024) return KDT_ERR_BAD_SHAPE;
+    if (a->D_c != kDc || a->D_r != kDr) return KDT_ERR_UNSUPPORTED;
+    if (a->out_dtype != KDT_F32 && a->out_dtype != KDT_BF16) return KDT_ERR_UNSUPPORTED;
+    const int shift = page_shift(a->page_size);
+    if (a->num_splits < 0 || shift < 0 || a->n_pages < 1 || (int64_t)a->n_pages << shift > kMaxKv || a->table_width < 1)
+        return KDT_ERR_BAD_SHAPE;
+    if (a->table_row_stride && a->table_row_stride < a->table_width) return KDT_ERR_BAD_SHAPE;
+    if (a->max_kv_len < a->T || a->max_kv_len > kMaxKv || (int64_t)a->max_kv_len > (int64_t)a->table_width << shift)
+        return KDT_ERR_BAD_SHAPE;
+    if ((int64_t)a->B * a->T * a->H > INT32_MAX) return KDT_ERR_BAD_SHAPE;
+    if ((a->q_nope_row_stride && (a->q_nope_row_stride < kDc || a->q_nope_row_stride % 8)) ||
+        (a->q_pe_row_stride && (a->q_pe_row_stride < kDr || a->q_pe_row_stride % 8)))
+        return KDT_ERR_BAD_SHAPE;
+    if (!(a->scale == a->scale) || isinf(a->scale)) return KDT_ERR_BAD_SHAPE;
+    if (a->B == 0) return KDT_OK;
+    if (!a->q_nope || !a->q_pe || !a->c_kv || !a->k_pe || !a->table || !a->prefix_len || !a->out) return KDT_ERR_NULL_ARG;
+    if (a->parent && a->vis) return KDT_ERR_NULL_ARG;
+    if (!a->parent && !a->vis && a->T > 1) return KDT_ERR_NULL_ARG;
+    for (const void *p : {a->q_nope, a->q_pe, a->c_kv, a->k_pe, (const void *)a->out})
+        if (!aligned(p, 16)) return KDT_ERR_BAD_SHAPE;
+    for (const void *p : {(const void *)a->table, (const void *)a->prefix_len, (const void *)a->n_rows, (const void *)a->parent,
+                          (const void *)a->vis, (const void *)a->lse, (const void *)a->err})
+        if (!aligned(p, 4)) return KDT_ERR_BAD_SHAPE;
+    return KDT_OK;
+}
+
+// Pure function of host-side fields.
+kdt_status make_plan(const kdt_verify_paged_args *a, PagedPlan *out) {
+    const kdt_status st = check_args(a);
+    if (st != KDT_OK) return st;
+    PagedPlan p;
+    if (a->B == 0) {
+        *out = p;
+        return KDT_OK;
+    }
+    p.ctas = a->B * a->T * a->H;
+    p.splits = 1;
+    size_t off = 0;
+    p.vis = a->parent != nullptr;
+    if (p.vis) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
+    p.ws_bytes = off;
+    p.launches = (p.vis ? 1 : 0) + 1;
+    *out = p;
+    return KDT_OK;
+}
+
+}  // namespace
+}  // namespace kdt
+
+using namespace kdt;
+
+extern "C" {
+
+size_t kdt_verify_attn_paged_workspace_size(const kdt_verify_paged_args *a) {
+    PagedPlan p;
+    return make_plan(a, &p) == KDT_OK ? p.ws_bytes : 0;
+}
+
+kdt_status kdt_verify_attn_paged_plan(const kdt_verify_paged_args *a, kdt_plan *out) {
+    if (!out) return KDT_ERR_NULL_ARG;
+    PagedPlan p;
+    const kdt_status st = make_plan(a, &p);
+    if (st != KDT_OK) return st;
+    out->impl = KDT_IMPL_TCGEN05;
+    out->num_splits = p.splits;
+    out->num_launches = p.launches;
+    out->ctas = p.ctas;
+    out->workspace_bytes = p.ws_bytes;
+    return KDT_OK;
+}
+
+kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    PagedPlan p;
+    kdt_status st = make_plan(a, &p);
+    if (st != KDT_OK) return st;
+    if (a->B == 0) return KDT_OK;
+    if (p.ws_bytes > 0 && (!workspace || ws_bytes < p.ws_bytes || !aligned(workspace, kAlign))) return KDT_ERR_WORKSPACE;
+    if ((st = check_on_current_device({a->q_nope, a->q_pe, a->c_kv, a->k_pe, a->table, a->prefix_len, a->n_rows, a->parent,
+                                       a->vis, a->out, a->lse, a->err, p.ws_bytes ? workspace : nullptr})) != KDT_OK)
+        return st;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    const uint32_t *vis = a->vis;
+    if (p.vis) {
+        uint32_t *bits = reinterpret_cast<uint32_t *>(ws + p.vis_off);
+        if (launch_build_visibility(a->parent, a->B, a->T, bits, a->err, stream) != cudaSuccess) return KDT_ERR_CUDA;
+        vis = bits;
+    } else if (a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t), stream) != cudaSuccess) {
+        return KDT_ERR_CUDA;
+    }
+    PagedParams q = {};
+    q.B = a->B;
+    q.T = a->T;
+    q.H = a->H;
+    q.W = (a->T + 31) / 32;
+    q.rows_seq = a->T * a->H;
+    q.max_kv = a->max_kv_len;
+    q.q_nope = static_cast<const __nv_bfloat16 *>(a->q_nope);
+    q.q_pe = static_cast<const __nv_bfloat16 *>(a->q_pe);
+    q.q_nope_stride = a->q_nope_row_stride ? a->q_nope_row_stride : kDc;
+    q.q_pe_stride = a->q_pe_row_stride ? a->q_pe_row_stride : kDr;
+    q.c_kv = static_cast<const __nv_bfloat16 *>(a->c_kv);
+    q.k_pe = static_cast<const __nv_bfloat16 *>(a->k_pe);
+    q.n_pages = a->n_pages;
+    q.shift = page_shift(a->page_size);
+    q.table = a->table;
+    q.table_stride = a->table_row_stride ? a->table_row_stride : a->table_width;
+    q.prefix_len = a->prefix_len;
+    q.n_rows = a->n_rows;
+    q.vis = vis;
+    q.scale_log2 = a->scale * 1.4426950408889634f;
+    q.out = a->out;
+    q.out_bf16 = a->out_dtype == KDT_BF16;
+    q.lse = a->lse;
+    q.err = a->err;
+    return launch_verify_paged(q, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+}
+
+}  // extern "C"

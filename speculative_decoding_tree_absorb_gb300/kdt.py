@@ -31,7 +31,9 @@ EXPORTS = ("kdt_status_str", "kdt_version", "kdt_build_visibility", "kdt_verify_
            "kdt_verify_attn_host", "kdt_verify_attn_host_buffer_size", "kdt_vc_up_proj",
            "kdt_test_verify_attn_wait_expiry", "kdt_latent_write_q8", "kdt_latent_read_q8", "kdt_kv_compact_q8",
            "kdt_verify_attn_q8", "kdt_verify_attn_q8_workspace_size", "kdt_verify_attn_q8_plan",
-           "kdt_tree_sample")
+           "kdt_tree_sample", "kdt_page_assign", "kdt_latent_write_paged", "kdt_kv_compact_paged",
+           "kdt_verify_attn_paged", "kdt_verify_attn_paged_workspace_size", "kdt_verify_attn_paged_plan",
+           "kdt_sample")
 
 
 class KdtError(RuntimeError):
@@ -94,6 +96,57 @@ class VerifyQ8Args(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("err", ctypes.c_void_p),
         ("impl", ctypes.c_int), ("num_splits", ctypes.c_int),
+    ]
+
+
+class PageArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("W", ctypes.c_int),
+        ("table", ctypes.c_void_p), ("table_row_stride", ctypes.c_int64),
+        ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("new_len", ctypes.c_void_p), ("start", ctypes.c_void_p), ("T", ctypes.c_int),
+        ("slots", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class LatentWritePagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int), ("D_c", ctypes.c_int), ("D_r", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("c", ctypes.c_void_p), ("c_row_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("k_row_stride", ctypes.c_int64),
+        ("gamma", ctypes.c_void_p), ("eps", ctypes.c_float),
+        ("pos", ctypes.c_void_p), ("base", ctypes.c_double),
+        ("slots", ctypes.c_void_p), ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p), ("n_slots", ctypes.c_int),
+    ]
+
+
+class VerifyPagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("D_c", ctypes.c_int), ("D_r", ctypes.c_int),
+        ("q_nope", ctypes.c_void_p), ("q_nope_row_stride", ctypes.c_int64),
+        ("q_pe", ctypes.c_void_p), ("q_pe_row_stride", ctypes.c_int64),
+        ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("table", ctypes.c_void_p), ("table_width", ctypes.c_int), ("table_row_stride", ctypes.c_int64),
+        ("prefix_len", ctypes.c_void_p), ("n_rows", ctypes.c_void_p), ("max_kv_len", ctypes.c_int),
+        ("parent", ctypes.c_void_p), ("vis", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("err", ctypes.c_void_p),
+        ("num_splits", ctypes.c_int),
+    ]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int), ("V", ctypes.c_int),
+        ("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("row_stride", ctypes.c_int64),
+        ("u", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p), ("temperature_all", ctypes.c_double),
+        ("top_k", ctypes.c_void_p), ("top_k_all", ctypes.c_int),
+        ("top_p", ctypes.c_void_p), ("top_p_all", ctypes.c_double),
+        ("min_p", ctypes.c_void_p), ("min_p_all", ctypes.c_double),
+        ("token", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("err", ctypes.c_void_p),
     ]
 
 
@@ -168,6 +221,22 @@ def lib():
         L.kdt_tree_sample.argtypes = [vp, vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64,
                                       ctypes.c_double, vp, vp, vp, vp, vp, vp, vp, vp]
         L.kdt_tree_sample.restype = ctypes.c_int
+        L.kdt_page_assign.argtypes = [ctypes.POINTER(PageArgs), vp]
+        L.kdt_page_assign.restype = ctypes.c_int
+        L.kdt_latent_write_paged.argtypes = [ctypes.POINTER(LatentWritePagedArgs), vp]
+        L.kdt_latent_write_paged.restype = ctypes.c_int
+        L.kdt_kv_compact_paged.argtypes = [vp, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
+                                           ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, vp,
+                                           ctypes.c_int, vp]
+        L.kdt_kv_compact_paged.restype = ctypes.c_int
+        L.kdt_verify_attn_paged.argtypes = [ctypes.POINTER(VerifyPagedArgs), vp, ctypes.c_size_t, vp]
+        L.kdt_verify_attn_paged.restype = ctypes.c_int
+        L.kdt_verify_attn_paged_workspace_size.argtypes = [ctypes.POINTER(VerifyPagedArgs)]
+        L.kdt_verify_attn_paged_workspace_size.restype = ctypes.c_size_t
+        L.kdt_verify_attn_paged_plan.argtypes = [ctypes.POINTER(VerifyPagedArgs), ctypes.POINTER(Plan)]
+        L.kdt_verify_attn_paged_plan.restype = ctypes.c_int
+        L.kdt_sample.argtypes = [ctypes.POINTER(SampleArgs), vp]
+        L.kdt_sample.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -629,3 +698,189 @@ def tree_sample(parent, tok, logits, u_node, u_bonus, *, temperature=1.0, err=No
                                  float(temperature), _ptr(u_node), _ptr(u_bonus), _ptr(acc), _ptr(n), _ptr(bonus),
                                  _ptr(logp), _err_of(err), _stream_ptr(stream)), "kdt_tree_sample")
     return acc, n, bonus, logp
+
+
+def _check_paged_cache(c_kv, k_pe):
+    """The two arrays of a paged cache: [n_pages, page, 512] and [n_pages, page, 64] bf16, contiguous.
+    Returns (n_pages, page)."""
+    import torch
+    n, page, D = c_kv.shape
+    if D != 512 or k_pe.shape != (n, page, 64) or c_kv.dtype != torch.bfloat16 or k_pe.dtype != torch.bfloat16:
+        raise ValueError("a paged cache is c_kv [n_pages,page,512] and k_pe [n_pages,page,64], both bf16")
+    if not (c_kv.is_contiguous() and k_pe.is_contiguous()):
+        raise ValueError("the arrays of a paged cache must be contiguous")
+    return n, page
+
+
+def _check_table(table, B):
+    """A page table int32 [B,W], its rows contiguous, at equal distances and not overlapping. Returns (W, row stride)."""
+    import torch
+    W = table.shape[1]
+    stride = table.stride(0) if B > 1 else W
+    if table.shape[0] != B or table.dtype != torch.int32 or (W > 1 and table.stride(1) != 1) or stride < W:
+        raise ValueError("table must be an int32 [B,W] tensor whose rows are contiguous and do not overlap")
+    return W, stride
+
+
+def page_assign(table, held, free_pages, n_free, new_len, page_size, *, start=None, T=0, slots=None, err=None,
+                stream=None):
+    """Pages for requests' new lengths, and the slots of their rows (kdt_page_assign).
+
+    ``table`` int32 [B,W], ``held`` int32 [B], ``free_pages`` int32 [n_pages] (a stack) and ``n_free``
+    int32 [1] are updated in place; ``new_len`` int32 [B] is what each request is to have room for. With
+    ``T`` > 0, returns int32 [B,T]: the cache row of row start[b] + i, -1 at or beyond new_len[b]; else None.
+    """
+    import torch
+    B = table.shape[0]
+    W, stride = _check_table(table, B)
+    _int32_of(held, B, "held"), _int32_of(new_len, B, "new_len"), _int32_of(n_free, 1, "n_free")
+    _int32_of(free_pages, free_pages.numel(), "free_pages"), _int32_of(start, B, "start")
+    T = int(T)
+    if T > 0:
+        if start is None:
+            raise ValueError("start is needed for slots")
+        if slots is None:
+            slots = _empty((B, T), torch.int32, table.device, stream)
+        _int32_of(slots, B * T, "slots")
+    else:
+        slots = None
+    a = PageArgs(B, W, table.data_ptr(), stride, held.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+                 free_pages.numel(), int(page_size), new_len.data_ptr(), _ptr(start), T, _ptr(slots), _err_of(err))
+    _check(lib().kdt_page_assign(ctypes.byref(a), _stream_ptr(stream)), "kdt_page_assign")
+    return slots
+
+
+def latent_write_paged(c, k, c_kv, k_pe, slots, *, gamma=None, eps=1e-6, pos=None, base=10000.0, stream=None):
+    """Norm, rotate and store new rows of a paged cache at their slots (kdt_latent_write_paged).
+
+    ``c`` [B,T,512] and ``k`` [B,T,64] (float32 or bf16) may be slices of one combined [B,T,576] buffer;
+    row (b,i) goes to cache row slots[b,i] (int32 [B,T], e.g. of page_assign; one outside the cache is not
+    written). ``gamma`` [512] is the RMS norm's weight (None: no norm), ``pos`` int32 [B,T] the rotary
+    positions (None: k as it is). The cache (bf16 [n_pages,page,512] and [n_pages,page,64]) is updated in place.
+    """
+    n, page = _check_paged_cache(c_kv, k_pe)
+    B, T = c.shape[:2]
+    if c.shape != (B, T, 512) or k.shape != (B, T, 64) or k.dtype != c.dtype:
+        raise ValueError("c must be [B,T,512] and k [B,T,64] of the same type")
+    if gamma is not None and (gamma.numel() != 512 or gamma.dtype != c.dtype or not gamma.is_contiguous()):
+        raise ValueError("gamma must be a contiguous [512] tensor of c's type")
+    if slots is None:
+        raise ValueError("slots is needed")
+    _int32_of(slots, B * T, "slots"), _int32_of(pos, B * T, "pos")
+    a = LatentWritePagedArgs(B * T, 512, 64, _dtype_code(c), c.data_ptr(), _row_stride3(c, "c"), k.data_ptr(),
+                             _row_stride3(k, "k"), _ptr(gamma), float(eps), _ptr(pos), float(base), slots.data_ptr(),
+                             c_kv.data_ptr(), k_pe.data_ptr(), n * page)
+    _check(lib().kdt_latent_write_paged(ctypes.byref(a), _stream_ptr(stream)), "kdt_latent_write_paged")
+
+
+def kv_compact_paged(c_kv, k_pe, table, prefix_len, acc_nodes, n_acc, update_prefix=True, stream=None):
+    """Move the accepted path's rows of a paged cache to prefix_len + k, in place (kdt_kv_compact_paged)."""
+    n, page = c_kv.shape[:2]
+    B, T = acc_nodes.shape
+    if k_pe.shape[:2] != (n, page) or k_pe.dtype != c_kv.dtype or not (c_kv.is_contiguous() and k_pe.is_contiguous()):
+        raise ValueError("the arrays of a paged cache must be contiguous [n_pages,page,.] tensors of one type")
+    W, stride = _check_table(table, B)
+    _int32_of(prefix_len, B, "prefix_len"), _int32_of(acc_nodes, B * T, "acc_nodes"), _int32_of(n_acc, B, "n_acc")
+    _check(lib().kdt_kv_compact_paged(_ptr(c_kv), _ptr(k_pe), _dtype_code(c_kv), c_kv.shape[2], k_pe.shape[2], n, page,
+                                      _ptr(table), W, stride, B, T, _ptr(prefix_len), _ptr(acc_nodes), _ptr(n_acc),
+                                      1 if update_prefix else 0, _stream_ptr(stream)), "kdt_kv_compact_paged")
+
+
+def verify_attn_paged_plan(B, T, H, max_kv_len, page_size, *, out_dtype=None, bits=False, num_splits=0) -> dict:
+    """What verify_attn_paged launches for these sizes (``bits``: visibility given as bits, not parents; with
+    T = 1, neither)."""
+    import torch
+    fake = 1 << 12
+    W = -(-int(max_kv_len) // int(page_size)) if page_size > 0 else 1
+    a = VerifyPagedArgs(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, 1, int(page_size), fake, max(W, 1), 0, fake, None,
+                        int(max_kv_len), None if bits or T == 1 else fake, fake if bits else None, 1.0, fake,
+                        KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, int(num_splits))
+    p = Plan()
+    _check(lib().kdt_verify_attn_paged_plan(ctypes.byref(a), ctypes.byref(p)), "kdt_verify_attn_paged_plan")
+    return dict(impl=IMPL_NAMES.get(p.impl, p.impl), num_splits=p.num_splits, num_launches=p.num_launches,
+                ctas=p.ctas, workspace_bytes=int(p.workspace_bytes))
+
+
+def verify_attn_paged_workspace_size(B, T, H, max_kv_len, page_size, *, out_dtype=None, bits=False, num_splits=0) -> int:
+    """Bytes of workspace verify_attn_paged needs for these sizes."""
+    return verify_attn_paged_plan(B, T, H, max_kv_len, page_size, out_dtype=out_dtype, bits=bits,
+                                  num_splits=num_splits)["workspace_bytes"]
+
+
+def verify_attn_paged(q_nope, q_pe, c_kv, k_pe, table, prefix_len, *, n_rows=None, parent=None, vis=None, max_kv_len=None,
+                      scale=DEFAULT_SCALE, out=None, out_dtype=None, lse=None, err=None, num_splits=0, workspace=None,
+                      stream=None, want_lse=True):
+    """Tree-verify attention over a paged latent cache (kdt_verify_attn_paged); T = 1 is plain decoding.
+
+    ``q_nope`` [B,T,H,512] and ``q_pe`` [B,T,H,64] are bf16 (slices of a combined [B,T,H,576] buffer are
+    taken where they lie); the cache is c_kv [n_pages,page,512] and k_pe [n_pages,page,64] bf16, ``table``
+    int32 [B,W] names each sequence's pages. ``parent`` int32 [B,T] or ``vis`` gives the tree (neither is
+    needed with T = 1); ``n_rows`` int32 [B] the nodes of each sequence of a padded batch. Returns
+    (out [B,T,H,512], lse [B,T,H] fp32 or None); ``out_dtype`` is float32 (the default) or bfloat16.
+    ``max_kv_len`` defaults to the table's width in rows.
+    """
+    import torch
+    n, page = _check_paged_cache(c_kv, k_pe)
+    B, T, H = q_nope.shape[:3]
+    W, stride = _check_table(table, B)
+    if q_nope.shape != (B, T, H, 512) or q_pe.shape != (B, T, H, 64):
+        raise ValueError("q_nope must be [B,T,H,512] and q_pe [B,T,H,64]")
+    if q_nope.dtype != torch.bfloat16 or q_pe.dtype != torch.bfloat16:
+        raise TypeError("queries must be bfloat16")
+    _int32_of(prefix_len, B, "prefix_len"), _int32_of(n_rows, B, "n_rows"), _int32_of(parent, B * T, "parent")
+    if vis is not None and (vis.numel() != B * T * ((T + 31) // 32) or vis.element_size() != 4 or not vis.is_contiguous()):
+        raise ValueError("vis must be a contiguous 32-bit [B,T,ceil(T/32)] tensor")
+    if out is None:
+        out = _empty((B, T, H, 512), out_dtype or torch.float32, q_nope.device, stream)
+    elif out.shape != (B, T, H, 512) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError("out must be a contiguous [B,T,H,512] tensor of out_dtype")
+    if lse is None and want_lse:
+        lse = _empty((B, T, H), torch.float32, q_nope.device, stream)
+    elif lse is not None and (lse.numel() != B * T * H or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [B,T,H] tensor")
+    a = VerifyPagedArgs(B, T, H, 512, 64, q_nope.data_ptr(), _row_stride(q_nope), q_pe.data_ptr(), _row_stride(q_pe),
+                        c_kv.data_ptr(), k_pe.data_ptr(), n, page, table.data_ptr(), W, stride, prefix_len.data_ptr(),
+                        _ptr(n_rows), min(W * page, 2 ** 31 - 257) if max_kv_len is None else int(max_kv_len), _ptr(parent), _ptr(vis),
+                        float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), _err_of(err), int(num_splits))
+    if workspace is None:
+        need = int(lib().kdt_verify_attn_paged_workspace_size(ctypes.byref(a)))
+        workspace = _empty(need, torch.uint8, q_nope.device, stream) if need else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kdt_verify_attn_paged(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream_ptr(stream)),
+           "kdt_verify_attn_paged")
+    return out, lse
+
+
+def _setting(v, R, dtype, name, off):
+    """A sampling setting as (address of an array of one a row or None, one number for all rows)."""
+    import torch
+    if v is None:
+        return None, off
+    if torch.is_tensor(v):
+        if v.dtype != dtype or v.numel() != R or not v.is_contiguous():
+            raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor of {R} elements")
+        return v.data_ptr(), off
+    return None, type(off)(v)
+
+
+def sample(logits, u, *, temperature=1.0, top_k=None, top_p=None, min_p=None, err=None, want_logp=True, stream=None):
+    """One token a row under temperature, top-k, top-p and min-p (kdt_sample). ``logits`` [R,V] float32 or bf16
+    (equally spaced rows, a contiguous last dim), ``u`` float32 [R] random numbers in [0, 1). A setting is a
+    number, or a tensor of one a row (float32; top_k int32); None leaves a filter out; temperature 0 is greedy.
+    Returns token [R] int32 and logp [R] float32 (or None)."""
+    import torch
+    R, V = logits.shape
+    stride = logits.stride(0) if R > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or stride < V:
+        raise ValueError("logits must be [R,V] with a contiguous last dim and rows that do not overlap")
+    if u.dtype != torch.float32 or u.numel() != R or not u.is_contiguous():
+        raise ValueError(f"u must be a contiguous float32 tensor of {R} elements")
+    temp = _setting(temperature, R, torch.float32, "temperature", 1.0)
+    k, p, low = (_setting(top_k, R, torch.int32, "top_k", 0), _setting(top_p, R, torch.float32, "top_p", 1.0),
+                 _setting(min_p, R, torch.float32, "min_p", 0.0))
+    token = _empty(R, torch.int32, logits.device, stream)
+    logp = _empty(R, torch.float32, logits.device, stream) if want_logp else None
+    a = SampleArgs(R, V, logits.data_ptr(), _dtype_code(logits), stride, u.data_ptr(), *temp, *k, *p, *low,
+                   token.data_ptr(), _ptr(logp), _err_of(err))
+    _check(lib().kdt_sample(ctypes.byref(a), _stream_ptr(stream)), "kdt_sample")
+    return token, logp
