@@ -159,6 +159,14 @@ cudaError_t launch_verify_q8_rows(const Q8Params &p, cudaStream_t s);
 
 // K6: tree-verify attention over a paged bf16 latent cache (kdt_verify_attn_paged), everything
 // validated on the host.
+// Where a share of the work starts, left by the attention kernel for the merge: in positions of the
+// (group of row tiles, key block) list, with the group that position is in.
+struct PagedShare {
+    int64_t start, t0, t1;     // the group's positions [t0, t1)
+    int64_t row0;              // its first query row over all sequences
+    int rows;                  // its sequence's rows from there on
+};
+
 struct PagedParams {
     int B, T, H, W;            // W = ceil(T/32) visibility words per query
     int rows_seq;              // T * H
@@ -176,7 +184,16 @@ struct PagedParams {
     bool out_bf16;
     float *lse;
     int32_t *err;
+    int tile;                  // rows of a tile: 16, 32 or 64
+    int group;                 // row tiles that walk the same keys side by side, a CTA each
+    int shares;                // the work is cut into at most this many
+    int least;                 // blocks a share has at least, where there are enough
+    bool pieces;               // groups may be cut between shares: a second kernel joins their pieces
+    bool overlap_vis;          // launched right behind this call's visibility kernel
+    float *part_o, *part_lse;  // [2 * shares * group][tile] piece states
+    PagedShare *cuts;          // [shares + 1]
 };
+constexpr int kPagedKeys = 64; // keys of a block
 cudaError_t launch_verify_paged(const PagedParams &p, cudaStream_t s);
 
 // log2 of a page size that the paged cache takes (8 .. 1024 rows), or -1.

@@ -1,81 +1,897 @@
-// K6: tree-verify attention over a paged bf16 latent cache. The simplest kernel that is right: a CTA a query row.
+// K6: tree-verify attention over a paged bf16 latent cache (single tokens, small trees): tcgen05 with the
+// KEYS on the M side.
+//
+// The definition is kdt_verify_attn's, key j of a sequence read from the page its table names: scores s_j =
+// scale (q_nope . c_j + q_pe . k_j) of a row over its visible keys, softmax, out = sum p_j c_j, lse.
+//
+//  * A tile is up to 64 query rows (heads x tree nodes) of one sequence, 16 or 32 when it has no more. The
+//    tensor cores are filled from the keys' side: S^T = K Q^T with M = 64 keys, N = rows, and O^T = V^T P^T
+//    with M = 128 latent dims (four accumulators), N = rows. O^T takes 4 N of tensor memory's 512 columns and
+//    S^T 2 N, so that a block's scores are made while the one before is in its softmax.
+//  * A block is 64 keys: 576 dims as nine 128-byte swizzled tiles, the latent in four stages of two tiles.
+//    ONE copy serves both contractions: K-major A operand of S^T, MN-major A operand of O^T. TMA boxes of
+//    min(64, page) rows bring it, a box a page where pages are smaller; the stages form a ring of two blocks
+//    or more, and each is given back as soon as its part of O^T is done. Boxes behind the last row, and pages that are none, lie outside the tensor map: zeros, no traffic.
+//  * One thread issues all MMAs, and never waits for one thing while it could do another: it polls for the
+//    next block's stages and for P^T in turn, so that neither a late page holds up O^T, which frees the
+//    ring, nor softmax the scores.
+//  * In S^T a thread owns two keys and a few rows, so a row's maximum lies across threads. The running
+//    maximum is lazy: a block only votes whether some score exceeds its row's reference by more than 2^20;
+//    exact maxima and the rescale of O^T are taken when one does, and for the first block of an item. p <=
+//    2^20 keeps l and O (float32) far from overflow, and the result does not depend on the reference. Sums
+//    stay with the threads until the item's end.
+//  * Row tiles of a sequence (a "group" of up to 8) walk the same keys side by side, a CTA each, so that DRAM
+//    is read once and the others hit L2. The (group, key block) pairs of the batch are cut into equal
+//    contiguous shares; groups cut by a share's end leave normalised pieces that a second kernel joins by
+//    log-sum-exp.
+//  * Masks, rows of other sequences' leftovers behind the last key, and latents that are not finite concern
+//    the blocks with tree keys only: there the softmax warps zero what may not enter a product (0 * NaN), and
+//    mark its key, whose score is NaN for the rows that see it.
+//  * Every wait is bounded; one that runs out records a status in the error word and the kernel drains its
+//    MMAs, frees tensor memory and returns.
+#include <cuda.h>
+#include <float.h>
 #include <math.h>
+#include <string.h>
 
 #include "kdt_internal.cuh"
+#include "q8.cuh"
+#include "tc_ptx.cuh"
 
 namespace kdt {
 namespace {
 
-constexpr int kThreads = 256;
+using namespace tc;
 
-__global__ void __launch_bounds__(kThreads) verify_paged_kernel(const PagedParams p) {
-    __shared__ float q[kDqk], s[64];
-    __shared__ int64_t row[64];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t g = blockIdx.x;                                    // (b, i, h)
-    const int b = (int)(g / p.rows_seq), i = (int)(g % p.rows_seq) / p.H;
-    const int n = p.n_rows ? min(max(p.n_rows[b], 0), p.T) : p.T;
-    if (i >= n) return;
-    const int P = min(max(p.prefix_len[b], 0), p.max_kv - n);
-    for (int d = tid; d < kDqk; d += kThreads)
-        q[d] = d < kDc ? __bfloat162float(p.q_nope[g * p.q_nope_stride + d]) : __bfloat162float(p.q_pe[g * p.q_pe_stride + d - kDc]);
-    float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-    for (int k0 = 0; k0 < P + n; k0 += 64) {
-        __syncthreads();
-        for (int k = warp; k < 64; k += 8) {
-            const int j = k0 + k, t = j - P;
-            bool see = j < P + n;
-            if (see && t >= 0 && p.vis) see = (p.vis[((int64_t)b * p.T + i) * p.W + (t >> 5)] >> (t & 31)) & 1u;
-            float x = 0.f;
-            int64_t at = -1;
-            if (see) {
-                const int32_t page = p.table[b * p.table_stride + (j >> p.shift)];
-                if (page >= 0 && page < p.n_pages) at = ((int64_t)page << p.shift) + (j & ((1 << p.shift) - 1));
-                if (at < 0) {
-                    if (lane == 0) record_error(p.err, (int32_t)min((int64_t)INT32_MAX, 1 + (int64_t)p.B * p.T + b));
+constexpr int kKeysB = kPagedKeys;                  // keys of a block (M of S^T)
+// Warps: 0 loads keys, 1 issues the MMAs, 2 loads queries, 3 only helps to set up, 4-11 softmax.
+constexpr int kSoft0 = 4, kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
+constexpr int kThreads = 32 * (kSoft0 + kSoftWarps);
+constexpr int kStages = 4;                          // of a block's latent
+constexpr int kTileBytes = kKeysB * 128;            // [64 keys x 64 dims] bf16
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kColS = 256;                     // S^T columns (two buffers of N); O^T part q at N q
+constexpr float kRaise = 20.f;                      // log2 units
+// Minus the reference of a row that has seen no score yet but -inf: large enough that any other score votes
+// for a rise, and finite, so that -inf stays -inf, of weight 0.
+constexpr float kNoReference = FLT_MAX;
+constexpr uint64_t kWait = 200000000ull;            // ns
+
+template <int kRows> struct Layout {
+    static constexpr int kRing = kRows == 64 ? 8 : (kRows == 32 ? 10 : 11);         // latent stages
+    static constexpr int kRopeRing = kRows == 64 ? 2 : 3;
+    static constexpr int kQTile = kRows * 128;      // [rows x 64 dims] bf16
+    static constexpr int kOffR = kRing * kStageBytes;
+    static constexpr int kOffQ = kOffR + kRopeRing * kTileBytes;
+    static constexpr int kOffP = kOffQ + 9 * kQTile;
+    static constexpr int kPBytes = kRows * 128 < 512 * kSoftWarps ? 512 * kSoftWarps : kRows * 128;
+    static constexpr int kSmem = kOffP + kPBytes + 1024;                            // + alignment slack
+};
+
+struct Bars {
+    uint64_t kfull[11], kempty[11];     // a stage landed; O^T's MMAs have read it
+    uint64_t rfull[3], rempty[3];       // rope keys
+    uint64_t sfull[2];                  // scores of the block in tensor memory
+    uint64_t pfull;                     // P^T stored, O^T rescaled if needed
+    uint64_t pdone;                     // the block's O^T complete, P^T's space free
+    uint64_t qfull, qempty;             // queries of the item landed; its scores are all made
+    uint64_t ofree;                     // O^T of the item read out
+    uint64_t drain;
+    uint32_t tmem;
+    int abort_flag;
+    int work[5];                        // this share: blocks, first sequence, group, block
+};
+
+template <int kRows> struct Shared {
+    Bars bar;
+    alignas(16) float m[kRows];         // the reference, log2 units
+    alignas(16) float alpha[kRows];     // of a rise; at an item's end 1 / l
+    float red[4][kRows];                // by keys' quarter
+    uint32_t bad[2];                    // keys whose latent is not finite
+};
+
+__device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+    if (*reinterpret_cast<volatile int *>(&bar.abort_flag)) return false;
+    if (mbar_wait(b, parity, kWait)) return true;
+    bar.abort_flag = 1;
+    if (err) atomicCAS(err, 0, code);
+    return false;
+}
+
+__device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+    return __all_sync(0xffffffffu, wait_for(bar, b, parity, err, code));
+}
+
+__device__ __forceinline__ bool soft_or(bool flag) {       // over the softmax warps
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pin, pout;\n\t"
+        "setp.ne.u32 pin, %1, 0;\n\t"
+        "bar.red.or.pred pout, 1, %2, pin;\n\t"
+        "selp.u32 %0, 1, 0, pout;\n\t}"
+        : "=r"(r)
+        : "r"(flag ? 1u : 0u), "n"(kSoftThreads)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Tree nodes and prefix of sequence b, brought into the caller's bounds.
+__device__ __forceinline__ int nodes_of(const PagedParams &p, int b) {
+    return p.n_rows ? min(max(p.n_rows[b], 0), p.T) : p.T;
+}
+__device__ __forceinline__ int prefix_of(const PagedParams &p, int b, int n) {
+    return min(max(p.prefix_len[b], 0), p.max_kv - n);
+}
+__device__ __forceinline__ int groups_of(const PagedParams &p, int n) {
+    return (n * p.H + p.tile * p.group - 1) / (p.tile * p.group);
+}
+
+// The item a role is at: blocks [kb, kb + nb) of group grp of sequence b. The share's items follow in order;
+// an item ends where its group or the share does.
+struct Item {
+    int left;               // blocks of the share from this item on
+    int b, grp, kb, nb;
+    int n, P, kv;           // nodes, prefix, keys of the sequence
+    int idx;                // items of the share before this one
+};
+
+__device__ __forceinline__ bool fill(const PagedParams &p, Item &it) {
+    if (it.left <= 0) return false;
+    while (it.b < p.B && (it.n = nodes_of(p, it.b)) == 0) ++it.b;
+    if (it.b >= p.B) return false;
+    it.P = prefix_of(p, it.b, it.n);
+    it.kv = it.P + it.n;
+    it.nb = min((it.kv + kKeysB - 1) / kKeysB - it.kb, it.left);
+    return true;
+}
+
+__device__ __forceinline__ bool advance(const PagedParams &p, Item &it) {
+    it.left -= it.nb;
+    it.kb = 0;
+    ++it.idx;
+    if (++it.grp >= groups_of(p, it.n)) {
+        it.grp = 0;
+        ++it.b;
+    }
+    return fill(p, it);
+}
+
+__device__ __forceinline__ bool first_item(const PagedParams &p, const int *work, Item &it) {
+    it.left = work[0];
+    it.b = work[1];
+    it.grp = work[2];
+    it.kb = work[3];
+    it.nb = it.n = it.P = it.kv = it.idx = 0;
+    return fill(p, it);
+}
+
+// The row tile of this CTA (g-th of the group), or -1 when the sequence has none there.
+__device__ __forceinline__ int tile_of(const PagedParams &p, const Item &it, int g) {
+    const int rt = it.grp * p.group + g;
+    return rt * p.tile < it.n * p.H ? rt : -1;
+}
+
+// Positions: sequence-major, group-major, block order; W of them, cut into `C` shares. One warp finds share
+// c's first item {blocks, b, grp, kb}, and leaves for the merge where the share starts and which group that
+// is in.
+__device__ __forceinline__ void find_share(const PagedParams &p, int c, bool writes, int lane, int *out) {
+    int64_t W = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int n = nodes_of(p, b);
+        if (n) W += (int64_t)groups_of(p, n) * ((prefix_of(p, b, n) + n + kKeysB - 1) / kKeysB);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
+    const int64_t C = min((int64_t)p.shares, max((W + p.least - 1) / p.least, (int64_t)1));
+    const int64_t s0 = c < C ? W * c / C : W, s1 = c < C ? W * (c + 1) / C : W;
+    if (lane == 0) {
+        out[0] = (int)(s1 - s0);
+        out[1] = out[2] = out[3] = 0;
+        if (writes) {
+            p.cuts[c].start = s0;
+            p.cuts[c].t0 = p.cuts[c].t1 = s0;                 // (an empty share behind the last position)
+            p.cuts[c].rows = 0;
+            if (c == p.shares - 1) p.cuts[p.shares].start = W;
+        }
+    }
+    __syncwarp();
+    int64_t before = 0;
+    for (int base = 0; base < p.B && s0 < s1; base += 32) {
+        const int b = base + lane;
+        const int n = b < p.B ? nodes_of(p, b) : 0;
+        const int nb = n ? (prefix_of(p, b, n) + n + kKeysB - 1) / kKeysB : 1;
+        const int64_t w = n ? (int64_t)groups_of(p, n) * nb : 0;
+        int64_t incl = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        const int64_t at = before + incl - w;
+        const bool hit = s0 >= at && s0 < at + w;
+        if (hit) {
+            const int grp = (int)((s0 - at) / nb);
+            out[1] = b;
+            out[2] = grp;
+            out[3] = (int)(s0 - at - (int64_t)grp * nb);
+            if (writes) {
+                const int row = grp * p.group * p.tile;
+                p.cuts[c].t0 = at + (int64_t)grp * nb;
+                p.cuts[c].t1 = p.cuts[c].t0 + nb;
+                p.cuts[c].row0 = (int64_t)b * p.rows_seq + row;
+                p.cuts[c].rows = min(n * p.H - row, p.group * p.tile);
+            }
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+        if (__any_sync(0xffffffffu, hit)) break;
+    }
+    __syncwarp();
+}
+
+// Waits for this warp's loads from tensor memory. They write their registers when they complete: nothing
+// that uses one may move ahead of the wait, and without an operand of its own the wait holds back only
+// memory accesses.
+template <int kN> __device__ __forceinline__ void loaded(uint32_t (&r)[kN]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(r[k])::"memory");
+}
+
+__device__ __forceinline__ uint32_t lane_addr(uint32_t base, int warp, uint32_t col) {
+    return base + ((uint32_t)(32 * (warp & 3)) << 16) + col;
+}
+
+template <int kRows, bool kBf16Out>
+__global__ void __launch_bounds__(kThreads, 1)
+    verify_paged_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qp, const PagedParams p) {
+    using L = Layout<kRows>;
+    constexpr int kHalf = kRows / 2;                // rows of a softmax warpgroup
+    constexpr int kCols = kHalf / 8;                // groups of 8 of them
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Shared<kRows> sh;
+    Bars &bar = sh.bar;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = blockIdx.x / p.group, g_of = blockIdx.x % p.group;
+
+    if (warp == 0) tmem_alloc(&bar.tmem, 512);
+    if (warp == 4) find_share(p, share, p.pieces && g_of == 0, lane, bar.work);
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < L::kRing; ++i) {
+            mbar_init(&bar.kfull[i], 1);
+            mbar_init(&bar.kempty[i], 1);
+        }
+        for (int i = 0; i < L::kRopeRing; ++i) {
+            mbar_init(&bar.rfull[i], 1);
+            mbar_init(&bar.rempty[i], 1);
+        }
+        mbar_init(&bar.sfull[0], 1);
+        mbar_init(&bar.sfull[1], 1);
+        mbar_init(&bar.pfull, kSoftWarps);
+        mbar_init(&bar.pdone, 1);
+        mbar_init(&bar.qfull, 1);
+        mbar_init(&bar.qempty, 1);
+        mbar_init(&bar.ofree, kSoftWarps);
+        mbar_init(&bar.drain, 1);
+        bar.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&map_c);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_qn);
+        tma_prefetch_desc(&map_qp);
+    }
+    if (warp == 0) tmem_relinquish();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+
+    if (warp >= kSoft0) {
+        // ------------------------- softmax, correction and epilogue -------------------------
+        // A warp has 16 keys of S^T and half of the rows: this thread keys ka and ka + 8, rows row_of(i, e).
+        Item it;
+        bool have = first_item(p, bar.work, it);
+        uint32_t g = 0;                                      // blocks so far
+        const int w4 = warp & 3, half = (warp - kSoft0) >> 2, ka = 16 * w4 + (lane >> 2);
+        const int srow = (int)threadIdx.x - 32 * kSoft0;
+        bool ok = true, vis_ready = false;
+        auto row_of = [&](int i, int e) { return kHalf * half + 8 * i + 2 * (lane & 3) + e; };
+        // where this lane's 16 bytes of stmatrix go: matrix 2 i + (keys + 8), row r of it
+        const int mrow = lane & 7, mhalf = (lane >> 3) & 1, mi = (lane >> 4) & 1;
+        const uint32_t pdst = smem + L::kOffP + (kHalf * half + mrow) * 128 + (((2 * w4 + mhalf) ^ mrow) << 4);
+        for (; have; have = advance(p, it)) {
+            const int rt = tile_of(p, it, g_of);
+            if (rt < 0) continue;
+            float l[2 * kCols], nm[2 * kCols];
+#pragma unroll
+            for (int k = 0; k < 2 * kCols; ++k) l[k] = 0.f;
+            if (srow < kRows) sh.m[srow] = -INFINITY;        // (read by others behind the first block's barriers)
+            bool fail = false;
+            for (int j = 0; j < it.nb; ++j, ++g) {
+                const int key0 = (it.kb + j) * kKeysB;
+                const bool masked = key0 + kKeysB > it.P;
+                // bit 2 k + h: row k of this thread's sees key ka + 8 h
+                uint32_t see = ~0u;
+                if (masked) {
+                    see = 0u;
+                    const int ta = key0 + ka - it.P;
+                    if (p.vis && !vis_ready) {
+                        griddep_wait();
+                        vis_ready = true;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2 * kCols; ++k) {
+                        const int node = (rt * kRows + row_of(k >> 1, k & 1)) / p.H;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int t = ta + 8 * h;
+                            bool v = t < 0;
+                            if (t >= 0 && t < it.n && node < it.n)
+                                v = !p.vis || ((__ldcg(p.vis + ((int64_t)it.b * p.T + node) * p.W + (t >> 5)) >> (t & 31)) & 1u);
+                            see |= (v ? 1u : 0u) << (2 * k + h);
+                        }
+                    }
+                }
+                ok = ok && warp_wait(bar, &bar.sfull[g & 1], (g >> 1) & 1, p.err, -61);
+                tc_fence_after();
+                uint32_t is_bad = 0u;
+                if (masked) {
+                    // rows behind the last key are zeroed, and, where nodes hide keys, what is not finite
+                    const uint32_t u0 = kStages * g;
+                    for (int c = 0; c < kStages; ++c)        // (long since: this thread's view of what landed)
+                        ok = ok && warp_wait(bar, &bar.kfull[(u0 + c) % L::kRing], ((u0 + c) / L::kRing) & 1, p.err, -62);
+                    auto at = [&](int r, int x) {            // 16-byte chunk x of 64 of key row r
+                        return smem + ((u0 + (x >> 4)) % L::kRing) * kStageBytes + ((x >> 3) & 1) * kTileBytes + r * 128 + ((x & 7) << 4);
+                    };
+                    const int first = min(it.kv - key0, kKeysB);
+                    for (int x = srow; x < (kKeysB - first) * 64; x += kSoftThreads) st_shared_v4(at(first + (x >> 6), x & 63), 0u, 0u, 0u, 0u);
+                    if (p.vis) {
+                        if (srow < 2) sh.bad[srow] = 0u;
+                        soft_or(false);
+                        const int from = max(it.P - key0, 0);
+                        for (int x = srow; x < (first - from) * 64; x += kSoftThreads) {
+                            const int r = from + (x >> 6);
+                            uint32_t v[4];
+                            ld_shared_v4(at(r, x & 63), v);
+                            bool inf = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                inf |= (v[k] & 0x7f800000u) == 0x7f800000u || (v[k] & 0x7f80u) == 0x7f80u;
+                            if (inf) {
+                                st_shared_v4(at(r, x & 63), 0u, 0u, 0u, 0u);
+                                atomicOr(&sh.bad[r >> 5], 1u << (r & 31));
+                            }
+                        }
+                        soft_or(false);
+                        is_bad = ((sh.bad[ka >> 5] >> (ka & 31)) & 1u) | (((sh.bad[(ka + 8) >> 5] >> ((ka + 8) & 31)) & 1u) << 1);
+                    }
+                }
+                uint32_t raw[4 * kCols];
+                tmem_ld_frag(lane_addr(tmem + kColS + (g & 1) * kRows, warp, kHalf * half), raw);
+                loaded(raw);
+                float x[4 * kCols];                          // [i][key][e]
+                auto scores = [&](bool shifted) {
+#pragma unroll
+                    for (int k = 0; k < 4 * kCols; ++k) {
+                        const int r = 2 * (k >> 2) + (k & 1), h = (k >> 1) & 1;
+                        x[k] = fmaf(__uint_as_float(raw[k]), p.scale_log2, shifted ? nm[r] : 0.f);
+                        if (masked) {
+                            if ((is_bad >> h) & 1u) x[k] = __uint_as_float(0x7fffffffu);
+                            x[k] = (see >> (2 * r + h)) & 1u ? x[k] : -INFINITY;
+                        }
+                    }
+                };
+                bool rise = j == 0;                          // (no reference yet)
+                if (j > 0) {
+                    scores(true);
+                    float top = x[0];
+#pragma unroll
+                    for (int k = 1; k < 4 * kCols; ++k) top = fmaxf(top, x[k]);
+                    rise = soft_or(top > kRaise || !ok);
+                }
+                if (rise) {
+                    scores(false);
+#pragma unroll
+                    for (int k = 0; k < 2 * kCols; ++k) {
+                        float v = fmaxf(x[4 * (k >> 1) + (k & 1)], x[4 * (k >> 1) + 2 + (k & 1)]);
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                        if (lane < 4) sh.red[w4][row_of(k >> 1, k & 1)] = v;
+                    }
+                    // O^T of the block before is complete
+                    if (j > 0) ok = ok && warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -63);
+                    if ((fail = soft_or(!ok))) break;
+                    if (srow < kRows) {
+                        const float to = fmaxf(fmaxf(sh.red[0][srow], sh.red[1][srow]), fmaxf(sh.red[2][srow], sh.red[3][srow]));
+                        const float m = sh.m[srow];
+                        float a = 1.f;
+                        if (to > m + kRaise) {
+                            a = m == -INFINITY ? 1.f : ex2(m - to);
+                            sh.m[srow] = to;
+                        }
+                        sh.alpha[srow] = a;
+                    }
+                    soft_or(false);
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < 4 * kCols; ++q) {
+                            const int col = kHalf * half + 8 * (q % kCols);
+                            const uint32_t addr = lane_addr(tmem, warp, kRows * (q / kCols) + col);
+                            uint32_t o[8];
+                            tc_fence_after();
+                            tmem_ld8(addr, o);
+                            loaded(o);
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[col + r]);
+                            tmem_st8(addr, o);
+                            tmem_wait_st();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2 * kCols; ++k) l[k] *= sh.alpha[row_of(k >> 1, k & 1)];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2 * kCols; ++k) {
+                        const float m = sh.m[row_of(k >> 1, k & 1)];
+                        nm[k] = m == -INFINITY ? kNoReference : -m;
+                    }
+                    scores(true);
+                }
+                // p = 2^(score - m), to P^T's place once O^T's MMAs of the block before have read it
+                uint32_t pk[2 * kCols];                      // [i][key]
+#pragma unroll
+                for (int k = 0; k < 2 * kCols; ++k) {
+                    x[2 * k] = ex2(x[2 * k]);
+                    x[2 * k + 1] = ex2(x[2 * k + 1]);
+                    pk[k] = q8::pack_bf16(x[2 * k], x[2 * k + 1]);
+                }
+                if (g > 0) ok = ok && warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -64);
+                tc_fence_before();
+                if constexpr (kCols == 1) {
+                    stmatrix_trans(pdst, pk);                // (two matrices: lanes 0 - 15 give the addresses)
                 } else {
-                    for (int d = lane; d < kDc; d += 32) x = fmaf(q[d], __bfloat162float(p.c_kv[at * kDc + d]), x);
-                    for (int d = lane; d < kDr; d += 32) x = fmaf(q[kDc + d], __bfloat162float(p.k_pe[at * kDr + d]), x);
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 2) {
+                        const uint32_t four[4] = {pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]};
+                        stmatrix_trans(pdst + (i + mi) * 1024, four);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pfull);
+#pragma unroll
+                for (int k = 0; k < 2 * kCols; ++k) l[k] += x[4 * (k >> 1) + (k & 1)] + x[4 * (k >> 1) + 2 + (k & 1)];
+            }
+            if (fail) break;
+            // l over the keys, then out = O / l and lse = ln2 (m + log2 l)
+#pragma unroll
+            for (int k = 0; k < 2 * kCols; ++k) {
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+                if (lane < 4) sh.red[w4][row_of(k >> 1, k & 1)] = l[k];
+            }
+            ok = ok && warp_wait(bar, &bar.pdone, (g - 1) & 1, p.err, -65);
+            if (soft_or(!ok)) break;
+            // all blocks of the group: final rows; else a piece, in slot 2 x for the share's first item
+            const bool whole = it.kb == 0 && it.nb == (it.kv + kKeysB - 1) / kKeysB;
+            const int live = min(kRows, it.n * p.H - rt * kRows);
+            const int64_t first = whole ? (int64_t)it.b * p.rows_seq + rt * kRows
+                                        : (2 * (int64_t)blockIdx.x + (it.idx ? 1 : 0)) * kRows;
+            if (srow < kRows) {
+                const float lt = sh.red[0][srow] + sh.red[1][srow] + sh.red[2][srow] + sh.red[3][srow];
+                sh.alpha[srow] = lt == 0.f ? 0.f : 1.f / lt;
+                float *lse = whole ? p.lse : p.part_lse;
+                if (lse && srow < live) lse[first + srow] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (sh.m[srow] + log2f(lt));
+            }
+            soft_or(false);
+            tc_fence_after();
+            // A thread has one dim of 8 rows; 512 bytes of P^T's space a warp turn them into 16-byte pieces of rows
+            const uint32_t stage = smem + L::kOffP + 512 * (warp - kSoft0);
+#pragma unroll 1
+            for (int q = 0; q < 4 * kCols; ++q) {
+                const int col = kHalf * half + 8 * (q % kCols);
+                uint32_t o[8];
+                tmem_ld8(lane_addr(tmem, warp, kRows * (q / kCols) + col), o);
+                loaded(o);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[col + r]);
+                const int64_t at = (first + col) * kDc + 128 * (q / kCols) + 32 * w4;
+                if (whole && kBf16Out) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const unsigned short h = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[r])));
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + r * 64 + 2 * lane), "h"(h) : "memory");
+                    }
+                    __syncwarp();
+                    uint32_t v[4];
+                    ld_shared_v4(stage + 16 * lane, v);
+                    if (col + (lane >> 2) < live)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + (lane >> 2) * kDc + 8 * (lane & 3)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    __syncwarp();
+                } else {
+                    float *dst = (whole ? static_cast<float *>(p.out) : p.part_o) + at + (lane >> 3) * kDc + 4 * (lane & 7);
+#pragma unroll
+                    for (int g4 = 0; g4 < 8; g4 += 4) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + r * 128 + 4 * lane), "r"(o[g4 + r]) : "memory");
+                        __syncwarp();
+                        uint32_t v[4];
+                        ld_shared_v4(stage + 16 * lane, v);
+                        if (col + g4 + (lane >> 3) < live) *reinterpret_cast<uint4 *>(dst + g4 * kDc) = make_uint4(v[0], v[1], v[2], v[3]);
+                        __syncwarp();
+                    }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.ofree);
+        }
+    } else if (warp == 0) {
+        // ------------------------------------ keys ------------------------------------
+        if (elect_one()) {
+            const int box = min(kKeysB, 1 << p.shift);
+            const int nowhere = p.n_pages << p.shift;        // a row outside the tensor maps
+            // cache row of the box that starts at a key of an item
+            auto place = [&](const Item &i, int key) {
+                if (key >= i.kv) return nowhere;
+                const int32_t page = __ldg(p.table + i.b * p.table_stride + (key >> p.shift));
+                if (page >= 0 && page < p.n_pages) return (page << p.shift) + (key & ((1 << p.shift) - 1));
+                record_error(p.err, (int32_t)min((int64_t)INT32_MAX, 1 + (int64_t)p.B * p.T + i.b));
+                return nowhere;
+            };
+            Item it;
+            bool ok = true;
+            uint32_t slot = 0, phase = 1, rslot = 0, rphase = 1;
+            for (bool have = first_item(p, bar.work, it); have && ok; have = advance(p, it)) {
+                if (tile_of(p, it, g_of) < 0) continue;
+                for (int j = 0; j < it.nb; ++j) {
+                    const int key0 = (it.kb + j) * kKeysB;
+                    int rows[kKeysB / 8];                    // of the block's boxes
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-            if (lane == 0) {
-                s[k] = see ? x * p.scale_log2 : -INFINITY;
-                row[k] = see ? at : -2;
+                    for (int k = 0; k < kKeysB / 8; ++k)
+                        if (k * box < kKeysB) rows[k] = place(it, key0 + k * box);
+                    if (!(ok = wait_for(bar, &bar.rempty[rslot], rphase, p.err, -66))) break;
+                    mbar_arrive_expect_tx(&bar.rfull[rslot], kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < kKeysB / 8; ++k)
+                        if (k * box < kKeysB)
+                            tma_load_2d_at(smem + L::kOffR + rslot * kTileBytes + k * box * 128, &map_k, &bar.rfull[rslot], 0, rows[k]);
+                    if (++rslot == L::kRopeRing) {
+                        rslot = 0;
+                        rphase ^= 1;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < kStages; ++c) {
+                        if (!(ok = wait_for(bar, &bar.kempty[slot], phase, p.err, -67))) break;
+                        mbar_arrive_expect_tx(&bar.kfull[slot], kStageBytes);
+                        const uint32_t dst = smem + slot * kStageBytes;
+                        if (box == kKeysB) {                 // one box of both tiles
+                            tma_load_3d_at(dst, &map_c, &bar.kfull[slot], 0, rows[0], 2 * c);
+                        } else {                             // a box a tile and page
+#pragma unroll
+                            for (int k = 0; k < kKeysB / 8; ++k)
+                                if (k * box < kKeysB) {
+                                    tma_load_3d_at(dst + k * box * 128, &map_c, &bar.kfull[slot], 0, rows[k], 2 * c);
+                                    tma_load_3d_at(dst + kTileBytes + k * box * 128, &map_c, &bar.kfull[slot], 0, rows[k], 2 * c + 1);
+                                }
+                        }
+                        if (++slot == L::kRing) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (!ok) break;
+                }
             }
         }
-        __syncthreads();
-        float top = m;
-        for (int k = 0; k < 64; ++k) top = fmaxf(top, s[k]);
-        const float a = m == top ? 1.f : exp2f(m - top);
-        l *= a;
-        o[0] *= a;
-        o[1] *= a;
-        m = top;
-        for (int k = 0; k < 64; ++k) {
-            const float w = s[k] == -INFINITY ? 0.f : exp2f(s[k] - m);
-            if (row[k] == -2) continue;                               // (0 times what is not finite is NaN)
-            l += w;
-            if (row[k] < 0) continue;
-            o[0] = fmaf(w, __bfloat162float(p.c_kv[row[k] * kDc + tid]), o[0]);
-            o[1] = fmaf(w, __bfloat162float(p.c_kv[row[k] * kDc + tid + 256]), o[1]);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ----------------------------------- queries -----------------------------------
+        if (elect_one()) {
+            Item it;
+            uint32_t ii = 0;
+            for (bool have = first_item(p, bar.work, it); have; have = advance(p, it)) {
+                const int rt = tile_of(p, it, g_of);
+                if (rt < 0) continue;
+                if (ii > 0 && !wait_for(bar, &bar.qempty, (ii - 1) & 1, p.err, -68)) break;
+                const int row = it.b * p.rows_seq + rt * kRows;
+                mbar_arrive_expect_tx(&bar.qfull, 9 * L::kQTile);
+                tma_load_3d_at(smem + L::kOffQ, &map_qn, &bar.qfull, 0, row, 0);
+                tma_load_2d_at(smem + L::kOffQ + 8 * L::kQTile, &map_qp, &bar.qfull, 0, row);
+                ++ii;
+            }
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------- MMA issuer --------------------------------
+        if (elect_one()) {
+            const uint32_t id_s = idesc_bf16_f32(kKeysB, kRows, 0, 0), id_o = idesc_bf16_f32(128, kRows, 1, 0);
+            // Descriptors differ only in their low words (address and leading stride); each use adds a
+            // constant to a base the compiler cannot see through, or it would keep all of them live.
+            const uint32_t dhi = (uint32_t)(sdesc_sw128(0, 0, 1024) >> 32);
+            const uint32_t base = smem >> 4, lbo_k = (16u >> 4) << 16, lbo_mn = ((uint32_t)kTileBytes >> 4) << 16;
+            auto desc = [&](uint32_t lo) { return ((uint64_t)dhi << 32) | lo; };
+            auto opaque = [](uint32_t v) {
+                asm volatile("" : "+r"(v));
+                return v;
+            };
+            // the scores' and the output's places in the list of items
+            Item si;
+            bool smore = first_item(p, bar.work, si);
+            while (smore && tile_of(p, si, g_of) < 0) smore = advance(p, si);
+            Item pi = si;
+            bool pmore = smore;
+            int sj = 0, pj = 0, stage = -1;                  // blocks within the item; -1: rope keys first
+            uint32_t sg = 0, pg = 0, sii = 0, pii = 0;       // blocks and items so far
+            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, oslot = 0;
+            uint64_t since = 0;
+            int idle = 0;
+            while (pmore) {
+                bool moved = false;
+                if (pg < sg && mbar_test(&bar.pfull, pg & 1) && (pj > 0 || pii == 0 || mbar_test(&bar.ofree, (pii - 1) & 1))) {
+                    tc_fence_after();
+                    const uint32_t pd = opaque(base + lbo_k + (L::kOffP >> 4));
+#pragma unroll 1
+                    for (int c = 0; c < kStages; ++c) {
+                        const uint32_t vd = opaque(base + lbo_mn + oslot * (kStageBytes >> 4));
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)          // 16 keys each
+                            mma_ss(tmem + kRows * c, desc(vd + (t * 2048 >> 4)), desc(pd + 2 * t), id_o, (pj > 0 || t > 0) ? 1u : 0u);
+                        mma_commit(&bar.kempty[oslot]);
+                        if (++oslot == L::kRing) oslot = 0;
+                    }
+                    mma_commit(&bar.pdone);
+                    ++pg;
+                    if (++pj == pi.nb) {
+                        pj = 0;
+                        ++pii;
+                        do pmore = advance(p, pi);
+                        while (pmore && tile_of(p, pi, g_of) < 0);
+                    }
+                    moved = true;
+                }
+                // one stage of the next block's scores: its buffer has been read when the block two before is in O^T
+                if (smore && sg <= pg + 1) {
+                    if (stage < 0) {
+                        if ((sj > 0 || mbar_test(&bar.qfull, sii & 1)) && mbar_test(&bar.rfull[rslot], rphase)) {
+                            tc_fence_after();
+                            const uint32_t rd = opaque(base + lbo_k + (L::kOffR >> 4) + rslot * (kTileBytes >> 4));
+                            const uint32_t qr = opaque(base + lbo_k + ((L::kOffQ + 8 * L::kQTile) >> 4));
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                mma_ss(tmem + kColS + (sg & 1) * kRows, desc(rd + 2 * t), desc(qr + 2 * t), id_s, t > 0 ? 1u : 0u);
+                            mma_commit(&bar.rempty[rslot]);
+                            if (++rslot == L::kRopeRing) {
+                                rslot = 0;
+                                rphase ^= 1;
+                            }
+                            stage = 0;
+                            moved = true;
+                        }
+                    } else if (mbar_test(&bar.kfull[slot], phase)) {
+                        tc_fence_after();
+                        const uint32_t kd = opaque(base + lbo_k + slot * (kStageBytes >> 4));
+                        const uint32_t qd = opaque(base + lbo_k + (L::kOffQ >> 4) + 2 * stage * (L::kQTile >> 4));
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)          // tile 2 stage + t / 4, 16 dims each
+                            mma_ss(tmem + kColS + (sg & 1) * kRows, desc(kd + (((t >> 2) * kTileBytes + (t & 3) * 32) >> 4)),
+                                   desc(qd + (((t >> 2) * L::kQTile + (t & 3) * 32) >> 4)), id_s, 1u);
+                        if (++slot == L::kRing) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                        if (++stage == kStages) {
+                            mma_commit(&bar.sfull[sg & 1]);
+                            stage = -1;
+                            ++sg;
+                            if (++sj == si.nb) {
+                                mma_commit(&bar.qempty);
+                                sj = 0;
+                                ++sii;
+                                do smore = advance(p, si);
+                                while (smore && tile_of(p, si, g_of) < 0);
+                            }
+                        }
+                        moved = true;
+                    }
+                }
+                if (moved) {
+                    idle = 0;
+                    since = 0;
+                } else if (++idle == 64) {                   // the clock every 64 polls
+                    idle = 0;
+                    const uint64_t now = global_ns();
+                    if (!since) since = now;
+                    const bool late = now - since > kWait;
+                    if (late) {
+                        bar.abort_flag = 1;
+                        if (p.err) atomicCAS(p.err, 0, -69);
+                    }
+                    if (late || *reinterpret_cast<volatile int *>(&bar.abort_flag)) break;
+                }
+            }
+            mma_commit(&bar.drain);                          // every MMA done before tensor memory goes
+            mbar_wait(&bar.drain, 0, kWait);
+        }
+        __syncwarp();
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*reinterpret_cast<volatile int *>(&bar.abort_flag)) {   // error path only: loads in flight land before the CTA leaves
+        const uint64_t t0 = global_ns();
+        do __nanosleep(1000);
+        while (global_ns() - t0 < 200000ull);
+    }
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the groups that a share's end cut. A NaN in a piece's lse reaches the row. The shares'
+// bounds are read, not computed again. Share k's slot: 2 k when it starts in the group (which is its first
+// item then), else 2 k + 1; -1: it does not meet the group, or is empty.
+__device__ __forceinline__ int64_t piece_slot(const PagedParams &p, int k, int64_t t0, int64_t t1, int g) {
+    if (k >= p.shares) return -1;
+    const int64_t a = p.cuts[k].start, e = p.cuts[k + 1].start;
+    return a >= t1 || a == e ? -1 : 2 * ((int64_t)k * p.group + g) + (a >= t0 ? 0 : 1);
+}
+
+constexpr int kMergeRows = 4;
+
+// CTA (c - 1, tile of the group and four rows of it) serves cut c (where share c begins) when it is the first
+// inside its group, two warps a row (256 columns each).
+template <bool kBf16Out>
+__global__ void __launch_bounds__(64 * kMergeRows) merge_paged_rows_kernel(const PagedParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
+    const PagedShare sh = p.cuts[c];
+    const int64_t before = p.cuts[c - 1].start;
+    if (sh.start == sh.t0 || before > sh.t0) return;          // between two groups, or not the first inside this one
+    const int grow = blockIdx.y * kMergeRows + (warp >> 1), g = grow / p.tile, row = grow % p.tile, col = 256 * (warp & 1) + 4 * lane;
+    if (grow >= sh.rows) return;
+    float M = -INFINITY;
+    bool nan = false;
+    for (int base = c - 1; base < p.shares && p.cuts[base].start < sh.t1; base += 32) {
+        const int64_t sl = piece_slot(p, base + lane, sh.t0, sh.t1, g);
+        const float v = sl >= 0 ? p.part_lse[sl * p.tile + row] : -INFINITY;
+        nan |= v != v;
+        M = fmaxf(M, v);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    nan = __any_sync(0xffffffffu, nan);
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float S = nan ? __uint_as_float(0x7fffffffu) : 0.f;
+    if (M > -INFINITY)
+        for (int base = c - 1; base < p.shares && p.cuts[base].start < sh.t1; base += 32) {
+            const int sl = (int)piece_slot(p, base + lane, sh.t0, sh.t1, g);
+            const float v = sl >= 0 ? p.part_lse[(int64_t)sl * p.tile + row] : -INFINITY;
+            const float wt = v == -INFINITY ? 0.f : __expf(v - M);
+            float ws = wt;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+            S += ws;
+            // the pieces that count (weight 0: no visible key, no such share), their loads independent
+            uint32_t live = __ballot_sync(0xffffffffu, wt != 0.f);
+            while (live) {
+                float4 a[4], d[4];
+                float wk[4];
+                int n = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wk[u] = 0.f;
+                    if (!live) continue;                      // (uniform)
+                    const int k = __ffs(live) - 1;
+                    live &= live - 1;
+                    wk[u] = __shfl_sync(0xffffffffu, wt, k);
+                    const float4 *src =
+                        reinterpret_cast<const float4 *>(p.part_o + ((int64_t)__shfl_sync(0xffffffffu, sl, k) * p.tile + row) * kDc + col);
+                    a[u] = src[0];
+                    d[u] = src[32];
+                    n = u + 1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u >= n) break;
+                    acc[0] = make_float4(fmaf(wk[u], a[u].x, acc[0].x), fmaf(wk[u], a[u].y, acc[0].y), fmaf(wk[u], a[u].z, acc[0].z),
+                                         fmaf(wk[u], a[u].w, acc[0].w));
+                    acc[1] = make_float4(fmaf(wk[u], d[u].x, acc[1].x), fmaf(wk[u], d[u].y, acc[1].y), fmaf(wk[u], d[u].z, acc[1].z),
+                                         fmaf(wk[u], d[u].w, acc[1].w));
+                }
+            }
+        }
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const int64_t out = sh.row0 + grow;
+#pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int64_t at = g * kDc + tid + 256 * h;
-        if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o[h] * inv);
-        else static_cast<float *>(p.out)[at] = o[h] * inv;
+        const float4 v = make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
+        if (kBf16Out)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out * kDc + col + 128 * h) =
+                make_uint2(q8::pack_bf16(v.x, v.y), q8::pack_bf16(v.z, v.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + out * kDc + col + 128 * h) = v;
     }
-    if (tid == 0 && p.lse) p.lse[g] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    if (col == 0 && p.lse) p.lse[out] = S == 0.f ? -INFINITY : M + logf(S);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    }
+    return fn;
+}
+
+// Rows of 64 * blocks bf16 values, `stride` elements apart, as [blocks][rows][64]: a box lands as tiles of 128-byte
+// swizzled rows.
+bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t stride, int blocks, int box_rows, int box_blocks) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks}, es[3] = {1, 1, 1};
+    memset(m, 0, sizeof(*m));
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks > 1 ? 3 : 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kRows, bool kBf16Out> cudaError_t launch(const PagedParams &p, cudaStream_t s) {
+    using L = Layout<kRows>;
+    const int64_t rows = (int64_t)p.B * p.rows_seq, slots = (int64_t)p.n_pages << p.shift;
+    const int box = 1 << p.shift < kKeysB ? 1 << p.shift : kKeysB;
+    CUtensorMap map_c, map_k, map_qn, map_qp;
+    if (!make_map(&map_c, p.c_kv, slots, kDc, kDc / 64, box, box == kKeysB ? 2 : 1) || !make_map(&map_k, p.k_pe, slots, kDr, 1, box, 1) ||
+        !make_map(&map_qn, p.q_nope, rows, p.q_nope_stride, kDc / 64, kRows, kDc / 64) ||
+        !make_map(&map_qp, p.q_pe, rows, p.q_pe_stride, 1, kRows, 1))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(verify_paged_kernel<kRows, kBf16Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess) return e;
+    // starts while the visibility kernel of the same call runs, and waits for it before it reads the bits
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.shares * p.group));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = p.overlap_vis ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, verify_paged_kernel<kRows, kBf16Out>, map_c, map_k, map_qn, map_qp, p)) != cudaSuccess) return e;
+    if (p.pieces) {
+        merge_paged_rows_kernel<kBf16Out><<<dim3((unsigned)(p.shares - 1), (unsigned)(p.group * p.tile / kMergeRows)),
+                                           64 * kMergeRows, 0, s>>>(p);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <int kRows> cudaError_t launch_rows(const PagedParams &p, cudaStream_t s) {
+    return p.out_bf16 ? launch<kRows, true>(p, s) : launch<kRows, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_verify_paged(const PagedParams &p, cudaStream_t s) {
-    verify_paged_kernel<<<(unsigned)(p.B * (int64_t)p.rows_seq), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.tile == 16 ? launch_rows<16>(p, s) : (p.tile == 32 ? launch_rows<32>(p, s) : launch_rows<64>(p, s));
 }
 
 }  // namespace kdt

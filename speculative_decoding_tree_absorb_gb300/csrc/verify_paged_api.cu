@@ -12,10 +12,15 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct PagedPlan {
-    int ctas = 0, launches = 0, splits = 0;
+    int ctas = 0, launches = 0, shares = 0;
+    int tile = 0, group = 0, least = 1;    // rows of a tile, tiles side by side, least blocks of a share
     bool vis = false;                      // the visibility kernel finds the words first
-    size_t vis_off = 0, ws_bytes = 0;
+    bool pieces = false;                   // a second kernel joins the pieces of what the split cut
+    size_t vis_off = 0, po_off = 0, pl_off = 0, cuts_off = 0, ws_bytes = 0;
 };
+
+constexpr int kMostGroup = 8;              // row tiles that walk the same keys side by side
+constexpr int kLeastBlocks = 2;
 
 kdt_status check_args(const kdt_verify_paged_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;
@@ -54,13 +59,45 @@ kdt_status make_plan(const kdt_verify_paged_args *a, PagedPlan *out) {
         *out = p;
         return KDT_OK;
     }
-    p.ctas = a->B * a->T * a->H;
-    p.splits = 1;
+    const int rows_seq = a->T * a->H;
+    p.tile = rows_seq <= 16 ? 16 : (rows_seq <= 32 ? 32 : 64);
+    const int tiles = (rows_seq + p.tile - 1) / p.tile, sms = sm_count();
+    // side by side: all of a sequence's row tiles, or of more than 8 the number from 5 to 8 that leaves the fewest idle
+    p.group = tiles;
+    if (tiles > kMostGroup) {
+        int best = INT32_MAX;
+        for (int g = kMostGroup; g >= 5; --g) {
+            const int used = (tiles + g - 1) / g * g;
+            if (used < best) {
+                best = used;
+                p.group = g;
+            }
+        }
+    }
+    const int nblk = (a->max_kv_len + kPagedKeys - 1) / kPagedKeys;
+    const int64_t groups = (int64_t)a->B * ((tiles + p.group - 1) / p.group), pairs = groups * nblk;
+    int64_t C = sms / p.group > 0 ? sms / p.group : 1;
+    if (a->num_splits > 0 && a->num_splits < C) C = a->num_splits;
+    if (C > pairs) C = pairs;
+    if (pairs / C > INT32_MAX / 2) return KDT_ERR_BAD_SHAPE;
+    p.shares = (int)C;
+    p.least = a->num_splits > 0 ? 1 : kLeastBlocks;
+    p.ctas = p.shares * p.group;
+    p.pieces = p.shares > 1 && nblk > 1;                      // a group of one block is never cut
     size_t off = 0;
     p.vis = a->parent != nullptr;
     if (p.vis) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
+    if (p.pieces) {
+        const size_t rows = (size_t)2 * p.ctas * p.tile;
+        p.po_off = off;
+        off = align_up(off + rows * kDc * sizeof(float));
+        p.pl_off = off;
+        off = align_up(off + rows * sizeof(float));
+        p.cuts_off = off;
+        off = align_up(off + (size_t)(p.shares + 1) * sizeof(PagedShare));
+    }
     p.ws_bytes = off;
-    p.launches = (p.vis ? 1 : 0) + 1;
+    p.launches = (p.vis ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
     *out = p;
     return KDT_OK;
 }
@@ -83,7 +120,7 @@ kdt_status kdt_verify_attn_paged_plan(const kdt_verify_paged_args *a, kdt_plan *
     const kdt_status st = make_plan(a, &p);
     if (st != KDT_OK) return st;
     out->impl = KDT_IMPL_TCGEN05;
-    out->num_splits = p.splits;
+    out->num_splits = p.shares;
     out->num_launches = p.launches;
     out->ctas = p.ctas;
     out->workspace_bytes = p.ws_bytes;
@@ -133,6 +170,15 @@ kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace
     q.out_bf16 = a->out_dtype == KDT_BF16;
     q.lse = a->lse;
     q.err = a->err;
+    q.tile = p.tile;
+    q.group = p.group;
+    q.shares = p.shares;
+    q.least = p.least;
+    q.pieces = p.pieces;
+    q.overlap_vis = p.vis;
+    q.part_o = reinterpret_cast<float *>(ws + p.po_off);
+    q.part_lse = reinterpret_cast<float *>(ws + p.pl_off);
+    q.cuts = reinterpret_cast<PagedShare *>(ws + p.cuts_off);
     return launch_verify_paged(q, stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
 
