@@ -1,9 +1,26 @@
 // One token a row under temperature, top-k, top-p and min-p, from given random numbers (kdt_sample).
 // See include/kdt.h for the definition: weights w = round(2^44 e^{(l - max) / temperature}), and every
-// filter keeps a prefix of the row's order (logit descending, index ascending).
+// filter keeps a prefix of the row's order (logit descending, index ascending), so that what is kept is
+// told by one key and a number: all logits above the key, and the first `number` tokens equal to it.
+//
+//  * A cluster of CTAs takes a row, each a contiguous slice, kept in shared memory where it fits.
+//  * Bins in the row's order, by the upper 16 bits of a logit's ordered bits (its bf16 value), counted in
+//    shared memory: 4096 of them from the maximum down, the values within 2^-6 of zero in one. In bf16 a
+//    bin is one value, so that the counts and one weight a bin give every sum exactly: top-k's and top-p's
+//    borders come from one scan. A float32 bin's tokens differ: where top-p needs masses their weights are
+//    summed (as two 32-bit halves), and the tokens of the bin that a border falls into are gathered in the
+//    first CTA, which halves the range of their keys.
+//  * The draw: every warp sums what is kept of its part of the slice (weights from the bins' table in
+//    bf16), the sums are scanned over warps and CTAs, and the part that holds u times the whole is taken
+//    apart again. All sums are integers: neither the cluster's size nor the order of the adds shows.
+//  * A bin with more tokens than the list holds (float32, thousands of nearly equal logits) is searched by
+//    the first CTA over the whole row.
 #include <math.h>
 
+#include <atomic>
+
 #include "sample_weights.cuh"
+#include "tc_ptx.cuh"
 
 namespace kdt {
 namespace {
@@ -11,6 +28,11 @@ namespace {
 using namespace weights;
 
 constexpr int kThreads = 1024, kWarps = 32;
+constexpr int kBins = 4096, kPerThread = kBins / kThreads;
+constexpr int kMaxCluster = 8;
+constexpr int kList = 4096, kHold = kList / kThreads; // tokens of one bin that a border falls into
+constexpr size_t kMostSmem = 200 * 1024;            // beside Shared
+constexpr uint32_t kPosTiny = 0xbc80u, kNegTiny = 0x437fu;     // upper ordered bits of 2^-6 and of -2^-6
 
 struct SampleParams {
     const void *logits;
@@ -22,6 +44,9 @@ struct SampleParams {
     int top_k_all;
     int32_t *token, *err;
     float *logp;
+    int slice;                                      // tokens a CTA takes (a multiple of 16)
+    int vec;                                        // rows start on 16-byte boundaries
+    int cache;                                      // a slice fits shared memory
 };
 
 __device__ __forceinline__ uint32_t order_key(float l) {           // ascending with the logit, one zero
@@ -31,12 +56,61 @@ __device__ __forceinline__ uint32_t order_key(float l) {           // ascending 
 
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
 
+// Bins in the row's order, the largest logit's first.
+struct Bins {
+    uint32_t top, low;                              // upper key bits of the maximum; of the first negative bin
+    int pos, neg;                                   // bins before the one around zero; and up to the negative ones
+    __device__ __forceinline__ void set(uint32_t max_key) {
+        top = max_key >> 16;
+        pos = top >= kPosTiny ? (int)(top - kPosTiny) + 1 : 0;
+        neg = pos + (top > kNegTiny ? 1 : 0);
+        low = min(top, kNegTiny);
+    }
+    __device__ __forceinline__ int of(uint32_t key) const {
+        const uint32_t h = key >> 16;
+        const int b = h >= kPosTiny ? (int)(top - h) : (h > kNegTiny ? pos : neg + (int)(low - h));
+        return min(b, kBins - 1);
+    }
+    // whether a bin holds one bf16 value only, and that value
+    __device__ __forceinline__ bool single(int b) const { return b < kBins - 1 && !(b == pos && neg > pos); }
+    __device__ __forceinline__ float value(int b) const {
+        const uint32_t h = b < pos ? top - (uint32_t)b : low - (uint32_t)(b - neg);
+        return key_logit(h & 0x8000u ? h << 16 : (h << 16) | 0xffffu);
+    }
+};
+
+struct Border {                                     // what a filter keeps: keys above `key`, and `ties` of it
+    uint32_t key;
+    uint32_t ties;
+};
+
 struct Shared {
     float2 tab[129 * kCopies];
     uint64_t part[kWarps];
+    uint32_t part2[kWarps];
+    float wm[kWarps];
+    // written by other CTAs of the cluster
+    float m[kMaxCluster];
+    uint64_t sum[kMaxCluster];                      // kept above the border, and ties, by CTA
+    uint32_t ties[kMaxCluster];
+    double z[kMaxCluster];
+    Border border;
+    uint64_t above;                                 // mass that the border keeps
+    // found by one thread of each CTA
+    int bin;
+    uint32_t before;                                // tokens, and
+    uint64_t mass_before;                           // mass, in front of that bin
+    uint32_t in_bin;
     uint64_t total;
-    float m[kWarps];
+    uint32_t list_n;
     int found;
+    uint64_t at;
+    uint32_t ties_at;
+    // settings and thresholds, found by one thread: an FP64 operation of all warps takes 500 clocks
+    float c_hi, c_lo;
+    int good;
+    uint64_t least, goal, t;
+    uint64_t turn[2][kWarps];                       // sums under way, by turn
 };
 
 template <typename T> __device__ __forceinline__ T warp_sum(T v) {
@@ -45,7 +119,7 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
-__device__ uint64_t block_sum(Shared &sh, uint64_t v) {
+__device__ __forceinline__ uint64_t block_sum(Shared &sh, uint64_t v) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     v = warp_sum(v);
     __syncthreads();
@@ -54,159 +128,659 @@ __device__ uint64_t block_sum(Shared &sh, uint64_t v) {
     return warp_sum(sh.part[lane]);
 }
 
-// Exclusive prefix sum over the threads; `total` gets the sum.
-__device__ uint64_t block_scan(Shared &sh, uint64_t v, uint64_t &total) {
+// Exclusive prefix sums of (a, c) over the threads; `ta`, `tc` get the sums.
+__device__ __forceinline__ void block_scan(Shared &sh, uint64_t a, uint32_t c, uint64_t &ea, uint32_t &ec, uint64_t &ta, uint32_t &tc) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t incl = v;
+    uint64_t ia = a;
+    uint32_t ic = c;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
+        const uint64_t x = __shfl_up_sync(0xffffffffu, ia, off);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, ic, off);
+        if (lane >= off) {
+            ia += x;
+            ic += y;
+        }
     }
     __syncthreads();
-    if (lane == 31) sh.part[warp] = incl;
-    __syncthreads();
-    uint64_t base = 0;
-    total = 0;
-    for (int k = 0; k < kWarps; ++k) {
-        if (k < warp) base += sh.part[k];
-        total += sh.part[k];
+    if (lane == 31) {
+        sh.part[warp] = ia;
+        sh.part2[warp] = ic;
     }
-    return base + incl - v;
+    __syncthreads();
+    const uint64_t pa = sh.part[lane];
+    const uint32_t pc = sh.part2[lane];
+    ea = warp_sum(lane < warp ? pa : 0) + ia - a;
+    ec = warp_sum(lane < warp ? pc : 0u) + ic - c;
+    ta = warp_sum(pa);
+    tc = warp_sum(pc);
 }
 
-// The simplest kernel that is right: a CTA a row, thresholds found by halving the range of keys.
+__device__ __forceinline__ void ld_cluster(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// w added to a 64-bit sum held as two words: the low word's old value tells the carry.
+__device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, uint64_t w) {
+    const uint32_t l = (uint32_t)w, old = atomicAdd(lo, l);
+    const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
+    if (h) atomicAdd(hi, h);
+}
+
+struct Dyn {                                        // dynamic shared memory
+    uint32_t count[kBins], lo[kBins], hi[kBins];    // tokens and mass of the slice's bins
+    uint64_t w[kBins];                              // a bf16 bin's weight
+};
+
 template <typename E>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const __grid_constant__ Exp2Table table) {
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, const __grid_constant__ Exp2Table table) {
+    extern __shared__ __align__(16) unsigned char dyn_raw[];
     __shared__ Shared sh;
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const E *x = static_cast<const E *>(p.logits) + (int64_t)r * p.row_stride;
+    Dyn &dy = *reinterpret_cast<Dyn *>(dyn_raw);
+    constexpr bool kSingle = sizeof(E) == 2;
+    uint64_t *list = reinterpret_cast<uint64_t *>(dyn_raw + sizeof(Dyn));
+    E *row = reinterpret_cast<E *>(dyn_raw + sizeof(Dyn) + kList * sizeof(uint64_t));
+    uint32_t rank, size;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    const int r = blockIdx.x / size, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int v0 = min((int)rank * p.slice, p.V), n = min(p.slice, p.V - v0);
+    const E *src = static_cast<const E *>(p.logits) + (int64_t)r * p.row_stride + v0;
     for (int k = tid; k < 129 * kCopies; k += kThreads) sh.tab[k] = make_float2(table.hi[k / kCopies], table.lo[k / kCopies]);
+    for (int k = tid; k < 3 * kBins / 4; k += kThreads) reinterpret_cast<uint4 *>(dyn_raw)[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) sh.list_n = 0;
     const float2 *tab = sh.tab + lane % kCopies;
-    const double temp = p.temperature ? (double)p.temperature[r] : p.temperature_all;
-    const double top_p = p.top_p ? (double)p.top_p[r] : p.top_p_all;
-    const double min_p = p.min_p ? (double)p.min_p[r] : p.min_p_all;
+    const double unit = 17592186044416.0;                      // 2^44
     int top_k = p.top_k ? p.top_k[r] : p.top_k_all;
-    if (top_k <= 0 || top_k > p.V) top_k = p.V;
-    const bool greedy = temp == 0.0;
+    const bool greedy = p.temperature ? p.temperature[r] == 0.f : p.temperature_all == 0.0;
     if (greedy) top_k = 1;
-    // the largest logit
+    const bool by_count = top_k > 0 && top_k < p.V, by_mass = !greedy && (p.top_p ? p.top_p[r] < 1.f : p.top_p_all < 1.0);
+    if (tid == kThreads - 1) {
+        const double temp = p.temperature ? (double)p.temperature[r] : p.temperature_all;
+        const double top_p = p.top_p ? (double)p.top_p[r] : p.top_p_all;
+        const double min_p = p.min_p ? (double)p.min_p[r] : p.min_p_all;
+        const double c = 1.4426950408889634074 / (greedy ? 1.0 : temp);
+        sh.c_hi = (float)c;
+        sh.c_lo = (float)(c - (double)sh.c_hi);
+        sh.least = (uint64_t)ceil(fmin(fmax(min_p, 0.0), 1.0) * unit);
+        sh.good = (greedy || (temp >= 1e-3 && temp <= 1e3)) && top_p == top_p && min_p == min_p;
+    }
+
+    // -- the largest logit (NaN wins), the slice to shared memory on the way
+    constexpr int kPer = 16 / (int)sizeof(E);
+    const int nv = n / kPer;
     float m = -INFINITY;
     bool nan = false;
-    for (int i = tid; i < p.V; i += kThreads) {
-        const float l = as_f32(x[i]);
-        nan |= l != l;
-        m = fmaxf(m, l);
+    auto see = [&](float x) {
+        nan |= x != x;
+        m = fmaxf(m, x);
+    };
+    if (p.vec) {
+#pragma unroll 4
+        for (int i = tid; i < nv; i += kThreads) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+            if (p.cache) reinterpret_cast<uint4 *>(row)[i] = v;
+            const E *e = reinterpret_cast<const E *>(&v);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) see(as_f32(e[k]));
+        }
+        for (int i = nv * kPer + tid; i < n; i += kThreads) {
+            if (p.cache) row[i] = src[i];
+            see(as_f32(src[i]));
+        }
+    } else {
+#pragma unroll 4
+        for (int i = tid; i < n; i += kThreads) {
+            const E v = src[i];
+            if (p.cache) row[i] = v;
+            see(as_f32(v));
+        }
     }
+    auto top = [](float a, float c) { return a != a ? a : (c != c ? c : fmaxf(a, c)); };
+    if (nan) m = __uint_as_float(0x7fffffffu);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) sh.m[warp] = m;
-    nan = __syncthreads_or(nan);
-    m = sh.m[lane];
+    for (int off = 16; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) sh.wm[warp] = m;
+    tc::cluster_sync();        // every CTA runs before another writes to its shared memory
+    if (warp == 0) {
+        m = sh.wm[lane];
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const bool settings = (greedy || (temp >= 1e-3 && temp <= 1e3)) && top_p == top_p && min_p == min_p;
-    if (nan || !settings || !(m > -INFINITY && m < INFINITY)) {
-        if (tid == 0) {
+        for (int off = 16; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (lane < (int)size) tc::st_cluster_f32(tc::map_to_rank(&sh.m[rank], (uint32_t)lane), m);
+    }
+    tc::cluster_sync();
+    m = lane < (int)size ? sh.m[lane] : -INFINITY;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (!sh.good || !(m > -INFINITY && m < INFINITY)) {      // (the cluster as one)
+        if (rank == 0 && tid == 0) {
             p.token[r] = -1;
             if (p.logp) p.logp[r] = 0.f;
             record_error(p.err, r + 1);
         }
         return;
     }
-    const double c = 1.4426950408889634074 / (greedy ? 1.0 : temp);
-    const float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
+    const E *data = p.cache ? row : src;
+    const float c_hi = sh.c_hi, c_lo = sh.c_lo;
+    const uint64_t least = sh.least;
     auto w_of = [&](float l) { return weight(l, m, c_hi, c_lo, tab); };
-    // tokens, or their mass, of key x0 or more
-    auto count = [&](uint32_t x0) {
-        uint64_t n = 0;
-        for (int i = tid; i < p.V; i += kThreads) n += order_key(as_f32(x[i])) >= x0;
-        return block_sum(sh, n);
+    Bins bins;
+    bins.set(order_key(m));
+    // every token of the slice, 16 bytes at a time where they can be had so
+    auto each = [&](auto &&f) {
+        if (p.cache || p.vec) {
+#pragma unroll 2
+            for (int i = tid; i < nv; i += kThreads) {
+                const uint4 v = reinterpret_cast<const uint4 *>(data)[i];
+                const E *e = reinterpret_cast<const E *>(&v);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) f(as_f32(e[k]), i * kPer + k);
+            }
+            for (int i = nv * kPer + tid; i < n; i += kThreads) f(as_f32(data[i]), i);
+        } else
+            for (int i = tid; i < n; i += kThreads) f(as_f32(data[i]), i);
     };
-    auto mass = [&](uint32_t x0) {
-        uint64_t s = 0;
-        for (int i = tid; i < p.V; i += kThreads) {
-            const float l = as_f32(x[i]);
-            if (order_key(l) >= x0) s += w_of(l);
+
+    // -- tokens a bin; in float32 also the sum of all weights, good enough for a log-probability
+    double z = 0.0;
+    if (!kSingle && p.logp && !greedy) {
+        float zf = 0.f;
+        int k = 0;
+        each([&](float l, int) {
+            const float d = l - m, y = d * c_hi, e = ex2(y);
+            zf += y < -60.f ? 0.f : fmaf(e, 0.6931471805599453f * fmaf(d, c_lo, fmaf(d, c_hi, -y)), e);
+            if (++k == 16) {
+                z += (double)zf;
+                zf = 0.f;
+                k = 0;
+            }
+        });
+        z += (double)zf;
+    }
+    Border border = {0u, (uint32_t)p.V};                       // everything
+    if (greedy) border = {order_key(m), 1u};
+    const bool table_w = kSingle && !greedy;                   // bins have weights
+    if (!greedy && (kSingle || by_count || by_mass)) {
+        if (kSingle || by_count) {
+            each([&](float l, int) {
+                const int b = bins.of(order_key(l));
+                atomicAdd(&dy.count[b], 1u);
+                if (kSingle && !bins.single(b)) add_to(&dy.lo[b], &dy.hi[b], w_of(l));
+            });
         }
-        return block_sum(sh, s);
-    };
-    // -- kept so far: keys above kx, and the first kr tokens (by index) of key kx
-    uint32_t kx = order_key(m);
-    uint64_t kr = 1;
-    if (!greedy) {
-        uint32_t lo = 0, hi = order_key(m);             // the largest key with top_k tokens at or above it
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (count(mid) >= (uint64_t)top_k) lo = mid;
-            else hi = mid - 1;
+        if (!kSingle && by_mass && !by_count) {
+            each([&](float l, int) {
+                const int b = bins.of(order_key(l));
+                atomicAdd(&dy.count[b], 1u);
+                add_to(&dy.lo[b], &dy.hi[b], w_of(l));
+            });
         }
-        kx = lo;
-        kr = (uint64_t)top_k - (kx == 0xffffffffu ? 0 : count(kx + 1));
-        if (top_p < 1.0) {
-            const uint64_t above = mass(kx + 1);
-            const double goal = fmax(top_p, 0.0) * (double)(above + kr * w_of(key_logit(kx)));
-            if (goal <= (double)above || kx == order_key(m)) {
-                uint32_t a = kx, e = order_key(m);      // the largest key with the goal's mass at or above it
-                while (a < e) {
-                    const uint32_t mid = a + (e - a + 1) / 2;
-                    if ((double)mass(mid) >= goal) a = mid;
-                    else e = mid - 1;
+        // the bins of the whole row, four a thread: tokens and mass
+        uint32_t cnt[kPerThread];
+        uint64_t mass[kPerThread];
+        auto collect = [&]() {
+            tc::cluster_sync();
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) {
+                cnt[k] = 0;
+                mass[k] = 0;
+            }
+            static_assert(kPerThread == 4, "a thread's bins are one 16-byte load");
+            for (uint32_t o = 0; o < size; ++o) {
+                uint32_t a[4], l[4], h[4];
+                ld_cluster(tc::map_to_rank(&dy.count[4 * tid], o), a);
+                ld_cluster(tc::map_to_rank(&dy.lo[4 * tid], o), l);
+                ld_cluster(tc::map_to_rank(&dy.hi[4 * tid], o), h);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    cnt[k] += a[k];
+                    mass[k] += ((uint64_t)h[k] << 32) + l[k];
                 }
-                const uint64_t wx = w_of(key_logit(a)), up = mass(a + 1);
-                const uint64_t most = a == kx ? kr : (uint64_t)p.V;
-                uint64_t n = 1;
-                if (wx > 0 && goal > (double)up) {
-                    n = (uint64_t)fmax((goal - (double)up) / (double)wx, 1.0);
-                    while (n > 1 && (double)(up + (n - 1) * wx) >= goal) --n;
-                    while ((double)(up + n * wx) < goal && n < most) ++n;
+            }
+        };
+        collect();
+        if (table_w) {
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) {
+                const int b = 4 * tid + k;
+                if (cnt[k] && bins.single(b)) {
+                    const uint64_t w = w_of(bins.value(b));
+                    dy.w[b] = w;
+                    mass[k] = w * cnt[k];
                 }
-                kx = a;
-                kr = n < most ? n : most;
+            }
+        }
+        uint64_t ma, mt;
+        uint32_t ca, ct;
+        uint64_t sm = mass[0] + mass[1] + mass[2] + mass[3];
+        uint32_t sc = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+        block_scan(sh, sm, sc, ma, ca, mt, ct);
+        const uint64_t z_all = mt;                             // (bf16: every token's weight)
+        if (kSingle && rank == 0 && tid == 0) z = (double)z_all / unit;
+        // the bin that holds the last token of `want`, or the first with `goal` of mass up to and with it
+        auto find_count = [&](uint32_t want) {
+            uint32_t b0 = ca;
+            uint64_t m0 = ma;
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) {
+                if (b0 < want && want <= b0 + cnt[k]) {
+                    sh.bin = 4 * tid + k;
+                    sh.before = b0;
+                    sh.mass_before = m0;
+                    sh.in_bin = cnt[k];
+                }
+                b0 += cnt[k];
+                m0 += mass[k];
+            }
+            __syncthreads();
+        };
+        auto find_mass = [&](uint64_t goal) {
+            uint32_t b0 = ca;
+            uint64_t m0 = ma;
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) {
+                const bool was = b0 > 0 && m0 >= goal, is = m0 + mass[k] >= goal;
+                if (cnt[k] && is && !was) {
+                    sh.bin = 4 * tid + k;
+                    sh.before = b0;
+                    sh.mass_before = m0;
+                    sh.in_bin = cnt[k];
+                }
+                b0 += cnt[k];
+                m0 += mass[k];
+            }
+            __syncthreads();
+        };
+        // the tokens of bin b to the first CTA, as (key, token)
+        auto gather = [&](int b) {
+            tc::cluster_sync();                                // (the list before has been read)
+            if (rank == 0 && tid == 0) sh.list_n = 0;
+            tc::cluster_sync();
+            const uint32_t counter = tc::map_to_rank(&sh.list_n, 0), base = tc::map_to_rank(list, 0);
+            each([&](float l, int i) {
+                const uint32_t key = order_key(l);
+                if (bins.of(key) == b) {
+                    uint32_t at;
+                    asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(counter) : "memory");
+                    if (at < kList) st_cluster(base + 8 * at, ((uint64_t)key << 32) | (uint32_t)(v0 + i));
+                }
+            });
+            tc::cluster_sync();
+        };
+        // ties of weight wx to keep so that `up` and they reach the goal: one at least, `cap` at most
+        auto ties_for = [&](uint64_t goal, uint64_t up, uint64_t wx, uint64_t cap) -> uint64_t {
+            if (wx == 0 || goal <= up) return 1;
+            return min((goal - up + wx - 1) / wx, cap);
+        };
+        // What the cluster is told: the border, and the mass up to and with it.
+        auto tell = [&](uint32_t key, uint64_t ties, uint64_t kept) {
+            if (tid < (int)size) {
+                const uint32_t d = tc::map_to_rank(&sh.border, (uint32_t)tid);
+                st_cluster(d, key);
+                st_cluster(d + 4, (uint32_t)ties);
+                st_cluster(tc::map_to_rank(&sh.above, (uint32_t)tid), kept);
+            }
+        };
+        // In the first CTA: of the listed tokens in order the least number with `want` tokens, or (want 0) with a mass
+        // that with `before` reaches the goal, of those that `most` keeps. The range of keys is halved, the tokens in
+        // registers.
+        auto select = [&](uint32_t want, uint64_t goal, uint64_t before, const Border &most) {
+            if (rank == 0) {
+                const uint32_t ln = sh.list_n;
+                uint32_t lo = 0u, hi = order_key(m);
+                if (bins.single(sh.bin)) {                     // its keys share their upper half
+                    const uint32_t h = sh.bin < bins.pos ? bins.top - (uint32_t)sh.bin : bins.low - (uint32_t)(sh.bin - bins.neg);
+                    lo = h << 16;
+                    hi = min(hi, lo | 0xffffu);
+                }
+                lo = max(lo, most.key);
+                uint32_t key[kHold];
+                uint64_t w[kHold];
+                uint32_t t = 0;
+#pragma unroll
+                for (int k = 0; k < kHold; ++k) {
+                    const uint32_t i = tid + k * kThreads;
+                    key[k] = i < ln ? (uint32_t)(list[i] >> 32) : 0u;
+                    w[k] = 0;
+                    if (__any_sync(0xffffffffu, i < ln)) w[k] = w_of(key_logit(key[k]));
+                    if (i >= ln || key[k] < most.key) {
+                        key[k] = 0u;                           // (below every key: order keys of numbers are not 0)
+                        w[k] = 0;
+                    }
+                    if (key[k] && key[k] == most.key) {
+                        ++t;
+                        w[k] = 0;                              // counted by `equal`
+                    }
+                }
+                uint64_t equal = 0;
+                if (most.key) equal = min(block_sum(sh, (uint64_t)t), (uint64_t)most.ties) * w_of(key_logit(most.key));
+                int turn = 0;
+                auto measure = [&](uint32_t x, bool mm) -> uint64_t {      // of keys x and above
+                    uint64_t s = 0;
+#pragma unroll
+                    for (int k = 0; k < kHold; ++k) s += key[k] >= x && key[k] ? (mm ? w[k] : 1) : 0;
+                    s = warp_sum(s);
+                    if (lane == 0) sh.turn[turn][warp] = s;
+                    __syncthreads();
+                    s = warp_sum(sh.turn[turn][lane]);
+                    turn ^= 1;
+                    return s + (mm && x <= most.key ? equal : 0);
+                };
+                const bool mm = want == 0;
+                while (lo < hi) {                              // the largest key with enough at or above it
+                    const uint32_t mid = lo + (hi - lo + 1) / 2;
+                    const uint64_t s = measure(mid, mm);
+                    if (mm ? before + s >= goal : s >= want) lo = mid;
+                    else hi = mid - 1;
+                }
+                const uint64_t up = lo == 0xffffffffu ? 0 : measure(lo + 1, mm), wx = w_of(key_logit(lo));
+                const uint64_t ties = mm ? ties_for(goal, before + up, wx, lo == most.key ? most.ties : 0xffffffffu) : want - up;
+                const uint64_t up_mass = mm ? up : (lo == 0xffffffffu ? 0 : measure(lo + 1, true));
+                tell(lo, ties, before + up_mass + ties * wx);
+            }
+            tc::cluster_sync();
+        };
+        // the same over the whole row, for bins that the list cannot hold
+        auto search_row = [&](uint32_t want, uint64_t goal, const Border &most) {
+            if (rank == 0) {
+                const E *whole = src;                          // (rank 0's slice starts the row)
+                auto measure = [&](uint32_t x, bool mm) -> uint64_t {
+                    uint64_t s = 0, t = 0;
+                    for (int i = tid; i < p.V; i += kThreads) {
+                        const float l = as_f32(whole[i]);
+                        const uint32_t k = order_key(l);
+                        if (k < x || k < most.key) continue;
+                        if (!mm) ++s;
+                        else if (k == most.key) ++t;
+                        else s += w_of(l);
+                    }
+                    s = block_sum(sh, s);
+                    if (mm) {
+                        t = block_sum(sh, t);
+                        if (t) s += min(t, (uint64_t)most.ties) * w_of(key_logit(most.key));
+                    }
+                    return s;
+                };
+                const bool mm = want == 0;
+                uint32_t lo = most.key, hi = order_key(m);
+                while (lo < hi) {
+                    const uint32_t mid = lo + (hi - lo + 1) / 2;
+                    const uint64_t s = measure(mid, mm);
+                    if (mm ? s >= goal : s >= want) lo = mid;
+                    else hi = mid - 1;
+                }
+                const uint64_t up = lo == 0xffffffffu ? 0 : measure(lo + 1, mm), wx = w_of(key_logit(lo));
+                const uint64_t ties = mm ? ties_for(goal, up, wx, lo == most.key ? most.ties : 0xffffffffu) : want - up;
+                const uint64_t up_mass = mm ? up : (lo == 0xffffffffu ? 0 : measure(lo + 1, true));
+                tell(lo, ties, up_mass + ties * wx);
+            }
+            tc::cluster_sync();
+        };
+        uint64_t kept_mass = mt;                               // of the top-k's tokens
+        if (by_count) {
+            find_count((uint32_t)top_k);
+            const int b = sh.bin;
+            if (kSingle && bins.single(b)) {
+                border = {order_key(bins.value(b)), (uint32_t)top_k - sh.before};
+                if (by_mass) kept_mass = sh.mass_before + (uint64_t)border.ties * w_of(bins.value(b));
+            } else if (sh.in_bin <= kList) {
+                gather(b);
+                const uint64_t before = kSingle ? sh.mass_before : 0;
+                select((uint32_t)top_k - sh.before, 0, before, Border{0u, 0u});
+                border = sh.border;
+                kept_mass = sh.above;
             } else {
-                const uint64_t wx = w_of(key_logit(kx));
-                uint64_t n = kr;
-                while (n > 1 && (double)(above + (n - 1) * wx) >= goal) --n;
-                kr = n;
+                search_row((uint32_t)top_k, 0, Border{0u, 0u});
+                border = sh.border;
+                kept_mass = sh.above;
+            }
+            if (!kSingle && by_mass) {                         // the masses of what top-k keeps, the border's bin whole
+                const int last = bins.of(border.key);
+                each([&](float l, int) {
+                    const int q = bins.of(order_key(l));
+                    if (q < last) add_to(&dy.lo[q], &dy.hi[q], w_of(l));
+                });
+                __syncthreads();
+                collect();
+                sm = mass[0] + mass[1] + mass[2] + mass[3];
+                block_scan(sh, sm, sc, ma, ca, mt, ct);
+                // (bins up to the border's are summed; the border's own kept mass is the list's, or the row's)
+                kept_mass = sh.in_bin <= kList ? mt + sh.above : sh.above;
+#pragma unroll
+                for (int k = 0; k < kPerThread; ++k)
+                    if (4 * tid + k == last) mass[k] = kept_mass - mt;
+                __syncthreads();
+                if (tid == last / 4) sm += kept_mass - mt;
+                block_scan(sh, sm, sc, ma, ca, mt, ct);
+            }
+        }
+        if (by_mass) {
+            if (tid == 0) {
+                const double top_p = p.top_p ? (double)p.top_p[r] : p.top_p_all;
+                sh.goal = (uint64_t)ceil(fmax(top_p, 0.0) * (double)kept_mass);
+            }
+            __syncthreads();
+            const uint64_t goal = sh.goal;
+            find_mass(goal);
+            const int b = sh.bin;
+            const Border most = by_count ? border : Border{0u, (uint32_t)p.V};
+            if (kSingle && bins.single(b)) {
+                const uint64_t wx = w_of(bins.value(b)), up = sh.mass_before;
+                const uint32_t key = order_key(bins.value(b));
+                const uint64_t cap = key == most.key ? most.ties : sh.in_bin;
+                border = {key, (uint32_t)ties_for(goal, up, wx, cap)};
+            } else {
+                if (sh.in_bin <= kList) {
+                    gather(b);
+                    select(0u, goal, sh.mass_before, most);
+                } else
+                    search_row(0u, goal, most);
+                border = sh.border;
             }
         }
     }
-    const double least = fmin(fmax(min_p, 0.0), 1.0) * 17592186044416.0;
-    // -- the draw, tokens in index order
-    const int per = (p.V + kThreads - 1) / kThreads, i0 = min(tid * per, p.V), i1 = min(i0 + per, p.V);
-    uint64_t equal = 0, all;
-    for (int i = i0; i < i1; ++i) equal += order_key(as_f32(x[i])) == kx;
-    const uint64_t equal0 = block_scan(sh, equal, all);
-    auto kept = [&](int i, uint64_t &e) -> uint64_t {
-        const float l = as_f32(x[i]);
-        const uint32_t k = order_key(l);
-        const bool in = k > kx || (k == kx && e < kr);
-        e += k == kx;
-        const uint64_t w = in ? w_of(l) : 0;
-        return (double)w >= least ? w : 0;
+    __syncthreads();
+
+    // -- what is kept of each warp's part: mass above the border, and its ties
+    const int part = (p.slice / 16 + kWarps - 1) / kWarps * 16;
+    const uint64_t wx = w_of(key_logit(border.key));
+    const bool ties_kept = wx >= least;
+    auto weigh = [&](float l, uint32_t key) -> uint64_t {
+        uint64_t w;
+        if (table_w) {
+            const int b = bins.of(key);
+            w = bins.single(b) ? dy.w[b] : w_of(l);
+        } else
+            w = w_of(l);
+        return w >= least ? w : 0;
     };
-    uint64_t e = equal0, mine = 0, z = 0;
-    for (int i = i0; i < i1; ++i) {
-        mine += kept(i, e);
-        z += w_of(as_f32(x[i]));
-    }
-    z = block_sum(sh, z);
-    const uint64_t before = block_scan(sh, mine, all);
-    const double td = (double)p.u[r] * (double)all;
-    uint64_t t = td > 0.0 ? (uint64_t)td : 0;
-    if (t >= all) t = all - 1;
-    if (t >= before && t < before + mine) {
-        uint64_t acc = before;
-        e = equal0;
-        int i = i0;
-        for (; i < i1; ++i) {
-            acc += kept(i, e);
-            if (acc > t) break;
+    auto measure = [&](int i0, int i1, uint64_t &sum, uint32_t &ties) {      // (a warp's lanes side by side)
+        uint64_t s = 0;
+        uint32_t t = 0;
+#pragma unroll 4
+        for (int i = i0 + lane; i < i1; i += 32) {
+            const float l = as_f32(data[i]);
+            const uint32_t key = order_key(l);
+            t += key == border.key;
+            if (key > border.key) s += weigh(l, key);
         }
-        p.token[r] = i;
-        if (p.logp)
-            p.logp[r] = greedy ? 0.f : (float)(((double)as_f32(x[i]) - (double)m) / temp - log((double)z / 17592186044416.0));
+        sum = warp_sum(s);
+        ties = warp_sum(t);
+    };
+    uint64_t sum;
+    uint32_t ties;
+    const int w0 = min(warp * part, n), w1 = min(w0 + part, n);
+    measure(w0, w1, sum, ties);
+    __syncthreads();
+    if (lane == 0) {
+        sh.part[warp] = sum;
+        sh.part2[warp] = ties;
     }
+    if (!kSingle) z = warp_sum(z);
+    __shared__ double zs[kWarps];
+    if (lane == 0) zs[warp] = z;
+    __syncthreads();
+    if (warp == 0) {
+        const uint64_t s = warp_sum(sh.part[lane]);
+        const uint32_t t = warp_sum(sh.part2[lane]);
+        const double zz = warp_sum(zs[lane]);
+        if (lane < (int)size) {
+            st_cluster(tc::map_to_rank(&sh.sum[rank], (uint32_t)lane), s);
+            st_cluster(tc::map_to_rank(&sh.ties[rank], (uint32_t)lane), t);
+            st_cluster(tc::map_to_rank(&sh.z[rank], (uint32_t)lane), (uint64_t)__double_as_longlong(zz));
+        }
+    }
+    tc::cluster_sync();
+    // ties are kept in index order: `left` of them from a place on
+    auto of_ties = [&](uint32_t left, uint32_t t) { return ties_kept ? (uint64_t)min(left, t) * wx : 0; };
+    uint64_t all = 0, before = 0, mine = 0;
+    uint32_t left = border.ties, left_mine = 0;
+    for (uint32_t o = 0; o < size; ++o) {
+        const uint64_t k = sh.sum[o] + of_ties(left, sh.ties[o]);
+        if (o == rank) {
+            before = all;
+            mine = k;
+            left_mine = left;
+        }
+        all += k;
+        left -= min(left, sh.ties[o]);
+    }
+    if (tid == 0) {
+        const double td = (double)p.u[r] * (double)all;
+        const uint64_t t = td > 0.0 ? (uint64_t)td : 0;
+        sh.t = t >= all ? all - 1 : t;
+    }
+    __syncthreads();
+    uint64_t t = sh.t;
+    if (t < before || t >= before + mine) return;              // another CTA's (nothing of this one is read from now on)
+    t -= before;
+    // which warp's part, then which of its 32 pieces, then which token
+    auto locate = [&](uint64_t base, uint32_t lf) {            // by every warp alike, over sh.part and sh.part2
+        const uint64_t s = sh.part[lane];
+        const uint32_t q = sh.part2[lane];
+        uint32_t iq = q;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, iq, off);
+            if (lane >= off) iq += y;
+        }
+        const uint32_t lf0 = lf - min(lf, iq - q);
+        uint64_t k = s + of_ties(lf0, q), ik = k;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, ik, off);
+            if (lane >= off) ik += y;
+        }
+        const bool here = t >= base + ik - k && t < base + ik;
+        const int o = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        __syncthreads();
+        if (warp == 0 && lane == o) {
+            sh.found = o;
+            sh.at = base + ik - k;
+            sh.ties_at = lf0;
+        }
+        __syncthreads();
+    };
+    locate(0, left_mine);
+    const int p0 = min(sh.found * part, n), p1 = min(p0 + part, n), piece = (p1 - p0 + kWarps - 1) / kWarps;
+    uint64_t base = sh.at;
+    uint32_t lf = sh.ties_at;
+    const int q0 = min(p0 + warp * piece, p1), q1 = min(q0 + piece, p1);
+    measure(q0, q1, sum, ties);
+    __syncthreads();
+    if (lane == 0) {
+        sh.part[warp] = sum;
+        sh.part2[warp] = ties;
+    }
+    __syncthreads();
+    locate(base, lf);
+    if (warp != sh.found) return;
+    base = sh.at;
+    lf = sh.ties_at;
+    for (int i0 = q0; i0 < q1; i0 += 32) {
+        const int i = i0 + lane;
+        const float l = i < q1 ? as_f32(data[i]) : -INFINITY;
+        const uint32_t key = order_key(l);
+        const bool tie = i < q1 && key == border.key;
+        const uint32_t tm = __ballot_sync(0xffffffffu, tie), tb = __popc(tm & ((1u << lane) - 1));
+        uint64_t w = 0;
+        if (i < q1 && key > border.key) w = weigh(l, key);
+        if (tie && tb < lf && ties_kept) w = wx;
+        uint64_t ik = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, ik, off);
+            if (lane >= off) ik += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + ik > t);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                p.token[r] = v0 + i;
+                if (p.logp) {
+                    double zz = 0.0;
+                    for (uint32_t o = 0; o < size; ++o) zz += sh.z[o];
+                    const double temp = p.temperature ? (double)p.temperature[r] : p.temperature_all;
+                    p.logp[r] = greedy ? 0.f : (float)(((double)l - (double)m) / temp - log(zz));
+                }
+            }
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, ik, 31);
+        lf -= min(lf, (uint32_t)__popc(tm));
+    }
+}
+
+// Clusters of C CTAs that the device holds at once.
+template <typename E> int resident(cudaLaunchConfig_t cfg, int C) {
+    static std::atomic<int> cached[64][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) dev = 0;
+    std::atomic<int> &slot = cached[dev & 63][C];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.dynamicSmemBytes = kMostSmem;
+    cfg.attrs[0].val.clusterDim.x = (unsigned)C;
+    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<E>, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();                                    // clear the query's error
+        return sm_count() / C;
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <typename E> cudaError_t launch(SampleParams p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kMaxCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    // CTAs a row: as many as the device holds at once for the batch, of 2048 tokens or more each
+    int C = kMaxCluster;
+    while (C > 1 && (p.V < 2048 * C || p.R > resident<E>(cfg, C))) C >>= 1;
+    p.slice = ((p.V + C - 1) / C + 15) / 16 * 16;
+    const size_t fixed = sizeof(Dyn) + kList * sizeof(uint64_t), slice = (size_t)p.slice * sizeof(E);
+    p.cache = fixed + slice <= kMostSmem;
+    at[0].val.clusterDim.x = (unsigned)C;
+    cfg.gridDim = dim3((unsigned)(p.R * C));
+    cfg.dynamicSmemBytes = fixed + (p.cache ? slice : 0);
+    static const Exp2Table table = make_table();
+    return cudaLaunchKernelEx(&cfg, sample_kernel<E>, p, table);
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -236,12 +810,9 @@ extern "C" kdt_status kdt_sample(const kdt_sample_args *a, cudaStream_t stream) 
         {a->logits, a->u, a->temperature, a->top_k, a->top_p, a->min_p, a->token, a->logp, a->err});
     if (st != KDT_OK) return st;
     if (a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t), stream) != cudaSuccess) return KDT_ERR_CUDA;
-    const SampleParams p = {a->logits, stride, a->R, a->V, a->u, a->temperature, a->top_p, a->min_p, a->top_k, a->temperature_all,
-                            a->top_p_all, a->min_p_all, a->top_k_all, a->token, a->err, a->logp};
-    static const Exp2Table table = make_table();
-    if (a->dtype == KDT_F32)
-        sample_kernel<float><<<a->R, kThreads, 0, stream>>>(p, table);
-    else
-        sample_kernel<__nv_bfloat16><<<a->R, kThreads, 0, stream>>>(p, table);
-    return cudaGetLastError() == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+    SampleParams p = {a->logits, stride, a->R, a->V, a->u, a->temperature, a->top_p, a->min_p, a->top_k, a->temperature_all,
+                            a->top_p_all, a->min_p_all, a->top_k_all, a->token, a->err, a->logp, 0, 0, 0};
+    p.vec = aligned(a->logits, 16) && (stride * esz) % 16 == 0;
+    const cudaError_t e = a->dtype == KDT_F32 ? launch<float>(p, stream) : launch<__nv_bfloat16>(p, stream);
+    return e == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
 }
