@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "sample_weights.cuh"
 #include "tc_ptx.cuh"
@@ -28,9 +29,10 @@ namespace {
 using namespace weights;
 
 constexpr int kThreads = 1024, kWarps = 32;
-constexpr int kBins = 4096, kPerThread = kBins / kThreads;
+constexpr int kBins = 4096;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 4096, kHold = kList / kThreads; // tokens of one bin that a border falls into
+constexpr int kList = 2048, kHold = kList / kThreads; // tokens of one bin that a border falls into
+constexpr uint32_t kShort = 256;                    // as many are ranked, a thread each
 constexpr size_t kMostSmem = 200 * 1024;            // beside Shared
 constexpr uint32_t kPosTiny = 0xbc80u, kNegTiny = 0x437fu;     // upper ordered bits of 2^-6 and of -2^-6
 
@@ -93,16 +95,16 @@ struct Shared {
     float m[kMaxCluster];
     uint64_t sum[kMaxCluster];                      // kept above the border, and ties, by CTA
     uint32_t ties[kMaxCluster];
-    double z[kMaxCluster];
-    Border border;
-    uint64_t above;                                 // mass that the border keeps
-    // found by one thread of each CTA
-    int bin;
-    uint32_t before;                                // tokens, and
-    uint64_t mass_before;                           // mass, in front of that bin
-    uint32_t in_bin;
-    uint64_t total;
-    uint32_t list_n;
+    uint64_t z[kMaxCluster];
+    Border border[2];                               // top-k's, top-p's
+    uint64_t above[2];                              // mass that the border keeps
+    uint64_t mass_of[kMaxCluster];                  // of the CTAs' shares of the bins
+    uint32_t count_of[kMaxCluster];
+    int bin[2];                                     // where a border falls
+    uint32_t before[2], in_bin[2];                  // tokens in front of it, and in it
+    uint64_t mass_before[2];
+    uint32_t list_n[2];
+    // of this CTA
     int found;
     uint64_t at;
     uint32_t ties_at;
@@ -110,7 +112,6 @@ struct Shared {
     float c_hi, c_lo;
     int good;
     uint64_t least, goal, t;
-    uint64_t turn[2][kWarps];                       // sums under way, by turn
 };
 
 template <typename T> __device__ __forceinline__ T warp_sum(T v) {
@@ -156,12 +157,6 @@ __device__ __forceinline__ void block_scan(Shared &sh, uint64_t a, uint32_t c, u
     tc = warp_sum(pc);
 }
 
-__device__ __forceinline__ void ld_cluster(uint32_t addr, uint32_t (&v)[4]) {
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
@@ -175,10 +170,25 @@ __device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, uint64_t w) {
     const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
     if (h) atomicAdd(hi, h);
 }
+// The same in another CTA of the cluster, by shared::cluster addresses.
+__device__ __forceinline__ uint32_t add_cluster(uint32_t addr, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ void add_to_cluster(uint32_t lo, uint32_t hi, uint64_t w) {
+    const uint32_t l = (uint32_t)w, old = add_cluster(lo, l);
+    const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
+    if (h) add_cluster(hi, h);
+}
 
-struct Dyn {                                        // dynamic shared memory
-    uint32_t count[kBins], lo[kBins], hi[kBins];    // tokens and mass of the slice's bins
-    uint64_t w[kBins];                              // a bf16 bin's weight
+// Dynamic shared memory. The slice's bins are counted here (their weights' sums where a bin has several values), then
+// added up in the CTA whose share of the bins they fall into.
+struct Dyn {
+    uint32_t count[kBins], lo[kBins], hi[kBins];    // of the slice
+    uint32_t all_count[kBins], all_lo[kBins], all_hi[kBins];       // of the row: this CTA's share
+    uint64_t w[kBins];                              // bf16: a bin's weight
+    uint64_t list_w[kShort];                        // of a short list's tokens
 };
 
 template <typename E>
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     Dyn &dy = *reinterpret_cast<Dyn *>(dyn_raw);
     constexpr bool kSingle = sizeof(E) == 2;
     uint64_t *list = reinterpret_cast<uint64_t *>(dyn_raw + sizeof(Dyn));
-    E *row = reinterpret_cast<E *>(dyn_raw + sizeof(Dyn) + kList * sizeof(uint64_t));
+    E *row = reinterpret_cast<E *>(dyn_raw + sizeof(Dyn) + 2 * kList * sizeof(uint64_t));
     uint32_t rank, size;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
@@ -196,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     const int v0 = min((int)rank * p.slice, p.V), n = min(p.slice, p.V - v0);
     const E *src = static_cast<const E *>(p.logits) + (int64_t)r * p.row_stride + v0;
     for (int k = tid; k < 129 * kCopies; k += kThreads) sh.tab[k] = make_float2(table.hi[k / kCopies], table.lo[k / kCopies]);
-    for (int k = tid; k < 3 * kBins / 4; k += kThreads) reinterpret_cast<uint4 *>(dyn_raw)[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid == 0) sh.list_n = 0;
+    for (int k = tid; k < 6 * kBins / 4; k += kThreads) reinterpret_cast<uint4 *>(dyn_raw)[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2) sh.list_n[tid] = 0;
     const float2 *tab = sh.tab + lane % kCopies;
     const double unit = 17592186044416.0;                      // 2^44
     int top_k = p.top_k ? p.top_k[r] : p.top_k_all;
@@ -278,20 +288,26 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     // every token of the slice, 16 bytes at a time where they can be had so
     auto each = [&](auto &&f) {
         if (p.cache || p.vec) {
-#pragma unroll 2
-            for (int i = tid; i < nv; i += kThreads) {
-                const uint4 v = reinterpret_cast<const uint4 *>(data)[i];
-                const E *e = reinterpret_cast<const E *>(&v);
+            for (int i0 = tid; i0 < nv; i0 += 4 * kThreads) {
+                uint4 v[4];                                    // (their latency is what a pass takes)
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) f(as_f32(e[k]), i * kPer + k);
+                for (int u = 0; u < 4; ++u)
+                    if (i0 + u * kThreads < nv) v[u] = reinterpret_cast<const uint4 *>(data)[i0 + u * kThreads];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (i0 + u * kThreads >= nv) break;
+                    const E *e = reinterpret_cast<const E *>(&v[u]);
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) f(as_f32(e[k]), (i0 + u * kThreads) * kPer + k);
+                }
             }
             for (int i = nv * kPer + tid; i < n; i += kThreads) f(as_f32(data[i]), i);
         } else
             for (int i = tid; i < n; i += kThreads) f(as_f32(data[i]), i);
     };
 
-    // -- tokens a bin; in float32 also the sum of all weights, good enough for a log-probability
-    double z = 0.0;
+    // -- tokens a bin; in float32 also the sum of all weights in units of 2^-40, good enough for a log-probability
+    uint64_t z = 0;
     if (!kSingle && p.logp && !greedy) {
         float zf = 0.f;
         int k = 0;
@@ -299,12 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             const float d = l - m, y = d * c_hi, e = ex2(y);
             zf += y < -60.f ? 0.f : fmaf(e, 0.6931471805599453f * fmaf(d, c_lo, fmaf(d, c_hi, -y)), e);
             if (++k == 16) {
-                z += (double)zf;
+                z += (uint64_t)(zf * 1099511627776.f);
                 zf = 0.f;
                 k = 0;
             }
         });
-        z += (double)zf;
+        z += (uint64_t)(zf * 1099511627776.f);
     }
     Border border = {0u, (uint32_t)p.V};                       // everything
     if (greedy) border = {order_key(m), 1u};
@@ -324,156 +340,187 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 add_to(&dy.lo[b], &dy.hi[b], w_of(l));
             });
         }
-        // the bins of the whole row, four a thread: tokens and mass
-        uint32_t cnt[kPerThread];
-        uint64_t mass[kPerThread];
-        auto collect = [&]() {
+        // the row's bins: each CTA adds what it counted to the CTAs whose share of the bins that is
+        const int share = kBins / (int)size, first = (int)rank * share, per = (share + kThreads - 1) / kThreads;
+        auto push = [&](bool counts, int from, int to) {           // (behind a barrier)
+            for (int b = from + tid; b < to; b += kThreads) {
+                const uint32_t o = (uint32_t)(b / share), n0 = dy.count[b], l = dy.lo[b], h = dy.hi[b];
+                if (counts && n0) add_cluster(tc::map_to_rank(&dy.all_count[b], o), n0);
+                if (l | h) add_to_cluster(tc::map_to_rank(&dy.all_lo[b], o), tc::map_to_rank(&dy.all_hi[b], o), ((uint64_t)h << 32) | l);
+            }
             tc::cluster_sync();
-#pragma unroll
-            for (int k = 0; k < kPerThread; ++k) {
-                cnt[k] = 0;
-                mass[k] = 0;
-            }
-            static_assert(kPerThread == 4, "a thread's bins are one 16-byte load");
-            for (uint32_t o = 0; o < size; ++o) {
-                uint32_t a[4], l[4], h[4];
-                ld_cluster(tc::map_to_rank(&dy.count[4 * tid], o), a);
-                ld_cluster(tc::map_to_rank(&dy.lo[4 * tid], o), l);
-                ld_cluster(tc::map_to_rank(&dy.hi[4 * tid], o), h);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    cnt[k] += a[k];
-                    mass[k] += ((uint64_t)h[k] << 32) + l[k];
-                }
-            }
         };
-        collect();
-        if (table_w) {
-#pragma unroll
-            for (int k = 0; k < kPerThread; ++k) {
-                const int b = 4 * tid + k;
-                if (cnt[k] && bins.single(b)) {
-                    const uint64_t w = w_of(bins.value(b));
-                    dy.w[b] = w;
-                    mass[k] = w * cnt[k];
-                }
-            }
-        }
-        uint64_t ma, mt;
+        // this thread's bins, `per` from b0 on, at most four; tokens and mass of the bins before them, and of all
+        const int b0 = first + tid * per, b1 = min(b0 + per, first + share);
+        uint32_t cnt[4];
+        uint64_t mass[4], ma, mt;
         uint32_t ca, ct;
-        uint64_t sm = mass[0] + mass[1] + mass[2] + mass[3];
-        uint32_t sc = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-        block_scan(sh, sm, sc, ma, ca, mt, ct);
-        const uint64_t z_all = mt;                             // (bf16: every token's weight)
-        if (kSingle && rank == 0 && tid == 0) z = (double)z_all / unit;
-        // the bin that holds the last token of `want`, or the first with `goal` of mass up to and with it
-        auto find_count = [&](uint32_t want) {
-            uint32_t b0 = ca;
-            uint64_t m0 = ma;
+        auto total_up = [&]() {
+            uint64_t sm = 0;
+            uint32_t sc = 0;
 #pragma unroll
-            for (int k = 0; k < kPerThread; ++k) {
-                if (b0 < want && want <= b0 + cnt[k]) {
-                    sh.bin = 4 * tid + k;
-                    sh.before = b0;
-                    sh.mass_before = m0;
-                    sh.in_bin = cnt[k];
-                }
-                b0 += cnt[k];
-                m0 += mass[k];
+            for (int k = 0; k < 4; ++k) {
+                const int b = b0 + k;
+                cnt[k] = b < b1 ? dy.all_count[b] : 0;
+                mass[k] = b < b1 ? ((uint64_t)dy.all_hi[b] << 32) + dy.all_lo[b] : 0;
+                if (kSingle && cnt[k] && bins.single(b)) mass[k] = w_of(bins.value(b)) * cnt[k];
+                sc += cnt[k];
+                sm += mass[k];
             }
-            __syncthreads();
-        };
-        auto find_mass = [&](uint64_t goal) {
-            uint32_t b0 = ca;
-            uint64_t m0 = ma;
-#pragma unroll
-            for (int k = 0; k < kPerThread; ++k) {
-                const bool was = b0 > 0 && m0 >= goal, is = m0 + mass[k] >= goal;
-                if (cnt[k] && is && !was) {
-                    sh.bin = 4 * tid + k;
-                    sh.before = b0;
-                    sh.mass_before = m0;
-                    sh.in_bin = cnt[k];
-                }
-                b0 += cnt[k];
-                m0 += mass[k];
+            block_scan(sh, sm, sc, ma, ca, mt, ct);
+            if (tid < (int)size) {
+                st_cluster(tc::map_to_rank(&sh.mass_of[rank], (uint32_t)tid), mt);
+                st_cluster(tc::map_to_rank(&sh.count_of[rank], (uint32_t)tid), ct);
             }
-            __syncthreads();
-        };
-        // the tokens of bin b to the first CTA, as (key, token)
-        auto gather = [&](int b) {
-            tc::cluster_sync();                                // (the list before has been read)
-            if (rank == 0 && tid == 0) sh.list_n = 0;
             tc::cluster_sync();
-            const uint32_t counter = tc::map_to_rank(&sh.list_n, 0), base = tc::map_to_rank(list, 0);
-            each([&](float l, int i) {
-                const uint32_t key = order_key(l);
-                if (bins.of(key) == b) {
-                    uint32_t at;
-                    asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(counter) : "memory");
-                    if (at < kList) st_cluster(base + 8 * at, ((uint64_t)key << 32) | (uint32_t)(v0 + i));
+            mt = 0;
+            for (uint32_t o = 0; o < size; ++o) {
+                if (o < rank) {
+                    ma += sh.mass_of[o];
+                    ca += sh.count_of[o];
                 }
-            });
-            tc::cluster_sync();
+                mt += sh.mass_of[o];
+            }
         };
+        __syncthreads();
+        if (table_w)                                           // weights of the slice's own values
+            for (int b = tid; b < kBins; b += kThreads)
+                if (dy.count[b] && bins.single(b)) dy.w[b] = w_of(bins.value(b));
+        push(true, 0, kBins);
+        total_up();
+        if (kSingle && rank == 0 && tid == 0) z = mt >> 4;     // (bf16: every token's weight)
         // ties of weight wx to keep so that `up` and they reach the goal: one at least, `cap` at most
         auto ties_for = [&](uint64_t goal, uint64_t up, uint64_t wx, uint64_t cap) -> uint64_t {
             if (wx == 0 || goal <= up) return 1;
             return min((goal - up + wx - 1) / wx, cap);
         };
-        // What the cluster is told: the border, and the mass up to and with it.
-        auto tell = [&](uint32_t key, uint64_t ties, uint64_t kept) {
-            if (tid < (int)size) {
-                const uint32_t d = tc::map_to_rank(&sh.border, (uint32_t)tid);
-                st_cluster(d, key);
-                st_cluster(d + 4, (uint32_t)ties);
-                st_cluster(tc::map_to_rank(&sh.above, (uint32_t)tid), kept);
+        // Where a border falls (stage 0: top-k's, 1: top-p's), told to the cluster by the one thread that finds it; for a
+        // bin of one value the border itself.
+        auto here = [&](int stage, int b, uint32_t before, uint32_t in, uint64_t m0, uint32_t want, uint64_t goal, const Border &most) {
+            Border bd = {0u, 0u};
+            uint64_t kept = 0;
+            if (kSingle && bins.single(b)) {
+                const uint64_t wx = w_of(bins.value(b));
+                bd.key = order_key(bins.value(b));
+                bd.ties = want ? want - before : (uint32_t)ties_for(goal, m0, wx, bd.key == most.key ? most.ties : in);
+                kept = m0 + bd.ties * wx;
+            }
+            for (uint32_t o = 0; o < size; ++o) {
+                st_cluster(tc::map_to_rank(&sh.bin[stage], o), (uint32_t)b);
+                st_cluster(tc::map_to_rank(&sh.before[stage], o), before);
+                st_cluster(tc::map_to_rank(&sh.in_bin[stage], o), in);
+                st_cluster(tc::map_to_rank(&sh.mass_before[stage], o), m0);
+                st_cluster(tc::map_to_rank(&sh.border[stage].key, o), bd.key);
+                st_cluster(tc::map_to_rank(&sh.border[stage].ties, o), bd.ties);
+                st_cluster(tc::map_to_rank(&sh.above[stage], o), kept);
             }
         };
+        // the bin that holds the last token of `want`, or the first with `goal` of mass up to and with it
+        auto find_count = [&](uint32_t want) {
+            uint32_t n0 = ca;
+            uint64_t m0 = ma;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (n0 < want && want <= n0 + cnt[k]) here(0, b0 + k, n0, cnt[k], m0, want, 0, Border{0u, 0u});
+                n0 += cnt[k];
+                m0 += mass[k];
+            }
+            tc::cluster_sync();
+        };
+        auto find_mass = [&](uint64_t goal, const Border &most) {
+            uint32_t n0 = ca;
+            uint64_t m0 = ma;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (cnt[k] && m0 + mass[k] >= goal && !(n0 > 0 && m0 >= goal)) here(1, b0 + k, n0, cnt[k], m0, 0u, goal, most);
+                n0 += cnt[k];
+                m0 += mass[k];
+            }
+            tc::cluster_sync();
+        };
+        // the tokens of a stage's bin to the first CTA, as (key, token)
+        auto gather = [&](int stage) {
+            const int b = sh.bin[stage];
+            const uint32_t counter = tc::map_to_rank(&sh.list_n[stage], 0), base = tc::map_to_rank(list + stage * kList, 0);
+            each([&](float l, int i) {
+                const uint32_t key = order_key(l);
+                if (bins.of(key) == b) {
+                    const uint32_t at = add_cluster(counter, 1u);
+                    if (at < kList) st_cluster(base + 8 * at, ((uint64_t)key << 32) | (uint32_t)(v0 + i));
+                }
+            });
+            tc::cluster_sync();
+        };
+        // What the cluster is told: the border, and the mass up to and with it.
+        auto tell = [&](int stage, uint32_t o, uint32_t key, uint64_t ties, uint64_t kept) {
+            st_cluster(tc::map_to_rank(&sh.border[stage].key, o), key);
+            st_cluster(tc::map_to_rank(&sh.border[stage].ties, o), (uint32_t)ties);
+            st_cluster(tc::map_to_rank(&sh.above[stage], o), kept);
+        };
         // In the first CTA: of the listed tokens in order the least number with `want` tokens, or (want 0) with a mass
-        // that with `before` reaches the goal, of those that `most` keeps. The range of keys is halved, the tokens in
-        // registers.
-        auto select = [&](uint32_t want, uint64_t goal, uint64_t before, const Border &most) {
-            if (rank == 0) {
-                const uint32_t ln = sh.list_n;
+        // that with `before` reaches the goal, of those that `most` keeps. Short lists: a thread a token, which counts
+        // and weighs those before its own; the one at the border tells. Others: the range of keys is halved, the tokens
+        // in registers.
+        auto select = [&](int stage, uint32_t want, uint64_t goal, uint64_t before, const Border &most) {
+            const uint32_t ln = sh.list_n[stage];
+            const uint64_t *li = list + stage * kList;
+            if (rank == 0 && ln <= kShort) {
+                if ((tid & ~31u) < ln) {
+                    const uint64_t w = w_of(key_logit(tid < ln ? (uint32_t)(li[tid] >> 32) : order_key(m)));
+                    if (tid < ln) dy.list_w[tid] = w;
+                }
+                __syncthreads();
+                if (tid < ln) {
+                    const uint32_t key = (uint32_t)(li[tid] >> 32), at = (uint32_t)li[tid];
+                    const uint64_t w = dy.list_w[tid];
+                    uint64_t up = before;                      // mass of larger ones
+                    uint32_t larger = 0, equal = 0;            // and their number; equal ones before this
+#pragma unroll 4
+                    for (uint32_t i = 0; i < ln; ++i) {
+                        const uint64_t e = li[i], we = dy.list_w[i];
+                        const uint32_t k = (uint32_t)(e >> 32);
+                        if (k > key) {
+                            ++larger;
+                            up += we;
+                        }
+                        equal += k == key && (uint32_t)e < at;
+                    }
+                    bool border;
+                    if (want) border = larger + equal + 1 == want;
+                    else {
+                        const bool may = key > most.key || (key == most.key && equal < most.ties);
+                        border = may && (larger + equal == 0 || up + equal * w < goal) && up + (equal + 1) * w >= goal;
+                    }
+                    if (border)
+                        for (uint32_t o = 0; o < size; ++o) tell(stage, o, key, equal + 1, up + (equal + 1) * w);
+                }
+            } else if (rank == 0) {
                 uint32_t lo = 0u, hi = order_key(m);
-                if (bins.single(sh.bin)) {                     // its keys share their upper half
-                    const uint32_t h = sh.bin < bins.pos ? bins.top - (uint32_t)sh.bin : bins.low - (uint32_t)(sh.bin - bins.neg);
+                const int b = sh.bin[stage];
+                if (bins.single(b)) {                          // its keys share their upper half
+                    const uint32_t h = b < bins.pos ? bins.top - (uint32_t)b : bins.low - (uint32_t)(b - bins.neg);
                     lo = h << 16;
                     hi = min(hi, lo | 0xffffu);
                 }
                 lo = max(lo, most.key);
                 uint32_t key[kHold];
-                uint64_t w[kHold];
-                uint32_t t = 0;
+                uint64_t w[kHold], t = 0;
 #pragma unroll
                 for (int k = 0; k < kHold; ++k) {
                     const uint32_t i = tid + k * kThreads;
-                    key[k] = i < ln ? (uint32_t)(list[i] >> 32) : 0u;
-                    w[k] = 0;
-                    if (__any_sync(0xffffffffu, i < ln)) w[k] = w_of(key_logit(key[k]));
-                    if (i >= ln || key[k] < most.key) {
-                        key[k] = 0u;                           // (below every key: order keys of numbers are not 0)
-                        w[k] = 0;
-                    }
-                    if (key[k] && key[k] == most.key) {
-                        ++t;
-                        w[k] = 0;                              // counted by `equal`
-                    }
+                    key[k] = i < ln ? (uint32_t)(li[i] >> 32) : 0u;        // 0 is no number's key
+                    w[k] = w_of(key_logit(i < ln ? key[k] : order_key(m)));
+                    if (i >= ln || key[k] < most.key) key[k] = 0u;
+                    if (key[k] && key[k] == most.key) ++t;
+                    if (key[k] <= most.key) w[k] = 0;          // (the border's own: `equal`, as many as are kept)
                 }
                 uint64_t equal = 0;
-                if (most.key) equal = min(block_sum(sh, (uint64_t)t), (uint64_t)most.ties) * w_of(key_logit(most.key));
-                int turn = 0;
-                auto measure = [&](uint32_t x, bool mm) -> uint64_t {      // of keys x and above
+                if (most.key) equal = min(block_sum(sh, t), (uint64_t)most.ties) * w_of(key_logit(most.key));
+                auto measure = [&](uint32_t x, bool mass_of) -> uint64_t {     // of keys x and above
                     uint64_t s = 0;
 #pragma unroll
-                    for (int k = 0; k < kHold; ++k) s += key[k] >= x && key[k] ? (mm ? w[k] : 1) : 0;
-                    s = warp_sum(s);
-                    if (lane == 0) sh.turn[turn][warp] = s;
-                    __syncthreads();
-                    s = warp_sum(sh.turn[turn][lane]);
-                    turn ^= 1;
-                    return s + (mm && x <= most.key ? equal : 0);
+                    for (int k = 0; k < kHold; ++k) s += key[k] >= x && key[k] ? (mass_of ? w[k] : 1) : 0;
+                    return block_sum(sh, s) + (mass_of && x <= most.key ? equal : 0);
                 };
                 const bool mm = want == 0;
                 while (lo < hi) {                              // the largest key with enough at or above it
@@ -482,15 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                     if (mm ? before + s >= goal : s >= want) lo = mid;
                     else hi = mid - 1;
                 }
-                const uint64_t up = lo == 0xffffffffu ? 0 : measure(lo + 1, mm), wx = w_of(key_logit(lo));
-                const uint64_t ties = mm ? ties_for(goal, before + up, wx, lo == most.key ? most.ties : 0xffffffffu) : want - up;
-                const uint64_t up_mass = mm ? up : (lo == 0xffffffffu ? 0 : measure(lo + 1, true));
-                tell(lo, ties, before + up_mass + ties * wx);
+                const uint64_t up = before + measure(lo + 1, true), wx = w_of(key_logit(lo));
+                const uint64_t ties = mm ? ties_for(goal, up, wx, lo == most.key ? most.ties : 0xffffffffu) : want - measure(lo + 1, false);
+                if (tid < (int)size) tell(stage, (uint32_t)tid, lo, ties, up + ties * wx);
             }
             tc::cluster_sync();
         };
         // the same over the whole row, for bins that the list cannot hold
-        auto search_row = [&](uint32_t want, uint64_t goal, const Border &most) {
+        auto search_row = [&](int stage, uint32_t want, uint64_t goal, const Border &most) {
             if (rank == 0) {
                 const E *whole = src;                          // (rank 0's slice starts the row)
                 auto measure = [&](uint32_t x, bool mm) -> uint64_t {
@@ -521,28 +567,23 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 const uint64_t up = lo == 0xffffffffu ? 0 : measure(lo + 1, mm), wx = w_of(key_logit(lo));
                 const uint64_t ties = mm ? ties_for(goal, up, wx, lo == most.key ? most.ties : 0xffffffffu) : want - up;
                 const uint64_t up_mass = mm ? up : (lo == 0xffffffffu ? 0 : measure(lo + 1, true));
-                tell(lo, ties, up_mass + ties * wx);
+                if (tid < (int)size) tell(stage, (uint32_t)tid, lo, ties, up_mass + ties * wx);
             }
             tc::cluster_sync();
         };
         uint64_t kept_mass = mt;                               // of the top-k's tokens
         if (by_count) {
             find_count((uint32_t)top_k);
-            const int b = sh.bin;
-            if (kSingle && bins.single(b)) {
-                border = {order_key(bins.value(b)), (uint32_t)top_k - sh.before};
-                if (by_mass) kept_mass = sh.mass_before + (uint64_t)border.ties * w_of(bins.value(b));
-            } else if (sh.in_bin <= kList) {
-                gather(b);
-                const uint64_t before = kSingle ? sh.mass_before : 0;
-                select((uint32_t)top_k - sh.before, 0, before, Border{0u, 0u});
-                border = sh.border;
-                kept_mass = sh.above;
-            } else {
-                search_row((uint32_t)top_k, 0, Border{0u, 0u});
-                border = sh.border;
-                kept_mass = sh.above;
+            const bool listed = sh.in_bin[0] <= kList;
+            if (!(kSingle && bins.single(sh.bin[0]))) {
+                if (listed) {
+                    gather(0);
+                    select(0, (uint32_t)top_k - sh.before[0], 0, kSingle ? sh.mass_before[0] : 0, Border{0u, 0u});
+                } else
+                    search_row(0, (uint32_t)top_k, 0, Border{0u, 0u});
             }
+            border = sh.border[0];
+            kept_mass = sh.above[0];
             if (!kSingle && by_mass) {                         // the masses of what top-k keeps, the border's bin whole
                 const int last = bins.of(border.key);
                 each([&](float l, int) {
@@ -550,17 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                     if (q < last) add_to(&dy.lo[q], &dy.hi[q], w_of(l));
                 });
                 __syncthreads();
-                collect();
-                sm = mass[0] + mass[1] + mass[2] + mass[3];
-                block_scan(sh, sm, sc, ma, ca, mt, ct);
-                // (bins up to the border's are summed; the border's own kept mass is the list's, or the row's)
-                kept_mass = sh.in_bin <= kList ? mt + sh.above : sh.above;
+                push(false, 0, last);
+                total_up();
+                // (the border's bin: what the list, or the row, has kept)
+                kept_mass = listed ? mt + sh.above[0] : sh.above[0];
 #pragma unroll
-                for (int k = 0; k < kPerThread; ++k)
-                    if (4 * tid + k == last) mass[k] = kept_mass - mt;
-                __syncthreads();
-                if (tid == last / 4) sm += kept_mass - mt;
-                block_scan(sh, sm, sc, ma, ca, mt, ct);
+                for (int k = 0; k < 4; ++k)
+                    if (b0 + k == last && b0 + k < b1) mass[k] = kept_mass - mt;
             }
         }
         if (by_mass) {
@@ -570,22 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             }
             __syncthreads();
             const uint64_t goal = sh.goal;
-            find_mass(goal);
-            const int b = sh.bin;
             const Border most = by_count ? border : Border{0u, (uint32_t)p.V};
-            if (kSingle && bins.single(b)) {
-                const uint64_t wx = w_of(bins.value(b)), up = sh.mass_before;
-                const uint32_t key = order_key(bins.value(b));
-                const uint64_t cap = key == most.key ? most.ties : sh.in_bin;
-                border = {key, (uint32_t)ties_for(goal, up, wx, cap)};
-            } else {
-                if (sh.in_bin <= kList) {
-                    gather(b);
-                    select(0u, goal, sh.mass_before, most);
+            find_mass(goal, most);
+            if (!(kSingle && bins.single(sh.bin[1]))) {
+                if (sh.in_bin[1] <= kList) {
+                    gather(1);
+                    select(1, 0u, goal, sh.mass_before[1], most);
                 } else
-                    search_row(0u, goal, most);
-                border = sh.border;
+                    search_row(1, 0u, goal, most);
             }
+            border = sh.border[1];
         }
     }
     __syncthreads();
@@ -606,13 +637,31 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     auto measure = [&](int i0, int i1, uint64_t &sum, uint32_t &ties) {      // (a warp's lanes side by side)
         uint64_t s = 0;
         uint32_t t = 0;
-#pragma unroll 4
-        for (int i = i0 + lane; i < i1; i += 32) {
-            const float l = as_f32(data[i]);
+        auto take = [&](float l) {
             const uint32_t key = order_key(l);
             t += key == border.key;
             if (key > border.key) s += weigh(l, key);
+        };
+        int i = i0;
+        if ((p.cache || p.vec) && i0 % kPer == 0) {            // (the slices' and the warps' parts start so)
+            const int nq = (i1 - i0) / kPer;
+            const uint4 *q = reinterpret_cast<const uint4 *>(data + i0);
+            for (int j0 = lane; j0 < nq; j0 += 4 * 32) {
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (j0 + 32 * u < nq) v[u] = q[j0 + 32 * u];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j0 + 32 * u >= nq) break;
+                    const E *e = reinterpret_cast<const E *>(&v[u]);
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) take(as_f32(e[k]));
+                }
+            }
+            i += nq * kPer;
         }
+        for (i += lane; i < i1; i += 32) take(as_f32(data[i]));
         sum = warp_sum(s);
         ties = warp_sum(t);
     };
@@ -626,17 +675,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         sh.part2[warp] = ties;
     }
     if (!kSingle) z = warp_sum(z);
-    __shared__ double zs[kWarps];
+    __shared__ uint64_t zs[kWarps];
     if (lane == 0) zs[warp] = z;
     __syncthreads();
     if (warp == 0) {
         const uint64_t s = warp_sum(sh.part[lane]);
         const uint32_t t = warp_sum(sh.part2[lane]);
-        const double zz = warp_sum(zs[lane]);
+        const uint64_t zz = warp_sum(zs[lane]);
         if (lane < (int)size) {
             st_cluster(tc::map_to_rank(&sh.sum[rank], (uint32_t)lane), s);
             st_cluster(tc::map_to_rank(&sh.ties[rank], (uint32_t)lane), t);
-            st_cluster(tc::map_to_rank(&sh.z[rank], (uint32_t)lane), (uint64_t)__double_as_longlong(zz));
+            st_cluster(tc::map_to_rank(&sh.z[rank], (uint32_t)lane), zz);
         }
     }
     tc::cluster_sync();
@@ -726,10 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             if (lane == __ffs(hit) - 1) {
                 p.token[r] = v0 + i;
                 if (p.logp) {
-                    double zz = 0.0;
+                    uint64_t zz = 0;                           // in units of 2^-40
                     for (uint32_t o = 0; o < size; ++o) zz += sh.z[o];
                     const double temp = p.temperature ? (double)p.temperature[r] : p.temperature_all;
-                    p.logp[r] = greedy ? 0.f : (float)(((double)l - (double)m) / temp - log(zz));
+                    p.logp[r] = greedy ? 0.f : (float)(((double)l - (double)m) / temp - log((double)zz * 9.094947017729282e-13));
                 }
             }
             return;
@@ -774,7 +823,7 @@ template <typename E> cudaError_t launch(SampleParams p, cudaStream_t s) {
     int C = kMaxCluster;
     while (C > 1 && (p.V < 2048 * C || p.R > resident<E>(cfg, C))) C >>= 1;
     p.slice = ((p.V + C - 1) / C + 15) / 16 * 16;
-    const size_t fixed = sizeof(Dyn) + kList * sizeof(uint64_t), slice = (size_t)p.slice * sizeof(E);
+    const size_t fixed = sizeof(Dyn) + 2 * kList * sizeof(uint64_t), slice = (size_t)p.slice * sizeof(E);
     p.cache = fixed + slice <= kMostSmem;
     at[0].val.clusterDim.x = (unsigned)C;
     cfg.gridDim = dim3((unsigned)(p.R * C));
