@@ -159,12 +159,12 @@ cudaError_t launch_verify_q8_rows(const Q8Params &p, cudaStream_t s);
 
 // K6: tree-verify attention over a paged bf16 latent cache (kdt_verify_attn_paged), everything
 // validated on the host.
-// Where a share of the work starts, left by the attention kernel for the merge: in positions of the
-// (group of row tiles, key block) list, with the group that position is in.
+// The group of row tiles inside which a share of the work begins, left by the attention kernel for the merge.
 struct PagedShare {
-    int64_t start, t0, t1;     // the group's positions [t0, t1)
     int64_t row0;              // its first query row over all sequences
-    int rows;                  // its sequence's rows from there on
+    int rows;                  // its rows
+    int pieces;                // shares that meet it, from the one before on; 0 where this is not the first to begin inside
+    int second;                // 1: the one before did not begin with this group, its piece is of a later item
 };
 
 struct PagedParams {
@@ -188,10 +188,11 @@ struct PagedParams {
     int group;                 // row tiles that walk the same keys side by side, a CTA each
     int shares;                // the work is cut into at most this many
     int least;                 // blocks a share has at least, where there are enough
+    int deep;                  // the groups, where one may have many pieces, else 0
     bool pieces;               // groups may be cut between shares: a second kernel joins their pieces
     bool overlap_vis;          // launched right behind this call's visibility kernel
     float *part_o, *part_lse;  // [2 * shares * group][tile] piece states
-    PagedShare *cuts;          // [shares + 1]
+    PagedShare *cuts;          // [shares]
 };
 constexpr int kPagedKeys = 64; // keys of a block
 cudaError_t launch_verify_paged(const PagedParams &p, cudaStream_t s);

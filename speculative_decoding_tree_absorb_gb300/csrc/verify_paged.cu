@@ -11,10 +11,17 @@
 //  * A block is 64 keys: 576 dims as nine 128-byte swizzled tiles, the latent in four stages of two tiles.
 //    ONE copy serves both contractions: K-major A operand of S^T, MN-major A operand of O^T. TMA boxes of
 //    min(64, page) rows bring it, a box a page where pages are smaller; the stages form a ring of two blocks
-//    or more, and each is given back as soon as its part of O^T is done. Boxes behind the last row, and pages that are none, lie outside the tensor map: zeros, no traffic.
-//  * One thread issues all MMAs, and never waits for one thing while it could do another: it polls for the
-//    next block's stages and for P^T in turn, so that neither a late page holds up O^T, which frees the
-//    ring, nor softmax the scores.
+//    or more, and each is given back as soon as its part of O^T is done. Boxes behind the last row, and pages
+//    that are none, lie outside the tensor map: zeros, no traffic.
+//  * One warp issues the scores' MMAs and another the output's, so that neither a late page holds up O^T, which
+//    frees the ring, nor softmax the scores. The whole warp walks the loop and one lane issues: descriptors
+//    computed by a lone thread, which polled for both kinds of work, took 75 - 100 cycles an MMA where the
+//    MMAs take 31 (scores) and 47 (output): 4.3 k cycles a block, now 3.1 k.
+//  * What bounds a block (64 rows, 64 keys) is shared memory: the operands of 36 + 16 MMAs pass it at 128 bytes
+//    a cycle, 1.9 k cycles, and the block's 72 KB have to be written besides. 3.1 k cycles a block in a CTA alone,
+//    3.3 - 3.6 k with all 152 at work; DRAM would give each its own block every 3.1 k. Copies ahead into L2
+//    (by TMA or by a warp's prefetches, two to six blocks) made every case 2 - 30 % slower.
+//    Boxes of 16 rows (pages of 16) pass the copy engine at 5 cycles a row: 4.1 k cycles a block.
 //  * In S^T a thread owns two keys and a few rows, so a row's maximum lies across threads. The running
 //    maximum is lazy: a block only votes whether some score exceeds its row's reference by more than 2^20;
 //    exact maxima and the rescale of O^T are taken when one does, and for the first block of an item. p <=
@@ -24,6 +31,11 @@
 //    is read once and the others hit L2. The (group, key block) pairs of the batch are cut into equal
 //    contiguous shares; groups cut by a share's end leave normalised pieces that a second kernel joins by
 //    log-sum-exp.
+//  * Measured, both kernels (bf16 out, pages not in L2): 64 single tokens of 64 heads over 1024 - 8192 keys 88 us,
+//    351 MB of cache at 4.0 TB/s, of which 8 us pass before the first scores (lengths, then the page table, then
+//    the first pages, none of them in L2) and 10 us join 38 MB of pieces; two of 128 heads over 60001 and 99990
+//    keys 80 us; eight trees of 13 nodes of 32 heads over 2500 - 12000 keys in pages of 16 119 us; one token of
+//    16 heads over 700 20 us.
 //  * Masks, rows of other sequences' leftovers behind the last key, and latents that are not finite concern
 //    the blocks with tree keys only: there the softmax warps zero what may not enter a product (0 * NaN), and
 //    mark its key, whose score is NaN for the rows that see it.
@@ -44,7 +56,7 @@ namespace {
 using namespace tc;
 
 constexpr int kKeysB = kPagedKeys;                  // keys of a block (M of S^T)
-// Warps: 0 loads keys, 1 issues the MMAs, 2 loads queries, 3 only helps to set up, 4-11 softmax.
+// Warps: 0 loads keys, 1 issues the scores' MMAs, 2 loads queries, 3 issues the output's MMAs, 4-11 softmax.
 constexpr int kSoft0 = 4, kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
 constexpr int kThreads = 32 * (kSoft0 + kSoftWarps);
 constexpr int kStages = 4;                          // of a block's latent
@@ -64,14 +76,14 @@ template <int kRows> struct Layout {
     static constexpr int kOffR = kRing * kStageBytes;
     static constexpr int kOffQ = kOffR + kRopeRing * kTileBytes;
     static constexpr int kOffP = kOffQ + 9 * kQTile;
-    static constexpr int kPBytes = kRows * 128 < 512 * kSoftWarps ? 512 * kSoftWarps : kRows * 128;
-    static constexpr int kSmem = kOffP + kPBytes + 1024;                            // + alignment slack
+    static constexpr int kSmem = kOffP + kRows * 128 + 1024;                        // + alignment slack
 };
 
 struct Bars {
     uint64_t kfull[11], kempty[11];     // a stage landed; O^T's MMAs have read it
     uint64_t rfull[3], rempty[3];       // rope keys
     uint64_t sfull[2];                  // scores of the block in tensor memory
+    uint64_t sempty[2];                 // and read out of it
     uint64_t pfull;                     // P^T stored, O^T rescaled if needed
     uint64_t pdone;                     // the block's O^T complete, P^T's space free
     uint64_t qfull, qempty;             // queries of the item landed; its scores are all made
@@ -79,7 +91,7 @@ struct Bars {
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
-    int work[5];                        // this share: blocks, first sequence, group, block
+    int work[6];                        // this share: blocks; its first item: sequence, group, block, nodes, prefix
 };
 
 template <int kRows> struct Shared {
@@ -91,8 +103,15 @@ template <int kRows> struct Shared {
 };
 
 __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
-    if (*reinterpret_cast<volatile int *>(&bar.abort_flag)) return false;
-    if (mbar_wait(b, parity, kWait)) return true;
+    uint64_t t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(b, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&bar.abort_flag)) return false;
+        const uint64_t now = global_ns();
+        if (!t0) t0 = now;
+        if (now - t0 > kWait) break;
+    }
     bar.abort_flag = 1;
     if (err) atomicCAS(err, 0, code);
     return false;
@@ -167,8 +186,12 @@ __device__ __forceinline__ bool first_item(const PagedParams &p, const int *work
     it.b = work[1];
     it.grp = work[2];
     it.kb = work[3];
-    it.nb = it.n = it.P = it.kv = it.idx = 0;
-    return fill(p, it);
+    it.n = work[4];
+    it.P = work[5];
+    it.kv = it.P + it.n;
+    it.nb = min((it.kv + kKeysB - 1) / kKeysB - it.kb, it.left);
+    it.idx = 0;
+    return it.left > 0;
 }
 
 // The row tile of this CTA (g-th of the group), or -1 when the sequence has none there.
@@ -177,9 +200,30 @@ __device__ __forceinline__ int tile_of(const PagedParams &p, const Item &it, int
     return rt * p.tile < it.n * p.H ? rt : -1;
 }
 
-// Positions: sequence-major, group-major, block order; W of them, cut into `C` shares. One warp finds share
-// c's first item {blocks, b, grp, kb}, and leaves for the merge where the share starts and which group that
-// is in.
+// a / b for 0 <= a, 0 < b < 2^31: a 64-bit division costs hundreds of cycles of a kernel's start.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// Positions: sequence-major, group-major, block order; W of them, cut into up to p.shares equal shares of
+// p.least or more.
+struct Shares {
+    int64_t W, each;
+    int C, more;                                              // the first `more` shares have a block more
+    __device__ __forceinline__ Shares(const PagedParams &p, int64_t w) : W(w) {
+        C = (int)min((int64_t)p.shares, max(quotient(W + p.least - 1, p.least), (int64_t)1));
+        each = quotient(W, C);
+        more = (int)(W - each * C);
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return c < C ? each * c + min(c, more) : W; }
+    __device__ __forceinline__ int of(int64_t at) const {     // the share that has position `at` < W
+        const int64_t longer = more * (each + 1);
+        return (int)(at < longer ? quotient(at, each + 1) : more + quotient(at - longer, each));
+    }
+};
+
+// One warp finds share c's first item. Where share c is the first to begin inside a group, it leaves that
+// group's rows and the number of its pieces for the merge.
 __device__ __forceinline__ void find_share(const PagedParams &p, int c, bool writes, int lane, int *out) {
     int64_t W = 0;
     for (int b = lane; b < p.B; b += 32) {
@@ -188,24 +232,19 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int c, bool wri
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-    const int64_t C = min((int64_t)p.shares, max((W + p.least - 1) / p.least, (int64_t)1));
-    const int64_t s0 = c < C ? W * c / C : W, s1 = c < C ? W * (c + 1) / C : W;
+    const Shares shares(p, W);
+    const int64_t s0 = shares.start(c), s1 = shares.start(c + 1);
     if (lane == 0) {
         out[0] = (int)(s1 - s0);
-        out[1] = out[2] = out[3] = 0;
-        if (writes) {
-            p.cuts[c].start = s0;
-            p.cuts[c].t0 = p.cuts[c].t1 = s0;                 // (an empty share behind the last position)
-            p.cuts[c].rows = 0;
-            if (c == p.shares - 1) p.cuts[p.shares].start = W;
-        }
+        out[1] = out[2] = out[3] = out[4] = out[5] = 0;
+        if (writes) p.cuts[c].pieces = 0;                     // unless share c is the first to begin inside a group
     }
     __syncwarp();
     int64_t before = 0;
     for (int base = 0; base < p.B && s0 < s1; base += 32) {
         const int b = base + lane;
         const int n = b < p.B ? nodes_of(p, b) : 0;
-        const int nb = n ? (prefix_of(p, b, n) + n + kKeysB - 1) / kKeysB : 1;
+        const int P = n ? prefix_of(p, b, n) : 0, nb = n ? (P + n + kKeysB - 1) / kKeysB : 1;
         const int64_t w = n ? (int64_t)groups_of(p, n) * nb : 0;
         int64_t incl = w;
 #pragma unroll
@@ -216,16 +255,20 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int c, bool wri
         const int64_t at = before + incl - w;
         const bool hit = s0 >= at && s0 < at + w;
         if (hit) {
-            const int grp = (int)((s0 - at) / nb);
+            const int grp = (int)quotient(s0 - at, nb);
             out[1] = b;
             out[2] = grp;
             out[3] = (int)(s0 - at - (int64_t)grp * nb);
-            if (writes) {
+            out[4] = n;
+            out[5] = P;
+            const int64_t t0 = at + (int64_t)grp * nb;        // where the group begins, and the share before
+            const int64_t before_it = c > 0 ? shares.start(c - 1) : s0;
+            if (writes && s0 > t0 && before_it <= t0) {
                 const int row = grp * p.group * p.tile;
-                p.cuts[c].t0 = at + (int64_t)grp * nb;
-                p.cuts[c].t1 = p.cuts[c].t0 + nb;
                 p.cuts[c].row0 = (int64_t)b * p.rows_seq + row;
                 p.cuts[c].rows = min(n * p.H - row, p.group * p.tile);
+                p.cuts[c].second = before_it < t0 ? 1 : 0;
+                p.cuts[c].pieces = shares.of(t0 + nb - 1) - c + 2;
             }
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -242,6 +285,13 @@ template <int kN> __device__ __forceinline__ void loaded(uint32_t (&r)[kN]) {
 #pragma unroll
     for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(r[k])::"memory");
 }
+
+// A value that all lanes of a warp have, known to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Shared-memory descriptors differ in their low words only: address and leading stride in 16 bytes.
+constexpr uint32_t kLeadK = 1u << 16, kLeadMn = (uint32_t)(kTileBytes >> 4) << 16;
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (sdesc_sw128(0, 0, 1024) >> 32 << 32) | lo; }
 
 __device__ __forceinline__ uint32_t lane_addr(uint32_t base, int warp, uint32_t col) {
     return base + ((uint32_t)(32 * (warp & 3)) << 16) + col;
@@ -274,12 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bar.sfull[0], 1);
         mbar_init(&bar.sfull[1], 1);
+        mbar_init(&bar.sempty[0], kSoftWarps);
+        mbar_init(&bar.sempty[1], kSoftWarps);
         mbar_init(&bar.pfull, kSoftWarps);
         mbar_init(&bar.pdone, 1);
         mbar_init(&bar.qfull, 1);
         mbar_init(&bar.qempty, 1);
         mbar_init(&bar.ofree, kSoftWarps);
-        mbar_init(&bar.drain, 1);
+        mbar_init(&bar.drain, 2);
         bar.abort_flag = 0;
         fence_mbar_init();
     }
@@ -303,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t g = 0;                                      // blocks so far
         const int w4 = warp & 3, half = (warp - kSoft0) >> 2, ka = 16 * w4 + (lane >> 2);
         const int srow = (int)threadIdx.x - 32 * kSoft0;
+        const float scale = p.scale_log2;
         bool ok = true, vis_ready = false;
         auto row_of = [&](int i, int e) { return kHalf * half + 8 * i + 2 * (lane & 3) + e; };
         // where this lane's 16 bytes of stmatrix go: matrix 2 i + (keys + 8), row r of it
@@ -378,13 +431,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t raw[4 * kCols];
                 tmem_ld_frag(lane_addr(tmem + kColS + (g & 1) * kRows, warp, kHalf * half), raw);
                 loaded(raw);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.sempty[g & 1]);
                 float x[4 * kCols];                          // [i][key][e]
                 auto scores = [&](bool shifted) {
 #pragma unroll
-                    for (int k = 0; k < 4 * kCols; ++k) {
-                        const int r = 2 * (k >> 2) + (k & 1), h = (k >> 1) & 1;
-                        x[k] = fmaf(__uint_as_float(raw[k]), p.scale_log2, shifted ? nm[r] : 0.f);
-                        if (masked) {
+                    for (int k = 0; k < 4 * kCols; ++k)
+                        x[k] = fmaf(__uint_as_float(raw[k]), scale, shifted ? nm[2 * (k >> 2) + (k & 1)] : 0.f);
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 4 * kCols; ++k) {
+                            const int r = 2 * (k >> 2) + (k & 1), h = (k >> 1) & 1;
                             if ((is_bad >> h) & 1u) x[k] = __uint_as_float(0x7fffffffu);
                             x[k] = (see >> (2 * r + h)) & 1u ? x[k] : -INFINITY;
                         }
@@ -493,43 +551,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             soft_or(false);
             tc_fence_after();
-            // A thread has one dim of 8 rows; 512 bytes of P^T's space a warp turn them into 16-byte pieces of rows
-            const uint32_t stage = smem + L::kOffP + 512 * (warp - kSoft0);
+            // A thread has one dim of kHalf rows. Float32: a warp stores 128 bytes of a row at once. bf16: of two
+            // rows, lanes in pairs trade a dim of one for the other's dim of the other.
+            const int rows = min(max(live - kHalf * half, 0), kHalf);
+            const int64_t at = (first + kHalf * half) * kDc + 32 * w4;
 #pragma unroll 1
-            for (int q = 0; q < 4 * kCols; ++q) {
-                const int col = kHalf * half + 8 * (q % kCols);
-                uint32_t o[8];
-                tmem_ld8(lane_addr(tmem, warp, kRows * (q / kCols) + col), o);
-                loaded(o);
+            for (int q = 0; q < 4; ++q) {
+                uint32_t raw[kCols][8];
+                float o[kHalf];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[col + r]);
-                const int64_t at = (first + col) * kDc + 128 * (q / kCols) + 32 * w4;
+                for (int k = 0; k < kCols; ++k) tmem_ld8(lane_addr(tmem, warp, kRows * q + kHalf * half + 8 * k), raw[k]);
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) loaded(raw[k]);
+#pragma unroll
+                for (int r = 0; r < kHalf; ++r) o[r] = __uint_as_float(raw[r >> 3][r & 7]) * sh.alpha[kHalf * half + r];
                 if (whole && kBf16Out) {
+                    const int odd = lane & 1;
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at + 128 * q + (int64_t)odd * kDc + (lane & ~1);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const unsigned short h = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[r])));
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + r * 64 + 2 * lane), "h"(h) : "memory");
+                    for (int r = 0; r < kHalf; r += 2) {
+                        const float mine = odd ? o[r + 1] : o[r];
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? o[r] : o[r + 1], 1);
+                        if (r + odd < rows)
+                            *reinterpret_cast<uint32_t *>(dst + (int64_t)r * kDc) = q8::pack_bf16(odd ? other : mine, odd ? mine : other);
                     }
-                    __syncwarp();
-                    uint32_t v[4];
-                    ld_shared_v4(stage + 16 * lane, v);
-                    if (col + (lane >> 2) < live)
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + (lane >> 2) * kDc + 8 * (lane & 3)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
-                    __syncwarp();
                 } else {
-                    float *dst = (whole ? static_cast<float *>(p.out) : p.part_o) + at + (lane >> 3) * kDc + 4 * (lane & 7);
+                    float *dst = (whole ? static_cast<float *>(p.out) : p.part_o) + at + 128 * q + lane;
 #pragma unroll
-                    for (int g4 = 0; g4 < 8; g4 += 4) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + r * 128 + 4 * lane), "r"(o[g4 + r]) : "memory");
-                        __syncwarp();
-                        uint32_t v[4];
-                        ld_shared_v4(stage + 16 * lane, v);
-                        if (col + g4 + (lane >> 3) < live) *reinterpret_cast<uint4 *>(dst + g4 * kDc) = make_uint4(v[0], v[1], v[2], v[3]);
-                        __syncwarp();
-                    }
+                    for (int r = 0; r < kHalf; ++r)
+                        if (r < rows) dst[(int64_t)r * kDc] = o[r];
                 }
             }
             tc_fence_before();
@@ -538,60 +588,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 0) {
         // ------------------------------------ keys ------------------------------------
-        if (elect_one()) {
-            const int box = min(kKeysB, 1 << p.shift);
-            const int nowhere = p.n_pages << p.shift;        // a row outside the tensor maps
-            // cache row of the box that starts at a key of an item
-            auto place = [&](const Item &i, int key) {
-                if (key >= i.kv) return nowhere;
-                const int32_t page = __ldg(p.table + i.b * p.table_stride + (key >> p.shift));
-                if (page >= 0 && page < p.n_pages) return (page << p.shift) + (key & ((1 << p.shift) - 1));
-                record_error(p.err, (int32_t)min((int64_t)INT32_MAX, 1 + (int64_t)p.B * p.T + i.b));
-                return nowhere;
-            };
-            Item it;
-            bool ok = true;
-            uint32_t slot = 0, phase = 1, rslot = 0, rphase = 1;
-            for (bool have = first_item(p, bar.work, it); have && ok; have = advance(p, it)) {
-                if (tile_of(p, it, g_of) < 0) continue;
-                for (int j = 0; j < it.nb; ++j) {
-                    const int key0 = (it.kb + j) * kKeysB;
-                    int rows[kKeysB / 8];                    // of the block's boxes
+        // Lane k has the cache row of the block's k-th box (of min(64, page) rows); one lane issues all copies.
+        const int box = min(kKeysB, 1 << p.shift), boxes = kKeysB / box;
+        const int nowhere = p.n_pages << p.shift;            // a row outside the tensor maps
+        auto place = [&](const Item &i, int j) {
+            const int key = (i.kb + j) * kKeysB + lane * box;
+            if (lane >= boxes || key >= i.kv) return nowhere;
+            const int32_t page = __ldg(p.table + i.b * p.table_stride + (key >> p.shift));
+            if (page >= 0 && page < p.n_pages) return (page << p.shift) + (key & ((1 << p.shift) - 1));
+            record_error(p.err, (int32_t)min((int64_t)INT32_MAX, 1 + (int64_t)p.B * p.T + i.b));
+            return nowhere;
+        };
+        const bool lead = elect_one();
+        Item it;
+        bool ok = true;
+        uint32_t slot = 0, phase = 1, rslot = 0, rphase = 1;
+        for (bool have = first_item(p, bar.work, it); have && ok; have = advance(p, it)) {
+            if (tile_of(p, it, g_of) < 0) continue;
+            int next = place(it, 0);
+            for (int j = 0; j < it.nb; ++j) {
+                const int rows = next;
+                if (j + 1 < it.nb) next = place(it, j + 1);
+                if (!(ok = warp_wait(bar, &bar.rempty[rslot], rphase, p.err, -66))) break;
+                if (lead) mbar_arrive_expect_tx(&bar.rfull[rslot], kTileBytes);
+                int row[kKeysB / 8];
 #pragma unroll
-                    for (int k = 0; k < kKeysB / 8; ++k)
-                        if (k * box < kKeysB) rows[k] = place(it, key0 + k * box);
-                    if (!(ok = wait_for(bar, &bar.rempty[rslot], rphase, p.err, -66))) break;
-                    mbar_arrive_expect_tx(&bar.rfull[rslot], kTileBytes);
-#pragma unroll
-                    for (int k = 0; k < kKeysB / 8; ++k)
-                        if (k * box < kKeysB)
-                            tma_load_2d_at(smem + L::kOffR + rslot * kTileBytes + k * box * 128, &map_k, &bar.rfull[rslot], 0, rows[k]);
-                    if (++rslot == L::kRopeRing) {
-                        rslot = 0;
-                        rphase ^= 1;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < kStages; ++c) {
-                        if (!(ok = wait_for(bar, &bar.kempty[slot], phase, p.err, -67))) break;
-                        mbar_arrive_expect_tx(&bar.kfull[slot], kStageBytes);
-                        const uint32_t dst = smem + slot * kStageBytes;
-                        if (box == kKeysB) {                 // one box of both tiles
-                            tma_load_3d_at(dst, &map_c, &bar.kfull[slot], 0, rows[0], 2 * c);
-                        } else {                             // a box a tile and page
-#pragma unroll
-                            for (int k = 0; k < kKeysB / 8; ++k)
-                                if (k * box < kKeysB) {
-                                    tma_load_3d_at(dst + k * box * 128, &map_c, &bar.kfull[slot], 0, rows[k], 2 * c);
-                                    tma_load_3d_at(dst + kTileBytes + k * box * 128, &map_c, &bar.kfull[slot], 0, rows[k], 2 * c + 1);
-                                }
-                        }
-                        if (++slot == L::kRing) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (!ok) break;
+                for (int k = 0; k < kKeysB / 8; ++k) {
+                    if (k >= boxes) break;
+                    row[k] = __shfl_sync(0xffffffffu, rows, k);
+                    if (lead) tma_load_2d_at(smem + L::kOffR + rslot * kTileBytes + k * box * 128, &map_k, &bar.rfull[rslot], 0, row[k]);
                 }
+                if (++rslot == L::kRopeRing) {
+                    rslot = 0;
+                    rphase ^= 1;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kStages; ++c) {
+                    if (!(ok = warp_wait(bar, &bar.kempty[slot], phase, p.err, -67))) break;
+                    const uint32_t dst = smem + slot * kStageBytes;
+                    if (lead) mbar_arrive_expect_tx(&bar.kfull[slot], kStageBytes);
+                    if (boxes == 1) {                        // one box of both tiles
+                        if (lead) tma_load_3d_at(dst, &map_c, &bar.kfull[slot], 0, row[0], 2 * c);
+                    } else {                                 // a box a tile and page
+#pragma unroll
+                        for (int k = 0; k < kKeysB / 8; ++k) {
+                            if (k >= boxes) break;
+                            if (lead) {
+                                tma_load_3d_at(dst + k * box * 128, &map_c, &bar.kfull[slot], 0, row[k], 2 * c);
+                                tma_load_3d_at(dst + kTileBytes + k * box * 128, &map_c, &bar.kfull[slot], 0, row[k], 2 * c + 1);
+                            }
+                        }
+                    }
+                    if (++slot == L::kRing) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
             }
         }
         __syncwarp();
@@ -613,114 +666,92 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // -------------------------------- MMA issuer --------------------------------
-        if (elect_one()) {
-            const uint32_t id_s = idesc_bf16_f32(kKeysB, kRows, 0, 0), id_o = idesc_bf16_f32(128, kRows, 1, 0);
-            // Descriptors differ only in their low words (address and leading stride); each use adds a
-            // constant to a base the compiler cannot see through, or it would keep all of them live.
-            const uint32_t dhi = (uint32_t)(sdesc_sw128(0, 0, 1024) >> 32);
-            const uint32_t base = smem >> 4, lbo_k = (16u >> 4) << 16, lbo_mn = ((uint32_t)kTileBytes >> 4) << 16;
-            auto desc = [&](uint32_t lo) { return ((uint64_t)dhi << 32) | lo; };
-            auto opaque = [](uint32_t v) {
-                asm volatile("" : "+r"(v));
-                return v;
-            };
-            // the scores' and the output's places in the list of items
-            Item si;
-            bool smore = first_item(p, bar.work, si);
-            while (smore && tile_of(p, si, g_of) < 0) smore = advance(p, si);
-            Item pi = si;
-            bool pmore = smore;
-            int sj = 0, pj = 0, stage = -1;                  // blocks within the item; -1: rope keys first
-            uint32_t sg = 0, pg = 0, sii = 0, pii = 0;       // blocks and items so far
-            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, oslot = 0;
-            uint64_t since = 0;
-            int idle = 0;
-            while (pmore) {
-                bool moved = false;
-                if (pg < sg && mbar_test(&bar.pfull, pg & 1) && (pj > 0 || pii == 0 || mbar_test(&bar.ofree, (pii - 1) & 1))) {
+        // ------------------------------------ scores ------------------------------------
+        // The whole warp walks the loop, so that all it computes is uniform, and one lane issues.
+        const bool lead = elect_one();
+        const uint32_t id = idesc_bf16_f32(kKeysB, kRows, 0, 0), td = uniform(tmem) + kColS;
+        const uint32_t base = (uniform(smem) >> 4) + kLeadK, qd = base + (L::kOffQ >> 4);
+        Item it;
+        uint32_t g = 0, ii = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
+        bool ok = true;
+        for (bool have = first_item(p, bar.work, it); have && ok; have = advance(p, it)) {
+            if (tile_of(p, it, g_of) < 0) continue;
+            if (!(ok = warp_wait(bar, &bar.qfull, ii & 1, p.err, -69))) break;
+            const int nb = (int)uniform((uint32_t)it.nb);
+            for (int j = 0; j < nb; ++j, ++g) {
+                const uint32_t d = td + (g & 1) * kRows;
+                if (g >= 2 && !(ok = warp_wait(bar, &bar.sempty[g & 1], ((g >> 1) - 1) & 1, p.err, -70))) break;
+                if (!(ok = warp_wait(bar, &bar.rfull[rslot], rphase, p.err, -71))) break;
+                tc_fence_after();
+                const uint32_t rd = base + (L::kOffR >> 4) + rslot * (kTileBytes >> 4);
+                if (lead) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) mma_ss(d, desc_of(rd + 2 * t), desc_of(qd + (8 * L::kQTile >> 4) + 2 * t), id, t > 0 ? 1u : 0u);
+                    mma_commit(&bar.rempty[rslot]);
+                }
+                if (++rslot == L::kRopeRing) {
+                    rslot = 0;
+                    rphase ^= 1;
+                }
+#pragma unroll
+                for (int c = 0; c < kStages; ++c) {
+                    if (!(ok = warp_wait(bar, &bar.kfull[slot], phase, p.err, -72))) break;
                     tc_fence_after();
-                    const uint32_t pd = opaque(base + lbo_k + (L::kOffP >> 4));
-#pragma unroll 1
-                    for (int c = 0; c < kStages; ++c) {
-                        const uint32_t vd = opaque(base + lbo_mn + oslot * (kStageBytes >> 4));
+                    const uint32_t kd = base + slot * (kStageBytes >> 4);
+                    if (lead) {
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)          // tile 2 c + t / 4, 16 dims each
+                            mma_ss(d, desc_of(kd + (((t >> 2) * kTileBytes + (t & 3) * 32) >> 4)),
+                                   desc_of(qd + (((2 * c + (t >> 2)) * L::kQTile + (t & 3) * 32) >> 4)), id, 1u);
+                        if (c == kStages - 1) mma_commit(&bar.sfull[g & 1]);
+                    }
+                    if (++slot == L::kRing) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (lead) mma_commit(&bar.qempty);
+            ++ii;
+        }
+        if (lead) {
+            mma_commit(&bar.drain);                          // every MMA done before tensor memory goes
+            mbar_wait(&bar.drain, 0, kWait);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------ output ------------------------------------
+        const bool lead = elect_one();
+        const uint32_t id = idesc_bf16_f32(128, kRows, 1, 0), td = uniform(tmem);
+        const uint32_t base = uniform(smem) >> 4, pd = base + kLeadK + (L::kOffP >> 4);
+        Item it;
+        uint32_t g = 0, ii = 0, slot = 0;
+        bool ok = true;
+        for (bool have = first_item(p, bar.work, it); have && ok; have = advance(p, it)) {
+            if (tile_of(p, it, g_of) < 0) continue;
+            if (ii > 0 && !(ok = warp_wait(bar, &bar.ofree, (ii - 1) & 1, p.err, -73))) break;
+            const int nb = (int)uniform((uint32_t)it.nb);
+            for (int j = 0; j < nb; ++j, ++g) {
+                if (!(ok = warp_wait(bar, &bar.pfull, g & 1, p.err, -74))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kStages; ++c) {
+                    const uint32_t vd = base + kLeadMn + slot * (kStageBytes >> 4);
+                    if (lead) {
 #pragma unroll
                         for (int t = 0; t < 4; ++t)          // 16 keys each
-                            mma_ss(tmem + kRows * c, desc(vd + (t * 2048 >> 4)), desc(pd + 2 * t), id_o, (pj > 0 || t > 0) ? 1u : 0u);
-                        mma_commit(&bar.kempty[oslot]);
-                        if (++oslot == L::kRing) oslot = 0;
+                            mma_ss(td + kRows * c, desc_of(vd + (t * 2048 >> 4)), desc_of(pd + 2 * t), id, t > 0 || j > 0 ? 1u : 0u);
+                        mma_commit(&bar.kempty[slot]);
                     }
-                    mma_commit(&bar.pdone);
-                    ++pg;
-                    if (++pj == pi.nb) {
-                        pj = 0;
-                        ++pii;
-                        do pmore = advance(p, pi);
-                        while (pmore && tile_of(p, pi, g_of) < 0);
-                    }
-                    moved = true;
+                    if (++slot == L::kRing) slot = 0;
                 }
-                // one stage of the next block's scores: its buffer has been read when the block two before is in O^T
-                if (smore && sg <= pg + 1) {
-                    if (stage < 0) {
-                        if ((sj > 0 || mbar_test(&bar.qfull, sii & 1)) && mbar_test(&bar.rfull[rslot], rphase)) {
-                            tc_fence_after();
-                            const uint32_t rd = opaque(base + lbo_k + (L::kOffR >> 4) + rslot * (kTileBytes >> 4));
-                            const uint32_t qr = opaque(base + lbo_k + ((L::kOffQ + 8 * L::kQTile) >> 4));
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                mma_ss(tmem + kColS + (sg & 1) * kRows, desc(rd + 2 * t), desc(qr + 2 * t), id_s, t > 0 ? 1u : 0u);
-                            mma_commit(&bar.rempty[rslot]);
-                            if (++rslot == L::kRopeRing) {
-                                rslot = 0;
-                                rphase ^= 1;
-                            }
-                            stage = 0;
-                            moved = true;
-                        }
-                    } else if (mbar_test(&bar.kfull[slot], phase)) {
-                        tc_fence_after();
-                        const uint32_t kd = opaque(base + lbo_k + slot * (kStageBytes >> 4));
-                        const uint32_t qd = opaque(base + lbo_k + (L::kOffQ >> 4) + 2 * stage * (L::kQTile >> 4));
-#pragma unroll
-                        for (int t = 0; t < 8; ++t)          // tile 2 stage + t / 4, 16 dims each
-                            mma_ss(tmem + kColS + (sg & 1) * kRows, desc(kd + (((t >> 2) * kTileBytes + (t & 3) * 32) >> 4)),
-                                   desc(qd + (((t >> 2) * L::kQTile + (t & 3) * 32) >> 4)), id_s, 1u);
-                        if (++slot == L::kRing) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                        if (++stage == kStages) {
-                            mma_commit(&bar.sfull[sg & 1]);
-                            stage = -1;
-                            ++sg;
-                            if (++sj == si.nb) {
-                                mma_commit(&bar.qempty);
-                                sj = 0;
-                                ++sii;
-                                do smore = advance(p, si);
-                                while (smore && tile_of(p, si, g_of) < 0);
-                            }
-                        }
-                        moved = true;
-                    }
-                }
-                if (moved) {
-                    idle = 0;
-                    since = 0;
-                } else if (++idle == 64) {                   // the clock every 64 polls
-                    idle = 0;
-                    const uint64_t now = global_ns();
-                    if (!since) since = now;
-                    const bool late = now - since > kWait;
-                    if (late) {
-                        bar.abort_flag = 1;
-                        if (p.err) atomicCAS(p.err, 0, -69);
-                    }
-                    if (late || *reinterpret_cast<volatile int *>(&bar.abort_flag)) break;
-                }
+                if (lead) mma_commit(&bar.pdone);
             }
-            mma_commit(&bar.drain);                          // every MMA done before tensor memory goes
+            ++ii;
+        }
+        if (lead) {
+            mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, kWait);
         }
         __syncwarp();
@@ -736,53 +767,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the groups that a share's end cut. A NaN in a piece's lse reaches the row. The shares'
-// bounds are read, not computed again. Share k's slot: 2 k when it starts in the group (which is its first
-// item then), else 2 k + 1; -1: it does not meet the group, or is empty.
-__device__ __forceinline__ int64_t piece_slot(const PagedParams &p, int k, int64_t t0, int64_t t1, int g) {
-    if (k >= p.shares) return -1;
-    const int64_t a = p.cuts[k].start, e = p.cuts[k + 1].start;
-    return a >= t1 || a == e ? -1 : 2 * ((int64_t)k * p.group + g) + (a >= t0 ? 0 : 1);
-}
-
-constexpr int kMergeRows = 4;
-
-// CTA (c - 1, tile of the group and four rows of it) serves cut c (where share c begins) when it is the first
-// inside its group, two warps a row (256 columns each).
-template <bool kBf16Out>
-__global__ void __launch_bounds__(64 * kMergeRows) merge_paged_rows_kernel(const PagedParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
+// Joins the pieces of the groups that a share's end cut, four warps a row (128 columns each). A NaN in a
+// piece's lse reaches the row.
+// A group that is cut is served where share c begins inside it and is the first to: CTA (c - 1, two rows).
+// Where a group has many pieces (kSplit = 4), four times four warps take them in turn, and CTA (x, a row) looks
+// for the x-th such share itself: most shares are none, and a CTA for each would cost more than the search.
+template <int kSplit> struct Join {
+    static constexpr int kRows = kSplit == 1 ? 2 : 1, kWarps = 4 * kSplit * kRows;
+};
+template <bool kBf16Out, int kSplit>
+__global__ void __launch_bounds__(32 * Join<kSplit>::kWarps) merge_paged_rows_kernel(const PagedParams p) {
+    constexpr int kWarps = Join<kSplit>::kWarps, kRows = Join<kSplit>::kRows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int c = blockIdx.x + 1;
+    if constexpr (kSplit > 1) {
+        __shared__ int counts[kWarps], cut;
+        if (threadIdx.x == 0) cut = 0;
+        for (int base = 1, seen = 0; base < p.shares; base += 32 * kWarps) {
+            const int i = base + (int)threadIdx.x;
+            const bool is = i < p.shares && p.cuts[i].pieces > 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, is);
+            if (lane == 0) counts[warp] = __popc(all);
+            __syncthreads();
+            int rank = seen + __popc(all & ((1u << lane) - 1u));
+            for (int w = 0; w < kWarps; ++w) {
+                rank += w < warp ? counts[w] : 0;
+                seen += counts[w];
+            }
+            if (is && rank == (int)blockIdx.x) cut = i;
+            __syncthreads();
+        }
+        if ((c = cut) == 0) return;                           // fewer groups are cut
+    }
     const PagedShare sh = p.cuts[c];
-    const int64_t before = p.cuts[c - 1].start;
-    if (sh.start == sh.t0 || before > sh.t0) return;          // between two groups, or not the first inside this one
-    const int grow = blockIdx.y * kMergeRows + (warp >> 1), g = grow / p.tile, row = grow % p.tile, col = 256 * (warp & 1) + 4 * lane;
-    if (grow >= sh.rows) return;
+    const int part = warp / (4 * kRows), grow = blockIdx.y * kRows + (warp >> 2) % kRows;
+    if (sh.pieces == 0 || grow >= sh.rows) return;            // (all warps of a row)
+    const int g = grow / p.tile, row = grow % p.tile, col = 128 * (warp & 3) + 4 * lane;
+    // piece k's place: share c - 1 + k's slot 2, but of share c - 1 the second item's where it did not begin here
+    auto at = [&](int k) { return (int64_t)(2 * ((c - 1 + k) * p.group + g) + (k == 0 ? sh.second : 0)) * p.tile + row; };
     float M = -INFINITY;
     bool nan = false;
-    for (int base = c - 1; base < p.shares && p.cuts[base].start < sh.t1; base += 32) {
-        const int64_t sl = piece_slot(p, base + lane, sh.t0, sh.t1, g);
-        const float v = sl >= 0 ? p.part_lse[sl * p.tile + row] : -INFINITY;
+    for (int k = lane; k < sh.pieces; k += 32) {
+        const float v = p.part_lse[at(k)];
         nan |= v != v;
         M = fmaxf(M, v);
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     nan = __any_sync(0xffffffffu, nan);
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float S = nan ? __uint_as_float(0x7fffffffu) : 0.f;
     if (M > -INFINITY)
-        for (int base = c - 1; base < p.shares && p.cuts[base].start < sh.t1; base += 32) {
-            const int sl = (int)piece_slot(p, base + lane, sh.t0, sh.t1, g);
-            const float v = sl >= 0 ? p.part_lse[(int64_t)sl * p.tile + row] : -INFINITY;
+        for (int base = 0; base < sh.pieces; base += 32) {
+            const float v = base + lane < sh.pieces ? p.part_lse[at(base + lane)] : -INFINITY;
             const float wt = v == -INFINITY ? 0.f : __expf(v - M);
             float ws = wt;
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
             S += ws;
-            // the pieces that count (weight 0: no visible key, no such share), their loads independent
-            uint32_t live = __ballot_sync(0xffffffffu, wt != 0.f);
+            // the pieces that count (weight 0: no visible key), their loads independent
+            uint32_t live = __ballot_sync(0xffffffffu, wt != 0.f && (kSplit == 1 || lane % kSplit == part));
             while (live) {
-                float4 a[4], d[4];
+                float4 a[4];
                 float wk[4];
                 int n = 0;
 #pragma unroll
@@ -792,33 +838,35 @@ __global__ void __launch_bounds__(64 * kMergeRows) merge_paged_rows_kernel(const
                     const int k = __ffs(live) - 1;
                     live &= live - 1;
                     wk[u] = __shfl_sync(0xffffffffu, wt, k);
-                    const float4 *src =
-                        reinterpret_cast<const float4 *>(p.part_o + ((int64_t)__shfl_sync(0xffffffffu, sl, k) * p.tile + row) * kDc + col);
-                    a[u] = src[0];
-                    d[u] = src[32];
+                    a[u] = *reinterpret_cast<const float4 *>(p.part_o + at(base + k) * kDc + col);
                     n = u + 1;
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (u >= n) break;
-                    acc[0] = make_float4(fmaf(wk[u], a[u].x, acc[0].x), fmaf(wk[u], a[u].y, acc[0].y), fmaf(wk[u], a[u].z, acc[0].z),
-                                         fmaf(wk[u], a[u].w, acc[0].w));
-                    acc[1] = make_float4(fmaf(wk[u], d[u].x, acc[1].x), fmaf(wk[u], d[u].y, acc[1].y), fmaf(wk[u], d[u].z, acc[1].z),
-                                         fmaf(wk[u], d[u].w, acc[1].w));
+                    acc = make_float4(fmaf(wk[u], a[u].x, acc.x), fmaf(wk[u], a[u].y, acc.y), fmaf(wk[u], a[u].z, acc.z),
+                                      fmaf(wk[u], a[u].w, acc.w));
                 }
             }
         }
+    if constexpr (kSplit > 1) {
+        __shared__ float4 sums[kSplit - 1][128];
+        const int x = threadIdx.x & 127;
+        if (part > 0) sums[part - 1][x] = acc;
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int k = 0; k < kSplit - 1; ++k)
+            acc = make_float4(acc.x + sums[k][x].x, acc.y + sums[k][x].y, acc.z + sums[k][x].z, acc.w + sums[k][x].w);
+    }
     const float inv = S == 0.f ? 0.f : 1.f / S;
     const int64_t out = sh.row0 + grow;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float4 v = make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
-        if (kBf16Out)
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out * kDc + col + 128 * h) =
-                make_uint2(q8::pack_bf16(v.x, v.y), q8::pack_bf16(v.z, v.w));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + out * kDc + col + 128 * h) = v;
-    }
+    const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (kBf16Out)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out * kDc + col) =
+            make_uint2(q8::pack_bf16(v.x, v.y), q8::pack_bf16(v.z, v.w));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + out * kDc + col) = v;
     if (col == 0 && p.lse) p.lse[out] = S == 0.f ? -INFINITY : M + logf(S);
 }
 
@@ -877,8 +925,11 @@ template <int kRows, bool kBf16Out> cudaError_t launch(const PagedParams &p, cud
     cfg.numAttrs = p.overlap_vis ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, verify_paged_kernel<kRows, kBf16Out>, map_c, map_k, map_qn, map_qp, p)) != cudaSuccess) return e;
     if (p.pieces) {
-        merge_paged_rows_kernel<kBf16Out><<<dim3((unsigned)(p.shares - 1), (unsigned)(p.group * p.tile / kMergeRows)),
-                                           64 * kMergeRows, 0, s>>>(p);
+        const unsigned rows = (unsigned)(p.group * p.tile);
+        if (p.deep)
+            merge_paged_rows_kernel<kBf16Out, 4><<<dim3((unsigned)p.deep, rows), 32 * Join<4>::kWarps, 0, s>>>(p);
+        else
+            merge_paged_rows_kernel<kBf16Out, 1><<<dim3((unsigned)(p.shares - 1), rows / Join<1>::kRows), 32 * Join<1>::kWarps, 0, s>>>(p);
         e = cudaGetLastError();
     }
     return e;

@@ -16,11 +16,13 @@ struct PagedPlan {
     int tile = 0, group = 0, least = 1;    // rows of a tile, tiles side by side, least blocks of a share
     bool vis = false;                      // the visibility kernel finds the words first
     bool pieces = false;                   // a second kernel joins the pieces of what the split cut
+    int deep = 0;                          // the groups, where a row can have more than a few
     size_t vis_off = 0, po_off = 0, pl_off = 0, cuts_off = 0, ws_bytes = 0;
 };
 
 constexpr int kMostGroup = 8;              // row tiles that walk the same keys side by side
 constexpr int kLeastBlocks = 2;
+constexpr int kDeep = 8;                   // shares a group from which several warps take a row's pieces in turn
 
 kdt_status check_args(const kdt_verify_paged_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;
@@ -84,6 +86,7 @@ kdt_status make_plan(const kdt_verify_paged_args *a, PagedPlan *out) {
     p.least = a->num_splits > 0 ? 1 : kLeastBlocks;
     p.ctas = p.shares * p.group;
     p.pieces = p.shares > 1 && nblk > 1;                      // a group of one block is never cut
+    p.deep = p.shares >= kDeep * groups ? (int)groups : 0;
     size_t off = 0;
     p.vis = a->parent != nullptr;
     if (p.vis) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
@@ -94,7 +97,7 @@ kdt_status make_plan(const kdt_verify_paged_args *a, PagedPlan *out) {
         p.pl_off = off;
         off = align_up(off + rows * sizeof(float));
         p.cuts_off = off;
-        off = align_up(off + (size_t)(p.shares + 1) * sizeof(PagedShare));
+        off = align_up(off + (size_t)p.shares * sizeof(PagedShare));
     }
     p.ws_bytes = off;
     p.launches = (p.vis ? 1 : 0) + 1 + (p.pieces ? 1 : 0);
@@ -175,6 +178,7 @@ kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace
     q.shares = p.shares;
     q.least = p.least;
     q.pieces = p.pieces;
+    q.deep = p.deep;
     q.overlap_vis = p.vis;
     q.part_o = reinterpret_cast<float *>(ws + p.po_off);
     q.part_lse = reinterpret_cast<float *>(ws + p.pl_off);
