@@ -22,10 +22,16 @@ using namespace rows;
 //    each, in shared memory), then the cluster's threads share the pages, each found by a binary
 //    search over the scanned counts, then the rows' slots, read through the new table.
 //  * State that every CTA reads (held, n_free) is written behind a cluster barrier.
+//  * Latency bounds it: a launch, the requests' lengths, a page's search and its read, the table again for the
+//    rows. So a thread has four pages and a lane 16 rows in flight at once. 8 requests of 64 new rows, and back:
+//    11 us a call, of it 5 - 7 on the device; 256 prompts of 2001 rows in pages of 16, 32256 pages and 512256
+//    slots: 22 us, of which the slots take 14 (a row at a time 33); their return 8 (one CTA 29).
 constexpr int kAssignThreads = 1024;
 constexpr int kAssignCluster = 8;
 constexpr int kMaxAssign = 16384;                   // requests: their scans lie in shared memory
-constexpr int kRowsACta = 16384;                    // slots that one CTA takes before another joins
+constexpr int kRowsALane = 16;                      // rows whose page a lane looks up at once
+constexpr int kPagesAThread = 4;
+constexpr int kRowsACta = 16384, kPagesACta = 4096; // slots, table entries that one CTA takes before another joins
 
 struct AssignParams {
     int32_t *table, *held, *free_pages, *n_free;
@@ -120,37 +126,61 @@ __global__ void __launch_bounds__(kAssignThreads) page_assign_kernel(const Assig
         return need >= 0 && !(need > have && takes[b] + need - have > room);
     };
     // -- pages: those taken to their tables, those given and not taken to the stack
-    const int step = (int)size * kAssignThreads;
-    for (int k = (int)rank * kAssignThreads + tid; k < max(taken, given); k += step) {
-        int32_t page;
-        if (k < given) {
-            const int b = owner_of(gives, p.B, k);
-            int need, have;
-            served(b, need, have);
-            page = p.table[b * p.table_stride + need + (k - gives[b])];
-        } else
-            page = p.free_pages[n_free - 1 - (k - given)];
-        if (k < taken) {
-            const int b = owner_of(takes, p.B, k);
-            int need, have;
-            if (served(b, need, have) && need > have) p.table[b * p.table_stride + have + (k - takes[b])] = page;
-        } else if (room - 1 - k < p.n_pages)
-            p.free_pages[room - 1 - k] = page;
+    // (nothing read here is written here: a thread reads several before it writes)
+    const uint32_t step = size * kAssignThreads, all = (uint32_t)max(taken, given);     // (below 2^31: k is free to pass it)
+    for (uint32_t k0 = rank * kAssignThreads + tid; k0 < all; k0 += kPagesAThread * step) {
+        int32_t page[kPagesAThread];
+#pragma unroll
+        for (int i = 0; i < kPagesAThread; ++i) {
+            const int64_t k = k0 + i * step;
+            page[i] = 0;
+            if (k < given) {
+                const int b = owner_of(gives, p.B, (int)k);
+                int need, have;
+                served(b, need, have);
+                page[i] = p.table[b * p.table_stride + need + (k - gives[b])];
+            } else if (k < all)
+                page[i] = p.free_pages[n_free - 1 - (k - given)];
+        }
+#pragma unroll
+        for (int i = 0; i < kPagesAThread; ++i) {
+            const int64_t k = k0 + i * step;
+            if (k < taken) {
+                const int b = owner_of(takes, p.B, (int)k);
+                int need, have;
+                if (served(b, need, have) && need > have) p.table[b * p.table_stride + have + (k - takes[b])] = page[i];
+            } else if (k < given && room - 1 - k < p.n_pages)
+                p.free_pages[room - 1 - k] = page[i];
+        }
     }
     // -- every row's slot
     if (p.slots) {
         if (size > 1) tc::cluster_sync();
         else __syncthreads();
-        const int64_t total = (int64_t)p.B * p.T;
-        for (int64_t n = (int64_t)rank * kAssignThreads + tid; n < total; n += step) {
-            const int b = (int)(n / p.T);
-            const int64_t row = (int64_t)p.start[b] + (n - (int64_t)b * p.T);
-            int need, have, slot = -1;
-            if (row >= 0 && row < p.new_len[b] && served(b, need, have)) {
-                const int32_t page = __ldcg(p.table + b * p.table_stride + (row >> p.shift));
-                if (page >= 0 && page < p.n_pages) slot = (int)(((int64_t)page << p.shift) + (row & ((1 << p.shift) - 1)));
+        // a run of rows of one request is shared by as many lanes, up to 32, as it has rows
+        const uint32_t T = (uint32_t)p.T;
+        uint32_t lanes = 1;
+        while (lanes < 32 && lanes < T) lanes *= 2;
+        const uint32_t chunks = (T + lanes * kRowsALane - 1) / (lanes * kRowsALane), units = (uint32_t)p.B * chunks;
+        const uint32_t abreast = 32 / lanes, stride = size * (kAssignThreads / 32) * abreast;
+        for (uint32_t u = (rank * (kAssignThreads / 32) + warp) * abreast + lane / lanes; u < units; u += stride) {
+            const uint32_t b = u / chunks, t0 = (u - b * chunks) * lanes * kRowsALane + (lane & (lanes - 1));
+            int need, have;
+            const int64_t start = p.start[b], len = served((int)b, need, have) ? p.new_len[b] : 0;
+            const int32_t *pages = p.table + b * p.table_stride;
+            int32_t *slots = p.slots + (int64_t)b * p.T;
+            int32_t page[kRowsALane];
+#pragma unroll
+            for (int i = 0; i < kRowsALane; ++i) {
+                const int64_t row = start + t0 + i * lanes;
+                page[i] = t0 + i * lanes < T && row >= 0 && row < len ? __ldcg(pages + (row >> p.shift)) : -1;
             }
-            p.slots[n] = slot;
+#pragma unroll
+            for (int i = 0; i < kRowsALane; ++i) {
+                const int row = (int)(start + t0 + i * lanes);
+                const bool lies = page[i] >= 0 && page[i] < p.n_pages;
+                if (t0 + i * lanes < T) slots[t0 + i * lanes] = lies ? (page[i] << p.shift) + (row & ((1 << p.shift) - 1)) : -1;
+            }
         }
     }
     // -- what every CTA has read
@@ -254,7 +284,9 @@ kdt_status kdt_page_assign(const kdt_page_args *a, cudaStream_t stream) {
     const AssignParams p = {a->table, a->held, a->free_pages, a->n_free, a->new_len, a->start, a->T > 0 ? a->slots : nullptr,
                             a->err,   stride,  a->B,          a->W,      a->T,       a->n_pages, shift};
     int S = 1;
-    while (S < kAssignCluster && (int64_t)a->B * a->T > (int64_t)S * kRowsACta) S <<= 1;
+    while (S < kAssignCluster &&
+           ((int64_t)a->B * a->T > (int64_t)S * kRowsACta || (int64_t)a->B * a->W > (int64_t)S * kPagesACta))
+        S <<= 1;
     const size_t smem = (size_t)a->B * 2 * sizeof(int);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(page_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxAssign * 2 * sizeof(int))) !=
