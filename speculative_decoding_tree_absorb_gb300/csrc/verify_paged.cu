@@ -205,13 +205,13 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// Positions: sequence-major, group-major, block order; W of them, cut into up to p.shares equal shares of
-// p.least or more.
+// Positions: sequence-major, group-major, block order; W of them in G groups, cut into up to p.shares equal
+// shares: one a group, or more of p.least blocks or more.
 struct Shares {
     int64_t W, each;
     int C, more;                                              // the first `more` shares have a block more
-    __device__ __forceinline__ Shares(const PagedParams &p, int64_t w) : W(w) {
-        C = (int)min((int64_t)p.shares, max(quotient(W + p.least - 1, p.least), (int64_t)1));
+    __device__ __forceinline__ Shares(const PagedParams &p, int64_t w, int64_t G) : W(w) {
+        C = (int)min((int64_t)p.shares, max(max(quotient(W + p.least - 1, p.least), G), (int64_t)1));
         each = quotient(W, C);
         more = (int)(W - each * C);
     }
@@ -225,14 +225,20 @@ struct Shares {
 // One warp finds share c's first item. Where share c is the first to begin inside a group, it leaves that
 // group's rows and the number of its pieces for the merge.
 __device__ __forceinline__ void find_share(const PagedParams &p, int c, bool writes, int lane, int *out) {
-    int64_t W = 0;
+    int64_t W = 0, G = 0;
     for (int b = lane; b < p.B; b += 32) {
         const int n = nodes_of(p, b);
-        if (n) W += (int64_t)groups_of(p, n) * ((prefix_of(p, b, n) + n + kKeysB - 1) / kKeysB);
+        if (n) {
+            G += groups_of(p, n);
+            W += (int64_t)groups_of(p, n) * ((prefix_of(p, b, n) + n + kKeysB - 1) / kKeysB);
+        }
     }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-    const Shares shares(p, W);
+    for (int off = 16; off >= 1; off >>= 1) {
+        W += __shfl_xor_sync(0xffffffffu, W, off);
+        G += __shfl_xor_sync(0xffffffffu, G, off);
+    }
+    const Shares shares(p, W, G);
     const int64_t s0 = shares.start(c), s1 = shares.start(c + 1);
     if (lane == 0) {
         out[0] = (int)(s1 - s0);

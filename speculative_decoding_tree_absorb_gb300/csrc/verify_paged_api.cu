@@ -21,8 +21,13 @@ struct PagedPlan {
 };
 
 constexpr int kMostGroup = 8;              // row tiles that walk the same keys side by side
+// Key blocks that a share has at least, unless it is a whole group: of one block each, or three or four, one
+// sequence of 13 nodes of 128 heads over 400 keys takes 33, 37, 39 us for 33, a batch of 64 single tokens over 200
+// 24, 26, 24 for 24. (Two whole sequences of one block in one share took 30 us, a share each 20.)
 constexpr int kLeastBlocks = 2;
-constexpr int kDeep = 8;                   // shares a group from which several warps take a row's pieces in turn
+// Shares a group from which several warps take a row's pieces in turn: 152 pieces of one token of 64 heads over 32768
+// keys 46 us for 60, 38 a row of two long contexts 89 for 91; but 2 - 3 pieces a row of 64 sequences 108 for 96.
+constexpr int kDeep = 8;
 
 kdt_status check_args(const kdt_verify_paged_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;
