@@ -5,7 +5,7 @@
 //
 //  * A cluster of CTAs takes a row, each a contiguous slice, kept in shared memory where it fits.
 //  * Bins in the row's order, by the upper 16 bits of a logit's ordered bits (its bf16 value), counted in
-//    shared memory: 4096 of them from the maximum down, the values within 2^-6 of zero in one. In bf16 a
+//    shared memory: 4096 of them from the maximum down, the values within 2^-10 of zero in one. In bf16 a
 //    bin is one value, so that the counts and one weight a bin give every sum exactly: top-k's and top-p's
 //    borders come from one scan. A float32 bin's tokens differ: where top-p needs masses their weights are
 //    summed (as two 32-bit halves), and the tokens of the bin that a border falls into are gathered in the
@@ -15,6 +15,11 @@
 //    apart again. All sums are integers: neither the cluster's size nor the order of the adds shows.
 //  * A bin with more tokens than the list holds (float32, thousands of nearly equal logits) is searched by
 //    the first CTA over the whole row.
+//  * Measured: one row of 32000 tokens in float32 under all filters 30 us, a chain of passes over 4000 tokens a
+//    CTA and of a dozen barriers of the cluster. 64 rows of 160000 in bf16 with settings of their own 47 us: two
+//    CTAs a row, 80000 tokens each, of its 78 k cycles 11 for the maximum (the row comes from DRAM, 20 MB), 18
+//    for the counts (7 cycles for a warp's 32 adds, 20 instructions a token), 12 for bins and borders, 28 for the
+//    masses where nothing is filtered (a 64-bit look-up a token), 5 where 60 tokens are kept.
 #include <math.h>
 
 #include <atomic>
@@ -34,7 +39,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 2048, kHold = kList / kThreads; // tokens of one bin that a border falls into
 constexpr uint32_t kShort = 256;                    // as many are ranked, a thread each
 constexpr size_t kMostSmem = 200 * 1024;            // beside Shared
-constexpr uint32_t kPosTiny = 0xbc80u, kNegTiny = 0x437fu;     // upper ordered bits of 2^-6 and of -2^-6
+constexpr uint32_t kPosTiny = 0xba80u, kNegTiny = 0x457fu;     // upper ordered bits of 2^-10 and of -2^-10
 
 struct SampleParams {
     const void *logits;
@@ -56,25 +61,33 @@ __device__ __forceinline__ uint32_t order_key(float l) {           // ascending 
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ uint32_t bits_key(float l) {            // the same, but zeros of either sign differ
+    const uint32_t u = __float_as_uint(l);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
 
 // Bins in the row's order, the largest logit's first.
 struct Bins {
     uint32_t top, low;                              // upper key bits of the maximum; of the first negative bin
     int pos, neg;                                   // bins before the one around zero; and up to the negative ones
+    int zero, under;                                // the one around zero, or -1; a negative bin and its upper bits
     __device__ __forceinline__ void set(uint32_t max_key) {
         top = max_key >> 16;
         pos = top >= kPosTiny ? (int)(top - kPosTiny) + 1 : 0;
         neg = pos + (top > kNegTiny ? 1 : 0);
         low = min(top, kNegTiny);
+        zero = neg > pos ? pos : -1;
+        under = neg + (int)low;
     }
+    // top - h for positive ones, `pos` around zero (there under - h <= pos <= top - h), under - h for negative ones
     __device__ __forceinline__ int of(uint32_t key) const {
-        const uint32_t h = key >> 16;
-        const int b = h >= kPosTiny ? (int)(top - h) : (h > kNegTiny ? pos : neg + (int)(low - h));
-        return min(b, kBins - 1);
+        const int h = (int)(key >> 16);
+        return min(max(min((int)top - h, pos), under - h), kBins - 1);
     }
     // whether a bin holds one bf16 value only, and that value
-    __device__ __forceinline__ bool single(int b) const { return b < kBins - 1 && !(b == pos && neg > pos); }
+    __device__ __forceinline__ bool single(int b) const { return b < kBins - 1 && b != zero; }
     __device__ __forceinline__ float value(int b) const {
         const uint32_t h = b < pos ? top - (uint32_t)b : low - (uint32_t)(b - neg);
         return key_logit(h & 0x8000u ? h << 16 : (h << 16) | 0xffffu);
@@ -285,10 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     auto w_of = [&](float l) { return weight(l, m, c_hi, c_lo, tab); };
     Bins bins;
     bins.set(order_key(m));
-    // every token of the slice, 16 bytes at a time where they can be had so
-    auto each = [&](auto &&f) {
+    // every token of the slice, 16 bytes at a time where they can be had so. The loop is unrolled: `f` is short,
+    // and says of which tokens `rest` has to see (32 copies of a weight's code do not fit the instruction cache:
+    // 75 instructions' time a token).
+    auto each = [&](auto &&f, auto &&rest) {
         if (p.cache || p.vec) {
             for (int i0 = tid; i0 < nv; i0 += 4 * kThreads) {
+                uint32_t more = 0;
                 uint4 v[4];                                    // (their latency is what a pass takes)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -298,12 +314,26 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                     if (i0 + u * kThreads >= nv) break;
                     const E *e = reinterpret_cast<const E *>(&v[u]);
 #pragma unroll
-                    for (int k = 0; k < kPer; ++k) f(as_f32(e[k]), (i0 + u * kThreads) * kPer + k);
+                    for (int k = 0; k < kPer; ++k) more |= (f(as_f32(e[k]), (i0 + u * kThreads) * kPer + k) ? 1u : 0u) << (u * kPer + k);
+                }
+                while (more) {
+                    const int k = __ffs(more) - 1;
+                    more &= more - 1;
+                    rest(as_f32(data[(i0 + k / kPer * kThreads) * kPer + k % kPer]));
                 }
             }
-            for (int i = nv * kPer + tid; i < n; i += kThreads) f(as_f32(data[i]), i);
+#pragma unroll 1
+            for (int i = nv * kPer + tid; i < n; i += kThreads)
+                if (f(as_f32(data[i]), i)) rest(as_f32(data[i]));
         } else
-            for (int i = tid; i < n; i += kThreads) f(as_f32(data[i]), i);
+#pragma unroll 1
+            for (int i = tid; i < n; i += kThreads)
+                if (f(as_f32(data[i]), i)) rest(as_f32(data[i]));
+    };
+    auto none = [](float) {};
+    auto each_weighed = [&](auto &&f) {                        // one by one, for what is long
+#pragma unroll 1
+        for (int i = tid; i < n; i += kThreads) f(as_f32(data[i]));
     };
 
     // -- tokens a bin; in float32 also the sum of all weights in units of 2^-40, good enough for a log-probability
@@ -319,26 +349,50 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 zf = 0.f;
                 k = 0;
             }
-        });
+            return false;
+        }, none);
         z += (uint64_t)(zf * 1099511627776.f);
     }
     Border border = {0u, (uint32_t)p.V};                       // everything
     if (greedy) border = {order_key(m), 1u};
     const bool table_w = kSingle && !greedy;                   // bins have weights
     if (!greedy && (kSingle || by_count || by_mass)) {
-        if (kSingle || by_count) {
+        // (the last bin has what lies far below, a mask's -inf too: counted apart, as a word that all add to is slow)
+        const bool weighs = kSingle || (by_mass && !by_count);
+        uint32_t n_last = 0;
+        uint64_t w_last = 0, w_zero = 0;
+        if (!weighs || kSingle)
             each([&](float l, int) {
-                const int b = bins.of(order_key(l));
+                const int b = bins.of(bits_key(l));
+                if (b == kBins - 1) {
+                    ++n_last;
+                    return weighs && l > -INFINITY;
+                }
                 atomicAdd(&dy.count[b], 1u);
-                if (kSingle && !bins.single(b)) add_to(&dy.lo[b], &dy.hi[b], w_of(l));
+                return kSingle && b == bins.zero;
+            }, [&](float l) {
+                const int b = bins.of(bits_key(l));
+                if (b == kBins - 1 && l > -INFINITY) w_last += w_of(l);
+                if (b == bins.zero) w_zero += w_of(l);
             });
-        }
-        if (!kSingle && by_mass && !by_count) {
-            each([&](float l, int) {
-                const int b = bins.of(order_key(l));
-                atomicAdd(&dy.count[b], 1u);
-                add_to(&dy.lo[b], &dy.hi[b], w_of(l));
+        else
+            each_weighed([&](float l) {
+                const int b = bins.of(bits_key(l));
+                if (b == kBins - 1) {
+                    ++n_last;
+                    if (l > -INFINITY) w_last += w_of(l);
+                } else {
+                    atomicAdd(&dy.count[b], 1u);
+                    add_to(&dy.lo[b], &dy.hi[b], w_of(l));
+                }
             });
+        n_last = warp_sum(n_last);
+        w_last = warp_sum(w_last);
+        if (kSingle) w_zero = warp_sum(w_zero);
+        if (lane == 0) {
+            if (n_last) atomicAdd(&dy.count[kBins - 1], n_last);
+            if (w_last) add_to(&dy.lo[kBins - 1], &dy.hi[kBins - 1], w_last);
+            if (kSingle && w_zero) add_to(&dy.lo[bins.zero], &dy.hi[bins.zero], w_zero);
         }
         // the row's bins: each CTA adds what it counted to the CTAs whose share of the bins that is
         const int share = kBins / (int)size, first = (int)rank * share, per = (share + kThreads - 1) / kThreads;
@@ -448,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                     const uint32_t at = add_cluster(counter, 1u);
                     if (at < kList) st_cluster(base + 8 * at, ((uint64_t)key << 32) | (uint32_t)(v0 + i));
                 }
-            });
+                return false;
+            }, none);
             tc::cluster_sync();
         };
         // What the cluster is told: the border, and the mass up to and with it.
@@ -586,10 +641,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             kept_mass = sh.above[0];
             if (!kSingle && by_mass) {                         // the masses of what top-k keeps, the border's bin whole
                 const int last = bins.of(border.key);
-                each([&](float l, int) {
-                    const int q = bins.of(order_key(l));
+                auto add = [&](float l) {
+                    const int q = bins.of(bits_key(l));
                     if (q < last) add_to(&dy.lo[q], &dy.hi[q], w_of(l));
-                });
+                };
+                each([&](float l, int) { return bins.of(bits_key(l)) < last; }, add);
                 __syncthreads();
                 push(false, 0, last);
                 total_up();
@@ -625,22 +681,33 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     const int part = (p.slice / 16 + kWarps - 1) / kWarps * 16;
     const uint64_t wx = w_of(key_logit(border.key));
     const bool ties_kept = wx >= least;
-    auto weigh = [&](float l, uint32_t key) -> uint64_t {
-        uint64_t w;
-        if (table_w) {
-            const int b = bins.of(key);
-            w = bins.single(b) ? dy.w[b] : w_of(l);
-        } else
-            w = w_of(l);
+    auto exact = [&](float l, uint32_t key) -> uint64_t {      // of a token above the border or below
+        const uint64_t w = key > border.key && l > -INFINITY ? w_of(l) : 0;
         return w >= least ? w : 0;
     };
+    constexpr uint64_t kNone = ~0ull;                          // a bin of several values
+    if (table_w) {                                             // the table's weights are what is kept of them
+        for (int b = tid; b < kBins; b += kThreads)
+            if (dy.count[b])
+                dy.w[b] = !bins.single(b) ? kNone : (order_key(bins.value(b)) > border.key && dy.w[b] >= least ? dy.w[b] : 0);
+        __syncthreads();
+    }
+    auto table_of = [&](float l) -> uint64_t { return table_w ? dy.w[bins.of(bits_key(l))] : kNone; };
+    auto weigh = [&](float l) -> uint64_t {
+        const uint64_t w = table_of(l);
+        return (uint32_t)(w >> 32) != ~0u ? w : exact(l, order_key(l));
+    };
+    const float at_border = key_logit(border.key);             // (everything: NaN, equal to none and below none)
     auto measure = [&](int i0, int i1, uint64_t &sum, uint32_t &ties) {      // (a warp's lanes side by side)
         uint64_t s = 0;
         uint32_t t = 0;
-        auto take = [&](float l) {
-            const uint32_t key = order_key(l);
-            t += key == border.key;
-            if (key > border.key) s += weigh(l, key);
+        // like `each`: what the table has at once, the others one by one
+        auto take = [&](float l) -> bool {
+            t += l == at_border;
+            const uint64_t w = table_of(l);
+            const bool has = (uint32_t)(w >> 32) != ~0u;
+            s += has ? w : 0;
+            return !has && !(l <= at_border);
         };
         int i = i0;
         if ((p.cache || p.vec) && i0 % kPer == 0) {            // (the slices' and the warps' parts start so)
@@ -648,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             const uint4 *q = reinterpret_cast<const uint4 *>(data + i0);
             for (int j0 = lane; j0 < nq; j0 += 4 * 32) {
                 uint4 v[4];
+                uint32_t more = 0;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     if (j0 + 32 * u < nq) v[u] = q[j0 + 32 * u];
@@ -655,13 +723,31 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 for (int u = 0; u < 4; ++u) {
                     if (j0 + 32 * u >= nq) break;
                     const E *e = reinterpret_cast<const E *>(&v[u]);
+                    float most;                                // nothing kept: most vectors, where few tokens are
+                    if constexpr (kSingle) {
+                        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v[u]);
+                        const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+                        most = fmaxf(f.x, f.y);
+                    } else
+                        most = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+                    if (most < at_border) continue;
 #pragma unroll
-                    for (int k = 0; k < kPer; ++k) take(as_f32(e[k]));
+                    for (int k = 0; k < kPer; ++k) more |= (take(as_f32(e[k])) ? 1u : 0u) << (u * kPer + k);
+                }
+                while (more) {
+                    const int k = __ffs(more) - 1;
+                    more &= more - 1;
+                    const float l = as_f32(data[i0 + (j0 + 32 * (k / kPer)) * kPer + k % kPer]);
+                    s += exact(l, order_key(l));
                 }
             }
             i += nq * kPer;
         }
-        for (i += lane; i < i1; i += 32) take(as_f32(data[i]));
+#pragma unroll 1
+        for (i += lane; i < i1; i += 32) {
+            const float l = as_f32(data[i]);
+            if (take(l)) s += exact(l, order_key(l));
+        }
         sum = warp_sum(s);
         ties = warp_sum(t);
     };
@@ -762,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         const bool tie = i < q1 && key == border.key;
         const uint32_t tm = __ballot_sync(0xffffffffu, tie), tb = __popc(tm & ((1u << lane) - 1));
         uint64_t w = 0;
-        if (i < q1 && key > border.key) w = weigh(l, key);
+        if (i < q1 && key > border.key) w = weigh(l);
         if (tie && tb < lf && ties_kept) w = wx;
         uint64_t ik = w;
 #pragma unroll
