@@ -117,8 +117,24 @@ __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity
     return false;
 }
 
+// By a whole warp, all of it in step: a loop that lanes may leave one by one costs 100 cycles a wait, and a
+// block's chain has a dozen of them.
 __device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
-    return __all_sync(0xffffffffu, wait_for(bar, b, parity, err, code));
+    uint64_t t0 = 0;
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+        const uint64_t now = global_ns();
+        if (!t0) t0 = now;
+        const bool late = __any_sync(0xffffffffu, now - t0 > kWait) != 0;
+        if (late && (threadIdx.x & 31) == 0) {
+            bar.abort_flag = 1;
+            if (err) atomicCAS(err, 0, code);
+        }
+        if (late || __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&bar.abort_flag) != 0)) return false;
+    }
 }
 
 __device__ __forceinline__ bool soft_or(bool flag) {       // over the softmax warps
