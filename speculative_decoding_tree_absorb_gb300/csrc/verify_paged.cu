@@ -14,14 +14,15 @@
 //    or more, and each is given back as soon as its part of O^T is done. Boxes behind the last row, and pages
 //    that are none, lie outside the tensor map: zeros, no traffic.
 //  * One warp issues the scores' MMAs and another the output's, so that neither a late page holds up O^T, which
-//    frees the ring, nor softmax the scores. The whole warp walks the loop and one lane issues: descriptors
-//    computed by a lone thread, which polled for both kinds of work, took 75 - 100 cycles an MMA where the
-//    MMAs take 31 (scores) and 47 (output): 4.3 k cycles a block, now 3.1 k.
-//  * What bounds a block (64 rows, 64 keys) is shared memory: the operands of 36 + 16 MMAs pass it at 128 bytes
-//    a cycle, 1.9 k cycles, and the block's 72 KB have to be written besides. 3.1 k cycles a block in a CTA alone,
-//    3.3 - 3.6 k with all 152 at work; DRAM would give each its own block every 3.1 k. Copies ahead into L2
-//    (by TMA or by a warp's prefetches, two to six blocks) made every case 2 - 30 % slower.
-//    Boxes of 16 rows (pages of 16) pass the copy engine at 5 cycles a row: 4.1 k cycles a block.
+//    frees the ring, nor softmax the scores. The whole warp walks the loop and waits in step, and one lane
+//    issues: descriptors computed by a lone thread, which polled for both kinds of work, took 75 - 100 cycles an
+//    MMA where the MMAs take 31 (scores) and 47 (output): 4.3 k cycles a block, now 2.7 k.
+//  * What bounds a block (64 rows, 64 keys) in a CTA alone: the operands of 36 + 16 MMAs pass shared memory at
+//    128 bytes a cycle, 1.9 k cycles, and the ring of two blocks makes every second block wait for the chain
+//    load - scores - softmax - output, 5.3 k: 2.7 k a block. With all 152 at work and nothing in L2 3.0 - 3.4 k;
+//    DRAM would give each its own block every 3.1 k. Copies ahead into L2 (by TMA, by a warp of their own or by
+//    the loading warp, two to six blocks) made every case 1 - 30 % slower, and two buffers for P^T with one for
+//    the rope keys 2 %. Boxes of 16 rows (pages of 16) pass the copy engine at 5 cycles a row: 3.9 k a block.
 //  * In S^T a thread owns two keys and a few rows, so a row's maximum lies across threads. The running
 //    maximum is lazy: a block only votes whether some score exceeds its row's reference by more than 2^20;
 //    exact maxima and the rescale of O^T are taken when one does, and for the first block of an item. p <=
@@ -31,11 +32,12 @@
 //    is read once and the others hit L2. The (group, key block) pairs of the batch are cut into equal
 //    contiguous shares; groups cut by a share's end leave normalised pieces that a second kernel joins by
 //    log-sum-exp.
-//  * Measured, both kernels (bf16 out, pages not in L2): 64 single tokens of 64 heads over 1024 - 8192 keys 88 us,
-//    351 MB of cache at 4.0 TB/s, of which 8 us pass before the first scores (lengths, then the page table, then
+//  * Measured, both kernels (bf16 out, pages not in L2): 64 single tokens of 64 heads over 1024 - 8192 keys 85 us,
+//    351 MB of cache at 4.1 TB/s, of which 8 us pass before the first scores (lengths, then the page table, then
 //    the first pages, none of them in L2) and 10 us join 38 MB of pieces; two of 128 heads over 60001 and 99990
-//    keys 80 us; eight trees of 13 nodes of 32 heads over 2500 - 12000 keys in pages of 16 119 us; one token of
-//    16 heads over 700 20 us.
+//    keys 75 us; eight trees of 13 nodes of 32 heads over 2500 - 12000 keys in pages of 16 107 us; one token of
+//    16 heads over 700 18 us. Many rows a sequence: eight trees of 64 nodes of 64 heads over 8192 keys 667 us,
+//    0.88 PFLOP/s; the contiguous cache's kernel, whose clusters share a block's keys among 256 rows, takes 420.
 //  * Masks, rows of other sequences' leftovers behind the last key, and latents that are not finite concern
 //    the blocks with tree keys only: there the softmax warps zero what may not enter a product (0 * NaN), and
 //    mark its key, whose score is NaN for the rows that see it.
