@@ -166,20 +166,21 @@ __global__ void __launch_bounds__(kAssignThreads) page_assign_kernel(const Assig
         for (uint32_t u = (rank * (kAssignThreads / 32) + warp) * abreast + lane / lanes; u < units; u += stride) {
             const uint32_t b = u / chunks, t0 = (u - b * chunks) * lanes * kRowsALane + (lane & (lanes - 1));
             int need, have;
-            const int64_t start = p.start[b], len = served((int)b, need, have) ? p.new_len[b] : 0;
-            const int32_t *pages = p.table + b * p.table_stride;
-            int32_t *slots = p.slots + (int64_t)b * p.T;
+            // modulo 2^32: a row before the first lies beyond every length
+            const uint32_t row0 = (uint32_t)p.start[b] + t0, len = served((int)b, need, have) ? (uint32_t)p.new_len[b] : 0u;
+            const uint32_t mask = (1u << p.shift) - 1u;
+            const int32_t *pages = p.table + (int64_t)b * p.table_stride;
+            int32_t *slots = p.slots + (int64_t)b * p.T + t0;
             int32_t page[kRowsALane];
 #pragma unroll
             for (int i = 0; i < kRowsALane; ++i) {
-                const int64_t row = start + t0 + i * lanes;
-                page[i] = t0 + i * lanes < T && row >= 0 && row < len ? __ldcg(pages + (row >> p.shift)) : -1;
+                const uint32_t row = row0 + i * lanes;
+                page[i] = t0 + i * lanes < T && row < len ? __ldcg(pages + (row >> p.shift)) : -1;
             }
 #pragma unroll
             for (int i = 0; i < kRowsALane; ++i) {
-                const int row = (int)(start + t0 + i * lanes);
-                const bool lies = page[i] >= 0 && page[i] < p.n_pages;
-                if (t0 + i * lanes < T) slots[t0 + i * lanes] = lies ? (page[i] << p.shift) + (row & ((1 << p.shift) - 1)) : -1;
+                const int32_t slot = (int32_t)(((uint32_t)page[i] << p.shift) + ((row0 + i * lanes) & mask));
+                if (t0 + i * lanes < T) slots[i * lanes] = (uint32_t)page[i] < (uint32_t)p.n_pages ? slot : -1;
             }
         }
     }

@@ -90,6 +90,16 @@ def test_pages_and_slots(kdt, B, page, T):
             _same(_assign(kdt, state, back, page), want)
 
 
+def test_starts_anywhere(kdt):
+    """Rows before the first and behind the last have no slot, however far off."""
+    start = np.array([-5, 2 ** 31 - 1, -(2 ** 31), 3, 39, -40], dtype=np.int64)
+    state = _state(np.random.RandomState(8), 6, 6, 8, 40, 40)
+    new = np.array([40, 40, 40, 40, 40, 0])
+    for T in (1, 7, 33, 700):
+        want = op.page_assign(*state[:4], new, 8, start, T)
+        _same(_assign(kdt, state, new, 8, start.astype(np.int32), T), want)
+
+
 def test_refused_requests(kdt):
     rng = np.random.RandomState(5)
     state = _state(rng, 50, 6, 8, 120, 40)
