@@ -121,6 +121,22 @@ def test_masked_tokens(kdt):
         assert tok[0] == 0 and tok[1] >= 2990 and tok[2] < 7 and tok[3] == 2999 and tok[4] % 2 == 1
 
 
+@pytest.mark.parametrize("V", [700, 9000])
+@pytest.mark.parametrize("spread,temp", [(1000.0, 900.0), (2.0 ** -11, 1e-3), (2.0 ** -9, 2e-3), (60000.0, 1000.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_spreads_that_one_bin_holds(kdt, V, spread, temp, dtype):
+    """Logits far below the largest, or all within a hair of zero, that have weights all the same."""
+    import torch
+    rng = np.random.RandomState(V)
+    l = torch.from_numpy(rng.uniform(-spread, spread, (9, V))).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    l[4, ::3] = float("-inf")
+    u = rng.rand(9).astype(np.float32)
+    _check(kdt, l, u, temperature=temp)
+    _check(kdt, l, u, temperature=temp, top_p=rng.uniform(0.05, 0.99, 9))
+    _check(kdt, l, u, temperature=temp, top_k=rng.randint(1, V, 9), min_p=0.02)
+    _check(kdt, l, u, temperature=temp, top_k=V - 5, top_p=0.9, min_p=rng.uniform(0, 0.3, 9))
+
+
 def test_greedy_rows(kdt):
     rng = np.random.RandomState(5)
     logits = _logits(rng, 8, 7000, "ties", "bf16")
