@@ -133,7 +133,8 @@ __global__ void tree_accept_kernel(const int32_t *__restrict__ parent, const int
 // holds: only the vectors stay in registers (64 registers, four CTAs), places are found again, and
 // a batch that fills the device has one CTA a sequence. 96 sequences moving 119 rows of 656 bytes
 // take 15 us (33 with one CTA each and shared memory); 1024 of 256 nodes moving 5 rows of 1152
-// bytes 5.7 us (5.4 so, and 42 with eight CTAs each of 110 registers).
+// bytes 5.7 us (5.4 so, and 42 with eight CTAs each of 110 registers). In a paged cache a row's place takes
+// one more load: 8 sequences moving 5 rows 4.2 us, replayed, a launch; 96 moving 119 rows of 1152 bytes 16.5.
 constexpr int kCompactThreads = 256, kCompactHold = 8, kCompactCluster = 8, kCompactCtas = 4;
 constexpr int kCompactChunk = kCompactThreads * kCompactHold;      // vectors
 constexpr int kCompactMostBytes = 40 * 1024;                        // of a row's two arrays
