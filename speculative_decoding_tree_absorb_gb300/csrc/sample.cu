@@ -103,6 +103,8 @@ struct Shared {
     float2 tab[129 * kCopies];
     uint64_t part[kWarps];
     uint32_t part2[kWarps];
+    uint64_t total;
+    uint32_t total2;
     float wm[kWarps];
     // written by other CTAs of the cluster
     float m[kMaxCluster];
@@ -162,12 +164,32 @@ __device__ __forceinline__ void block_scan(Shared &sh, uint64_t a, uint32_t c, u
         sh.part2[warp] = ic;
     }
     __syncthreads();
-    const uint64_t pa = sh.part[lane];
-    const uint32_t pc = sh.part2[lane];
-    ea = warp_sum(lane < warp ? pa : 0) + ia - a;
-    ec = warp_sum(lane < warp ? pc : 0u) + ic - c;
-    ta = warp_sum(pa);
-    tc = warp_sum(pc);
+    if (warp == 0) {                                           // (the warps' sums by one warp: by each of 32 it costs more)
+        const uint64_t pa = sh.part[lane];
+        const uint32_t pc = sh.part2[lane];
+        uint64_t sa = pa;
+        uint32_t sc = pc;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t x = __shfl_up_sync(0xffffffffu, sa, off);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sc, off);
+            if (lane >= off) {
+                sa += x;
+                sc += y;
+            }
+        }
+        sh.part[lane] = sa - pa;
+        sh.part2[lane] = sc - pc;
+        if (lane == 31) {
+            sh.total = sa;
+            sh.total2 = sc;
+        }
+    }
+    __syncthreads();
+    ea = sh.part[warp] + ia - a;
+    ec = sh.part2[warp] + ic - c;
+    ta = sh.total;
+    tc = sh.total2;
 }
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
