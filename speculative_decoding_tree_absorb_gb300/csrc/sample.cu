@@ -15,7 +15,7 @@
 //    apart again. All sums are integers: neither the cluster's size nor the order of the adds shows.
 //  * A bin with more tokens than the list holds (float32, thousands of nearly equal logits) is searched by
 //    the first CTA over the whole row.
-//  * Measured: one row of 32000 tokens in float32 under all filters 30 us, a chain of passes over 4000 tokens a
+//  * Measured: one row of 32000 tokens in float32 under all filters 29 us, a chain of passes over 4000 tokens a
 //    CTA and of a dozen barriers of the cluster. 64 rows of 160000 in bf16 with settings of their own 47 us: two
 //    CTAs a row, 80000 tokens each, of its 78 k cycles 11 for the maximum (the row comes from DRAM, 20 MB), 18
 //    for the counts (7 cycles for a warp's 32 adds, 20 instructions a token), 12 for bins and borders, 28 for the
@@ -360,31 +360,34 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
 
     // -- tokens a bin; in float32 also the sum of all weights in units of 2^-40, good enough for a log-probability
     uint64_t z = 0;
-    if (!kSingle && p.logp && !greedy) {
-        float zf = 0.f;
-        int k = 0;
+    float zf = 0.f;
+    int zn = 0;
+    const bool sums = !kSingle && p.logp && !greedy, binned = !greedy && (kSingle || by_count || by_mass);
+    auto add_z = [&](float l) {
+        const float d = l - m, y = d * c_hi, e = ex2(y);
+        zf += y < -60.f ? 0.f : fmaf(e, 0.6931471805599453f * fmaf(d, c_lo, fmaf(d, c_hi, -y)), e);
+        if (++zn == 16) {
+            z += (uint64_t)(zf * 1099511627776.f);
+            zf = 0.f;
+            zn = 0;
+        }
+    };
+    if (sums && !binned)
         each([&](float l, int) {
-            const float d = l - m, y = d * c_hi, e = ex2(y);
-            zf += y < -60.f ? 0.f : fmaf(e, 0.6931471805599453f * fmaf(d, c_lo, fmaf(d, c_hi, -y)), e);
-            if (++k == 16) {
-                z += (uint64_t)(zf * 1099511627776.f);
-                zf = 0.f;
-                k = 0;
-            }
+            add_z(l);
             return false;
         }, none);
-        z += (uint64_t)(zf * 1099511627776.f);
-    }
     Border border = {0u, (uint32_t)p.V};                       // everything
     if (greedy) border = {order_key(m), 1u};
     const bool table_w = kSingle && !greedy;                   // bins have weights
-    if (!greedy && (kSingle || by_count || by_mass)) {
+    if (binned) {
         // (the last bin has what lies far below, a mask's -inf too: counted apart, as a word that all add to is slow)
         const bool weighs = kSingle || (by_mass && !by_count);
         uint32_t n_last = 0;
         uint64_t w_last = 0, w_zero = 0;
         if (!weighs || kSingle)
             each([&](float l, int) {
+                if (sums) add_z(l);
                 const int b = bins.of(bits_key(l));
                 if (b == kBins - 1) {
                     ++n_last;
@@ -399,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             });
         else
             each_weighed([&](float l) {
+                if (sums) add_z(l);
                 const int b = bins.of(bits_key(l));
                 if (b == kBins - 1) {
                     ++n_last;
@@ -782,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         sh.part[warp] = sum;
         sh.part2[warp] = ties;
     }
-    if (!kSingle) z = warp_sum(z);
+    if (!kSingle) z = warp_sum(z + (uint64_t)(zf * 1099511627776.f));
     __shared__ uint64_t zs[kWarps];
     if (lane == 0) zs[warp] = z;
     __syncthreads();
