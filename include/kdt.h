@@ -558,7 +558,8 @@ kdt_status kdt_verify_attn_q8_plan(const kdt_verify_q8_args *a, kdt_plan *plan);
  *         row slot % page_size of page slot / page_size.
  *   table int32 [B, W], row stride table_row_stride (0 = W): row j of sequence b lies in page
  *         table[b, j / page_size]. Entries behind the pages a call needs are never read as
- *         pages, whatever they hold.
+ *         pages, whatever they hold. The attention only reads: there sequences may share pages
+ *         (kdt_page_assign knows one holder of a page).
  * ------------------------------------------------------------------------------ */
 
 /* Arguments of kdt_page_assign. All arrays on the device. */

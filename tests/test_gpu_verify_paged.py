@@ -250,6 +250,18 @@ def test_nothing_but_minus_inf(kdt, splits):
     assert np.isnan(out).all() and np.isnan(lse).all()
 
 
+@pytest.mark.parametrize("T,H", [(1, 64), (9, 16)])
+def test_sequences_that_share_pages(kdt, T, H):
+    """A common prefix in the same pages, and a page that one sequence names twice."""
+    d = _inputs(61, T, H, [200, 150, 200, 129], page=16)
+    for b in range(1, 4):
+        d["table"][b, :8] = d["table"][0, :8]
+        d["rows"][b][:128] = d["rows"][0][:128]
+    d["table"][2, 5] = d["table"][2, 2]
+    d["rows"][2][80:96] = d["rows"][2][32:48]
+    _check(d, _call(kdt, d), 2.0 ** -24)
+
+
 def test_pages_that_are_none(kdt):
     """An entry outside the cache among those a sequence needs: named, its rows read as zeros, the others untouched."""
     import torch
