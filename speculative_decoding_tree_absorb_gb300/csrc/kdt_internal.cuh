@@ -178,7 +178,8 @@ struct PagedParams {
     const int32_t *table;
     int64_t table_stride;
     const int32_t *prefix_len, *n_rows;
-    const uint32_t *vis;       // [B,T,W], NULL with T = 1: the one row sees everything
+    const uint32_t *vis;       // [B,T,W], or, for T <= 32, parent; neither with T = 1: the one row sees everything
+    const int32_t *parent;     // [B,T]
     float scale_log2;          // scale * log2(e)
     void *out;                 // bf16 or float32
     bool out_bf16;

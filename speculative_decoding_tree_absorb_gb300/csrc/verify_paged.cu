@@ -102,6 +102,7 @@ template <int kRows> struct Shared {
     alignas(16) float alpha[kRows];     // of a rise; at an item's end 1 / l
     float red[4][kRows];                // by keys' quarter
     uint32_t bad[2];                    // keys whose latent is not finite
+    uint32_t up[32];                    // a short tree's nodes and their ancestors
 };
 
 __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
@@ -317,6 +318,28 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 constexpr uint32_t kLeadK = 1u << 16, kLeadMn = (uint32_t)(kTileBytes >> 4) << 16;
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (sdesc_sw128(0, 0, 1024) >> 32 << 32) | lo; }
 
+// By a warp: the words of a short tree's nodes, as the visibility kernel makes them. (A call: inlined, its code
+// costs the loop around it 1 %.)
+__device__ __noinline__ void walk_tree(const int32_t *parent, int32_t *err, int b, int T, int lane, uint32_t *up) {
+    const int32_t par = lane < T ? __ldg(parent + (int64_t)b * T + lane) : -1;
+    uint32_t acc = 1u << lane;
+    int at = lane;
+    bool walks = lane < T;
+    while (__any_sync(0xffffffffu, walks)) {
+        const int32_t next = __shfl_sync(0xffffffffu, par, at);
+        if (walks && (next < -1 || next >= at)) {            // malformed: the walk stops here
+            record_error(err, (int32_t)((int64_t)b * T + at + 1));
+            walks = false;
+        }
+        walks = walks && next >= 0;
+        if (walks) {
+            at = next;
+            acc |= 1u << at;
+        }
+    }
+    up[lane] = acc;
+}
+
 __device__ __forceinline__ uint32_t lane_addr(uint32_t base, int warp, uint32_t col) {
     return base + ((uint32_t)(32 * (warp & 3)) << 16) + col;
 }
@@ -392,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2 * kCols; ++k) l[k] = 0.f;
             if (srow < kRows) sh.m[srow] = -INFINITY;        // (read by others behind the first block's barriers)
+            if (p.parent && (it.kb + it.nb) * kKeysB > it.P) {   // the item has tree keys
+                if (warp == kSoft0) walk_tree(p.parent, p.err, it.b, p.T, lane, sh.up);
+                soft_or(false);
+            }
             bool fail = false;
             for (int j = 0; j < it.nb; ++j, ++g) {
                 const int key0 = (it.kb + j) * kKeysB;
@@ -412,8 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             const int t = ta + 8 * h;
                             bool v = t < 0;
-                            if (t >= 0 && t < it.n && node < it.n)
-                                v = !p.vis || ((__ldcg(p.vis + ((int64_t)it.b * p.T + node) * p.W + (t >> 5)) >> (t & 31)) & 1u);
+                            if (t >= 0 && t < it.n && node < it.n) {
+                                if (p.parent) v = (sh.up[node] >> t) & 1u;
+                                else v = !p.vis || ((__ldcg(p.vis + ((int64_t)it.b * p.T + node) * p.W + (t >> 5)) >> (t & 31)) & 1u);
+                            }
                             see |= (v ? 1u : 0u) << (2 * k + h);
                         }
                     }
@@ -431,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     const int first = min(it.kv - key0, kKeysB);
                     for (int x = srow; x < (kKeysB - first) * 64; x += kSoftThreads) st_shared_v4(at(first + (x >> 6), x & 63), 0u, 0u, 0u, 0u);
-                    if (p.vis) {
+                    if (p.vis || p.parent) {
                         if (srow < 2) sh.bad[srow] = 0u;
                         soft_or(false);
                         const int from = max(it.P - key0, 0);

@@ -93,7 +93,7 @@ kdt_status make_plan(const kdt_verify_paged_args *a, PagedPlan *out) {
     p.pieces = p.shares > 1 && nblk > 1;                      // a group of one block is never cut
     p.deep = p.shares >= kDeep * groups ? (int)groups : 0;
     size_t off = 0;
-    p.vis = a->parent != nullptr;
+    p.vis = a->parent && a->T > 32;                           // the kernel walks a short tree itself
     if (p.vis) off = align_up(off + (size_t)a->B * a->T * ((a->T + 31) / 32) * sizeof(uint32_t));
     if (p.pieces) {
         const size_t rows = (size_t)2 * p.ctas * p.tile;
@@ -173,6 +173,7 @@ kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace
     q.prefix_len = a->prefix_len;
     q.n_rows = a->n_rows;
     q.vis = vis;
+    q.parent = p.vis ? nullptr : a->parent;
     q.scale_log2 = a->scale * 1.4426950408889634f;
     q.out = a->out;
     q.out_bf16 = a->out_dtype == KDT_BF16;
