@@ -676,7 +676,7 @@ typedef struct {
  * output's sums are float32, the weights are rounded to bf16 for the second product, and the output
  * once to out_dtype. The work is split over the keys and joined by log-sum-exp. Meant for few rows a
  * sequence (T*H up to some 500): from there on kdt_verify_attn over a contiguous cache is faster, up
- * to 1.6 times at 4096 rows.
+ * to 1.5 times at 4096 rows.
  * A row that sees no key gets out = 0 and lse = -inf. A row that sees a key whose score is NaN or
  * +inf gets NaN (a score of -inf has weight 0), and infinite or NaN latents reach the rows that see
  * them; a row from which such a key is hidden is not affected by it. Cache rows at or beyond

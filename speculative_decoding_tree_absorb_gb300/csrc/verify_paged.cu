@@ -16,10 +16,10 @@
 //  * One warp issues the scores' MMAs and another the output's, so that neither a late page holds up O^T, which
 //    frees the ring, nor softmax the scores. The whole warp walks the loop and waits in step, and one lane
 //    issues: descriptors computed by a lone thread, which polled for both kinds of work, took 75 - 100 cycles an
-//    MMA where the MMAs take 31 (scores) and 47 (output): 4.3 k cycles a block, now 2.7 k.
+//    MMA where the MMAs take 31 (scores) and 47 (output): 4.3 k cycles a block, now 2.6 k.
 //  * What bounds a block (64 rows, 64 keys) in a CTA alone: the operands of 36 + 16 MMAs pass shared memory at
 //    128 bytes a cycle, 1.9 k cycles, and the ring of two blocks makes every second block wait for the chain
-//    load - scores - softmax - output, 5.3 k: 2.7 k a block. With all 152 at work and nothing in L2 3.0 - 3.4 k;
+//    load - scores - softmax - output, 5.2 k: 2.6 k a block. With all 152 at work and nothing in L2 2.8 - 3.3 k;
 //    DRAM would give each its own block every 3.1 k. Copies ahead into L2 (by TMA, by a warp of their own or by
 //    the loading warp, two to six blocks) made every case 1 - 30 % slower, and two buffers for P^T with one for
 //    the rope keys 2 %. Boxes of 16 rows (pages of 16) pass the copy engine at 5 cycles a row: 3.9 k a block.
@@ -32,12 +32,12 @@
 //    is read once and the others hit L2. The (group, key block) pairs of the batch are cut into equal
 //    contiguous shares; groups cut by a share's end leave normalised pieces that a second kernel joins by
 //    log-sum-exp.
-//  * Measured, both kernels (bf16 out, pages not in L2): 64 single tokens of 64 heads over 1024 - 8192 keys 85 us,
-//    351 MB of cache at 4.1 TB/s, of which 8 us pass before the first scores (lengths, then the page table, then
+//  * Measured, both kernels (bf16 out, pages not in L2): 64 single tokens of 64 heads over 1024 - 8192 keys 84 us,
+//    351 MB of cache at 4.2 TB/s, of which 8 us pass before the first scores (lengths, then the page table, then
 //    the first pages, none of them in L2) and 10 us join 38 MB of pieces; two of 128 heads over 60001 and 99990
-//    keys 75 us; eight trees of 13 nodes of 32 heads over 2500 - 12000 keys in pages of 16 107 us; one token of
-//    16 heads over 700 18 us. Many rows a sequence: eight trees of 64 nodes of 64 heads over 8192 keys 667 us,
-//    0.88 PFLOP/s; the contiguous cache's kernel, whose clusters share a block's keys among 256 rows, takes 420.
+//    keys 72 us; eight trees of 13 nodes of 32 heads over 2500 - 12000 keys in pages of 16 99 us; one token of
+//    16 heads over 700 14 us. Many rows a sequence: eight trees of 64 nodes of 64 heads over 8192 keys 621 us,
+//    0.94 PFLOP/s; the contiguous cache's kernel, whose clusters share a block's keys among 256 rows, takes 420.
 //  * Masks, rows of other sequences' leftovers behind the last key, and latents that are not finite concern
 //    the blocks with tree keys only: there the softmax warps zero what may not enter a product (0 * NaN), and
 //    mark its key, whose score is NaN for the rows that see it.
@@ -121,11 +121,11 @@ __device__ __forceinline__ bool wait_for(Bars &bar, uint64_t *b, uint32_t parity
 }
 
 // By a whole warp, all of it in step: a loop that lanes may leave one by one costs 100 cycles a wait, and a
-// block's chain has a dozen of them.
-__device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+// block's chain has a dozen of them. What comes after the first try is a call: inlined in every place, it took the
+// roles' loops out of the instruction caches (eight trees of 64 nodes of 64 heads over 8192 keys 660 us, 621 so).
+__device__ __noinline__ bool wait_on(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
     uint64_t t0 = 0;
     for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
@@ -138,6 +138,11 @@ __device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parit
         }
         if (late || __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&bar.abort_flag) != 0)) return false;
     }
+}
+
+__device__ __forceinline__ bool warp_wait(Bars &bar, uint64_t *b, uint32_t parity, int32_t *err, int code) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    return wait_on(bar, b, parity, err, code);
 }
 
 __device__ __forceinline__ bool soft_or(bool flag) {       // over the softmax warps
