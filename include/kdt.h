@@ -654,7 +654,8 @@ typedef struct {
     const int32_t *n_rows;  /* device [B]: sequence b has tree nodes i < n_rows[b] only (a padded batch; 0: it is
                                not there), or NULL: T. Rows of out and lse behind them are left as they were. */
     int max_kv_len;         /* host bound: >= max_b prefix_len[b] + T, <= table_width * page_size */
-    const int32_t *parent;  /* device [B,T] parent array, or NULL */
+    const int32_t *parent;  /* device [B,T] parent array, or NULL. Entries of a padded batch's missing nodes may be
+                               read, and reported when malformed: -1 is safe there */
     const uint32_t *vis;    /* device [B,T,ceil(T/32)] packed visibility bits, or NULL. With T = 1 both may be
                                NULL: the row sees its prefix and itself */
     float scale;
