@@ -29,6 +29,8 @@ using namespace rows;
 constexpr int kAssignThreads = 1024;
 constexpr int kAssignCluster = 8;
 constexpr int kMaxAssign = 16384;                   // requests: their scans lie in shared memory
+// Dynamic shared memory that a launch is given unasked: 48 KB less the kernel's static variables (below 1 KB).
+constexpr size_t kFreeSmem = 47 * 1024;
 constexpr int kRowsALane = 16;                      // rows whose page a lane looks up at once
 constexpr int kPagesAThread = 4;
 constexpr int kRowsACta = 16384, kPagesACta = 4096; // slots, table entries that one CTA takes before another joins
@@ -290,7 +292,7 @@ kdt_status kdt_page_assign(const kdt_page_args *a, cudaStream_t stream) {
            ((int64_t)a->B * a->T > (int64_t)S * kRowsACta || (int64_t)a->B * a->W > (int64_t)S * kPagesACta))
         S <<= 1;
     const size_t smem = (size_t)a->B * 2 * sizeof(int);
-    if (smem > 48 * 1024 &&
+    if (smem > kFreeSmem &&
         cudaFuncSetAttribute(page_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxAssign * 2 * sizeof(int))) !=
             cudaSuccess)
         return KDT_ERR_CUDA;

@@ -262,3 +262,24 @@ def test_another_device_memory_is_refused(kdt):
     with pytest.raises(kdt.KdtError) as e:
         kdt.page_assign(*(torch.zeros(s, dtype=torch.int32).pin_memory() for s in ((2, 3), 2, 6, 1, 2)), 8)
     assert e.value.status == 6
+
+
+def test_batches_around_the_shared_memory_given_unasked(kdt):
+    """Sizes on both sides of the leave that larger scans need, in a process that no larger batch has run in before."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import numpy as np
+import speculative_decoding_tree_absorb_gb300 as kdt
+from oracle import paged as op
+from tests.test_gpu_pages import _assign, _same, _state
+for B in (6015, 6016, 6017, 6110, 6111, 6144, 6145):
+    rng = np.random.RandomState(B)
+    state = _state(rng, B, 4, 8, 2 * B, 20)
+    new, start = rng.randint(0, 33, B), np.zeros(B, dtype=np.int32)
+    _same(_assign(kdt, state, new, 8, start, 3), op.page_assign(*state[:4], new, 8, start, 3))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
