@@ -358,19 +358,21 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         for (int i = tid; i < n; i += kThreads) f(as_f32(data[i]));
     };
 
-    // -- tokens a bin; in float32 also the sum of all weights in units of 2^-40, good enough for a log-probability
+    // -- tokens a bin; in float32 also the sum of all weights in units of 2^-42, good enough for a log-probability. A
+    // token's weight is rounded to them by itself, so that this sum has no order either: a multiple of 2^-20 and
+    // the rest, both the low bits of a sum with 1.5 * 2^23 of their units (|rest| <= 2^21 of them, and a thread has
+    // 512 tokens and a tail's at most).
     uint64_t z = 0;
-    float zf = 0.f;
-    int zn = 0;
+    int32_t z_hi = 0, z_lo = 0;
+    static_assert((kMaxVocab / kThreads + 8) * ((int64_t)1 << 21) < INT32_MAX, "a thread's sums");
     const bool sums = !kSingle && p.logp && !greedy, binned = !greedy && (kSingle || by_count || by_mass);
     auto add_z = [&](float l) {
-        const float d = l - m, y = d * c_hi, e = ex2(y);
-        zf += y < -60.f ? 0.f : fmaf(e, 0.6931471805599453f * fmaf(d, c_lo, fmaf(d, c_hi, -y)), e);
-        if (++zn == 16) {
-            z += (uint64_t)(zf * 1099511627776.f);
-            zf = 0.f;
-            zn = 0;
-        }
+        constexpr float kHi = 12.f, kLo = 2.86102294921875e-06f;             // 1.5 * 2^23 of 2^-20, of 2^-42
+        const float d = __fsub_rn(l, m), y = __fmul_rn(d, c_hi), e2 = ex2(y);
+        const float e = y < -60.f ? 0.f : __fmaf_rn(e2, __fmul_rn(0.6931471805599453f, __fmaf_rn(d, c_lo, __fmaf_rn(d, c_hi, -y))), e2);
+        const float h = __fadd_rn(e, kHi), rest = __fsub_rn(e, __fsub_rn(h, kHi));           // exact
+        z_hi += __float_as_int(h) - 0x41400000;
+        z_lo += __float_as_int(__fadd_rn(rest, kLo)) - 0x36400000;
     };
     if (sums && !binned)
         each([&](float l, int) {
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 if (dy.count[b] && bins.single(b)) dy.w[b] = w_of(bins.value(b));
         push(true, 0, kBins);
         total_up();
-        if (kSingle && rank == 0 && tid == 0) z = mt >> 4;     // (bf16: every token's weight)
+        if (kSingle && rank == 0 && tid == 0) z = mt >> 2;     // (bf16: every token's weight)
         // ties of weight wx to keep so that `up` and they reach the goal: one at least, `cap` at most
         auto ties_for = [&](uint64_t goal, uint64_t up, uint64_t wx, uint64_t cap) -> uint64_t {
             if (wx == 0 || goal <= up) return 1;
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         sh.part[warp] = sum;
         sh.part2[warp] = ties;
     }
-    if (!kSingle) z = warp_sum(z + (uint64_t)(zf * 1099511627776.f));
+    if (!kSingle) z = warp_sum((uint64_t)((int64_t)z_hi * (1 << 22) + z_lo));
     __shared__ uint64_t zs[kWarps];
     if (lane == 0) zs[warp] = z;
     __syncthreads();
@@ -887,10 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             if (lane == __ffs(hit) - 1) {
                 p.token[r] = v0 + i;
                 if (p.logp) {
-                    uint64_t zz = 0;                           // in units of 2^-40
+                    uint64_t zz = 0;                           // in units of 2^-42
                     for (uint32_t o = 0; o < size; ++o) zz += sh.z[o];
                     const double temp = p.temperature ? (double)p.temperature[r] : p.temperature_all;
-                    p.logp[r] = greedy ? 0.f : (float)(((double)l - (double)m) / temp - log((double)zz * 9.094947017729282e-13));
+                    p.logp[r] = greedy ? 0.f : (float)(((double)l - (double)m) / temp - log((double)zz * 2.2737367544323206e-13));
                 }
             }
             return;

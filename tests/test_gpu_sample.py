@@ -213,3 +213,25 @@ def test_not_device_memory_is_refused(kdt):
     with pytest.raises(kdt.KdtError) as e:
         kdt.sample(torch.zeros(2, 8, device="cuda"), torch.zeros(2).pin_memory())
     assert e.value.status == 6
+
+
+@pytest.mark.parametrize("V,most", [(1000, 200), (32000, 200), (160003, 80)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logp_has_no_order(kdt, V, most, dtype):
+    """A row's log-probability, before the filters by its definition, has the same bits alone and in batches of any size
+    (other clusters, other slices), under every filter, and from rows that start on no 16-byte boundary."""
+    import torch
+    rng = np.random.RandomState(V)
+    logits = _logits(rng, most, V, "normal", dtype)
+    logits[:, 0] = logits.amax(1) + 0.5          # u = 0 draws this token under every filter
+    off = torch.zeros((most, V + 3), dtype=logits.dtype, device="cuda")[:, 1:V + 1]
+    off.copy_(logits)
+    u = torch.zeros(most, device="cuda")
+    temp = torch.from_numpy(rng.uniform(0.5, 1.5, most).astype(np.float32)).cuda()
+    tok, want = kdt.sample(logits, u, temperature=temp)
+    assert (tok == 0).all()
+    for kw in (dict(), dict(top_p=0.9), dict(top_k=50), dict(top_k=V // 2, top_p=0.99), dict(min_p=1e-3)):
+        for n in (1, 2, 12, 30, 70, most):
+            for lg in (logits, off):
+                tok, logp = kdt.sample(lg[most - n:], u[:n], temperature=temp[most - n:], **kw)
+                assert (tok == 0).all() and torch.equal(logp, want[most - n:]), (kw, n)
