@@ -45,6 +45,18 @@ kdt_status check_on_current_device(std::initializer_list<const void *> ptrs) {
     return KDT_OK;
 }
 
+kdt_status clear_error(int32_t *err, cudaStream_t stream) {
+    if (!err) return KDT_OK;
+    int dev = -1;
+    cudaPointerAttributes at;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&at, err) != cudaSuccess) {
+        cudaGetLastError();
+        return KDT_OK;
+    }
+    if (at.type != cudaMemoryTypeDevice || at.device != dev) return KDT_OK;
+    return cudaMemsetAsync(err, 0, sizeof(int32_t), stream) == cudaSuccess ? KDT_OK : KDT_ERR_CUDA;
+}
+
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -358,7 +370,7 @@ kdt_status verify_attn_checked(const kdt_verify_args *a, void *workspace, size_t
     Plan p;
     kdt_status st = make_plan(a, &p);
     if (st != KDT_OK) return st;
-    if (a->B == 0) return KDT_OK;
+    if (a->B == 0) return clear_error(a->err, stream);
     if (p.ws_bytes > 0 && (!workspace || ws_bytes < p.ws_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return KDT_ERR_WORKSPACE;
     if (check_tensors &&
@@ -458,7 +470,7 @@ kdt_status kdt_verify_attn_host(const kdt_verify_args *a, int n_chunks, void *de
     HostLayout L;
     kdt_status st = host_layout(a, n_chunks, &L);
     if (st != KDT_OK) return st;
-    if (a->B == 0) return KDT_OK;
+    if (a->B == 0) return clear_error(a->err, stream);
     if (stream == stream_in || stream == stream_out || stream_in == stream_out) return KDT_ERR_BAD_SHAPE;
     if (!dev_buf || dev_bytes < L.total || (reinterpret_cast<uintptr_t>(dev_buf) & (kAlign - 1)))
         return KDT_ERR_WORKSPACE;
@@ -529,7 +541,7 @@ kdt_status kdt_vc_up_proj(const float *o, const void *w_vc, kdt_dtype w_dtype, i
                           float *v, int32_t *err, cudaStream_t stream) {
     if (R < 0 || H < 1 || H > 1024 || (int64_t)R * H > ((int64_t)1 << 31)) return KDT_ERR_BAD_SHAPE;
     if (D_c != kDc || (D_v != 64 && D_v != 128) || w_dtype != KDT_BF16) return KDT_ERR_UNSUPPORTED;
-    if (R == 0) return KDT_OK;
+    if (R == 0) return clear_error(err, stream);
     if (!o || !w_vc || !v) return KDT_ERR_NULL_ARG;
     if (!aligned16(o) || !aligned16(w_vc) || !aligned16(v) || (reinterpret_cast<uintptr_t>(err) & 3u))
         return KDT_ERR_BAD_SHAPE;

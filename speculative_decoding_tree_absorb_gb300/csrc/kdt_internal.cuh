@@ -208,6 +208,10 @@ int sm_count();
 // KDT_ERR_NOT_DEVICE (KDT_ERR_CUDA if the query itself fails).
 kdt_status check_on_current_device(std::initializer_list<const void *> ptrs);
 
+// The error word of a call over no rows: 0, as behind any call that finds no fault. Such a call looks at none of
+// its tensors, so a word that is not memory of the current device is left alone, not refused.
+kdt_status clear_error(int32_t *err, cudaStream_t stream);
+
 // kdt_verify_attn with the device-memory checks selectable: the caller's tensors
 // (check_tensors) and the workspace (check_workspace) must be device memory of the current
 // device. Entry points whose buffers are already known to be (the host pipeline's chunks

@@ -276,7 +276,7 @@ kdt_status kdt_page_assign(const kdt_page_args *a, cudaStream_t stream) {
     if (stride < a->W || (int64_t)a->B * a->W > INT32_MAX || (int64_t)a->B * a->T > INT32_MAX ||
         (int64_t)a->n_pages << shift > INT32_MAX)
         return KDT_ERR_BAD_SHAPE;
-    if (a->B == 0) return KDT_OK;
+    if (a->B == 0) return clear_error(a->err, stream);
     if (!a->table || !a->held || !a->free_pages || !a->n_free || !a->new_len) return KDT_ERR_NULL_ARG;
     if (a->T > 0 && (!a->slots || !a->start)) return KDT_ERR_NULL_ARG;
     for (const void *q : {(const void *)a->table, (const void *)a->held, (const void *)a->free_pages, (const void *)a->n_free,

@@ -963,7 +963,7 @@ extern "C" kdt_status kdt_sample(const kdt_sample_args *a, cudaStream_t stream) 
     if (!a->temperature && !(a->temperature_all == 0.0 || (a->temperature_all >= 1e-3 && a->temperature_all <= 1e3)))
         return KDT_ERR_BAD_SHAPE;
     if ((!a->top_p && a->top_p_all != a->top_p_all) || (!a->min_p && a->min_p_all != a->min_p_all)) return KDT_ERR_BAD_SHAPE;
-    if (a->R == 0) return a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t), stream) != cudaSuccess ? KDT_ERR_CUDA : KDT_OK;
+    if (a->R == 0) return clear_error(a->err, stream);
     if (!a->logits || !a->u || !a->token) return KDT_ERR_NULL_ARG;
     if (!aligned(a->logits, esz)) return KDT_ERR_BAD_SHAPE;
     for (const void *q : {(const void *)a->u, (const void *)a->temperature, (const void *)a->top_k, (const void *)a->top_p,

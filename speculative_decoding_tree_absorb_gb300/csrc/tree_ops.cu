@@ -520,7 +520,7 @@ kdt_status kdt_rope_neox(const kdt_rope_args *a, cudaStream_t stream) {
 kdt_status kdt_tree_accept(const int32_t *parent, const int32_t *tok, const int32_t *target, int B, int T,
                            int32_t *acc_nodes, int32_t *n_acc, int32_t *bonus, int32_t *err, cudaStream_t stream) {
     if (B < 0 || T < 1 || T > kMaxT) return KDT_ERR_BAD_SHAPE;
-    if (B == 0) return err && cudaMemsetAsync(err, 0, sizeof(int32_t), stream) != cudaSuccess ? KDT_ERR_CUDA : KDT_OK;
+    if (B == 0) return clear_error(err, stream);
     if (!parent || !tok || !target || !acc_nodes || !n_acc || !bonus) return KDT_ERR_NULL_ARG;
     if (err && cudaMemsetAsync(err, 0, sizeof(int32_t), stream) != cudaSuccess) return KDT_ERR_CUDA;
     const int threads = T < 256 ? ((T + 31) / 32) * 32 : 256;

@@ -514,7 +514,7 @@ kdt_status kdt_tree_sample(const int32_t *parent, const int32_t *tok, const void
                           (const void *)acc_nodes, (const void *)n_acc, (const void *)bonus, (const void *)logp,
                           (const void *)err})
         if (!aligned(q, 4)) return KDT_ERR_BAD_SHAPE;
-    if (B == 0) return KDT_OK;
+    if (B == 0) return clear_error(err, stream);
     const kdt_status st =
         check_on_current_device({parent, tok, logits, u_node, u_bonus, acc_nodes, n_acc, bonus, logp, err});
     if (st != KDT_OK) return st;

@@ -139,7 +139,7 @@ kdt_status kdt_verify_attn_paged(const kdt_verify_paged_args *a, void *workspace
     PagedPlan p;
     kdt_status st = make_plan(a, &p);
     if (st != KDT_OK) return st;
-    if (a->B == 0) return KDT_OK;
+    if (a->B == 0) return clear_error(a->err, stream);
     if (p.ws_bytes > 0 && (!workspace || ws_bytes < p.ws_bytes || !aligned(workspace, kAlign))) return KDT_ERR_WORKSPACE;
     if ((st = check_on_current_device({a->q_nope, a->q_pe, a->c_kv, a->k_pe, a->table, a->prefix_len, a->n_rows, a->parent,
                                        a->vis, a->out, a->lse, a->err, p.ws_bytes ? workspace : nullptr})) != KDT_OK)

@@ -140,7 +140,7 @@ kdt_status kdt_verify_attn_q8(const kdt_verify_q8_args *a, void *workspace, size
     Q8Plan p;
     kdt_status st = make_plan(a, &p);
     if (st != KDT_OK) return st;
-    if (a->B == 0) return KDT_OK;
+    if (a->B == 0) return clear_error(a->err, stream);
     if (p.ws_bytes > 0 && (!workspace || ws_bytes < p.ws_bytes || !aligned(workspace, kAlign))) return KDT_ERR_WORKSPACE;
     if ((st = check_on_current_device({a->q_nope, a->q_pe, a->c_q8, a->c_scale, a->k_pe, a->prefix_len, a->parent,
                                        a->vis, a->out, a->lse, a->err, p.ws_bytes ? workspace : nullptr})) != KDT_OK)
