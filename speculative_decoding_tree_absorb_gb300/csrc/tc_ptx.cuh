@@ -456,7 +456,17 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint16_t mask) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this warp's loads from tensor memory into `r`. They write their registers when they complete: nothing
+// that uses one may move ahead of the wait, and without an operand of its own the wait holds back only
+// memory accesses. So every load is followed by this, with all its registers, before any of them is used.
+template <typename... Regs> __device__ __forceinline__ void loaded(Regs &...r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    auto tie = [](auto &v) {
+#pragma unroll
+        for (auto &k : v) asm volatile("" : "+r"(k)::"memory");
+    };
+    (tie(r), ...);
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread t of the warp gets lane (base + t).

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
             for (int cc = 0; cc < p.Dv / 32; ++cc) {
                 uint32_t rv[32];
                 tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * kAccCols + (uint32_t)(32 * cc), rv);
-                tmem_wait_ld();
+                loaded(rv);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     *reinterpret_cast<float4 *>(stg + lane * 32 + ((u ^ (lane & 7)) << 2)) =

@@ -307,15 +307,6 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int c, bool wri
     __syncwarp();
 }
 
-// Waits for this warp's loads from tensor memory. They write their registers when they complete: nothing
-// that uses one may move ahead of the wait, and without an operand of its own the wait holds back only
-// memory accesses.
-template <int kN> __device__ __forceinline__ void loaded(uint32_t (&r)[kN]) {
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(r[k])::"memory");
-}
-
 // A value that all lanes of a warp have, known to be.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 

@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
         auto scores = [&](const float *off, bool masked, uint32_t see, float (&x)[32]) {
             uint32_t raw[32];
             tmem_ld32(lane_addr(tmem + kColS, warp, 32 * half), raw);
-            tmem_wait_ld();
+            loaded(raw);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float4 o = reinterpret_cast<const float4 *>(off + 32 * half)[q];
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                             uint32_t o[32];
                             const uint32_t addr = lane_addr(tmem, warp, kRowsT * q + 32 * half);
                             tmem_ld32(addr, o);
-                            tmem_wait_ld();
+                            loaded(o);
 #pragma unroll
                             for (int r = 0; r < 32; ++r)
                                 o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.alpha[32 * half + r]);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_q8_rows_kernel(const Q8Par
                 const int r0 = 16 * (e & 1);
                 uint32_t o[16];
                 tmem_ld16(lane_addr(tmem, warp, kRowsT * (e >> 1) + 32 * half + r0), o);
-                tmem_wait_ld();
+                loaded(o);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float4 iv = *reinterpret_cast<const float4 *>(sh.inv + 32 * half + r0 + 4 * m);

@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(512, 1) verify_simt_tm_kernel(const VerifyPara
             uint32_t t0[32], t1[32];
             tc::tmem_ld32(tmem_o, t0);
             tc::tmem_ld32(tmem_o + 32, t1);
-            tc::tmem_wait_ld();
+            tc::loaded(t0, t1);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -1128,7 +1128,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                     const uint32_t sbase = tmem_s0 + buf * kKeys + 64 * half;
                     tmem_ld32(tmem_lane_addr(sbase, warp, 0), r0v);
                     tmem_ld32(tmem_lane_addr(sbase, warp, 32), r1v);
-                    tmem_wait_ld();
+                    loaded(r0v, r1v);
                     if (warp == 4 && lane == 0) KDT_TC_TRACE(kEvSoftmaxLd, g);
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {             // raw scores
@@ -1482,7 +1482,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
                     uint32_t r[32];
                     const uint32_t addr = tmem_lane_addr(tmem, warp, col0 + c * 32);
                     tmem_ld32(addr, r);
-                    tmem_wait_ld();
+                    loaded(r);
 #pragma unroll
                     for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * a);
                     tmem_st32(addr, r);
@@ -1532,7 +1532,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kQ8 ? kThreadsQ8 : k
             for (int c = 0; c < kEpiGroupCols / 32; ++c) {
                 uint32_t r[32];
                 tmem_ld32(tmem_lane_addr(tmem, warp, col0 + c * 32), r);
-                tmem_wait_ld();
+                loaded(r);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
