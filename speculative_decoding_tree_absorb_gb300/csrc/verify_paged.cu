@@ -813,6 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         do __nanosleep(1000);
         while (global_ns() - t0 < 200000ull);
     }
+    // What follows on the stream waits for this kernel alone: it must not end before the one that finds the words, not
+    // even where it read none of them (a padded batch without nodes).
+    if (p.overlap_vis && threadIdx.x == 0) griddep_wait();
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

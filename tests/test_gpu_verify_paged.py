@@ -527,3 +527,38 @@ def test_not_device_memory_is_refused(kdt):
     with pytest.raises(kdt.KdtError) as e:
         kdt.verify_attn_paged(*a, parent=par, max_kv_len=43, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[128:])
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_batch_without_nodes_ends_behind_its_visibility(kdt, captured):
+    """Where n_rows leaves every sequence without a node the attention reads no visibility word; the call still ends only
+    once the words' kernel has: what it reports of the parents (in a chain of 4096, from its last walks) is there for what
+    follows on the stream. Rows of out and lse are left as they were."""
+    import torch
+    B, T, H = 3, 4096, 1
+    d = _inputs(91, 1, H, [5] * B)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    parent = torch.arange(-1, T - 1, **i32).repeat(B, 1)
+    parent[1, T - 1] = T - 1
+    q = torch.zeros(B, T, H, 576, dtype=torch.bfloat16, device="cuda")
+    table, prefix, none = torch.zeros(B, 65, **i32), torch.zeros(B, **i32), torch.zeros(B, **i32)
+    out, lse = torch.full((B, T, H, 512), 3.0, device="cuda"), torch.full((B, T, H), 4.0, device="cuda")
+    err = torch.zeros(1, **i32)
+    ws = torch.empty(kdt.verify_attn_paged_workspace_size(B, T, H, 65 * 64, 64), dtype=torch.uint8, device="cuda")
+
+    def call():
+        kdt.verify_attn_paged(q[..., :512], q[..., 512:], d["c"], d["k"], table, prefix, n_rows=none, parent=parent, out=out,
+                              lse=lse, err=err, workspace=ws)
+        return err.clone()
+    call()
+    torch.cuda.synchronize()
+    if captured:
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            seen = [call() for _ in range(3)]
+        graph.replay()
+    else:
+        seen = [call() for _ in range(3)]
+    torch.cuda.synchronize()
+    assert [int(e.item()) for e in seen] == [2 * T] * 3
+    assert (out == 3.0).all() and (lse == 4.0).all()
