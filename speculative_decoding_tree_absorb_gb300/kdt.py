@@ -261,6 +261,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _i32(v, name) -> int:
+    """A whole number that goes to the library as a C int (ctypes would drop its upper bits)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+    return v
+
+
 def _kept(t, stream):
     """A new tensor that a call uses on ``stream`` (None: the current one): its memory belongs to the current
     stream, which must not hand it out again while another one still uses it."""
@@ -295,7 +303,7 @@ def make_args(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=None, ma
     a.q_nope, a.q_pe, a.c_kv, a.k_pe = (t.data_ptr() for t in (q_nope, q_pe, c_kv, k_pe))
     a.kv_row_stride = L
     a.prefix_len = prefix_len.data_ptr()
-    a.max_kv_len = int(L if max_kv_len is None else max_kv_len)
+    a.max_kv_len = _i32(L if max_kv_len is None else max_kv_len, "max_kv_len")
     a.parent = None if parent is None else parent.data_ptr()
     a.vis = None if vis is None else vis.data_ptr()
     a.scale = float(scale)
@@ -303,7 +311,7 @@ def make_args(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=None, ma
     a.lse = None if lse is None else lse.data_ptr()
     a.err = None if err is None else err.data_ptr()
     a.impl = IMPLS[impl] if isinstance(impl, str) else int(impl)
-    a.num_splits = int(num_splits)
+    a.num_splits = _i32(num_splits, "num_splits")
     a.q_nope_row_stride = _row_stride(q_nope)
     a.q_pe_row_stride = _row_stride(q_pe)
     return a
@@ -370,7 +378,7 @@ def verify_attn(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=None, 
 
 
 def host_buffer_size(args: VerifyArgs, n_chunks=0) -> int:
-    return int(lib().kdt_verify_attn_host_buffer_size(ctypes.byref(args), int(n_chunks)))
+    return int(lib().kdt_verify_attn_host_buffer_size(ctypes.byref(args), _i32(n_chunks, "n_chunks")))
 
 
 def verify_attn_host(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=None, max_kv_len=None,
@@ -398,7 +406,7 @@ def verify_attn_host(q_nope, q_pe, c_kv, k_pe, prefix_len, *, parent=None, vis=N
     if streams is None:
         streams = (torch.cuda.current_stream(dev), torch.cuda.Stream(dev), torch.cuda.Stream(dev))
     s, s_in, s_out = (ctypes.c_void_p(x.cuda_stream) for x in streams)
-    _check(lib().kdt_verify_attn_host(ctypes.byref(a), int(n_chunks), _ptr(dev_buf), nbytes, s, s_in, s_out),
+    _check(lib().kdt_verify_attn_host(ctypes.byref(a), _i32(n_chunks, "n_chunks"), _ptr(dev_buf), nbytes, s, s_in, s_out),
            "kdt_verify_attn_host")
     return out, lse
 
@@ -504,7 +512,7 @@ def tree_build(cand_tok, cand_lp, N, root_tok=None, stream=None):
     dev = cand_lp.device
     parent, tok, depth = (_empty((B, N + 1), torch.int32, dev, stream) for _ in range(3))
     score = _empty((B, N + 1), torch.float32, dev, stream)
-    _check(lib().kdt_tree_build(_ptr(cand_tok), _ptr(cand_lp), B, D, K, int(N), _ptr(root_tok), _ptr(parent),
+    _check(lib().kdt_tree_build(_ptr(cand_tok), _ptr(cand_lp), B, D, K, _i32(N, "N"), _ptr(root_tok), _ptr(parent),
                                 _ptr(tok), _ptr(depth), _ptr(score), _stream_ptr(stream)), "kdt_tree_build")
     return parent, tok, depth, score
 
@@ -581,7 +589,7 @@ def latent_read_q8(c_q8, c_scale, k_pe, start, R, *, n_rows=None, dtype=None, ou
     int32 [B] the rows of c and k behind it are not written."""
     import torch
     B, L = _check_q8_cache(c_q8, c_scale, k_pe)
-    R = int(R)
+    R = _i32(R, "R")
     dtype = dtype or (out_c.dtype if out_c is not None else torch.bfloat16)
     _int32_of(start, B, "start"), _int32_of(n_rows, B, "n_rows")
     if out_c is None:
@@ -610,9 +618,9 @@ def _q8_size_args(B, T, H, max_kv_len, out_dtype, bits, impl, num_splits) -> Ver
     """Arguments with the sizes filled in and placeholder pointers: enough for a plan."""
     import torch
     fake = 1 << 12
-    a = VerifyQ8Args(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, fake, int(max_kv_len), fake, int(max_kv_len),
+    a = VerifyQ8Args(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, fake, _i32(max_kv_len, "max_kv_len"), fake, int(max_kv_len),
                      None if bits else fake, fake if bits else None, 1.0, fake,
-                     KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, IMPLS[impl], int(num_splits))
+                     KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, IMPLS[impl], _i32(num_splits, "num_splits"))
     return a
 
 
@@ -662,10 +670,10 @@ def verify_attn_q8(q_nope, q_pe, c_q8, c_scale, k_pe, prefix_len, *, parent=None
         raise ValueError("lse must be a contiguous float32 [B,T,H] tensor")
     a = VerifyQ8Args(B, T, H, 512, 64, q_nope.data_ptr(), _row_stride(q_nope), q_pe.data_ptr(), _row_stride(q_pe),
                      c_q8.data_ptr(), c_scale.data_ptr(), k_pe.data_ptr(), L, prefix_len.data_ptr(),
-                     L if max_kv_len is None else int(max_kv_len), None if parent is None else parent.data_ptr(),
+                     L if max_kv_len is None else _i32(max_kv_len, "max_kv_len"), None if parent is None else parent.data_ptr(),
                      None if vis is None else vis.data_ptr(), float(scale), out.data_ptr(), _dtype_code(out),
                      None if lse is None else lse.data_ptr(), _err_of(err),
-                     IMPLS[impl] if isinstance(impl, str) else int(impl), int(num_splits))
+                     IMPLS[impl] if isinstance(impl, str) else int(impl), _i32(num_splits, "num_splits"))
     if workspace is None:
         need = int(lib().kdt_verify_attn_q8_workspace_size(ctypes.byref(a)))
         workspace = _empty(need, torch.uint8, q_nope.device, stream) if need else None
@@ -735,7 +743,7 @@ def page_assign(table, held, free_pages, n_free, new_len, page_size, *, start=No
     W, stride = _check_table(table, B)
     _int32_of(held, B, "held"), _int32_of(new_len, B, "new_len"), _int32_of(n_free, 1, "n_free")
     _int32_of(free_pages, free_pages.numel(), "free_pages"), _int32_of(start, B, "start")
-    T = int(T)
+    T, page_size = _i32(T, "T"), _i32(page_size, "page_size")
     if T > 0:
         if start is None:
             raise ValueError("start is needed for slots")
@@ -745,7 +753,7 @@ def page_assign(table, held, free_pages, n_free, new_len, page_size, *, start=No
     else:
         slots = None
     a = PageArgs(B, W, table.data_ptr(), stride, held.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
-                 free_pages.numel(), int(page_size), new_len.data_ptr(), _ptr(start), T, _ptr(slots), _err_of(err))
+                 free_pages.numel(), page_size, new_len.data_ptr(), _ptr(start), T, _ptr(slots), _err_of(err))
     _check(lib().kdt_page_assign(ctypes.byref(a), _stream_ptr(stream)), "kdt_page_assign")
     return slots
 
@@ -791,10 +799,12 @@ def verify_attn_paged_plan(B, T, H, max_kv_len, page_size, *, out_dtype=None, bi
     T = 1, neither)."""
     import torch
     fake = 1 << 12
-    W = -(-int(max_kv_len) // int(page_size)) if page_size > 0 else 1
-    a = VerifyPagedArgs(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, 1, int(page_size), fake, max(W, 1), 0, fake, None,
-                        int(max_kv_len), None if bits or T == 1 else fake, fake if bits else None, 1.0, fake,
-                        KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, int(num_splits))
+    B, T, H, max_kv_len, page_size = (_i32(v, n) for v, n in ((B, "B"), (T, "T"), (H, "H"), (max_kv_len, "max_kv_len"),
+                                                              (page_size, "page_size")))
+    W = -(-max_kv_len // page_size) if page_size > 0 else 1
+    a = VerifyPagedArgs(B, T, H, 512, 64, fake, 0, fake, 0, fake, fake, 1, page_size, fake, max(W, 1), 0, fake, None,
+                        max_kv_len, None if bits or T == 1 else fake, fake if bits else None, 1.0, fake,
+                        KDT_BF16 if out_dtype == torch.bfloat16 else KDT_F32, None, None, _i32(num_splits, "num_splits"))
     p = Plan()
     _check(lib().kdt_verify_attn_paged_plan(ctypes.byref(a), ctypes.byref(p)), "kdt_verify_attn_paged_plan")
     return dict(impl=IMPL_NAMES.get(p.impl, p.impl), num_splits=p.num_splits, num_launches=p.num_launches,
@@ -840,8 +850,9 @@ def verify_attn_paged(q_nope, q_pe, c_kv, k_pe, table, prefix_len, *, n_rows=Non
         raise ValueError("lse must be a contiguous float32 [B,T,H] tensor")
     a = VerifyPagedArgs(B, T, H, 512, 64, q_nope.data_ptr(), _row_stride(q_nope), q_pe.data_ptr(), _row_stride(q_pe),
                         c_kv.data_ptr(), k_pe.data_ptr(), n, page, table.data_ptr(), W, stride, prefix_len.data_ptr(),
-                        _ptr(n_rows), min(W * page, 2 ** 31 - 257) if max_kv_len is None else int(max_kv_len), _ptr(parent), _ptr(vis),
-                        float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), _err_of(err), int(num_splits))
+                        _ptr(n_rows), min(W * page, 2 ** 31 - 257) if max_kv_len is None else _i32(max_kv_len, "max_kv_len"),
+                        _ptr(parent), _ptr(vis), float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), _err_of(err),
+                        _i32(num_splits, "num_splits"))
     if workspace is None:
         need = int(lib().kdt_verify_attn_paged_workspace_size(ctypes.byref(a)))
         workspace = _empty(need, torch.uint8, q_nope.device, stream) if need else None
@@ -860,7 +871,9 @@ def _setting(v, R, dtype, name, off):
         if v.dtype != dtype or v.numel() != R or not v.is_contiguous():
             raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor of {R} elements")
         return v.data_ptr(), off
-    return None, type(off)(v)
+    if type(off) is int:        # a number of tokens: any that passes 32 bits keeps all of them, as the largest that fits
+        return None, max(-1, min(int(v), 2 ** 31 - 1))
+    return None, float(v)
 
 
 def sample(logits, u, *, temperature=1.0, top_k=None, top_p=None, min_p=None, err=None, want_logp=True, stream=None):

@@ -191,3 +191,43 @@ def test_binding_refuses_wrong_tensors(kdt):
             [dict(u=u.double()), dict(u=u[:1]), dict(logits=lg[:, ::2]), dict(logits=lg[:1].expand(2, 10)),
              dict(temperature=u.double()), dict(top_k=u), dict(top_p=u[:1]), dict(min_p=torch.zeros(2, dtype=i32))])
     refused(kdt.sample, dict(logits=lg.half(), u=u), [{}], TypeError)
+
+
+def test_numbers_that_pass_32_bits(kdt, monkeypatch):
+    """ctypes drops what does not fit a C int: sizes that do not are refused, and a top-k that does not keeps all tokens."""
+    import torch
+    i32, bf, wrap = torch.int32, torch.bfloat16, 2 ** 32
+    c, k = torch.zeros(6, 16, 512, dtype=bf), torch.zeros(6, 16, 64, dtype=bf)
+    table, pre, par = torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(2, 3, dtype=i32)
+    q = torch.zeros(2, 3, 4, 576, dtype=bf)
+    qn, qp = q[..., :512], q[..., 512:]
+    dense, dk = torch.zeros(2, 40, 512, dtype=bf), torch.zeros(2, 40, 64, dtype=bf)
+    for kw in (dict(page_size=wrap + 16), dict(T=wrap + 2), dict(T=2 ** 31)):
+        with pytest.raises(ValueError):
+            kdt.page_assign(**{**dict(table=table, held=pre, free_pages=torch.zeros(6, dtype=i32), n_free=pre[:1], new_len=pre,
+                                      page_size=16, start=pre, T=0), **kw})
+    for kw in (dict(max_kv_len=wrap + 40), dict(num_splits=wrap + 1), dict(num_splits=-wrap)):
+        with pytest.raises(ValueError):
+            kdt.verify_attn_paged(qn, qp, c, k, table, pre, parent=par, **kw)
+        with pytest.raises(ValueError):
+            kdt.verify_attn(qn, qp, dense, dk, pre, parent=par, **kw)
+        with pytest.raises(ValueError):
+            kdt.verify_attn_paged_plan(**{**dict(B=2, T=3, H=4, max_kv_len=40, page_size=16), **kw})
+        with pytest.raises(ValueError):
+            kdt.verify_attn_q8_plan(**{**dict(B=2, T=3, H=4, max_kv_len=40), **kw})
+    for kw in (dict(B=wrap + 2), dict(T=wrap + 3), dict(H=wrap + 4), dict(page_size=wrap + 16)):
+        with pytest.raises(ValueError):
+            kdt.verify_attn_paged_plan(**{**dict(B=2, T=3, H=4, max_kv_len=40, page_size=16), **kw})
+
+    seen = []
+
+    class Lib:
+        @staticmethod
+        def kdt_sample(a, stream):
+            seen.append(a._obj.top_k_all)
+            return 0
+    monkeypatch.setattr(kdt.kdt, "lib", lambda: Lib)
+    monkeypatch.setattr(kdt.kdt, "_stream_ptr", lambda s: None)
+    for top_k in (wrap + 1, wrap, 2 ** 31, 2 ** 31 - 1, 10 ** 30, -wrap - 1, -2 ** 31 - 5, 0, None, 7, 7.0):
+        kdt.sample(torch.zeros(2, 10), torch.zeros(2), top_k=top_k)
+    assert all(v <= 0 or v >= 2 ** 31 - 1 for v in seen[:9]) and seen[9:] == [7, 7]
