@@ -25,9 +25,11 @@ constexpr int kMostGroup = 8;              // row tiles that walk the same keys 
 // sequence of 13 nodes of 128 heads over 400 keys takes 33, 37, 39 us for 33, a batch of 64 single tokens over 200
 // 24, 26, 24 for 24. (Two whole sequences of one block in one share took 30 us, a share each 20.)
 constexpr int kLeastBlocks = 2;
-// Shares a group from which several warps take a row's pieces in turn: 152 pieces of one token of 64 heads over 32768
-// keys 46 us for 60, 38 a row of two long contexts 89 for 91; but 2 - 3 pieces a row of 64 sequences 108 for 96.
-constexpr int kDeep = 8;
+// Shares a group from which several warps take a row's pieces in turn (us, L2 flushed, several warps / one): single
+// tokens of 64 heads over 8192 keys, 12.7 shares a group 55.9 / 54.3, 15.2 52.1 / 50.3, 19 47.7 / 48.2, 38 38.0 / 42.1;
+// of 128 heads 10.9 52.3 / 50.3, 19 42.1 / 42.1; 13 nodes of 32 heads over 4000 10.5 40.0 / 38.0, 21 31.6 / 31.8; of 16
+// heads over 2000 8 29.8 / 29.8, 15.2 27.7 / 28.3. With 3 - 8 pieces a row the several lose up to 29 %.
+constexpr int kDeep = 16;
 
 kdt_status check_args(const kdt_verify_paged_args *a) {
     if (!a) return KDT_ERR_NULL_ARG;

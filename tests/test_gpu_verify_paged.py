@@ -562,3 +562,11 @@ def test_a_batch_without_nodes_ends_behind_its_visibility(kdt, captured):
     torch.cuda.synchronize()
     assert [int(e.item()) for e in seen] == [2 * T] * 3
     assert (out == 3.0).all() and (lse == 4.0).all()
+
+
+@pytest.mark.parametrize("splits", [29, 30, 31, 32, 33, 48, 64])
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 30)])
+def test_both_joins_where_they_meet(kdt, T, H, splits):
+    """Two groups in shares on both sides of the number that decides how their pieces are joined."""
+    d = _inputs(T + splits, T, H, [4000, 3100])
+    _check(d, _call(kdt, d, num_splits=splits), 2.0 ** -24)
